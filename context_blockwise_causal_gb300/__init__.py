@@ -23,6 +23,16 @@ __all__ = [
     "cpattn_fwd_unfused",
     "cpattn_fwd_unfused_workspace_bytes",
     "cpattn_rope",
+    "cpattn_rope_frequencies",
+    "cpattn_qk_norm_rope",
+    "cpattn_qk_norm_rope_bwd",
+    "cpattn_fwd_window",
+    "cpattn_bwd_window",
+    "cpattn_bwd_window_workspace_bytes",
+    "cpattn_fwd_window_varlen",
+    "cpattn_bwd_window_varlen",
+    "cpattn_decode",
+    "cpattn_decode_workspace_bytes",
     "cpattn_fwd_varlen",
     "cpattn_bwd_varlen",
     "cpattn_bwd",
@@ -59,6 +69,20 @@ class CpattnError(RuntimeError):
 
 _LIB = None
 _i, _p, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_f, _i64 = ctypes.c_float, ctypes.c_int64
+
+
+class _Rows(ctypes.Structure):
+    """cpattn_rows: rows [b, n, h, d] with batch and token strides."""
+
+    _fields_ = [("data", _p), ("batch_stride", _i64), ("token_stride", _i64)]
+
+
+class _Rotary(ctypes.Structure):
+    """cpattn_rotary: a rotation plan."""
+
+    _fields_ = [("layout", _i), ("rot_dim", _i), ("magnitude", _f), ("s", _i), ("cp", _i), ("rank", _i),
+                ("cu_seqlens", _p), ("nseq", _i), ("positions", _p), ("positions_batch", _i64), ("inv_freq", _p)]
 
 
 _CHECKED = None
@@ -133,6 +157,34 @@ def _declare(lib):
     lib.cpattn_bwd_rank.restype = _i
     lib.cpattn_bwd_rank_stage.argtypes = [_i] + [_p] * 10 + [_sz] + [_i] * 8 + [ctypes.c_float, _p]
     lib.cpattn_bwd_rank_stage.restype = _i
+    rows, plan = ctypes.POINTER(_Rows), ctypes.POINTER(_Rotary)
+    lib.cpattn_rope_frequencies.argtypes = [_i, ctypes.c_double, _i] + [ctypes.c_double] * 4 + [_p]
+    lib.cpattn_rope_frequencies.restype = _i
+    lib.cpattn_rope_ex.argtypes = [rows, rows] + [_i] * 4 + [plan, _i, _p]
+    lib.cpattn_rope_ex.restype = _i
+    lib.cpattn_qk_norm_rope.argtypes = [rows, rows, _p, _p, _i, _f, rows, rows] + [_i] * 5 + [plan, _p]
+    lib.cpattn_qk_norm_rope.restype = _i
+    lib.cpattn_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i]
+    lib.cpattn_qk_norm_rope_bwd_workspace_bytes.restype = _sz
+    lib.cpattn_qk_norm_rope_bwd.argtypes = ([rows, rows, _p, _p, _i, _f] + [rows] * 4 + [_p, _p, _p, _sz] + [_i] * 5 +
+                                            [plan, _p])
+    lib.cpattn_qk_norm_rope_bwd.restype = _i
+    lib.cpattn_fwd_window.argtypes = [_p] * 5 + [_i] * 8 + [_f, _p]
+    lib.cpattn_fwd_window.restype = _i
+    lib.cpattn_bwd_window_workspace_bytes.argtypes = [_i] * 8
+    lib.cpattn_bwd_window_workspace_bytes.restype = _sz
+    lib.cpattn_bwd_window.argtypes = [_p] * 10 + [_sz] + [_i] * 8 + [_f, _p]
+    lib.cpattn_bwd_window.restype = _i
+    lib.cpattn_fwd_window_varlen.argtypes = [_p] * 6 + [_i] * 6 + [_f, _p]
+    lib.cpattn_fwd_window_varlen.restype = _i
+    lib.cpattn_bwd_window_varlen_workspace_bytes.argtypes = [_p] + [_i] * 6
+    lib.cpattn_bwd_window_varlen_workspace_bytes.restype = _sz
+    lib.cpattn_bwd_window_varlen.argtypes = [_p] * 10 + [_sz, _p] + [_i] * 6 + [_f, _p]
+    lib.cpattn_bwd_window_varlen.restype = _i
+    lib.cpattn_decode_workspace_bytes.argtypes = [_i] * 7
+    lib.cpattn_decode_workspace_bytes.restype = _sz
+    lib.cpattn_decode.argtypes = [_p] * 7 + [_sz] + [_i] * 5 + [_i64] * 7 + [_i, _i, _f, _p]
+    lib.cpattn_decode.restype = _i
     lib.cpattn_zigzag_index.argtypes = [_i, _i, _p]
     lib.cpattn_zigzag_index.restype = _i
     lib.cpattn_device_status.argtypes = [_p, ctypes.POINTER(_i)]
@@ -309,13 +361,29 @@ def cpattn_fwd_unfused(q, k, v, cp, causal=True, o=None, lse=None, workspace=Non
     return o, lse
 
 
-def cpattn_rope(x, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None, inverse=False, stream=None):
-    """Rotary position embedding of x [b, n, h, d] bf16, in place; returns x.
+def cpattn_rope(x, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None, inverse=False, stream=None, *,
+                positions=None, layout="half", rot_dim=None, inv_freq=None, magnitude=1.0, out=None):
+    """Rotary position embedding of x [b, n, h, d] bf16; returns the result.
 
     rank None: natural order (position = token index). rank r: x is virtual
     rank r's zigzag shard of a sequence of s tokens (n = s / cp).
     cu_seqlens: optional int32 CUDA tensor of packed-sample offsets (b == 1).
+    In place when ``out`` is None.
+
+    The keywords select the general form (cpattn_rope_ex): ``positions`` int32
+    CUDA tensor [n] or [b, n] in place of the sources above; ``layout``
+    "half" (features i and i + rot_dim/2 are a pair) or "interleaved" (2i and
+    2i + 1); ``rot_dim`` leading features that turn (a multiple of 16; default:
+    twice the length of inv_freq, or d); ``inv_freq`` host fp64 tensor of
+    rot_dim/2 radians per position (see cpattn_rope_frequencies) in place of
+    ``base``; ``magnitude`` multiplies the cosines and sines; ``out`` receives
+    the result. With any of them x and out may be strided: heads and features
+    contiguous, tokens and batch elements anywhere.
     """
+    if (positions is not None or layout != "half" or rot_dim is not None or inv_freq is not None or magnitude != 1.0 or
+            out is not None):
+        return _rope_ex(x, base, cp, rank, s, cu_seqlens, inverse, stream, positions, layout, rot_dim, inv_freq,
+                        magnitude, x if out is None else out)
     _check_act("x", x)
     if x.dim() != 4:
         raise ValueError("x must be [b, n, h, d]")
@@ -332,6 +400,181 @@ def cpattn_rope(x, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None, inver
     if rc:
         raise CpattnError(rc, "cpattn_rope")
     return x
+
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def cpattn_rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_len=0.0, low=1.0, high=32.0):
+    """Radians per position of each rotated pair, fp64 [rot_dim/2] (host).
+
+    ``scaling`` for contexts longer than the ``original_len`` trained on:
+    None; "linear" (frequencies divided by factor); "base" (base times
+    factor^(rot_dim/(rot_dim-2))); "turns" (pairs with at most ``low`` turns
+    over original_len divided by factor, with at least ``high`` kept, a mix
+    linear in the turns between); "index" (the same ends, the mix linear in
+    the pair's index)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}")
+    out = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    rc = library().cpattn_rope_frequencies(int(rot_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                           float(original_len), float(low), float(high), ctypes.c_void_p(out.data_ptr()))
+    if rc:
+        raise CpattnError(rc, "cpattn_rope_frequencies")
+    return out
+
+
+def _rows(name, t, shape=None):
+    """cpattn_rows of a bf16 tensor [b, n, h, d] with contiguous heads. A
+    stride of a dimension of one element means nothing and is not passed on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [b, n, h, d]")
+    b, n, h, d = t.shape
+    if shape is not None and (b, n, h, d) != tuple(shape):
+        raise ValueError(f"{name} has shape {(b, n, h, d)}, expected {tuple(shape)}")
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != d):
+        raise ValueError(f"{name} must have contiguous heads and features")
+    return _Rows(t.data_ptr(), sb if b > 1 else 0, sn if n > 1 else h * d)
+
+
+def _rotary(x, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude):
+    """cpattn_rotary for x [b, n, ...], and the tensors that must outlive it."""
+    b, n = x.shape[:2]
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {list(_ROPE_LAYOUTS)}")
+    if inv_freq is None:
+        inv_freq = cpattn_rope_frequencies(d if rot_dim is None else rot_dim, base)
+    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous fp64 host vector")
+    if rot_dim is None:
+        rot_dim = 2 * inv_freq.numel()
+    if inv_freq.numel() * 2 != rot_dim:
+        raise ValueError(f"inv_freq has {inv_freq.numel()} values, rot_dim {rot_dim} needs {rot_dim // 2}")
+    plan = _Rotary(layout=_ROPE_LAYOUTS[layout], rot_dim=int(rot_dim), magnitude=float(magnitude), cp=int(cp),
+                   rank=-1 if rank is None else int(rank), inv_freq=inv_freq.data_ptr())
+    plan.s = int(s) if s is not None else (n if rank is None else n * int(cp))
+    if cu_seqlens is not None:
+        if not cu_seqlens.is_cuda or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+            raise TypeError("cu_seqlens must be a contiguous int32 CUDA tensor")
+        plan.cu_seqlens, plan.nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+    if positions is not None:
+        if not positions.is_cuda or positions.dtype != torch.int32:
+            raise TypeError("positions must be an int32 CUDA tensor")
+        if tuple(positions.shape) not in ((n,), (b, n)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(n,)} or {(b, n)}")
+        if n > 1 and positions.stride(-1) != 1:
+            raise ValueError("the positions of a sequence must be contiguous")
+        plan.positions = positions.data_ptr()
+        plan.positions_batch = positions.stride(0) if positions.dim() == 2 and b > 1 else 0
+    return plan, inv_freq
+
+
+def _rope_ex(x, base, cp, rank, s, cu_seqlens, inverse, stream, positions, layout, rot_dim, inv_freq, magnitude, out):
+    xr = _rows("x", x)
+    outr = _rows("out", out, x.shape)
+    b, n, h, d = x.shape
+    plan, freq = _rotary(x, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    rc = library().cpattn_rope_ex(xr, outr, b, n, h, d, plan, 1 if inverse else 0,
+                                  _stream_handle(stream, x, out, cu_seqlens, positions))
+    if rc:
+        raise CpattnError(rc, "cpattn_rope_ex")
+    return out
+
+
+def _weights(q_weight, k_weight, d):
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"{name} must be a bf16 or fp32 CUDA tensor")
+        if tuple(w.shape) != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{d}] tensor")
+    if q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have one type")
+    return 1 if q_weight.dtype == torch.float32 else 0
+
+
+def _qk_dims(q, k):
+    qr, kr = _rows("q", q), _rows("k", k)
+    b, n, hq, d = q.shape
+    if k.shape[0] != b or k.shape[1] != n or k.shape[3] != d:
+        raise ValueError("k must be [b, n, hkv, d] matching q")
+    return qr, kr, b, n, hq, k.shape[2], d
+
+
+def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None,
+                        positions=None, layout="half", rot_dim=None, inv_freq=None, magnitude=1.0, q_out=None,
+                        k_out=None, stream=None):
+    """RMS norm of each head of q [b, n, hq, d] and k [b, n, hkv, d] with
+    weights [d] (bf16 or fp32), and the rotation of cpattn_rope, in one pass.
+
+    q, k and the outputs are bf16 and may be strided (e.g. parts of a fused
+    projection); an output may be its input. Positions and rotation as for
+    cpattn_rope. Returns (q_out, k_out), allocated contiguous when not given."""
+    qr, kr, b, n, hq, hkv, d = _qk_dims(q, k)
+    fp32 = _weights(q_weight, k_weight, d)
+    q_out = _empty(q.shape, q, stream) if q_out is None else q_out
+    k_out = _empty(k.shape, k, stream) if k_out is None else k_out
+    qo, ko = _rows("q_out", q_out, q.shape), _rows("k_out", k_out, k.shape)
+    plan, freq = _rotary(q, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    rc = library().cpattn_qk_norm_rope(qr, kr, q_weight.data_ptr(), k_weight.data_ptr(), fp32, float(eps), qo, ko, b, n,
+                                       hq, hkv, d, plan,
+                                       _stream_handle(stream, q, k, q_weight, k_weight, q_out, k_out, cu_seqlens,
+                                                      positions))
+    if rc:
+        raise CpattnError(rc, "cpattn_qk_norm_rope")
+    return q_out, k_out
+
+
+def cpattn_qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, eps=1e-6, base=10000.0, cp=1, rank=None, s=None,
+                            cu_seqlens=None, positions=None, layout="half", rot_dim=None, inv_freq=None, magnitude=1.0,
+                            dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Backward of cpattn_qk_norm_rope from its inputs q, k and the gradients
+    of its outputs. Returns (dq, dk, dq_weight, dk_weight); the weights'
+    gradients are fp32 [d], written (not accumulated)."""
+    qr, kr, b, n, hq, hkv, d = _qk_dims(q, k)
+    fp32 = _weights(q_weight, k_weight, d)
+    gq, gk = _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape)
+    dq = _empty(q.shape, q, stream) if dq is None else dq
+    dk = _empty(k.shape, k, stream) if dk is None else dk
+    dq_weight = _empty((d,), q, stream, torch.float32) if dq_weight is None else dq_weight
+    dk_weight = _empty((d,), q, stream, torch.float32) if dk_weight is None else dk_weight
+    _check_f32("dq_weight", dq_weight, (d,))
+    _check_f32("dk_weight", dk_weight, (d,))
+    rq, rk = _rows("dq", dq, q.shape), _rows("dk", dk, k.shape)
+    plan, freq = _rotary(q, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    lib = library()
+    workspace = _workspace(workspace, lib.cpattn_qk_norm_rope_bwd_workspace_bytes(d), q, stream)
+    rc = lib.cpattn_qk_norm_rope_bwd(qr, kr, q_weight.data_ptr(), k_weight.data_ptr(), fp32, float(eps), gq, gk, rq, rk,
+                                     dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), b, n, hq, hkv, d, plan,
+                                     _stream_handle(stream, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight,
+                                                    dk_weight, workspace, cu_seqlens, positions))
+    if rc:
+        raise CpattnError(rc, "cpattn_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _empty(shape, like, stream, dtype=torch.bfloat16):
+    """A new tensor beside ``like``, from the memory of the stream that the
+    call runs on: the caching allocator then hands it to nobody else before
+    that stream is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace(workspace, need, like, stream):
+    if workspace is None:
+        return _empty((max(int(need), 16),), like, stream, torch.uint8)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return workspace
 
 
 def _cu_host(cu_seqlens):
@@ -440,6 +683,176 @@ def cpattn_bwd(q, k, v, o, lse, do, cp, causal=True, dq=None, dk=None, dv=None, 
     if rc:
         raise CpattnError(rc, "cpattn_bwd" if stage is None else "cpattn_bwd_stage")
     return dq, dk, dv
+
+
+def _window_dims(q, k, v):
+    _check_act("q", q)
+    _check_act("k", k)
+    _check_act("v", v, k.shape)
+    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise ValueError("q must be [b, sq, hq, d] and k, v [b, skv, hkv, d]")
+    return q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3]
+
+
+def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, stream=None):
+    """Attention with a sliding window and visible first tokens, forward.
+
+    The query at position p sees key j when j <= p and p - j < window or
+    j < sinks. q [b, sq, hq, d]; k, v [b, skv, hkv, d] with skv >= sq: the
+    queries are the last sq positions. Returns (o like q, lse [b, hq, sq])."""
+    b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
+    o = _empty(q.shape, q, stream) if o is None else o
+    _check_act("o", o, q.shape)
+    lse = _empty((b, hq, sq), q, stream, torch.float32) if lse is None else lse
+    _check_f32("lse", lse, (b, hq, sq))
+    rc = library().cpattn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), b, sq, skv,
+                                     hq, hkv, d, int(window), int(sinks), 0.0 if scale is None else float(scale),
+                                     _stream_handle(stream, q, k, v, o, lse))
+    if rc:
+        raise CpattnError(rc, "cpattn_fwd_window")
+    return o, lse
+
+
+def cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks=0):
+    return int(library().cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, int(window), int(sinks)))
+
+
+def cpattn_bwd_window(q, k, v, o, lse, do, window, sinks=0, scale=None, dq=None, dk=None, dv=None, workspace=None,
+                      stream=None):
+    """Backward of cpattn_fwd_window from its o and lse. Returns (dq, dk, dv)."""
+    b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
+    _check_act("o", o, q.shape)
+    _check_act("do", do, q.shape)
+    _check_f32("lse", lse, (b, hq, sq))
+    dq = _empty(q.shape, q, stream) if dq is None else dq
+    dk = _empty(k.shape, k, stream) if dk is None else dk
+    dv = _empty(v.shape, v, stream) if dv is None else dv
+    _check_act("dq", dq, q.shape)
+    _check_act("dk", dk, k.shape)
+    _check_act("dv", dv, v.shape)
+    need = cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks)
+    workspace = _workspace(workspace, need, q, stream)
+    rc = library().cpattn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                     do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), b, sq, skv, hq, hkv, d, int(window),
+                                     int(sinks), 0.0 if scale is None else float(scale),
+                                     _stream_handle(stream, q, k, v, o, lse, do, dq, dk, dv, workspace))
+    if rc:
+        raise CpattnError(rc, "cpattn_bwd_window")
+    return dq, dk, dv
+
+
+def cpattn_fwd_window_varlen(q, k, v, cu_seqlens, window, sinks=0, scale=None, o=None, lse=None, stream=None):
+    """cpattn_fwd_window over packed samples, each with its own window and
+    first tokens. q [total, hq, d], k/v [total, hkv, d]; cu_seqlens: sample
+    offsets (host list/tensor). Returns (o [total, hq, d], lse [hq, total])."""
+    total, hq, hkv, d = _packed_dims(q, k, v)
+    cu, cu_p, nseq = _cu_host(cu_seqlens)
+    if int(cu[-1]) != total:
+        raise ValueError("cu_seqlens must end at the packed length")
+    o = _empty(q.shape, q, stream) if o is None else o
+    _check_act("o", o, q.shape)
+    lse = _empty((hq, total), q, stream, torch.float32) if lse is None else lse
+    _check_f32("lse", lse, (hq, total))
+    rc = library().cpattn_fwd_window_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                            cu_p, nseq, hq, hkv, d, int(window), int(sinks),
+                                            0.0 if scale is None else float(scale),
+                                            _stream_handle(stream, q, k, v, o, lse))
+    if rc:
+        raise CpattnError(rc, "cpattn_fwd_window_varlen")
+    return o, lse
+
+
+def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, scale=None, dq=None, dk=None, dv=None,
+                             workspace=None, stream=None):
+    """Backward of cpattn_fwd_window_varlen. Returns (dq, dk, dv)."""
+    total, hq, hkv, d = _packed_dims(q, k, v)
+    cu, cu_p, nseq = _cu_host(cu_seqlens)
+    if int(cu[-1]) != total:
+        raise ValueError("cu_seqlens must end at the packed length")
+    _check_act("o", o, q.shape)
+    _check_act("do", do, q.shape)
+    _check_f32("lse", lse, (hq, total))
+    dq = _empty(q.shape, q, stream) if dq is None else dq
+    dk = _empty(k.shape, k, stream) if dk is None else dk
+    dv = _empty(v.shape, v, stream) if dv is None else dv
+    _check_act("dq", dq, q.shape)
+    _check_act("dk", dk, k.shape)
+    _check_act("dv", dv, v.shape)
+    lib = library()
+    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, int(window), int(sinks))
+    workspace = _workspace(workspace, need, q, stream)
+    rc = lib.cpattn_bwd_window_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                      do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), cu_p, nseq, hq, hkv, d, int(window),
+                                      int(sinks), 0.0 if scale is None else float(scale),
+                                      _stream_handle(stream, q, k, v, o, lse, do, dq, dk, dv, workspace))
+    if rc:
+        raise CpattnError(rc, "cpattn_bwd_window_varlen")
+    return dq, dk, dv
+
+
+def cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
+    """Workspace bytes of cpattn_decode on the current device."""
+    return int(library().cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, int(window), int(sinks)))
+
+
+def _cache_strides(name, t):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [b, cap, hkv, d]")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have contiguous features")
+    b, cap, h, _ = t.shape
+    return sb if b > 1 else 0, st if cap > 1 else 0, sh if h > 1 else 0
+
+
+def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o=None, lse=None, workspace=None,
+                  stream=None):
+    """Attention of one new token per sequence over a cache.
+
+    q [b, hq, d]; k_cache, v_cache [b, cap, hkv, d] of any strides with
+    contiguous features (a transposed [b, hkv, cap, d] too); lengths int32
+    CUDA tensor [b]: tokens held of each sequence, the new one's key and value
+    among them. window 0: every key; otherwise the last ``window`` keys and
+    the first ``sinks``. Returns (o [b, hq, d], lse [b, hq])."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if q.dim() != 3:
+        raise ValueError("q must be [b, hq, d]")
+    b, hq, d = q.shape
+    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
+        raise ValueError("q must have contiguous heads and features")
+    kb, kt, kh = _cache_strides("k_cache", k_cache)
+    vb, vt, vh = _cache_strides("v_cache", v_cache)
+    if k_cache.shape != v_cache.shape or k_cache.shape[0] != b or k_cache.shape[3] != d:
+        raise ValueError("k_cache and v_cache must be [b, cap, hkv, d] matching q")
+    cap, hkv = k_cache.shape[1], k_cache.shape[2]
+    if not isinstance(lengths, torch.Tensor) or not lengths.is_cuda or lengths.dtype != torch.int32:
+        raise TypeError("lengths must be an int32 CUDA tensor")
+    if tuple(lengths.shape) != (b,) or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a contiguous [{b}] tensor")
+    o = _empty((b, hq, d), q, stream) if o is None else o
+    _check_act("o", o, (b, hq, d))
+    lse = _empty((b, hq), q, stream, torch.float32) if lse is None else lse
+    _check_f32("lse", lse, (b, hq))
+    handle = _stream_handle(stream, q, k_cache, v_cache, lengths, o, lse, workspace)
+    need = 16 if workspace is not None else cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window, sinks)
+    workspace = _workspace(workspace, need, q, stream)
+    rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
+                                 o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), b, hq, hkv, d, cap,
+                                 q.stride(0) if b > 1 else 0, kb, kt, kh, vb, vt, vh, int(window), int(sinks),
+                                 0.0 if scale is None else float(scale), handle)
+    if rc:
+        raise CpattnError(rc, "cpattn_decode")
+    return o, lse
 
 
 def _rank_dims(q, k, v, cp):

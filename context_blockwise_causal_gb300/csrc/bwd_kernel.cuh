@@ -30,6 +30,7 @@
 
 #include "cp_schedule.cuh"
 #include "ptx.cuh"
+#include "win_schedule.cuh"
 
 namespace cpattn {
 
@@ -56,6 +57,11 @@ struct BwdArgs {
   // extents for the checked build (bounds_ok): rows of the query-side and
   // key/value-side tensors, floats of lse and of each row vector
   int64_t q_rows, kv_rows, lse_len, vec_len;
+  // window form: fp32 dK and dV (unscaled) of the parts of cut walks,
+  // [parts][128][D] each (see win_schedule.cuh); part_len elements each
+  float* part_dk = nullptr;
+  float* part_dv = nullptr;
+  int64_t part_len = 0;
 };
 
 enum BwdStatusBits : unsigned int {
@@ -80,7 +86,7 @@ __device__ __forceinline__ int64_t ld_pos(const CpGeom& g, int ntp, int seq, int
 // rows (D/8 lanes x 16 bytes per row, so 32*16/(2D) rows per instruction),
 // the partial dot products are summed by xor shuffles inside each row's lane
 // group, and the lane that owns the row keeps its sum.
-template <int D>
+template <int D, bool kWin = false>
 __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
   constexpr int kLanesPerRow = D / 8;              // 16 (d = 128) or 8 (d = 64)
   constexpr int kRowsPerLoad = 32 / kLanesPerRow;  // rows one warp-wide load covers
@@ -146,11 +152,16 @@ __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
       seq = lo;
       tl = t - g.cu[lo];
     }
-    const SeqGeom q = seq_geom(g, seq);
-    int chunk = tl / q.c;  // rank-local form: 0 or 1, the rank's first or second chunk
-    const int in = tl - chunk * q.c;
-    if (g.rank >= 0) chunk = chunk ? 2 * g.cp - 1 - g.rank : g.rank;
-    const int64_t pos = ld_pos(g, a.ntp, seq, h, chunk, in / kTile, q.tpc, in % kTile);
+    int64_t pos;
+    if constexpr (kWin) {
+      pos = int64_t(seq * g.hq + h) * a.ntp + tl;
+    } else {
+      const SeqGeom q = seq_geom(g, seq);
+      int chunk = tl / q.c;  // rank-local form: 0 or 1, the rank's first or second chunk
+      const int in = tl - chunk * q.c;
+      if (g.rank >= 0) chunk = chunk ? 2 * g.cp - 1 - g.rank : g.rank;
+      pos = ld_pos(g, a.ntp, seq, h, chunk, in / kTile, q.tpc, in % kTile);
+    }
     const int64_t li = (int64_t(bi) * g.hq + h) * a.lse_stride + t;
     if (!bounds_ok(pos >= 0 && pos < a.vec_len && li < a.lse_len && idx < a.q_rows * g.hq, a.status)) continue;
     a.dvec[pos] = acc;
@@ -280,7 +291,43 @@ struct DkdvCfg {
 //   warps:        P(i+1) from S^T(i+1) ..............| dS(i+1)  |
 // Units walk their query tiles from the end of the sequence down (QWalk), so
 // the CTAs in flight read the same Q/dO tiles from L2.
-template <int D, bool kShortWaits = false>
+template <bool kWin>
+__device__ __forceinline__ auto dkdv_unit_of(const CpGeom& g, int idx) {
+  if constexpr (kWin)
+    return win_dkdv_unit(g, idx);
+  else
+    return bwd_decode_unit(g, idx);
+}
+// First key row of a unit's sequence, and its query tiles from the last down.
+template <bool kWin, class U>
+__device__ __forceinline__ int kv_first_row(const U& u) {
+  if constexpr (kWin)
+    return u.kv0;
+  else
+    return u.tok0;
+}
+struct WinQWalk {
+  int t, left;
+  __device__ WinQWalk(const CpGeom&, const BwdWinUnit& U) : t(U.qa + U.nq - 1), left(U.nq) {}
+  __device__ bool next(int& chunk, int& tile, bool& is_diag) {
+    if (left <= 0) return false;
+    --left;
+    chunk = 0;
+    tile = t--;
+    is_diag = false;
+    return true;
+  }
+};
+template <bool kWin>
+struct QWalkOf {
+  using type = QWalk;
+};
+template <>
+struct QWalkOf<true> {
+  using type = WinQWalk;
+};
+
+template <int D, bool kShortWaits = false, bool kWin = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cpattn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
@@ -321,7 +368,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int lane = threadIdx.x & 31;
   const CpGeom& g = a.g;
   const int G = g.hq / g.hkv;
-  const int num_units = bwd_num_units(g);
+  const int num_units = kWin ? int(win_dkdv_units(g)) : bwd_num_units(g);
   const int grid = gridDim.x;
 
   if (threadIdx.x == 0) {
@@ -371,8 +418,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t nq = 0;    // Q tiles issued: item, or item + 1 when a dO wait gave up
       uint32_t nkv = 0;   // K/V tile pairs issued
       int ul = 0;
-      auto load_item = [&](const BwdUnit& U, int chunk, int tile, int h) -> bool {
-        const int row = U.tok0 + q_chunk_row(g, chunk, U.c) + tile * kTile;
+      auto load_item = [&](const auto& U, int chunk, int tile, int h) -> bool {
+        const int row = U.tok0 + (kWin ? 0 : q_chunk_row(g, chunk, U.c)) + tile * kTile;
         bounds_ok(row >= 0 && row < a.q_rows && h >= 0 && h < g.hq, a.status);
         const uint32_t qs = item % C::kQStages, os = item % C::kOStages;
         if (item >= C::kQStages &&
@@ -399,9 +446,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const BwdUnit U = bwd_decode_unit(g, idx);
+        const auto U = dkdv_unit_of<kWin>(g, idx);
         if (U.items == 0) continue;  // a tile a shorter packed sample does not have
-        QWalk w(g, U);
+        typename QWalkOf<kWin>::type w(g, U);
         int chunk, tile;
         bool dg;
         bool first = true;
@@ -413,7 +460,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               first = false;
               if (ul > 0 && !(ok = mbar_wait_lean(kv_empty, (ul - 1) & 1, abort_flag, plimit))) break;
               mbar_arrive_expect_tx(kv_full, 2 * C::kTileBytes);
-              const int krow = U.tok0 + U.k_t0;
+              const int krow = kv_first_row<kWin>(U) + U.k_t0;
               bounds_ok(krow >= 0 && krow < a.kv_rows && U.g < g.hkv, a.status);
               for (int x = 0; x < D; x += 64) {
                 tma_load_3d(sK + (x / 64) * (kTile * 128), &tmk, kv_full, x, U.g, krow);
@@ -473,7 +520,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const BwdUnit U = bwd_decode_unit(g, idx);
+        const auto U = dkdv_unit_of<kWin>(g, idx);
         if (U.items == 0) continue;  // a tile a shorter packed sample does not have
         const int n = U.items;
         // prologue: S^T and dP^T of the unit's first block. The S^T columns
@@ -558,14 +605,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int rd = 0; ok; ++rd) {
       const int idx = snake_unit(rd, blockIdx.x, grid);
       if (idx >= num_units) break;
-      const BwdUnit U = bwd_decode_unit(g, idx);
+      const auto U = dkdv_unit_of<kWin>(g, idx);
       const bool key_ok = jr < U.k_valid;
       if (U.items == 0) {
         // No query of this call sees the tile. A tile a shorter packed sample
         // does not have has no rows (k_valid == 0); a real one (rank-local
         // form: no query of the rank reaches it) gets a zero share.
-        if (key_ok && bounds_ok(int64_t(U.tok0) + U.k_t0 + jr < a.kv_rows && U.g < g.hkv, a.status)) {
-          const int64_t off = ((int64_t(U.tok0) + U.k_t0 + jr) * g.hkv + U.g) * D + hf * (D / 2);
+        const int krow = kv_first_row<kWin>(U) + U.k_t0 + jr;
+        if (key_ok && bounds_ok(krow < a.kv_rows && U.g < g.hkv, a.status)) {
+          const int64_t off = (int64_t(krow) * g.hkv + U.g) * D + hf * (D / 2);
 #pragma unroll
           for (int c0 = 0; c0 < D / 2; c0 += 8) {
             *reinterpret_cast<uint4*>(a.dv + off + c0) = make_uint4(0u, 0u, 0u, 0u);
@@ -574,7 +622,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         continue;
       }
-      QWalk w(g, U);
+      typename QWalkOf<kWin>::type w(g, U);
       int chunk = 0, tile = 0;
       bool dg = false;
       int jh = 0;  // item j's head within the group (j mod G, counted)
@@ -601,7 +649,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int r = 0; r < 4; ++r) lv[cb][r] = *reinterpret_cast<const float2*>(Lq + 32 * cb + 8 * r);
         // Blocks away from the diagonal and from ragged chunk ends need no mask.
-        const bool full = !dg && q_valid == kTile && U.k_valid == kTile;
+        // window form: position of the block's first query, relative to its first key
+        [[maybe_unused]] int pq = 0;
+        bool full = !dg && q_valid == kTile && U.k_valid == kTile;
+        if constexpr (kWin) {
+          pq = U.off + tile * kTile - U.k_t0;
+          full = full && win_block_full(g, U.off + tile * kTile, U.k_t0);
+        }
         uint32_t valid[2][4];
         uint32_t pp[2][16];
         if (full) {
@@ -616,7 +670,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int f = 0; f < 4; ++f) {
               const int kr = wq * 32 + 8 * f + g4;  // key row of fragment row f (16u + 8e = 8f)
               const int qb = 64 * hf + 32 * cb;
-              valid[cb][f] = kr < U.k_valid ? bit_range(dg ? kr - qb : 0, q_valid - qb) : 0u;
+              if constexpr (kWin) {
+                // queries from the key's own position on, up to its window's
+                // last one unless it is a first token
+                const int from = kr - pq;
+                int to = q_valid;
+                if (U.k_t0 + kr >= g.sinks && from + g.window < to) to = from + g.window;
+                valid[cb][f] = kr < U.k_valid ? bit_range(from - qb, to - qb) : 0u;
+              } else {
+                valid[cb][f] = kr < U.k_valid ? bit_range(dg ? kr - qb : 0, q_valid - qb) : 0u;
+              }
             }
           softmax_p_frag<true>(ra, sl2, lv[0], valid[0], c4, pp[0]);
           softmax_p_frag<true>(rb, sl2, lv[1], valid[1], c4, pp[1]);
@@ -652,7 +715,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // ---- dK, dV of the tile: TMEM -> bf16 -> global, 32 columns at a time
       if (!(ok = mbar_wait_lean(dkv_full, ul & 1, abort_flag, kWaitLimitNs))) break;
       tc_fence_after();
-      const int64_t off = ((int64_t(U.tok0) + U.k_t0 + jr) * g.hkv + U.g) * D + hf * (D / 2);
+      const int krow = kv_first_row<kWin>(U) + U.k_t0 + jr;
+      const int64_t off = (int64_t(krow) * g.hkv + U.g) * D + hf * (D / 2);
 #pragma unroll
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
         uint32_t rv[32], rk[32];
@@ -664,7 +728,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(dkv_empty);
         }
-        if (key_ok && bounds_ok(int64_t(U.tok0) + U.k_t0 + jr < a.kv_rows && U.g < g.hkv, a.status)) {
+        if constexpr (kWin) {
+          if (U.slot >= 0) {  // a part of a cut walk: fp32, added up by cpattn_window_join_kernel
+            const int64_t po = (int64_t(U.slot) * kTile + jr) * D + hf * (D / 2) + c0;
+            if (bounds_ok(po + 32 <= a.part_len, a.status)) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4) {
+                *reinterpret_cast<uint4*>(a.part_dv + po + q) = make_uint4(rv[q], rv[q + 1], rv[q + 2], rv[q + 3]);
+                *reinterpret_cast<uint4*>(a.part_dk + po + q) = make_uint4(rk[q], rk[q + 1], rk[q + 2], rk[q + 3]);
+              }
+            }
+            continue;
+          }
+        }
+        if (key_ok && bounds_ok(krow < a.kv_rows && U.g < g.hkv, a.status)) {
 #pragma unroll
           for (int q = 0; q < 32; q += 8) {
             uint4 pv, pk;
@@ -774,7 +851,15 @@ struct DqCfg {
 //   S(j+1) | dQ(j) | dP(j+1) | S(j+2) | ...
 // so the exponentials of tile j overlap dQ(j-1) and dP(j), and only the dS
 // step of each warp's first 32 keys lies on the tensor core's critical path.
-template <int D, bool kShortWaits = false>
+template <bool kWin>
+__device__ __forceinline__ auto dq_unit_of(const CpGeom& g, int idx) {
+  if constexpr (kWin)
+    return win_dq_unit(g, idx);
+  else
+    return dq_decode_unit(g, idx);
+}
+
+template <int D, bool kShortWaits = false, bool kWin = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cpattn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
@@ -812,7 +897,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const CpGeom& g = a.g;
-  const int num_units = dq_num_units(g);
+  const int num_units = kWin ? int(win_dq_units(g)) : dq_num_units(g);
   const int grid = gridDim.x;
 
   if (threadIdx.x == 0) {
@@ -873,7 +958,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const FwdUnit U = dq_decode_unit(g, idx);
+        const auto U = dq_unit_of<kWin>(g, idx);
         if (U.n == 0) continue;  // a tile a shorter packed sample does not have
         // the Q/dO stage is free once the element-wise warps copied the
         // previous unit's tiles into TMEM
@@ -888,10 +973,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         KvWalk w(g, U);
         int chunk, tile;
         bool dg;
-        while (ok && w.next(chunk, tile, dg)) {
-          const int row = U.tok0 + kv_chunk_row(g, chunk, U.c) + tile * kTile;
-          // V before K: V is released by the dP MMA, K only after dQ
-          ok = load(&tmv, U.g0, row) && load(&tmk, U.g0, row);
+        // V before K: V is released by the dP MMA, K only after dQ
+        if constexpr (kWin) {
+          for (int j = 0; ok && j < U.n; ++j) {
+            const int row = U.kv0 + win_tile(U, j) * kTile;
+            ok = load(&tmv, U.g0, row) && load(&tmk, U.g0, row);
+          }
+        } else {
+          while (ok && w.next(chunk, tile, dg)) {
+            const int row = U.tok0 + kv_chunk_row(g, chunk, U.c) + tile * kTile;
+            ok = load(&tmv, U.g0, row) && load(&tmk, U.g0, row);
+          }
         }
         ++ul;
       }
@@ -943,7 +1035,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const FwdUnit U = dq_decode_unit(g, idx);
+        const auto U = dq_unit_of<kWin>(g, idx);
         if (U.n == 0) continue;  // a tile a shorter packed sample does not have
         const int n = U.n;
         // prologue: S and dP of the unit's first key tile, once Q/dO are in
@@ -1031,7 +1123,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int rd = 0; ok; ++rd) {
       const int idx = snake_unit(rd, blockIdx.x, grid);
       if (idx >= num_units) break;
-      const FwdUnit U = dq_decode_unit(g, idx);
+      const auto U = dq_unit_of<kWin>(g, idx);
       if (U.n == 0) continue;  // a tile a shorter packed sample does not have
       // ---- this row's Q and dO (columns hf*D/2 ..) into TMEM as packed bf16
       ok = mbar_wait_lean(q_full, ul & 1, abort_flag, kWaitLimitNs) &&
@@ -1085,12 +1177,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int chunk = 0, tile = 0;
         bool dg = false;
         int n_valid = kTile;
-        if (walkless) {
-          dg = j == jdiag;
-        } else {
-          w.next(chunk, tile, dg);
-          const int rem = U.c - tile * kTile;
-          n_valid = rem < kTile ? rem : kTile;
+        if constexpr (!kWin) {
+          if (walkless) {
+            dg = j == jdiag;
+          } else {
+            w.next(chunk, tile, dg);
+            const int rem = U.c - tile * kTile;
+            n_valid = rem < kTile ? rem : kTile;
+          }
         }
         if (!(ok = mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
@@ -1100,13 +1194,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
-        const bool full = !dg && n_valid == kTile;
-        // key column c (of this warp's 64) is valid when it is inside its
-        // chunk and (on the diagonal) c <= jr
         const int cb = hf * 64;
-        int hi = n_valid - cb;
-        if (dg && jr + 1 - cb < hi) hi = jr + 1 - cb;
-        const uint32_t v0 = full ? 0u : bit_range(0, hi), v1 = full ? 0u : bit_range(0, hi - 32);
+        bool full;
+        uint32_t v0 = 0u, v1 = 0u;  // bit c: key column c (of this warp's 64) is visible
+        if constexpr (kWin) {
+          const int p0 = U.off + U.q_t0, kb = win_tile(U, j) * kTile;
+          full = win_block_full(g, p0, kb);
+          if (!full) {
+            // columns up to the row's own position, from its window's first on or before the last first token
+            const int hi = p0 + jr + 1 - kb - cb, lo = hi - g.window;
+            const int first = g.sinks - kb - cb < hi ? g.sinks - kb - cb : hi;
+            v0 = bit_range(lo, hi) | bit_range(0, first);
+            v1 = bit_range(lo - 32, hi - 32) | bit_range(0, first - 32);
+          }
+        } else {
+          full = !dg && n_valid == kTile;
+          // key column c is valid when it is inside its chunk and (on the
+          // diagonal) c <= jr
+          int hi = n_valid - cb;
+          if (dg && jr + 1 - cb < hi) hi = jr + 1 - cb;
+          v0 = full ? 0u : bit_range(0, hi);
+          v1 = full ? 0u : bit_range(0, hi - 32);
+        }
         uint32_t pp0[16], pp1[16];
         if (full) {
           p_row32<false>(r0, sl2, l2, 0u, pp0);
@@ -1178,6 +1287,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+  }
+}
+
+// ================================================================ window form
+// dK and dV of the key tiles whose walks were cut (win_schedule.cuh): the
+// parts' fp32 results added in order, dK scaled, rounded once to bf16. One
+// block per (sequence, KV head, tile) and 32 rows; a few MB in all, so this
+// kernel is bound by its launch.
+template <int D>
+__global__ void __launch_bounds__(256) cpattn_window_join_kernel(const BwdArgs a) {
+  const CpGeom& g = a.g;
+  const int cut = win_cut_tiles(g);
+  const int rb = blockIdx.x & 3;  // 32-row quarter of the tile
+  const int x = blockIdx.x >> 2;
+  const int y = x / cut, kt = x - y * cut;
+  const int seq = y / g.hkv, h = y - seq * g.hkv;
+  const WinSeq s = win_seq(g, seq);
+  if (kt * kTile >= s.klen) return;
+  int qa, nq;
+  win_query_tiles(g, s, kt, qa, nq);
+  const int np = win_parts(g, nq);
+  constexpr int kVec = D / 4;
+  for (int i = threadIdx.x; i < 32 * kVec; i += blockDim.x) {
+    const int jr = rb * 32 + i / kVec, c = (i % kVec) * 4;
+    const int krow = s.kv0 + kt * kTile + jr;
+    if (kt * kTile + jr >= s.klen) continue;
+    float4 sk = make_float4(0.f, 0.f, 0.f, 0.f), sv = sk;
+    for (int p = 0; p < np; ++p) {
+      const int64_t po = ((int64_t(x) * g.sink_parts + p) * kTile + jr) * D + c;
+      if (!bounds_ok(po + 4 <= a.part_len, a.status)) continue;
+      const float4 k4 = *reinterpret_cast<const float4*>(a.part_dk + po);
+      const float4 v4 = *reinterpret_cast<const float4*>(a.part_dv + po);
+      sk.x += k4.x; sk.y += k4.y; sk.z += k4.z; sk.w += k4.w;
+      sv.x += v4.x; sv.y += v4.y; sv.z += v4.z; sv.w += v4.w;
+    }
+    if (!bounds_ok(krow < a.kv_rows && h < g.hkv, a.status)) continue;
+    const int64_t off = (int64_t(krow) * g.hkv + h) * D + c;
+    *reinterpret_cast<uint2*>(a.dk + off) = make_uint2(pack_bf16x2(sk.x * a.scale, sk.y * a.scale),
+                                                       pack_bf16x2(sk.z * a.scale, sk.w * a.scale));
+    *reinterpret_cast<uint2*>(a.dv + off) = make_uint2(pack_bf16x2(sv.x, sv.y), pack_bf16x2(sv.z, sv.w));
   }
 }
 

@@ -78,6 +78,12 @@ struct CpGeom {
   int tile_pairs = 0;    // forward units pair two query tiles of one head (see fwd_decode_unit)
   int tp_block = 0;      // tile pairs: (sequence, query head) combinations per unit block (0: one block)
   int tp_slots = 0;      // tile pairs: unit slots per block (its units, then empty slots)
+  // sliding-window form (win_schedule.cuh): s is the queries per sequence
+  int kv_s = 0;          // keys per sequence (>= s)
+  int window = 0;        // a query sees the last `window` keys up to its own ...
+  int sinks = 0;         // ... and the first `sinks` keys
+  int part_tiles = 0;    // dK/dV: query tiles per part of a cut walk
+  int sink_parts = 0;    // dK/dV: parts per cut walk (1: none is cut)
   // divisors of the backward's unit decodes (set_fast_divs; set again
   // whenever b, hq, hkv or tpc change)
   FastDiv fd_hq, fd_hkv, fd_G, fd_tpc, fd_bhq, fd_bhkv;

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "../../include/cpattn.h"
+#include "api_common.h"
 #include "bwd_kernel.cuh"
 #include "fwd_kernel.cuh"
 #include "merge_kernel.cuh"
@@ -29,24 +30,13 @@ static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratch
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-  bool init = false;
-  bool sm103 = false;
-  int num_sms = 0;
-  unsigned int* status = nullptr;
-  // kernel attributes already set, per kernel; set once, read by any thread
-  std::atomic<bool> fwd_attr[17] = {};  // [d == 128][step form][five-slot ring][tile pairs]; 16: self-test
-  std::atomic<bool> bwd_attr[3] = {};   // [d == 128]; 2: self-test
-};
 DeviceInfo g_devs[kMaxDevices];
 std::mutex g_mu;
 // Cap on the grid of the persistent attention kernels (0: one CTA per SM).
 std::atomic<int> g_max_ctas{0};
 
-// Grid of a persistent kernel over `units` work units: one CTA per SM, at
-// most the cap set by cpattn_set_max_ctas, at most one per unit.
+}  // namespace
+
 int persistent_grid(const DeviceInfo* di, int64_t units) {
   const int cap_set = g_max_ctas.load(std::memory_order_relaxed);
   const int cap = cap_set > 0 && cap_set < di->num_sms ? cap_set : di->num_sms;
@@ -77,7 +67,7 @@ int device_info(DeviceInfo** out) {
   return di.sm103 ? CPATTN_OK : CPATTN_ERR_UNSUPPORTED_ARCH;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 int check_geometry(int b, int s, int hq, int hkv, int d, int cp) {
   if (b < 1 || s < 1 || hq < 1 || hkv < 1 || cp < 1) return CPATTN_ERR_INVALID_ARG;
@@ -157,11 +147,6 @@ int launch_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
 }  // namespace cpattn
 
 using namespace cpattn;
-
-namespace {
-bool valid_scale(float scale) { return scale > 0.f && scale <= 3.0e38f; }
-double default_scale(int d) { return 1.0 / std::sqrt(double(d)); }
-}  // namespace
 
 namespace {
 // The fused forward. `geom` overrides the uniform geometry (packed samples,
@@ -394,8 +379,6 @@ extern "C" int cpattn_fwd_unfused(const void* q, const void* k, const void* v, v
 
 namespace cpattn {
 namespace {
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct BwdLayout {
   size_t lvec, dvec, total;

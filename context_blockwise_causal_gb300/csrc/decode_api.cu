@@ -1,0 +1,127 @@
+// C-ABI entry points of single-token attention over a cache (include/cpattn.h).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/cpattn.h"
+#include "api_common.h"
+#include "decode_kernel.cuh"
+
+using namespace cpattn;
+
+namespace {
+
+int check_shape(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
+  if (b < 1 || hq < 1 || hkv < 1 || cap < 1 || window < 0 || sinks < 0) return CPATTN_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || hq % hkv != 0) return CPATTN_ERR_INVALID_ARG;
+  if (cap > (1 << 30) || int64_t(b) * hq * kDecMaxSplit >= (int64_t(1) << 31)) return CPATTN_ERR_INVALID_ARG;
+  return CPATTN_OK;
+}
+
+// Keys a sequence can see at most.
+int64_t max_keys(int cap, int window, int sinks) {
+  if (window == 0) return cap;
+  const int64_t seen = int64_t(window) + sinks;
+  return seen < cap ? seen : cap;
+}
+
+// Runs per (sequence, KV head): two CTAs fit an SM. With long sequences four
+// CTAs per place level out their different lengths (runs of 512 keys or more,
+// whose fp32 results are under 2 % of what they read); with few sequences a
+// run goes down to one round of the warps, 64 keys.
+int choose_split(int num_sms, int64_t units, int64_t keys) {
+  const int64_t places = 2 * int64_t(num_sms);
+  int64_t s = (4 * places + units - 1) / units;
+  if (s > keys / 512) s = keys / 512;
+  int64_t fill = places / units;
+  if (fill > keys / 64) fill = keys / 64;
+  if (s < fill) s = fill;
+  return int(s < 1 ? 1 : (s > kDecMaxSplit ? kDecMaxSplit : s));
+}
+
+size_t workspace_for(int b, int hq, int d, int nsplit) {
+  if (nsplit <= 1) return 16;
+  const size_t rows = size_t(b) * hq * nsplit;
+  return align256(rows * d * 4) + align256(rows * 4);
+}
+
+bool strides_ok(int64_t batch, int64_t token, int64_t head) {
+  return batch >= 0 && token >= 0 && head >= 0 && batch % 8 == 0 && token % 8 == 0 && head % 8 == 0;
+}
+
+template <int D>
+int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
+  std::atomic<bool>& done = di->decode_attr[D == 128 ? 1 : 0];
+  if (!done.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(cpattn_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             DecodeCfg<D>::kSmemBytes) != cudaSuccess)
+      return CPATTN_ERR_CUDA;
+    done.store(true, std::memory_order_release);
+  }
+  const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
+  cpattn_decode_kernel<D><<<int(ctas), kDecWarps * 32, DecodeCfg<D>::kSmemBytes, st>>>(a);
+  if (a.nsplit > 1) {
+    const int64_t rows = int64_t(a.b) * a.hq;
+    cpattn_decode_join_kernel<D><<<int((rows + 3) / 4), 128, 0, st>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
+}
+
+}  // namespace
+
+extern "C" size_t cpattn_decode_workspace_bytes(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
+  if (check_shape(b, hq, hkv, d, cap, window, sinks)) return 0;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di)) return 0;
+  const int64_t units = int64_t(b) * hkv * ((hq / hkv + 15) / 16);
+  return workspace_for(b, hq, d, choose_split(di->num_sms, units, max_keys(cap, window, sinks)));
+}
+
+extern "C" int cpattn_decode(const void* q, const void* k_cache, const void* v_cache, const int* lengths, void* o,
+                             float* lse, void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d,
+                             int cap, int64_t q_batch, int64_t k_batch, int64_t k_token, int64_t k_head,
+                             int64_t v_batch, int64_t v_token, int64_t v_head, int window, int sinks, float scale,
+                             void* stream) {
+  if (!q || !k_cache || !v_cache || !lengths || !o || !lse || !workspace) return CPATTN_ERR_NULL_PTR;
+  int rc = check_shape(b, hq, hkv, d, cap, window, sinks);
+  if (rc) return rc;
+  if (!(scale == 0.f || valid_scale(scale))) return CPATTN_ERR_INVALID_ARG;
+  if (!strides_ok(k_batch, k_token, k_head) || !strides_ok(v_batch, v_token, v_head) || q_batch < 0 || q_batch % 8 != 0)
+    return CPATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(lse) ||
+      !aligned4(lengths) || !aligned16(workspace))
+    return CPATTN_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  DecodeArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k_cache);
+  a.v = static_cast<const __nv_bfloat16*>(v_cache);
+  a.lengths = lengths;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.q_batch = q_batch;
+  a.k_batch = k_batch;
+  a.k_token = k_token;
+  a.k_head = k_head;
+  a.v_batch = v_batch;
+  a.v_token = v_token;
+  a.v_head = v_head;
+  a.b = b;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.G = hq / hkv;
+  a.cap = cap;
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.row_groups = (a.G + 15) / 16;
+  const int64_t units = int64_t(b) * hkv * a.row_groups;
+  a.nsplit = choose_split(di->num_sms, units, max_keys(cap, window, sinks));
+  if (workspace_bytes < workspace_for(b, hq, d, a.nsplit)) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
+  a.scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
+  a.status = di->status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch<128>(a, di, st) : launch<64>(a, di, st);
+}

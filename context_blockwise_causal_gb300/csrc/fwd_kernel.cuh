@@ -30,6 +30,7 @@
 
 #include "cp_schedule.cuh"
 #include "ptx.cuh"
+#include "win_schedule.cuh"
 
 namespace cpattn {
 
@@ -113,9 +114,18 @@ enum FwdStatusBits : unsigned int {
 // its LSE ("大模型面试宝典 · Megatron-LM 篇", 3.2 step 4, before correction);
 // rows that take no part in the step get O = 0, L = -inf.
 // kTP: units are tile pairs (a.g.tile_pairs), not head pairs.
+// kWin: sliding-window attention (win_schedule.cuh) instead of the CP steps.
 // kShortWaits: the producer's waits for free buffers use a.producer_limit_ns
 // (the abort self-test) instead of the compile-time limit.
-template <int D, bool kStep, int kRing, bool kTP, bool kShortWaits = false>
+template <bool kTP, bool kWin>
+__device__ __forceinline__ auto fwd_unit_of(const CpGeom& g, int idx) {
+  if constexpr (kWin)
+    return win_fwd_unit<kTP>(g, idx);
+  else
+    return fwd_decode_unit_t<kTP>(g, idx);
+}
+
+template <int D, bool kStep, int kRing, bool kTP, bool kShortWaits = false, bool kWin = false>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     cpattn_fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const FwdArgs a) {
@@ -141,7 +151,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const CpGeom& g = a.g;
-  const int num_units = fwd_num_units(g);
+  const int num_units = kWin ? int(win_fwd_units(g, kTP)) : fwd_num_units(g);
   const int grid = gridDim.x;
 
   if (threadIdx.x == 0) {
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const FwdUnit U = fwd_decode_unit_t<kTP>(g, idx);
+        const auto U = fwd_unit_of<kTP, kWin>(g, idx);
         if (U.n == 0) continue;  // a tile a shorter packed sample does not have
         KvWalk w(g, U);
         if constexpr (kStep) {
@@ -224,10 +234,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           ++nload;
           return true;
         };
-        while (ok && w.next(chunk, tile, dg)) {
-          const int row = U.tok0 + kv_chunk_row(g, chunk, U.c) + tile * kTile;
-          ok = load(&tmk, U.g0, row) && (shared_kv || load(&tmk, U.g1, row)) && load(&tmv, U.g0, row) &&
-               (shared_kv || load(&tmv, U.g1, row));
+        if constexpr (kWin) {
+          for (int j = 0; ok && j < U.n; ++j) {
+            const int row = U.kv0 + win_tile(U, j) * kTile;
+            ok = load(&tmk, U.g0, row) && load(&tmv, U.g0, row);
+          }
+        } else {
+          while (ok && w.next(chunk, tile, dg)) {
+            const int row = U.tok0 + kv_chunk_row(g, chunk, U.c) + tile * kTile;
+            ok = load(&tmk, U.g0, row) && (shared_kv || load(&tmk, U.g1, row)) && load(&tmv, U.g0, row) &&
+                 (shared_kv || load(&tmv, U.g1, row));
+          }
         }
         ++ul;
       }
@@ -285,7 +302,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
-        const FwdUnit U = fwd_decode_unit_t<kTP>(g, idx);
+        const auto U = fwd_unit_of<kTP, kWin>(g, idx);
         if (U.n == 0) continue;
         const bool shared_kv = U.g0 == U.g1;
         const int n = kStep ? KvWalk(g, U).step_tiles(a.step) : U.n;
@@ -384,13 +401,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int rd = 0; ok; ++rd) {
       const int idx = snake_unit(rd, blockIdx.x, grid);
       if (idx >= num_units) break;
-      const FwdUnit U = fwd_decode_unit_t<kTP>(g, idx);
+      const auto U = fwd_unit_of<kTP, kWin>(g, idx);
       if (U.n == 0) continue;
       // this sub-tile's query rows (a second head, or the next query tile)
       const int q_t = sub ? U.q_t1 : U.q_t0;
       const int q_valid = sub ? U.q_valid1 : U.q_valid;
       // tile pairs: the position of sub-tile 0's fully masked tile (-1: none)
-      const int jd = kTP ? fwd_dead_pos(g, U, sub, kStep ? a.step : -1) : -1;
+      const int jd = kTP && !kWin ? fwd_dead_pos(g, U, sub, kStep ? a.step : -1) : -1;
       KvWalk w(g, U);
       int n = U.n;
       if constexpr (kStep) {
@@ -423,17 +440,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         int chunk = 0, tile = 0;
         bool walk_dg = false, dg = false, dead = false;
         int n_valid = kTile;
-        if (walkless) {
-          walk_dg = j == jdiag;
+        [[maybe_unused]] int p0 = 0, kb = 0;  // window form: position of this sub-tile's row 0, first key of the tile
+        if constexpr (kWin) {
+          p0 = U.off + q_t;
+          kb = win_tile(U, j) * kTile;
         } else {
-          w.next(chunk, tile, walk_dg);
-          const int rem = U.c - tile * kTile;
-          n_valid = rem < kTile ? rem : kTile;
+          if (walkless) {
+            walk_dg = j == jdiag;
+          } else {
+            w.next(chunk, tile, walk_dg);
+            const int rem = U.c - tile * kTile;
+            n_valid = rem < kTile ? rem : kTile;
+          }
+          if constexpr (kTP)
+            fwd_pos_mask(jd, j, walk_dg, dg, dead);
+          else
+            dg = walk_dg;
         }
-        if constexpr (kTP)
-          fwd_pos_mask(jd, j, walk_dg, dg, dead);
-        else
-          dg = walk_dg;
         if (!(ok = mbar_wait_bounded(&s_full[sub], scnt & 1, abort_flag, kWaitLimitNs))) break;
         ++scnt;
         tc_fence_after();
@@ -455,11 +478,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // row max: from the load itself, except on a masked tile (the diagonal
         // or a ragged chunk end), where it is taken over the unmasked scores
         float m_raw = hw_max;
-        if (dg || dead || n_valid < kTile) {
-          const int lim = dead ? -1 : dg ? (row < n_valid - 1 ? row : n_valid - 1) : n_valid - 1;
+        if (kWin ? !win_block_full(g, p0, kb) : (dg || dead || n_valid < kTile)) {
+          if constexpr (kWin) {
+            // this row sees keys lo .. lim of the tile, and those before `first`
+            const int lim = p0 + row - kb;
+            const int lo = lim - g.window + 1;
+            const int first = g.sinks - kb;
 #pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            if (i > lim) s[i] = -INFINITY;
+            for (int i = 0; i < kTile; ++i)
+              if (i > lim || (i < lo && i >= first)) s[i] = -INFINITY;
+          } else {
+            const int lim = dead ? -1 : dg ? (row < n_valid - 1 ? row : n_valid - 1) : n_valid - 1;
+#pragma unroll
+            for (int i = 0; i < kTile; ++i)
+              if (i > lim) s[i] = -INFINITY;
+          }
           // row max: eight independent chains of 3-input maxima, chain k over
           // the scores k, k+8, ..., k+120
           float mx[8];

@@ -106,7 +106,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
 // The same waits with the slow path out of line, so that the fast path
 // (phase already complete) is one test and no loop. For kernels without a
 // register split (a call inside a setmaxnreg region does not allocate).
-__device__ __noinline__ bool mbar_wait_loop_ool(uint64_t* bar, uint32_t parity, volatile int* abort,
+static __device__ __noinline__ bool mbar_wait_loop_ool(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                 uint64_t limit_ns) {
   return mbar_wait_loop(bar, parity, abort, limit_ns);
 }

@@ -34,7 +34,9 @@ struct RopeArgs {
   double turns_per_pos[kRopeMaxHalf];  // base^(-2i/d) / (2 pi), i < d/2
 };
 
-__device__ __forceinline__ int rope_position(const RopeArgs& a, int tok) {
+// Position of token `tok` (of n) by the fields s, cp, rank, cu_seqlens, nseq.
+template <class Args>
+__device__ __forceinline__ int rope_position(const Args& a, int tok) {
   int gpos = tok;
   if (a.rank >= 0) {
     const int c = a.s / (2 * a.cp);

@@ -1,0 +1,308 @@
+// Work decomposition of sliding-window attention with visible first tokens.
+//
+// Query at position p of its sequence sees key j when
+//     j <= p  and  (p - j < window  or  j < sinks).
+// A sequence has qlen queries and klen >= qlen keys; its queries are the last
+// qlen positions (query row t is position off + t, off = klen - qlen), so a
+// chunk of a prompt can attend to what was read before it. Tiles are 128
+// queries or keys counted from the sequence's first row.
+//
+// Forward and dQ units: a query tile (two, see win_fwd_unit) visits the key
+// tiles that hold visible first tokens, then the tiles its windows cover.
+// dK/dV units: a key tile visits the query tiles whose windows reach it; a
+// tile holding first tokens is seen by every later query, so its walk is cut
+// into parts of about two ordinary tiles' work, each a unit of its own, whose
+// fp32 results a second kernel adds in a fixed order.
+//
+// Window units differ little in cost, so their order follows the data:
+// consecutive units are neighbouring tiles of one KV head, and the CTAs in
+// flight read the same K/V (or Q/dO) rows from L2.
+#pragma once
+#include "cp_schedule.cuh"
+
+namespace cpattn {
+
+// A sequence's rows and lengths in the window form.
+struct WinSeq {
+  int q0, kv0;     // first row on the query side and on the key/value side
+  int qlen, klen;
+  int off;         // position of query row 0
+};
+
+__host__ __device__ inline WinSeq win_seq(const CpGeom& g, int seq) {
+  WinSeq s;
+  if (g.nseq > 0) {
+    s.q0 = s.kv0 = g.cu[seq];
+    s.qlen = s.klen = g.cu[seq + 1] - g.cu[seq];
+  } else {
+    s.q0 = seq * g.s;
+    s.kv0 = seq * g.kv_s;
+    s.qlen = g.s;
+    s.klen = g.kv_s;
+  }
+  s.off = s.klen - s.qlen;
+  return s;
+}
+
+struct WinUnit : FwdUnit {
+  int kv0;      // first key row of the unit's sequence
+  int off;      // position of its query row 0
+  int ns, w0;   // tiles of first tokens visited, then tiles from w0 on
+};
+
+// Query tiles (kPairs: pairs of tiles) of a sequence of qlen queries.
+__host__ __device__ inline int win_unit_tiles(int qlen, bool pairs) {
+  const int t = (qlen + kTile - 1) / kTile;
+  return pairs ? (t + 1) / 2 : t;
+}
+
+// Packed samples: prefix sums of the tiles (or tile pairs, or key tiles) of
+// the samples; a uniform batch needs none.
+__host__ __device__ inline void win_finish(CpGeom& g, bool pairs) {
+  g.tpc = win_unit_tiles(g.s, false);
+  if (g.nseq > 0) {
+    g.b = 1;
+    g.s = g.kv_s = g.cu[g.nseq];
+    g.tpc = 0;
+    g.tile0[0] = 0;
+    for (int i = 0; i < g.nseq; ++i) {
+      const int len = g.cu[i + 1] - g.cu[i];
+      const int t = win_unit_tiles(len, false);
+      g.tpc = t > g.tpc ? t : g.tpc;
+      g.tile0[i + 1] = g.tile0[i] + win_unit_tiles(len, pairs);
+    }
+  }
+}
+
+// Key tile of walk position j.
+__host__ __device__ inline int win_tile(const WinUnit& U, int j) { return j < U.ns ? j : U.w0 + (j - U.ns); }
+
+// Key tiles that the positions p_first .. p_last see.
+__host__ __device__ inline void win_fill_walk(const CpGeom& g, WinUnit& U, int p_first, int p_last) {
+  const int lo = p_first - g.window + 1;
+  U.w0 = lo > 0 ? lo / kTile : 0;
+  const int st = (g.sinks + kTile - 1) / kTile;
+  U.ns = st < U.w0 ? st : U.w0;
+  U.n = U.ns + p_last / kTile - U.w0 + 1;
+}
+
+// Whether a block of 128 queries from position p0 and 128 keys from kb is
+// visible as a whole.
+__host__ __device__ inline bool win_block_full(const CpGeom& g, int p0, int kb) {
+  return kb + kTile - 1 <= p0 && (p0 + kTile - 1 - kb < g.window || kb + kTile <= g.sinks);
+}
+
+// Forward units per launch: a query tile for a pair of query heads of one KV
+// group, or -- when the group's heads are odd in number -- two query tiles of
+// one head (kPairs), so that both sub-tiles always share their K/V tiles.
+__host__ __device__ inline int64_t win_fwd_units(const CpGeom& g, bool pairs) {
+  const int64_t heads = pairs ? g.hq : g.hq / 2;
+  return heads * (g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_unit_tiles(g.s, pairs));
+}
+
+template <bool kPairs>
+__host__ __device__ inline WinUnit win_fwd_unit(const CpGeom& g, int idx) {
+  WinUnit U;
+  const int G = g.hq / g.hkv;
+  const int per = kPairs ? G : G / 2;  // units of one tile and KV head
+  int tile, hp;                        // the unit's tile (or pair) and its head (or head pair)
+  if (g.nseq > 0) {
+    const int heads = g.hkv * per;
+    const int p = idx / heads;
+    hp = idx - p * heads;
+    int local;
+    U.seq = packed_sample_of(g, p, local);
+    tile = g.tile0[U.seq + 1] - g.tile0[U.seq] - 1 - local;
+  } else {
+    const int T = win_unit_tiles(g.s, kPairs);
+    int x = idx / per;
+    hp = idx - x * per;
+    const int y = x / T;
+    tile = T - 1 - (x - y * T);  // the shorter walks of the first tiles come last
+    U.seq = y / g.hkv;
+    hp += (y - U.seq * g.hkv) * per;
+  }
+  const WinSeq s = win_seq(g, U.seq);
+  U.bi = g.nseq > 0 ? 0 : U.seq;
+  U.tok0 = s.q0;
+  U.lse_t0 = g.nseq > 0 ? s.q0 : 0;
+  U.kv0 = s.kv0;
+  U.off = s.off;
+  U.c = s.qlen;
+  U.tpc = g.tpc;
+  U.k = U.r = U.half = 0;
+  U.h0 = kPairs ? hp : 2 * hp;
+  U.h1 = kPairs ? hp : 2 * hp + 1;
+  U.g0 = U.g1 = U.h0 / G;
+  U.store1 = true;
+  U.u = U.u0 = kPairs ? 2 * tile : tile;
+  U.q_t0 = U.q_t1 = U.u0 * kTile;
+  const int rem = s.qlen - U.q_t0;
+  U.q_valid = U.q_valid1 = rem < kTile ? rem : kTile;
+  int last = U.q_t0 + U.q_valid - 1;
+  if (kPairs) {
+    if (rem > kTile) {
+      U.q_t1 = U.q_t0 + kTile;
+      U.q_valid1 = rem - kTile < kTile ? rem - kTile : kTile;
+      last = U.q_t1 + U.q_valid1 - 1;
+    } else {
+      U.store1 = false;  // an odd tile count: sub-tile 1 repeats sub-tile 0 and stores nothing
+    }
+  }
+  win_fill_walk(g, U, s.off + U.q_t0, s.off + last);
+  return U;
+}
+
+// dQ units: one query tile of one head.
+__host__ __device__ inline int64_t win_dq_units(const CpGeom& g) {
+  return int64_t(g.hq) * (g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * g.tpc);
+}
+
+__host__ __device__ inline WinUnit win_dq_unit(const CpGeom& g, int idx) {
+  WinUnit U;
+  const int G = g.hq / g.hkv;
+  if (g.nseq > 0) {
+    const int p = idx / g.hq;
+    U.h0 = idx - p * g.hq;
+    int local;
+    U.seq = packed_sample_of(g, p, local);
+    U.u = g.tile0[U.seq + 1] - g.tile0[U.seq] - 1 - local;
+  } else {
+    const int x = idx / G;
+    const int y = x / g.tpc;
+    U.u = g.tpc - 1 - (x - y * g.tpc);
+    U.seq = y / g.hkv;
+    U.h0 = (y - U.seq * g.hkv) * G + (idx - x * G);
+  }
+  const WinSeq s = win_seq(g, U.seq);
+  U.bi = g.nseq > 0 ? 0 : U.seq;
+  U.tok0 = s.q0;
+  U.lse_t0 = g.nseq > 0 ? s.q0 : 0;
+  U.kv0 = s.kv0;
+  U.off = s.off;
+  U.c = s.qlen;
+  U.tpc = g.tpc;
+  U.k = U.r = U.half = 0;
+  U.h1 = U.h0;
+  U.g0 = U.g1 = U.h0 / G;
+  U.store1 = false;
+  U.u0 = U.u;
+  U.q_t0 = U.q_t1 = U.u * kTile;
+  const int rem = s.qlen - U.q_t0;
+  U.q_valid = U.q_valid1 = rem < kTile ? rem : kTile;
+  win_fill_walk(g, U, s.off + U.q_t0, s.off + U.q_t0 + U.q_valid - 1);
+  return U;
+}
+
+// ---------------------------------------------------------------- dK / dV
+struct BwdWinUnit : BwdUnit {
+  int kv0;      // first key row of the unit's sequence
+  int off;      // position of its query row 0
+  int qlen;
+  int qa;       // first query tile visited (nq of them; the walk comes down from the last)
+  int slot;     // a part of a cut walk: index of its fp32 result; -1: the whole walk
+};
+
+// Query tiles in which some query sees a key of tile kt: [qa, qa + nq).
+__host__ __device__ inline void win_query_tiles(const CpGeom& g, const WinSeq& s, int kt, int& qa, int& nq) {
+  const int k0 = kt * kTile;
+  const int k1 = k0 + kTile < s.klen ? k0 + kTile - 1 : s.klen - 1;  // last key
+  const int lo = k0 > s.off ? k0 - s.off : 0;
+  int hi = s.qlen - 1;
+  if (k0 >= g.sinks) {
+    const int64_t reach = int64_t(k1) + g.window - 1 - s.off;
+    if (reach < hi) hi = int(reach);
+  }
+  qa = lo / kTile;
+  nq = hi < lo ? 0 : hi / kTile - qa + 1;
+}
+
+// Parts of a cut walk: query tiles [qa + part * per, ...) with per =
+// part_tiles; the number of parts that have any.
+__host__ __device__ inline int win_parts(const CpGeom& g, int nq) { return (nq + g.part_tiles - 1) / g.part_tiles; }
+
+// Tiles whose walk is cut, per sequence and KV head (0 when no walk is).
+__host__ __device__ inline int win_cut_tiles(const CpGeom& g) {
+  return g.sink_parts > 1 ? (g.sinks + kTile - 1) / kTile : 0;
+}
+__host__ __device__ inline int64_t win_cut_units(const CpGeom& g) {
+  return int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g) * g.sink_parts;
+}
+__host__ __device__ inline int win_key_tiles(const CpGeom& g) { return (g.kv_s + kTile - 1) / kTile; }
+__host__ __device__ inline int64_t win_dkdv_units(const CpGeom& g) {
+  return win_cut_units(g) + int64_t(g.hkv) * (g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_key_tiles(g));
+}
+
+__host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
+  BwdWinUnit U;
+  const int cut = win_cut_tiles(g);
+  const int ncut = int(win_cut_units(g));
+  int kt, part = 0;
+  U.slot = -1;
+  if (idx < ncut) {
+    U.slot = idx;
+    int x = idx / g.sink_parts;
+    part = idx - x * g.sink_parts;
+    const int y = x / cut;
+    kt = x - y * cut;
+    U.seq = y / g.hkv;
+    U.g = y - U.seq * g.hkv;
+  } else {
+    idx -= ncut;
+    if (g.nseq > 0) {
+      const int p = idx / g.hkv;
+      U.g = idx - p * g.hkv;
+      U.seq = packed_sample_of(g, p, kt);
+    } else {
+      const int T = win_key_tiles(g);
+      const int y = idx / T;
+      kt = idx - y * T;
+      U.seq = y / g.hkv;
+      U.g = y - U.seq * g.hkv;
+    }
+  }
+  const WinSeq s = win_seq(g, U.seq);
+  U.bi = g.nseq > 0 ? 0 : U.seq;
+  U.tok0 = s.q0;
+  U.kv0 = s.kv0;
+  U.off = s.off;
+  U.c = U.qlen = s.qlen;
+  U.tpc = g.tpc;
+  U.kc = 0;
+  U.v = U.gt = kt;
+  U.k_t0 = kt * kTile;
+  U.qa = 0;
+  // no such key tile, or an ordinary unit of a tile whose walk is cut
+  if (U.k_t0 >= s.klen || (U.slot < 0 && kt < cut)) {
+    U.k_t0 = U.k_valid = U.nq = U.items = 0;
+    return U;
+  }
+  const int rem = s.klen - U.k_t0;
+  U.k_valid = rem < kTile ? rem : kTile;
+  win_query_tiles(g, s, kt, U.qa, U.nq);
+  if (U.slot >= 0) {
+    const int from = part * g.part_tiles;
+    const int left = U.nq - from;
+    U.qa += from;
+    U.nq = left < 0 ? 0 : (left < g.part_tiles ? left : g.part_tiles);
+    if (U.nq == 0) U.k_valid = 0;  // a part that the walk does not reach writes nothing
+  }
+  U.items = U.nq * (g.hq / g.hkv);
+  return U;
+}
+
+// Cuts the walks of the tiles that hold first tokens when the longest of them
+// is over twice an ordinary tile's: an ordinary tile is seen by about
+// window/128 + 1 query tiles, a cut part covers twice as many (at least 8).
+__host__ __device__ inline void win_set_parts(CpGeom& g) {
+  g.sink_parts = 1;
+  g.part_tiles = g.tpc > 0 ? g.tpc : 1;
+  if (g.sinks == 0) return;
+  const int per = 2 * (g.window / kTile + 2);
+  const int tiles = per > 8 ? per : 8;
+  if (g.tpc <= tiles) return;
+  g.part_tiles = tiles;
+  g.sink_parts = (g.tpc + tiles - 1) / tiles;
+}
+
+}  // namespace cpattn

@@ -336,6 +336,175 @@ int cpattn_bwd_rank_stage(int stage, const void* q, const void* k_all, const voi
                           int rank, int causal, float scale, void* stream);
 
 /*
+ * ---- Rotary positions in general, and norms of q and k with the rotation ----
+ *
+ * cpattn_rope turns whole heads in the half layout, in place. The calls below
+ * take a plan of the rotation instead: its layout, how much of a head turns,
+ * its frequencies (scaled for contexts longer than those trained on) and where
+ * the positions come from. The layouts and scalings are those of published
+ * models; the pages give none (item M016 describes RoPE itself).
+ */
+
+/* Rows [b, n, h, d] of a tensor, bf16: features and heads contiguous, tokens
+ * and batch elements any multiple of 8 elements apart (for instance q or k
+ * inside the fused projection's rows). Tokens of a tensor must not overlap; an
+ * output may be its own input (same data and strides), element for element. */
+typedef struct cpattn_rows {
+  void* data;           /* device, 16-byte aligned; inputs are not written */
+  int64_t batch_stride; /* elements */
+  int64_t token_stride; /* elements, >= h * d */
+} cpattn_rows;
+
+enum {
+  CPATTN_ROPE_HALF = 0,        /* pair i: features i and i + rot_dim/2 */
+  CPATTN_ROPE_INTERLEAVED = 1  /* pair i: features 2i and 2i + 1       */
+};
+
+enum { /* how cpattn_rope_frequencies scales f_i = base^(-2i/rot_dim) */
+  CPATTN_ROPE_UNSCALED = 0,
+  CPATTN_ROPE_LINEAR = 1,   /* every f_i divided by factor */
+  CPATTN_ROPE_BASE = 2,     /* base multiplied by factor^(rot_dim / (rot_dim - 2)) */
+  CPATTN_ROPE_BY_TURNS = 3, /* f_i divided by factor where the pair makes at most `low` turns over
+                               original_len positions, kept where it makes at least `high`,
+                               a mix linear in its turns in between */
+  CPATTN_ROPE_BY_INDEX = 4  /* the same two ends, the mix linear in the pair's index between the
+                               (rounded outwards) indexes that make `high` and `low` turns */
+};
+
+/*
+ * Host helper: inv_freq[i] (rot_dim / 2 doubles, HOST), radians per position
+ * of pair i. base > 1; factor >= 1, and original_len > 0, 0 < low < high where
+ * the scaling uses them (ignored otherwise). rot_dim even.
+ */
+int cpattn_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double low,
+                            double high, double* inv_freq);
+
+/*
+ * A rotation plan. The first rot_dim features of a head turn (a multiple of
+ * 16, at most d), the others pass. magnitude (> 0) multiplies the cosines and
+ * sines (the attention factor of some scalings; 1 otherwise).
+ * Positions, in this order:
+ *   positions != NULL: device int32, position of token t of batch element bi
+ *       is positions[bi * positions_batch + t] (positions_batch 0: shared by
+ *       all); any int32, so that single tokens of sequences of different
+ *       lengths go in one call. rank must be < 0 and cu_seqlens NULL.
+ *   otherwise as cpattn_rope: natural order (rank < 0, n == s), or a zigzag
+ *       shard, with optional packed-sample offsets (b == 1).
+ * inv_freq: HOST, rot_dim / 2 values in [0, 1e6], read during the call only.
+ */
+typedef struct cpattn_rotary {
+  int layout;
+  int rot_dim;
+  float magnitude;
+  int s, cp, rank;
+  const int* cu_seqlens;
+  int nseq;
+  const int* positions;
+  int64_t positions_batch;
+  const double* inv_freq;
+} cpattn_rotary;
+
+/*
+ * y = x rotated by the plan ([b, n, h, d], d in {64, 128}); inverse != 0 turns
+ * back (the gradient: dx from dy; the magnitude stays). Phases are exact to
+ * far below fp32 at any int32 position. Errors: NULL_PTR, INVALID_ARG,
+ * MISALIGNED, UNSUPPORTED_ARCH, LAUNCH_FAILED.
+ */
+int cpattn_rope_ex(const cpattn_rows* x, const cpattn_rows* y, int b, int n, int h, int d,
+                   const cpattn_rotary* rotary, int inverse, void* stream);
+
+/*
+ * RMS norm of each head of q [b, n, hq, d] and k [b, n, hkv, d] and the
+ * rotation in one pass: r = 1 / sqrt(mean(x^2) + eps), out = R(x * r * w), in
+ * fp32, rounded once.
+ *   q_weight, k_weight: device [d], fp32 (weight_fp32 != 0) or bf16, 16-byte
+ *                       aligned. eps >= 0.
+ * Errors as cpattn_rope_ex.
+ */
+int cpattn_qk_norm_rope(const cpattn_rows* q, const cpattn_rows* k, const void* q_weight, const void* k_weight,
+                        int weight_fp32, float eps, const cpattn_rows* q_out, const cpattn_rows* k_out, int b, int n,
+                        int hq, int hkv, int d, const cpattn_rotary* rotary, void* stream);
+
+/*
+ * Its backward from the inputs q, k and the gradients dq_out, dk_out of its
+ * outputs: dq, dk (bf16) and the weights' gradients dq_weight, dk_weight
+ * (device fp32 [d], written, not accumulated; summed over tokens and heads in
+ * a fixed order: deterministic). workspace: device, 16-byte aligned, at least
+ * cpattn_qk_norm_rope_bwd_workspace_bytes(d) bytes, contents irrelevant.
+ */
+size_t cpattn_qk_norm_rope_bwd_workspace_bytes(int d);
+int cpattn_qk_norm_rope_bwd(const cpattn_rows* q, const cpattn_rows* k, const void* q_weight, const void* k_weight,
+                            int weight_fp32, float eps, const cpattn_rows* dq_out, const cpattn_rows* dk_out,
+                            const cpattn_rows* dq, const cpattn_rows* dk, float* dq_weight, float* dk_weight,
+                            void* workspace, size_t workspace_bytes, int b, int n, int hq, int hkv, int d,
+                            const cpattn_rotary* rotary, void* stream);
+
+/*
+ * ---- Attention with a sliding window and visible first tokens ----
+ *
+ * The query at position p of its sequence sees key j when j <= p and
+ *     p - j < window   or   j < sinks
+ * (window >= 1, sinks >= 0; either may exceed the sequence, window >= skv is
+ * causal attention). q, o, dout, dq: [b, sq, hq, d]; k, v, dk, dv:
+ * [b, skv, hkv, d], skv >= sq: the queries are the last sq positions, so a
+ * chunk of a prompt attends to what was read before it. lse [b, hq, sq]. Any
+ * lengths (no divisibility); other layouts, limits, pointers and errors as
+ * cpattn_fwd; scale 0 selects 1/sqrt(d). b * skv < 2^31, skv <= 2^30.
+ * Keys hidden from a query are masked after the product of whole 128-key
+ * tiles: a non-finite value in a V row can reach queries within 127 positions
+ * of those that see it.
+ */
+int cpattn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int b, int sq, int skv, int hq,
+                      int hkv, int d, int window, int sinks, float scale, void* stream);
+
+/* Backward from the saved o and lse; workspace as cpattn_bwd's. The keys that
+ * later queries all see (the first tokens) are summed in parts in a fixed
+ * order: deterministic. */
+size_t cpattn_bwd_window_workspace_bytes(int b, int sq, int skv, int hq, int hkv, int d, int window, int sinks);
+int cpattn_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                      void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int b, int sq, int skv,
+                      int hq, int hkv, int d, int window, int sinks, float scale, void* stream);
+
+/* Packed samples, laid out as for cpattn_fwd_varlen (cu_seqlens: HOST int32
+ * [nseq + 1], any sample lengths, 0 too); windows and first tokens are each
+ * sample's own. Up to 512 samples run in one launch per kernel. */
+int cpattn_fwd_window_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_seqlens,
+                             int nseq, int hq, int hkv, int d, int window, int sinks, float scale, void* stream);
+size_t cpattn_bwd_window_varlen_workspace_bytes(const int* cu_seqlens, int nseq, int hq, int hkv, int d, int window,
+                                                int sinks);
+int cpattn_bwd_window_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                             const int* cu_seqlens, int nseq, int hq, int hkv, int d, int window, int sinks,
+                             float scale, void* stream);
+
+/*
+ * The same attention for one new token per sequence over a cache of keys and
+ * values (the new token's own among them).
+ *   q, o:     [b, hq, d] bf16, o contiguous, q's batch elements q_batch
+ *             elements apart; lse [b, hq] fp32, natural log.
+ *   k_cache, v_cache: bf16; token t of KV head h of sequence bi at
+ *             bi * batch + t * token + h * head elements (strides multiples
+ *             of 8, so [b, cap, hkv, d] and [b, hkv, cap, d] both fit), cap
+ *             tokens of room per sequence.
+ *   lengths:  device int32 [b], tokens held of each sequence (clamped to
+ *             [0, cap]); 0 gives o = 0 and lse = -inf. Nothing past a
+ *             sequence's length is read.
+ *   window:   0: every key; otherwise as above, with the first `sinks` keys.
+ *   workspace: device, 16-byte aligned, at least
+ *             cpattn_decode_workspace_bytes(...) bytes (of the current
+ *             device; 0 for an unsupported shape or device), contents
+ *             irrelevant. Calls that may overlap need one each.
+ * scale 0 selects 1/sqrt(d). d in {64, 128}. Deterministic. Errors: NULL_PTR,
+ * INVALID_ARG, MISALIGNED, WORKSPACE_TOO_SMALL, UNSUPPORTED_ARCH,
+ * LAUNCH_FAILED.
+ */
+size_t cpattn_decode_workspace_bytes(int b, int hq, int hkv, int d, int cap, int window, int sinks);
+int cpattn_decode(const void* q, const void* k_cache, const void* v_cache, const int* lengths, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d, int cap, int64_t q_batch,
+                  int64_t k_batch, int64_t k_token, int64_t k_head, int64_t v_batch, int64_t v_token, int64_t v_head,
+                  int window, int sinks, float scale, void* stream);
+
+/*
  * Host helper: the zigzag index map. Fills global_of_local (HOST memory,
  * cp * 2c int64 values, row-major [cp][2c]) with the global token position
  * of virtual rank r's local position u: chunk r then chunk 2cp-1-r, each in

@@ -39,3 +39,5 @@ from .context_parallel import (  # noqa: F401
 )
 from .rope import rope_angles, rope_apply, natural_positions, rank_local_positions  # noqa: F401
 from .varlen import varlen_attention_forward, varlen_attention_backward  # noqa: F401
+from .window import window_mask, window_attention, decode_attention  # noqa: F401
+from .qk_norm import scaled_frequencies, rotate, norm_rotate, norm_rotate_backward  # noqa: F401
