@@ -7,8 +7,11 @@ pointers, sizes and the current CUDA stream to the library. Every step of the
 computation runs in the library's CUDA kernels; there is no fallback. If the
 library has not been built the calls raise.
 """
+import array
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -72,17 +75,18 @@ _i, _p, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _f, _i64 = ctypes.c_float, ctypes.c_int64
 
 
-class _Rows(ctypes.Structure):
-    """cpattn_rows: rows [b, n, h, d] with batch and token strides."""
-
-    _fields_ = [("data", _p), ("batch_stride", _i64), ("token_stride", _i64)]
-
-
-class _Rotary(ctypes.Structure):
-    """cpattn_rotary: a rotation plan."""
-
-    _fields_ = [("layout", _i), ("rot_dim", _i), ("magnitude", _f), ("s", _i), ("cp", _i), ("rank", _i),
-                ("cu_seqlens", _p), ("nseq", _i), ("positions", _p), ("positions_batch", _i64), ("inv_freq", _p)]
+# cpattn_rows (data, batch_stride, token_stride) and cpattn_rotary (layout,
+# rot_dim, magnitude, s, cp, rank, cu_seqlens, nseq, positions,
+# positions_batch, inv_freq) as the bytes of the C structs: packing them costs
+# a fraction of building ctypes structures, which counts in calls that run for
+# a few microseconds.
+_ROWS = struct.Struct("@Pqq").pack
+_PLAN = struct.Struct("@iifiiiPiPqP").pack
+# The current device and a device's current stream without the Python objects
+# around them, for the same reason.
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_BF16, _F32, _I32, _F64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
 
 
 _CHECKED = None
@@ -157,17 +161,15 @@ def _declare(lib):
     lib.cpattn_bwd_rank.restype = _i
     lib.cpattn_bwd_rank_stage.argtypes = [_i] + [_p] * 10 + [_sz] + [_i] * 8 + [ctypes.c_float, _p]
     lib.cpattn_bwd_rank_stage.restype = _i
-    rows, plan = ctypes.POINTER(_Rows), ctypes.POINTER(_Rotary)
     lib.cpattn_rope_frequencies.argtypes = [_i, ctypes.c_double, _i] + [ctypes.c_double] * 4 + [_p]
     lib.cpattn_rope_frequencies.restype = _i
-    lib.cpattn_rope_ex.argtypes = [rows, rows] + [_i] * 4 + [plan, _i, _p]
+    lib.cpattn_rope_ex.argtypes = [_p, _p] + [_i] * 4 + [_p, _i, _p]
     lib.cpattn_rope_ex.restype = _i
-    lib.cpattn_qk_norm_rope.argtypes = [rows, rows, _p, _p, _i, _f, rows, rows] + [_i] * 5 + [plan, _p]
+    lib.cpattn_qk_norm_rope.argtypes = [_p] * 4 + [_i, _f, _p, _p] + [_i] * 5 + [_p, _p]
     lib.cpattn_qk_norm_rope.restype = _i
     lib.cpattn_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i]
     lib.cpattn_qk_norm_rope_bwd_workspace_bytes.restype = _sz
-    lib.cpattn_qk_norm_rope_bwd.argtypes = ([rows, rows, _p, _p, _i, _f] + [rows] * 4 + [_p, _p, _p, _sz] + [_i] * 5 +
-                                            [plan, _p])
+    lib.cpattn_qk_norm_rope_bwd.argtypes = [_p] * 4 + [_i, _f] + [_p] * 7 + [_sz] + [_i] * 5 + [_p, _p]
     lib.cpattn_qk_norm_rope_bwd.restype = _i
     lib.cpattn_fwd_window.argtypes = [_p] * 5 + [_i] * 8 + [_f, _p]
     lib.cpattn_fwd_window.restype = _i
@@ -425,85 +427,115 @@ def cpattn_rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, ori
     return out
 
 
+def _on(stream, *tensors):
+    """The stream to launch on (the current one by default), as a handle; every
+    tensor given must be on the current device, and so must the stream."""
+    cur = _device()
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            if not t.is_cuda:
+                raise TypeError("every tensor must be a CUDA tensor")
+            raise ValueError(f"a tensor is on {t.device} but the current CUDA device is cuda:{cur}; "
+                             f"call under torch.cuda.device({t.device})")
+    if stream is None:
+        return _raw_stream(cur)
+    if stream.device.index != cur:
+        raise ValueError(f"the stream belongs to {stream.device}, the current CUDA device is cuda:{cur}")
+    return stream.cuda_stream
+
+
+def _empty(shape, like, stream, dtype=_BF16):
+    """A new tensor beside ``like``, from the memory of the stream that the
+    call runs on: the caching allocator then hands it to nobody else before
+    that stream is done with it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _dense(name, t, dtype, shape):
+    """A contiguous tensor of a type and shape, beside ``_on``'s checks."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _rows(name, t, shape=None):
     """cpattn_rows of a bf16 tensor [b, n, h, d] with contiguous heads. A
     stride of a dimension of one element means nothing and is not passed on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [b, n, h, d]")
     b, n, h, d = t.shape
-    if shape is not None and (b, n, h, d) != tuple(shape):
-        raise ValueError(f"{name} has shape {(b, n, h, d)}, expected {tuple(shape)}")
     sb, sn, sh, sd = t.stride()
     if sd != 1 or (h > 1 and sh != d):
         raise ValueError(f"{name} must have contiguous heads and features")
-    return _Rows(t.data_ptr(), sb if b > 1 else 0, sn if n > 1 else h * d)
+    return _ROWS(t.data_ptr(), sb if b > 1 else 0, sn if n > 1 else h * d)
 
 
-def _rotary(x, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude):
-    """cpattn_rotary for x [b, n, ...], and the tensors that must outlive it."""
-    b, n = x.shape[:2]
+def _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude):
+    """cpattn_rotary for b x n tokens, and inv_freq, which must outlive it."""
     if layout not in _ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {list(_ROPE_LAYOUTS)}")
     if inv_freq is None:
         inv_freq = cpattn_rope_frequencies(d if rot_dim is None else rot_dim, base)
-    if inv_freq.dtype != torch.float64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+    elif inv_freq.dtype is not _F64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous fp64 host vector")
-    if rot_dim is None:
-        rot_dim = 2 * inv_freq.numel()
-    if inv_freq.numel() * 2 != rot_dim:
-        raise ValueError(f"inv_freq has {inv_freq.numel()} values, rot_dim {rot_dim} needs {rot_dim // 2}")
-    plan = _Rotary(layout=_ROPE_LAYOUTS[layout], rot_dim=int(rot_dim), magnitude=float(magnitude), cp=int(cp),
-                   rank=-1 if rank is None else int(rank), inv_freq=inv_freq.data_ptr())
-    plan.s = int(s) if s is not None else (n if rank is None else n * int(cp))
+    pairs = inv_freq.shape[0]
+    if rot_dim is not None and 2 * pairs != rot_dim:
+        raise ValueError(f"inv_freq has {pairs} values, rot_dim {rot_dim} needs {rot_dim // 2}")
+    if s is None:
+        s = n if rank is None else n * int(cp)
+    cu = nseq = pos = pos_batch = 0
     if cu_seqlens is not None:
-        if not cu_seqlens.is_cuda or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        if cu_seqlens.dtype is not _I32 or not cu_seqlens.is_contiguous():
             raise TypeError("cu_seqlens must be a contiguous int32 CUDA tensor")
-        plan.cu_seqlens, plan.nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
+        cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
     if positions is not None:
-        if not positions.is_cuda or positions.dtype != torch.int32:
+        if positions.dtype is not _I32:
             raise TypeError("positions must be an int32 CUDA tensor")
-        if tuple(positions.shape) not in ((n,), (b, n)):
+        if positions.shape != (n,) and positions.shape != (b, n):
             raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(n,)} or {(b, n)}")
         if n > 1 and positions.stride(-1) != 1:
             raise ValueError("the positions of a sequence must be contiguous")
-        plan.positions = positions.data_ptr()
-        plan.positions_batch = positions.stride(0) if positions.dim() == 2 and b > 1 else 0
-    return plan, inv_freq
+        pos = positions.data_ptr()
+        pos_batch = positions.stride(0) if positions.dim() == 2 and b > 1 else 0
+    return _PLAN(_ROPE_LAYOUTS[layout], 2 * pairs, magnitude, s, cp, -1 if rank is None else rank, cu, nseq, pos,
+                 pos_batch, inv_freq.data_ptr()), inv_freq
 
 
 def _rope_ex(x, base, cp, rank, s, cu_seqlens, inverse, stream, positions, layout, rot_dim, inv_freq, magnitude, out):
     xr = _rows("x", x)
-    outr = _rows("out", out, x.shape)
+    outr = xr if out is x else _rows("out", out, x.shape)
     b, n, h, d = x.shape
-    plan, freq = _rotary(x, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
     rc = library().cpattn_rope_ex(xr, outr, b, n, h, d, plan, 1 if inverse else 0,
-                                  _stream_handle(stream, x, out, cu_seqlens, positions))
+                                  _on(stream, x, out, cu_seqlens, positions))
     if rc:
         raise CpattnError(rc, "cpattn_rope_ex")
     return out
 
 
-def _weights(q_weight, k_weight, d):
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype not in (torch.bfloat16, torch.float32):
-            raise TypeError(f"{name} must be a bf16 or fp32 CUDA tensor")
-        if tuple(w.shape) != (d,) or not w.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{d}] tensor")
-    if q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must have one type")
-    return 1 if q_weight.dtype == torch.float32 else 0
-
-
-def _qk_dims(q, k):
+def _qk(q, k, q_weight, k_weight):
+    """Rows of q and k, weights and sizes of a q/k norm call."""
     qr, kr = _rows("q", q), _rows("k", k)
     b, n, hq, d = q.shape
-    if k.shape[0] != b or k.shape[1] != n or k.shape[3] != d:
+    hkv = k.shape[2]
+    if k.shape != (b, n, hkv, d):
         raise ValueError("k must be [b, n, hkv, d] matching q")
-    return qr, kr, b, n, hq, k.shape[2], d
+    wt = q_weight.dtype
+    if wt is not _F32 and wt is not _BF16:
+        raise TypeError("q_weight and k_weight must be bf16 or fp32 CUDA tensors")
+    return (qr, kr, _dense("q_weight", q_weight, wt, (d,)), _dense("k_weight", k_weight, wt, (d,)),
+            1 if wt is _F32 else 0), b, n, hq, hkv, d
 
 
 def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None,
@@ -515,16 +547,15 @@ def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, 
     q, k and the outputs are bf16 and may be strided (e.g. parts of a fused
     projection); an output may be its input. Positions and rotation as for
     cpattn_rope. Returns (q_out, k_out), allocated contiguous when not given."""
-    qr, kr, b, n, hq, hkv, d = _qk_dims(q, k)
-    fp32 = _weights(q_weight, k_weight, d)
-    q_out = _empty(q.shape, q, stream) if q_out is None else q_out
-    k_out = _empty(k.shape, k, stream) if k_out is None else k_out
-    qo, ko = _rows("q_out", q_out, q.shape), _rows("k_out", k_out, k.shape)
-    plan, freq = _rotary(q, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
-    rc = library().cpattn_qk_norm_rope(qr, kr, q_weight.data_ptr(), k_weight.data_ptr(), fp32, float(eps), qo, ko, b, n,
-                                       hq, hkv, d, plan,
-                                       _stream_handle(stream, q, k, q_weight, k_weight, q_out, k_out, cu_seqlens,
-                                                      positions))
+    ins, b, n, hq, hkv, d = _qk(q, k, q_weight, k_weight)
+    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    handle = _on(stream, q, k, q_weight, k_weight, q_out, k_out, cu_seqlens, positions)
+    if q_out is None:
+        q_out = _empty((b, n, hq, d), q, stream)
+    if k_out is None:
+        k_out = _empty((b, n, hkv, d), k, stream)
+    rc = library().cpattn_qk_norm_rope(*ins, eps, _rows("q_out", q_out, q.shape), _rows("k_out", k_out, k.shape), b, n,
+                                       hq, hkv, d, plan, handle)
     if rc:
         raise CpattnError(rc, "cpattn_qk_norm_rope")
     return q_out, k_out
@@ -536,45 +567,49 @@ def cpattn_qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, eps=1e-6, 
     """Backward of cpattn_qk_norm_rope from its inputs q, k and the gradients
     of its outputs. Returns (dq, dk, dq_weight, dk_weight); the weights'
     gradients are fp32 [d], written (not accumulated)."""
-    qr, kr, b, n, hq, hkv, d = _qk_dims(q, k)
-    fp32 = _weights(q_weight, k_weight, d)
-    gq, gk = _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape)
-    dq = _empty(q.shape, q, stream) if dq is None else dq
-    dk = _empty(k.shape, k, stream) if dk is None else dk
-    dq_weight = _empty((d,), q, stream, torch.float32) if dq_weight is None else dq_weight
-    dk_weight = _empty((d,), q, stream, torch.float32) if dk_weight is None else dk_weight
-    _check_f32("dq_weight", dq_weight, (d,))
-    _check_f32("dk_weight", dk_weight, (d,))
-    rq, rk = _rows("dq", dq, q.shape), _rows("dk", dk, k.shape)
-    plan, freq = _rotary(q, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
-    lib = library()
-    workspace = _workspace(workspace, lib.cpattn_qk_norm_rope_bwd_workspace_bytes(d), q, stream)
-    rc = lib.cpattn_qk_norm_rope_bwd(qr, kr, q_weight.data_ptr(), k_weight.data_ptr(), fp32, float(eps), gq, gk, rq, rk,
-                                     dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), b, n, hq, hkv, d, plan,
-                                     _stream_handle(stream, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight,
-                                                    dk_weight, workspace, cu_seqlens, positions))
+    ins, b, n, hq, hkv, d = _qk(q, k, q_weight, k_weight)
+    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
+    handle = _on(stream, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, cu_seqlens,
+                 positions)
+    if dq is None:
+        dq = _empty((b, n, hq, d), q, stream)
+    if dk is None:
+        dk = _empty((b, n, hkv, d), k, stream)
+    if dq_weight is None:
+        dq_weight = _empty((d,), q, stream, _F32)
+    if dk_weight is None:
+        dk_weight = _empty((d,), q, stream, _F32)
+    ws, ws_bytes, workspace = _workspace(workspace, _qk_bwd_bytes(d), q, stream)
+    rc = library().cpattn_qk_norm_rope_bwd(*ins, eps, _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape),
+                                           _rows("dq", dq, q.shape), _rows("dk", dk, k.shape),
+                                           _dense("dq_weight", dq_weight, _F32, (d,)),
+                                           _dense("dk_weight", dk_weight, _F32, (d,)), ws, ws_bytes, b, n, hq, hkv, d,
+                                           plan, handle)
     if rc:
         raise CpattnError(rc, "cpattn_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
 
 
-def _empty(shape, like, stream, dtype=torch.bfloat16):
-    """A new tensor beside ``like``, from the memory of the stream that the
-    call runs on: the caching allocator then hands it to nobody else before
-    that stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+# Workspace sizes by shape alone (and device, where it matters).
+@functools.lru_cache(maxsize=64)
+def _qk_bwd_bytes(d):
+    return int(library().cpattn_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_bytes(device, *shape):
+    return int(library().cpattn_decode_workspace_bytes(*shape))
 
 
 def _workspace(workspace, need, like, stream):
+    """Pointer and bytes of the workspace given, or of a new one."""
     if workspace is None:
-        return _empty((max(int(need), 16),), like, stream, torch.uint8)
+        need = need if need > 16 else 16
+        workspace = _empty((need,), like, stream, torch.uint8)
+        return workspace.data_ptr(), need, workspace
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _cu_host(cu_seqlens):
@@ -686,12 +721,15 @@ def cpattn_bwd(q, k, v, o, lse, do, cp, causal=True, dq=None, dk=None, dv=None, 
 
 
 def _window_dims(q, k, v):
-    _check_act("q", q)
-    _check_act("k", k)
-    _check_act("v", v, k.shape)
-    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+    """Pointers and sizes b, sq, skv, hq, hkv, d of a window call."""
+    if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [b, sq, hq, d] and k, v [b, skv, hkv, d]")
-    return q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3]
+    b, sq, hq, d = q.shape
+    skv, hkv = k.shape[1], k.shape[2]
+    kv = (b, skv, hkv, d)
+    if k.shape != kv:
+        raise ValueError("q must be [b, sq, hq, d] and k, v [b, skv, hkv, d]")
+    return (_dense("q", q, _BF16, q.shape), _dense("k", k, _BF16, kv), _dense("v", v, _BF16, kv)), b, sq, skv, hq, hkv, d
 
 
 def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, stream=None):
@@ -700,14 +738,14 @@ def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, st
     The query at position p sees key j when j <= p and p - j < window or
     j < sinks. q [b, sq, hq, d]; k, v [b, skv, hkv, d] with skv >= sq: the
     queries are the last sq positions. Returns (o like q, lse [b, hq, sq])."""
-    b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
-    o = _empty(q.shape, q, stream) if o is None else o
-    _check_act("o", o, q.shape)
-    lse = _empty((b, hq, sq), q, stream, torch.float32) if lse is None else lse
-    _check_f32("lse", lse, (b, hq, sq))
-    rc = library().cpattn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), b, sq, skv,
-                                     hq, hkv, d, int(window), int(sinks), 0.0 if scale is None else float(scale),
-                                     _stream_handle(stream, q, k, v, o, lse))
+    ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
+    handle = _on(stream, q, k, v, o, lse)
+    if o is None:
+        o = _empty((b, sq, hq, d), q, stream)
+    if lse is None:
+        lse = _empty((b, hq, sq), q, stream, _F32)
+    rc = library().cpattn_fwd_window(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (b, hq, sq)), b, sq,
+                                     skv, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_fwd_window")
     return o, lse
@@ -720,44 +758,52 @@ def cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks=0):
 def cpattn_bwd_window(q, k, v, o, lse, do, window, sinks=0, scale=None, dq=None, dk=None, dv=None, workspace=None,
                       stream=None):
     """Backward of cpattn_fwd_window from its o and lse. Returns (dq, dk, dv)."""
-    b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
-    _check_act("o", o, q.shape)
-    _check_act("do", do, q.shape)
-    _check_f32("lse", lse, (b, hq, sq))
-    dq = _empty(q.shape, q, stream) if dq is None else dq
-    dk = _empty(k.shape, k, stream) if dk is None else dk
-    dv = _empty(v.shape, v, stream) if dv is None else dv
-    _check_act("dq", dq, q.shape)
-    _check_act("dk", dk, k.shape)
-    _check_act("dv", dv, v.shape)
-    need = cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks)
-    workspace = _workspace(workspace, need, q, stream)
-    rc = library().cpattn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                     do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), b, sq, skv, hq, hkv, d, int(window),
-                                     int(sinks), 0.0 if scale is None else float(scale),
-                                     _stream_handle(stream, q, k, v, o, lse, do, dq, dk, dv, workspace))
+    ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
+    handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
+    if dq is None:
+        dq = _empty((b, sq, hq, d), q, stream)
+    if dk is None:
+        dk = _empty((b, skv, hkv, d), q, stream)
+    if dv is None:
+        dv = _empty((b, skv, hkv, d), q, stream)
+    lib = library()
+    need = lib.cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks)
+    ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
+    rc = lib.cpattn_bwd_window(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (b, hq, sq)),
+                               _dense("do", do, _BF16, q.shape), _dense("dq", dq, _BF16, q.shape),
+                               _dense("dk", dk, _BF16, k.shape), _dense("dv", dv, _BF16, k.shape), ws, ws_bytes, b, sq,
+                               skv, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_bwd_window")
     return dq, dk, dv
+
+
+def _packed_window(q, k, v, cu_seqlens):
+    """Pointers, offsets (an int32 buffer) and sizes of a packed window call."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("packed q must be [total, hq, d] and k, v [total, hkv, d]")
+    total, hq, d = q.shape
+    hkv = k.shape[1]
+    kv = (total, hkv, d)
+    cu = array.array("i", cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
+    if not cu or cu[-1] != total:
+        raise ValueError("cu_seqlens must end at the packed length")
+    return (_dense("q", q, _BF16, q.shape), _dense("k", k, _BF16, kv), _dense("v", v, _BF16, kv)), cu, total, hq, hkv, d
 
 
 def cpattn_fwd_window_varlen(q, k, v, cu_seqlens, window, sinks=0, scale=None, o=None, lse=None, stream=None):
     """cpattn_fwd_window over packed samples, each with its own window and
     first tokens. q [total, hq, d], k/v [total, hkv, d]; cu_seqlens: sample
     offsets (host list/tensor). Returns (o [total, hq, d], lse [hq, total])."""
-    total, hq, hkv, d = _packed_dims(q, k, v)
-    cu, cu_p, nseq = _cu_host(cu_seqlens)
-    if int(cu[-1]) != total:
-        raise ValueError("cu_seqlens must end at the packed length")
-    o = _empty(q.shape, q, stream) if o is None else o
-    _check_act("o", o, q.shape)
-    lse = _empty((hq, total), q, stream, torch.float32) if lse is None else lse
-    _check_f32("lse", lse, (hq, total))
-    rc = library().cpattn_fwd_window_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                            cu_p, nseq, hq, hkv, d, int(window), int(sinks),
-                                            0.0 if scale is None else float(scale),
-                                            _stream_handle(stream, q, k, v, o, lse))
+    ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
+    handle = _on(stream, q, k, v, o, lse)
+    if o is None:
+        o = _empty((total, hq, d), q, stream)
+    if lse is None:
+        lse = _empty((hq, total), q, stream, _F32)
+    rc = library().cpattn_fwd_window_varlen(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (hq, total)),
+                                            cu.buffer_info()[0], len(cu) - 1, hq, hkv, d, window, sinks,
+                                            0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_fwd_window_varlen")
     return o, lse
@@ -766,27 +812,21 @@ def cpattn_fwd_window_varlen(q, k, v, cu_seqlens, window, sinks=0, scale=None, o
 def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, scale=None, dq=None, dk=None, dv=None,
                              workspace=None, stream=None):
     """Backward of cpattn_fwd_window_varlen. Returns (dq, dk, dv)."""
-    total, hq, hkv, d = _packed_dims(q, k, v)
-    cu, cu_p, nseq = _cu_host(cu_seqlens)
-    if int(cu[-1]) != total:
-        raise ValueError("cu_seqlens must end at the packed length")
-    _check_act("o", o, q.shape)
-    _check_act("do", do, q.shape)
-    _check_f32("lse", lse, (hq, total))
-    dq = _empty(q.shape, q, stream) if dq is None else dq
-    dk = _empty(k.shape, k, stream) if dk is None else dk
-    dv = _empty(v.shape, v, stream) if dv is None else dv
-    _check_act("dq", dq, q.shape)
-    _check_act("dk", dk, k.shape)
-    _check_act("dv", dv, v.shape)
-    lib = library()
-    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, int(window), int(sinks))
-    workspace = _workspace(workspace, need, q, stream)
-    rc = lib.cpattn_bwd_window_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                      do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), cu_p, nseq, hq, hkv, d, int(window),
-                                      int(sinks), 0.0 if scale is None else float(scale),
-                                      _stream_handle(stream, q, k, v, o, lse, do, dq, dk, dv, workspace))
+    ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
+    handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
+    if dq is None:
+        dq = _empty((total, hq, d), q, stream)
+    if dk is None:
+        dk = _empty((total, hkv, d), q, stream)
+    if dv is None:
+        dv = _empty((total, hkv, d), q, stream)
+    lib, cu_p, nseq = library(), cu.buffer_info()[0], len(cu) - 1
+    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, window, sinks)
+    ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
+    rc = lib.cpattn_bwd_window_varlen(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (hq, total)),
+                                      _dense("do", do, _BF16, q.shape), _dense("dq", dq, _BF16, q.shape),
+                                      _dense("dk", dk, _BF16, k.shape), _dense("dv", dv, _BF16, k.shape), ws, ws_bytes,
+                                      cu_p, nseq, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_bwd_window_varlen")
     return dq, dk, dv
@@ -795,20 +835,6 @@ def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, s
 def cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
     """Workspace bytes of cpattn_decode on the current device."""
     return int(library().cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, int(window), int(sinks)))
-
-
-def _cache_strides(name, t):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [b, cap, hkv, d]")
-    sb, st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must have contiguous features")
-    b, cap, h, _ = t.shape
-    return sb if b > 1 else 0, st if cap > 1 else 0, sh if h > 1 else 0
 
 
 def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o=None, lse=None, workspace=None,
@@ -820,36 +846,38 @@ def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o
     CUDA tensor [b]: tokens held of each sequence, the new one's key and value
     among them. window 0: every key; otherwise the last ``window`` keys and
     the first ``sinks``. Returns (o [b, hq, d], lse [b, hq])."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        raise TypeError("q must be a CUDA tensor")
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q must be bfloat16")
-    if q.dim() != 3:
-        raise ValueError("q must be [b, hq, d]")
+    if q.dtype is not _BF16 or k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
+        raise TypeError("q, k_cache and v_cache must be bfloat16 CUDA tensors")
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [b, hq, d] and k_cache, v_cache [b, cap, hkv, d]")
     b, hq, d = q.shape
-    if q.stride(2) != 1 or (hq > 1 and q.stride(1) != d):
-        raise ValueError("q must have contiguous heads and features")
-    kb, kt, kh = _cache_strides("k_cache", k_cache)
-    vb, vt, vh = _cache_strides("v_cache", v_cache)
-    if k_cache.shape != v_cache.shape or k_cache.shape[0] != b or k_cache.shape[3] != d:
+    _, cap, hkv, _ = k_cache.shape
+    if k_cache.shape != (b, cap, hkv, d) or v_cache.shape != (b, cap, hkv, d):
         raise ValueError("k_cache and v_cache must be [b, cap, hkv, d] matching q")
-    cap, hkv = k_cache.shape[1], k_cache.shape[2]
-    if not isinstance(lengths, torch.Tensor) or not lengths.is_cuda or lengths.dtype != torch.int32:
-        raise TypeError("lengths must be an int32 CUDA tensor")
-    if tuple(lengths.shape) != (b,) or not lengths.is_contiguous():
-        raise ValueError(f"lengths must be a contiguous [{b}] tensor")
-    o = _empty((b, hq, d), q, stream) if o is None else o
-    _check_act("o", o, (b, hq, d))
-    lse = _empty((b, hq), q, stream, torch.float32) if lse is None else lse
-    _check_f32("lse", lse, (b, hq))
-    handle = _stream_handle(stream, q, k_cache, v_cache, lengths, o, lse, workspace)
-    need = 16 if workspace is not None else cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window, sinks)
-    workspace = _workspace(workspace, need, q, stream)
-    rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), lengths.data_ptr(),
-                                 o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), b, hq, hkv, d, cap,
-                                 q.stride(0) if b > 1 else 0, kb, kt, kh, vb, vt, vh, int(window), int(sinks),
-                                 0.0 if scale is None else float(scale), handle)
+    qb, qh, q1 = q.stride()
+    kb, kt, kh, k1 = k_cache.stride()
+    vb, vt, vh, v1 = v_cache.stride()
+    if q1 != 1 or k1 != 1 or v1 != 1 or (hq > 1 and qh != d):
+        raise ValueError("q's heads and the features of q and of the cache must be contiguous")
+    # a stride of a dimension of one element means nothing
+    if b == 1:
+        qb = kb = vb = 0
+    if cap == 1:
+        kt = vt = 0
+    if hkv == 1:
+        kh = vh = 0
+    ln = _dense("lengths", lengths, _I32, (b,))
+    handle = _on(stream, q, k_cache, v_cache, lengths, o, lse, workspace)
+    if o is None:
+        o = _empty((b, hq, d), q, stream)
+    if lse is None:
+        lse = _empty((b, hq), q, stream, _F32)
+    ws, ws_bytes, workspace = _workspace(workspace, _decode_bytes(_device(), b, hq, hkv, d, cap, window, sinks), q,
+                                         stream)
+    rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ln,
+                                 _dense("o", o, _BF16, (b, hq, d)), _dense("lse", lse, _F32, (b, hq)), ws, ws_bytes, b,
+                                 hq, hkv, d, cap, qb, kb, kt, kh, vb, vt, vh, window, sinks,
+                                 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_decode")
     return o, lse

@@ -245,6 +245,63 @@ __device__ __forceinline__ void ds_frag(const uint32_t (&pp)[16], const uint32_t
       }
 }
 
+// The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
+// to bf16 there too, as above, costs a third of the gradients' error (relative
+// L2 3.0e-3 against 2.4e-3, dK and dQ at a window of 300). A masked block zeroes P, and
+// dS = P (dP - D) with it, by testing query 8r + 2 c4 + j + c0 against the key
+// row's visible range [from, from + len) (an unsigned compare does both ends).
+template <bool kMasked>
+__device__ __forceinline__ void softmax_p_frag32(uint32_t (&rs)[32], float sl2, const float2 (&lv)[4],
+                                                 const int (&from)[4], const uint32_t (&len)[4], uint32_t (&pp)[16]) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 16 * u + 4 * r + 2 * e;
+        const int o = 8 * u + 2 * r + e;
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[i]), __uint_as_float(rs[i + 1])), sl2x2,
+                         f2_pack(-lv[r].x, -lv[r].y)),
+                  x0, x1);
+        x0 = ex2_approx(x0);
+        x1 = ex2_approx(x1);
+        if constexpr (kMasked) {
+          const int f = 2 * u + e;
+          x0 = uint32_t(8 * r - from[f]) < len[f] ? x0 : 0.f;
+          x1 = uint32_t(8 * r + 1 - from[f]) < len[f] ? x1 : 0.f;
+        }
+        rs[i] = __float_as_uint(x0);
+        rs[i + 1] = __float_as_uint(x1);
+        pp[o] = pack_bf16x2(x0, x1);
+      }
+}
+// kMasked: padding queries' dP - D may be anything (their L and D are not
+// set), so dS is selected by P != 0 there.
+template <bool kMasked>
+__device__ __forceinline__ void ds_frag32(const uint32_t (&ps)[32], const uint32_t (&rp)[32], const float2 (&dv)[4],
+                                          uint32_t (&pd)[16]) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int i = 16 * u + 4 * r + 2 * e;
+        float g0, g1;
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(ps[i]), __uint_as_float(ps[i + 1])),
+                         f2_sub(f2_pack(__uint_as_float(rp[i]), __uint_as_float(rp[i + 1])), f2_pack(dv[r].x, dv[r].y))),
+                  g0, g1);
+        if constexpr (kMasked) {
+          g0 = ps[i] == 0u ? 0.f : g0;
+          g1 = ps[i + 1] == 0u ? 0.f : g1;
+        }
+        pd[8 * u + 2 * r + e] = pack_bf16x2(g0, g1);
+      }
+}
+
 template <int D>
 struct DkdvCfg {
   static constexpr int kTileBytes = kTile * D * 2;  // 128 x D bf16
@@ -649,16 +706,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int r = 0; r < 4; ++r) lv[cb][r] = *reinterpret_cast<const float2*>(Lq + 32 * cb + 8 * r);
         // Blocks away from the diagonal and from ragged chunk ends need no mask.
-        // window form: position of the block's first query, relative to its first key
-        [[maybe_unused]] int pq = 0;
         bool full = !dg && q_valid == kTile && U.k_valid == kTile;
-        if constexpr (kWin) {
-          pq = U.off + tile * kTile - U.k_t0;
-          full = full && win_block_full(g, U.off + tile * kTile, U.k_t0);
-        }
         uint32_t valid[2][4];
         uint32_t pp[2][16];
-        if (full) {
+        if constexpr (kWin) {
+          full = q_valid == kTile && win_block_full(g, U.off + tile * kTile, U.k_t0);
+          if (full) {
+            const int from[4] = {0, 0, 0, 0};
+            const uint32_t len[4] = {0, 0, 0, 0};
+            softmax_p_frag32<false>(ra, sl2, lv[0], from, len, pp[0]);
+            softmax_p_frag32<false>(rb, sl2, lv[1], from, len, pp[1]);
+          } else {
+            // A key row is seen by the block's queries from its own position
+            // on, up to its window's last one unless it is a first token.
+            // (Rows past the last key only reach their own rows of dK, dV,
+            // which are not stored.)
+            const int pq = U.off + tile * kTile - U.k_t0;  // first query's position, from the first key
+            int from[4];
+            uint32_t len[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int kr = wq * 32 + 8 * f + g4;  // key row of fragment row f (16u + 8e = 8f)
+              int a0 = kr - pq, a1 = q_valid;
+              if (U.k_t0 + kr >= g.sinks && a0 + g.window < a1) a1 = a0 + g.window;
+              a0 = a0 > 0 ? a0 : 0;
+              from[f] = a0 - 64 * hf - 2 * c4;
+              len[f] = a1 > a0 ? a1 - a0 : 0;
+            }
+            softmax_p_frag32<true>(ra, sl2, lv[0], from, len, pp[0]);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) from[f] -= 32;
+            softmax_p_frag32<true>(rb, sl2, lv[1], from, len, pp[1]);
+          }
+        } else if (full) {
           softmax_p_frag<false>(ra, sl2, lv[0], none, c4, pp[0]);
           softmax_p_frag<false>(rb, sl2, lv[1], none, c4, pp[1]);
         } else {
@@ -670,40 +750,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int f = 0; f < 4; ++f) {
               const int kr = wq * 32 + 8 * f + g4;  // key row of fragment row f (16u + 8e = 8f)
               const int qb = 64 * hf + 32 * cb;
-              if constexpr (kWin) {
-                // queries from the key's own position on, up to its window's
-                // last one unless it is a first token
-                const int from = kr - pq;
-                int to = q_valid;
-                if (U.k_t0 + kr >= g.sinks && from + g.window < to) to = from + g.window;
-                valid[cb][f] = kr < U.k_valid ? bit_range(from - qb, to - qb) : 0u;
-              } else {
-                valid[cb][f] = kr < U.k_valid ? bit_range(dg ? kr - qb : 0, q_valid - qb) : 0u;
-              }
+              valid[cb][f] = kr < U.k_valid ? bit_range(dg ? kr - qb : 0, q_valid - qb) : 0u;
             }
           softmax_p_frag<true>(ra, sl2, lv[0], valid[0], c4, pp[0]);
           softmax_p_frag<true>(rb, sl2, lv[1], valid[1], c4, pp[1]);
         }
+        if constexpr (!kWin) {
 #pragma unroll
-        for (int cb = 0; cb < 2; ++cb)
+          for (int cb = 0; cb < 2; ++cb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) dv[cb][r] = *reinterpret_cast<const float2*>(Lq + kTile + 32 * cb + 8 * r);
+            for (int r = 0; r < 4; ++r) dv[cb][r] = *reinterpret_cast<const float2*>(Lq + kTile + 32 * cb + 8 * r);
+        }
         // dP^T of the same keys and queries
         if (!(ok = mbar_wait_lean(dp_full, i & 1, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        tmem_ld16x256b_2x2(tP, tP + kL16, tP + 32, tP + kL16 + 32, ra, rb);
-        // P^T -> [64h, 64h+32) of the dP^T columns just read: dV may start
-        tmem_st16x128b_2x2(tP, tP + kL16, tP + 16, tP + kL16 + 16, pp[0], pp[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(pt_full);
         uint32_t pd[2][16];
-        if (full) {
-          ds_frag<false>(pp[0], ra, dv[0], none, c4, pd[0]);
-          ds_frag<false>(pp[1], rb, dv[1], none, c4, pd[1]);
+        if constexpr (kWin) {
+          // P stays in fp32 in ra, rb, so dP^T is taken 32 queries at a time
+          uint32_t rc[32];
+          tmem_ld16x256b_x2(tP, tP + kL16, rc);
+          // P^T -> [64h, 64h+32), the dP^T columns just read: dV may start
+          tmem_st16x128b_2x2(tP, tP + kL16, tP + 16, tP + kL16 + 16, pp[0], pp[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pt_full);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dv[0][r] = *reinterpret_cast<const float2*>(Lq + kTile + 8 * r);
+          if (q_valid == kTile)
+            ds_frag32<false>(ra, rc, dv[0], pd[0]);
+          else
+            ds_frag32<true>(ra, rc, dv[0], pd[0]);
+          tmem_ld16x256b_x2(tP + 32, tP + kL16 + 32, rc);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) dv[1][r] = *reinterpret_cast<const float2*>(Lq + kTile + 32 + 8 * r);
+          if (q_valid == kTile)
+            ds_frag32<false>(rb, rc, dv[1], pd[1]);
+          else
+            ds_frag32<true>(rb, rc, dv[1], pd[1]);
         } else {
-          ds_frag<true>(pp[0], ra, dv[0], valid[0], c4, pd[0]);
-          ds_frag<true>(pp[1], rb, dv[1], valid[1], c4, pd[1]);
+          tmem_ld16x256b_2x2(tP, tP + kL16, tP + 32, tP + kL16 + 32, ra, rb);
+          // P^T -> [64h, 64h+32) of the dP^T columns just read: dV may start
+          tmem_st16x128b_2x2(tP, tP + kL16, tP + 16, tP + kL16 + 16, pp[0], pp[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pt_full);
+          if (full) {
+            ds_frag<false>(pp[0], ra, dv[0], none, c4, pd[0]);
+            ds_frag<false>(pp[1], rb, dv[1], none, c4, pd[1]);
+          } else {
+            ds_frag<true>(pp[0], ra, dv[0], valid[0], c4, pd[0]);
+            ds_frag<true>(pp[1], rb, dv[1], valid[1], c4, pd[1]);
+          }
         }
         // dS^T -> [64h+32, 64h+64)
         tmem_st16x128b_2x2(tP + 32, tP + kL16 + 32, tP + 48, tP + kL16 + 48, pd[0], pd[1]);
@@ -805,6 +902,38 @@ __device__ __forceinline__ void ds_row32(const uint32_t (&pp)[16], const uint32_
     pd[i] = pack_bf16x2(g0, g1);
     if constexpr (kMasked)
       pd[i] &= ((valid >> (2 * i)) & 1u ? 0x0000ffffu : 0u) | ((valid >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+  }
+}
+
+// The window form's versions, P kept in fp32 (see softmax_p_frag32): key c of
+// the 32 is visible when c lies in [from, from + len) or below first.
+template <bool kMasked>
+__device__ __forceinline__ void p_row32_fp32(uint32_t (&rs)[32], float sl2, float l2, int from, uint32_t len, int first) {
+  const uint64_t sl2x2 = f2_pack(sl2, sl2), nl2 = f2_pack(-l2, -l2);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(rs[i]), __uint_as_float(rs[i + 1])), sl2x2, nl2), x0, x1);
+    x0 = ex2_approx(x0);
+    x1 = ex2_approx(x1);
+    if constexpr (kMasked) {
+      x0 = uint32_t(i - from) < len || i < first ? x0 : 0.f;
+      x1 = uint32_t(i + 1 - from) < len || i + 1 < first ? x1 : 0.f;
+    }
+    rs[i] = __float_as_uint(x0);
+    rs[i + 1] = __float_as_uint(x1);
+  }
+}
+__device__ __forceinline__ void ds_row32_fp32(const uint32_t (&ps)[32], const uint32_t (&rp)[32], float dd,
+                                              uint32_t (&pd)[16]) {
+  const uint64_t ddx2 = f2_pack(dd, dd);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float g0, g1;
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(ps[i]), __uint_as_float(ps[i + 1])),
+                     f2_sub(f2_pack(__uint_as_float(rp[i]), __uint_as_float(rp[i + 1])), ddx2)),
+              g0, g1);
+    pd[i / 2] = pack_bf16x2(g0, g1);
   }
 }
 
@@ -1197,15 +1326,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int cb = hf * 64;
         bool full;
         uint32_t v0 = 0u, v1 = 0u;  // bit c: key column c (of this warp's 64) is visible
+        uint32_t pp0[16], pp1[16];
         if constexpr (kWin) {
           const int p0 = U.off + U.q_t0, kb = win_tile(U, j) * kTile;
           full = win_block_full(g, p0, kb);
-          if (!full) {
-            // columns up to the row's own position, from its window's first on or before the last first token
-            const int hi = p0 + jr + 1 - kb - cb, lo = hi - g.window;
+          if (full) {
+            p_row32_fp32<false>(r0, sl2, l2, 0, 0, 0);
+            p_row32_fp32<false>(r1, sl2, l2, 0, 0, 0);
+          } else {
+            // columns up to the row's own position, from its window's first
+            // on or before the last first token
+            const int hi = p0 + jr + 1 - kb - cb;
+            const int from = hi - g.window;
             const int first = g.sinks - kb - cb < hi ? g.sinks - kb - cb : hi;
-            v0 = bit_range(lo, hi) | bit_range(0, first);
-            v1 = bit_range(lo - 32, hi - 32) | bit_range(0, first - 32);
+            p_row32_fp32<true>(r0, sl2, l2, from, g.window, first);
+            p_row32_fp32<true>(r1, sl2, l2, from - 32, g.window, first - 32);
           }
         } else {
           full = !dg && n_valid == kTile;
@@ -1215,22 +1350,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (dg && jr + 1 - cb < hi) hi = jr + 1 - cb;
           v0 = full ? 0u : bit_range(0, hi);
           v1 = full ? 0u : bit_range(0, hi - 32);
-        }
-        uint32_t pp0[16], pp1[16];
-        if (full) {
-          p_row32<false>(r0, sl2, l2, 0u, pp0);
-          p_row32<false>(r1, sl2, l2, 0u, pp1);
-        } else {
-          p_row32<true>(r0, sl2, l2, v0, pp0);
-          p_row32<true>(r1, sl2, l2, v1, pp1);
+          if (full) {
+            p_row32<false>(r0, sl2, l2, 0u, pp0);
+            p_row32<false>(r1, sl2, l2, 0u, pp1);
+          } else {
+            p_row32<true>(r0, sl2, l2, v0, pp0);
+            p_row32<true>(r1, sl2, l2, v1, pp1);
+          }
         }
         if (!(ok = mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        tmem_ld32x2(tdP, tdP + 32, r0, r1);
+        [[maybe_unused]] uint32_t s0[32], s1[32];
+        if constexpr (kWin)
+          tmem_ld32x2(tdP, tdP + 32, s0, s1);
+        else
+          tmem_ld32x2(tdP, tdP + 32, r0, r1);
         uint32_t pd0[16], pd1[16];
         // dS packed into [64h, 64h+32) of the dP columns (read above), its
         // first 32 keys published before the second are formed
-        if (full)
+        if constexpr (kWin)
+          ds_row32_fp32(r0, s0, dd, pd0);
+        else if (full)
           ds_row32<false>(pp0, r0, dd, 0u, pd0);
         else
           ds_row32<true>(pp0, r0, dd, v0, pd0);
@@ -1238,7 +1378,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_half);
-        if (full)
+        if constexpr (kWin)
+          ds_row32_fp32(r1, s1, dd, pd1);
+        else if (full)
           ds_row32<false>(pp1, r1, dd, 0u, pd1);
         else
           ds_row32<true>(pp1, r1, dd, v1, pd1);

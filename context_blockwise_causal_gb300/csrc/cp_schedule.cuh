@@ -84,6 +84,7 @@ struct CpGeom {
   int sinks = 0;         // ... and the first `sinks` keys
   int part_tiles = 0;    // dK/dV: query tiles per part of a cut walk
   int sink_parts = 0;    // dK/dV: parts per cut walk (1: none is cut)
+  FastDiv fd_per, fd_T, fd_kt, fd_parts, fd_cut;  // divisors of its unit decodes (win_set_divs)
   // divisors of the backward's unit decodes (set_fast_divs; set again
   // whenever b, hq, hkv or tpc change)
   FastDiv fd_hq, fd_hkv, fd_G, fd_tpc, fd_bhq, fd_bhkv;

@@ -419,6 +419,16 @@ __device__ __forceinline__ void tmem_ld16x256b_2x2(uint32_t ta0, uint32_t ta1, u
       : "r"(ta0), "r"(ta1), "r"(tb0), "r"(tb1)
       : "memory");
 }
+// Two of them (lanes +0 and +16 of one column range) with one wait.
+__device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t ta0, uint32_t ta1, uint32_t (&ra)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : CPATTN_RA8(0), CPATTN_RA8(8), CPATTN_RA8(16), CPATTN_RA8(24)
+      : "r"(ta0), "r"(ta1)
+      : "memory");
+}
 #undef CPATTN_RA8
 #undef CPATTN_RB8
 

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kQkThreads) cpattn_qk_fwd_kernel(const __grid_
 // added across the CTA in a fixed order at the end and across CTAs by
 // cpattn_qk_dw_kernel: no atomics, the same bits every time.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kQkThreads) cpattn_qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   constexpr int kT = D / 16, kRows = 32 / kT, kWarps = kQkThreads / 32, kU = 2;
   __shared__ float red[kWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

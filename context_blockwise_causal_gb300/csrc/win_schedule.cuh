@@ -115,12 +115,13 @@ __host__ __device__ inline WinUnit win_fwd_unit(const CpGeom& g, int idx) {
     tile = g.tile0[U.seq + 1] - g.tile0[U.seq] - 1 - local;
   } else {
     const int T = win_unit_tiles(g.s, kPairs);
-    int x = idx / per;
+    const int x = g.fd_per.div(idx);
     hp = idx - x * per;
-    const int y = x / T;
+    const int y = g.fd_T.div(x);
     tile = T - 1 - (x - y * T);  // the shorter walks of the first tiles come last
-    U.seq = y / g.hkv;
-    hp += (y - U.seq * g.hkv) * per;
+    U.seq = g.fd_hkv.div(y);
+    const int kvh = y - U.seq * g.hkv;
+    hp += kvh * per;
   }
   const WinSeq s = win_seq(g, U.seq);
   U.bi = g.nseq > 0 ? 0 : U.seq;
@@ -133,7 +134,7 @@ __host__ __device__ inline WinUnit win_fwd_unit(const CpGeom& g, int idx) {
   U.k = U.r = U.half = 0;
   U.h0 = kPairs ? hp : 2 * hp;
   U.h1 = kPairs ? hp : 2 * hp + 1;
-  U.g0 = U.g1 = U.h0 / G;
+  U.g0 = U.g1 = g.fd_G.div(U.h0);
   U.store1 = true;
   U.u = U.u0 = kPairs ? 2 * tile : tile;
   U.q_t0 = U.q_t1 = U.u0 * kTile;
@@ -168,10 +169,10 @@ __host__ __device__ inline WinUnit win_dq_unit(const CpGeom& g, int idx) {
     U.seq = packed_sample_of(g, p, local);
     U.u = g.tile0[U.seq + 1] - g.tile0[U.seq] - 1 - local;
   } else {
-    const int x = idx / G;
-    const int y = x / g.tpc;
+    const int x = g.fd_G.div(idx);
+    const int y = g.fd_tpc.div(x);
     U.u = g.tpc - 1 - (x - y * g.tpc);
-    U.seq = y / g.hkv;
+    U.seq = g.fd_hkv.div(y);
     U.h0 = (y - U.seq * g.hkv) * G + (idx - x * G);
   }
   const WinSeq s = win_seq(g, U.seq);
@@ -184,7 +185,7 @@ __host__ __device__ inline WinUnit win_dq_unit(const CpGeom& g, int idx) {
   U.tpc = g.tpc;
   U.k = U.r = U.half = 0;
   U.h1 = U.h0;
-  U.g0 = U.g1 = U.h0 / G;
+  U.g0 = U.g1 = g.fd_G.div(U.h0);
   U.store1 = false;
   U.u0 = U.u;
   U.q_t0 = U.q_t1 = U.u * kTile;
@@ -241,11 +242,11 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   U.slot = -1;
   if (idx < ncut) {
     U.slot = idx;
-    int x = idx / g.sink_parts;
+    const int x = g.fd_parts.div(idx);
     part = idx - x * g.sink_parts;
-    const int y = x / cut;
+    const int y = g.fd_cut.div(x);
     kt = x - y * cut;
-    U.seq = y / g.hkv;
+    U.seq = g.fd_hkv.div(y);
     U.g = y - U.seq * g.hkv;
   } else {
     idx -= ncut;
@@ -255,9 +256,9 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
       U.seq = packed_sample_of(g, p, kt);
     } else {
       const int T = win_key_tiles(g);
-      const int y = idx / T;
+      const int y = g.fd_kt.div(idx);
       kt = idx - y * T;
-      U.seq = y / g.hkv;
+      U.seq = g.fd_hkv.div(y);
       U.g = y - U.seq * g.hkv;
     }
   }
@@ -303,6 +304,19 @@ __host__ __device__ inline void win_set_parts(CpGeom& g) {
   if (g.tpc <= tiles) return;
   g.part_tiles = tiles;
   g.sink_parts = (g.tpc + tiles - 1) / tiles;
+}
+
+// The divisors of the decodes above; after win_finish and win_set_parts.
+__host__ __device__ inline void win_set_divs(CpGeom& g, bool pairs) {
+  const int G = g.hq / g.hkv, T = win_unit_tiles(g.s, pairs), cut = win_cut_tiles(g);
+  g.fd_hkv = make_fastdiv(g.hkv);
+  g.fd_G = make_fastdiv(G);
+  g.fd_tpc = make_fastdiv(g.tpc > 0 ? g.tpc : 1);
+  g.fd_per = make_fastdiv(pairs ? G : (G > 1 ? G / 2 : 1));
+  g.fd_T = make_fastdiv(T > 0 ? T : 1);
+  g.fd_kt = make_fastdiv(win_key_tiles(g) > 0 ? win_key_tiles(g) : 1);
+  g.fd_parts = make_fastdiv(g.sink_parts);
+  g.fd_cut = make_fastdiv(cut > 0 ? cut : 1);
 }
 
 }  // namespace cpattn

@@ -52,6 +52,7 @@ CpGeom win_geom(const WinShape& w, const int* cu, int nseq, bool pairs) {
   for (int i = 0; i <= nseq && cu; ++i) g.cu[i] = cu[i];
   win_finish(g, pairs);
   win_set_parts(g);
+  win_set_divs(g, pairs);
   return g;
 }
 

@@ -8,6 +8,26 @@ import torch
 
 import oracle
 
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+    @property
+    def _as_parameter_(self):
+        return ctypes.byref(self)
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("rot_dim", ctypes.c_int), ("magnitude", ctypes.c_float), ("s", ctypes.c_int),
+                ("cp", ctypes.c_int), ("rank", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p), ("nseq", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("positions_batch", ctypes.c_int64), ("inv_freq", ctypes.c_void_p)]
+
+    @property
+    def _as_parameter_(self):
+        return ctypes.byref(self)
+
+
 P = ctypes.c_void_p(4096)
 ODD = ctypes.c_void_p(4096 + 8)
 ARG, NULL, MISALIGNED, ARCH, SMALL = -1, -2, -3, -4, -5
@@ -83,16 +103,14 @@ def test_decode_arguments(lib):
 
 
 def test_rotary_arguments(lib):
-    import context_blockwise_causal_gb300 as pkg
-
     freq = torch.ones(64, dtype=torch.float64)
 
     def plan(**kw):
         a = {"layout": 0, "rot_dim": 64, "magnitude": 1.0, "s": 10, "cp": 1, "rank": -1, "inv_freq": freq.data_ptr()} | kw
-        return pkg._Rotary(**a)
+        return Rotary(**a)
 
     def rows(data=4096, batch=1280, token=128):
-        return pkg._Rows(data, batch, token)
+        return Rows(data, batch, token)
 
     def f(x=None, y=None, pl=None, b=2, n=10, h=2, d=64):
         return lib.cpattn_rope_ex(x or rows(), y or rows(), b, n, h, d, pl or plan(), 0, None)
@@ -145,3 +163,16 @@ def test_frequencies(lib):
                 (64, 1e4, 3, 2.0, 0.0, 1.0, 4.0), (64, 1e4, 3, 2.0, 8192.0, 4.0, 1.0), (64, 1e4, 4, 2.0, 8192.0, 0.0, 1.0),
                 (64, float("inf"), 0, 1.0, 0.0, 0.0, 0.0)):
         assert f(*bad, out) == ARG, bad
+
+
+def test_packed_structs_match_the_header():
+    """The binding packs cpattn_rows and cpattn_rotary as bytes: the same
+    layout as the C structs (checked against ctypes', field by field)."""
+    import context_blockwise_causal_gb300 as pkg
+
+    assert bytes(Rows(4096, 5, 6)) == pkg._ROWS(4096, 5, 6)
+    r = Rotary(1, 64, 1.5, 7, 2, -1, 4096, 3, 8192, 9, 12288)
+    got = pkg._PLAN(1, 64, 1.5, 7, 2, -1, 4096, 3, 8192, 9, 12288)
+    assert len(got) == ctypes.sizeof(Rotary)
+    for name, _ in Rotary._fields_:
+        assert getattr(Rotary.from_buffer_copy(got), name) == getattr(r, name), name

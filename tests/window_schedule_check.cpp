@@ -72,6 +72,8 @@ static int block(const CpGeom& g, const WinSeq& s, Count& n, int h, int qt, int 
 template <bool kPairs>
 static int forward(CpGeom g, long* pairs) {
   win_finish(g, kPairs);
+  win_set_parts(g);
+  win_set_divs(g, kPairs);
   const int qrows = g.b * g.s, kvrows = g.b * g.kv_s;
   Count n(g.hq, qrows);
   const long units = win_fwd_units(g, kPairs);
@@ -100,6 +102,7 @@ static int forward(CpGeom g, long* pairs) {
 static int backward(CpGeom g, long* dq_pairs, long* kv_pairs) {
   win_finish(g, false);
   win_set_parts(g);
+  win_set_divs(g, false);
   const int qrows = g.b * g.s, kvrows = g.b * g.kv_s, G = g.hq / g.hkv;
   Count n(g.hq, qrows);
   for (long idx = 0; idx < win_dq_units(g); ++idx) {
