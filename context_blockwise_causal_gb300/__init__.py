@@ -449,9 +449,9 @@ def _empty(shape, like, stream, dtype=_BF16):
     call runs on: the caching allocator then hands it to nobody else before
     that stream is done with it."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _dense(name, t, dtype, shape):
@@ -833,7 +833,7 @@ def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, s
 
 
 def cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
-    """Workspace bytes of cpattn_decode on the current device."""
+    """Workspace bytes of cpattn_decode on the current device (0: none)."""
     return int(library().cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, int(window), int(sinks)))
 
 
@@ -872,8 +872,8 @@ def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o
         o = _empty((b, hq, d), q, stream)
     if lse is None:
         lse = _empty((b, hq), q, stream, _F32)
-    ws, ws_bytes, workspace = _workspace(workspace, _decode_bytes(_device(), b, hq, hkv, d, cap, window, sinks), q,
-                                         stream)
+    need = _decode_bytes(_device(), b, hq, hkv, d, cap, window, sinks)
+    ws, ws_bytes, workspace = (None, 0, None) if need == 0 else _workspace(workspace, need, q, stream)
     rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ln,
                                  _dense("o", o, _BF16, (b, hq, d)), _dense("lse", lse, _F32, (b, hq)), ws, ws_bytes, b,
                                  hq, hkv, d, cap, qb, kb, kt, kh, vb, vt, vh, window, sinks,

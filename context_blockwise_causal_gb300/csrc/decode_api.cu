@@ -25,10 +25,12 @@ int64_t max_keys(int cap, int window, int sinks) {
   return seen < cap ? seen : cap;
 }
 
-// Runs per (sequence, KV head): two CTAs fit an SM. With long sequences four
-// CTAs per place level out their different lengths (runs of 512 keys or more,
-// whose fp32 results are under 2 % of what they read); with few sequences a
-// run goes down to one round of the warps, 64 keys.
+// Runs per (sequence, KV head): two CTAs fit an SM. With many keys four CTAs
+// per place level out different lengths (runs of 512 keys or more); with few
+// sequences a run goes down to one round of the warps, 64 keys. Runs of one
+// cluster are a power of two; only when 16 of them leave over half of the
+// chip idle, on runs of at least 2048 keys, are there more (device memory and
+// the second kernel).
 int choose_split(int num_sms, int64_t units, int64_t keys) {
   const int64_t places = 2 * int64_t(num_sms);
   int64_t s = (4 * places + units - 1) / units;
@@ -36,11 +38,18 @@ int choose_split(int num_sms, int64_t units, int64_t keys) {
   int64_t fill = places / units;
   if (fill > keys / 64) fill = keys / 64;
   if (s < fill) s = fill;
-  return int(s < 1 ? 1 : (s > kDecMaxSplit ? kDecMaxSplit : s));
+  if (s > kDecMaxCluster && 2 * kDecMaxCluster * units <= num_sms && keys / 2048 > kDecMaxCluster) {
+    s = keys / 2048 < s ? keys / 2048 : s;
+    return int(s < kDecMaxSplit ? s : kDecMaxSplit);
+  }
+  int p = 1;
+  while (2 * p <= s && 2 * p <= kDecMaxCluster) p *= 2;
+  return p;
 }
 
+// Workspace bytes (0: none).
 size_t workspace_for(int b, int hq, int d, int nsplit) {
-  if (nsplit <= 1) return 16;
+  if (nsplit <= kDecMaxCluster) return 0;
   const size_t rows = size_t(b) * hq * nsplit;
   return align256(rows * d * 4) + align256(rows * 4);
 }
@@ -54,13 +63,30 @@ int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
   std::atomic<bool>& done = di->decode_attr[D == 128 ? 1 : 0];
   if (!done.load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(cpattn_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             DecodeCfg<D>::kSmemBytes) != cudaSuccess)
+                             DecodeCfg<D>::kSmemBytes) != cudaSuccess ||
+        cudaFuncSetAttribute(cpattn_decode_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return CPATTN_ERR_CUDA;
     done.store(true, std::memory_order_release);
   }
   const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
-  cpattn_decode_kernel<D><<<int(ctas), kDecWarps * 32, DecodeCfg<D>::kSmemBytes, st>>>(a);
-  if (a.nsplit > 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.dynamicSmemBytes = DecodeCfg<D>::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = unsigned(a.nsplit);
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  if (a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
+    cfg.attrs = &cluster;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, cpattn_decode_kernel<D>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return CPATTN_ERR_LAUNCH_FAILED;
+  }
+  if (a.nsplit > kDecMaxCluster) {
     const int64_t rows = int64_t(a.b) * a.hq;
     cpattn_decode_join_kernel<D><<<int((rows + 3) / 4), 128, 0, st>>>(a);
   }
@@ -82,7 +108,7 @@ extern "C" int cpattn_decode(const void* q, const void* k_cache, const void* v_c
                              int cap, int64_t q_batch, int64_t k_batch, int64_t k_token, int64_t k_head,
                              int64_t v_batch, int64_t v_token, int64_t v_head, int window, int sinks, float scale,
                              void* stream) {
-  if (!q || !k_cache || !v_cache || !lengths || !o || !lse || !workspace) return CPATTN_ERR_NULL_PTR;
+  if (!q || !k_cache || !v_cache || !lengths || !o || !lse) return CPATTN_ERR_NULL_PTR;
   int rc = check_shape(b, hq, hkv, d, cap, window, sinks);
   if (rc) return rc;
   if (!(scale == 0.f || valid_scale(scale))) return CPATTN_ERR_INVALID_ARG;
@@ -117,7 +143,9 @@ extern "C" int cpattn_decode(const void* q, const void* k_cache, const void* v_c
   a.row_groups = (a.G + 15) / 16;
   const int64_t units = int64_t(b) * hkv * a.row_groups;
   a.nsplit = choose_split(di->num_sms, units, max_keys(cap, window, sinks));
-  if (workspace_bytes < workspace_for(b, hq, d, a.nsplit)) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = workspace_for(b, hq, d, a.nsplit);
+  if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
+  if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
   a.scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));

@@ -21,7 +21,10 @@
 // its own running maximum, sum and O, so warps never wait for one another
 // until the end. Keys past the run are never read: their slots are filled
 // with zeros and their scores masked, whatever the cache holds there. Warps
-// and then runs are joined through their log-sum-exp in a fixed order.
+// and then runs are joined through their log-sum-exp in a fixed order. Up to
+// 16 runs are the CTAs of one cluster, which read one another's results from
+// shared memory: one launch and no workspace. More runs (a few very long
+// sequences) go through device memory and a second kernel.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -34,6 +37,7 @@ namespace cpattn {
 constexpr int kDecWarps = 4;
 constexpr int kDecStages = 3;
 constexpr int kDecBlock = 16;  // keys per block
+constexpr int kDecMaxCluster = 16;
 constexpr int kDecMaxSplit = 64;
 
 struct DecodeArgs {
@@ -43,7 +47,7 @@ struct DecodeArgs {
   const int* lengths;      // [b] device
   __nv_bfloat16* o;        // [b, hq, D]
   float* lse;              // [b, hq]
-  float* part_o;           // nsplit > 1: [b, hq, nsplit, D] normalised
+  float* part_o;           // nsplit > kDecMaxCluster: [b, hq, nsplit, D] normalised
   float* part_lse;         // [b, hq, nsplit], base-2
   int64_t q_batch;
   int64_t k_batch, k_token, k_head, v_batch, v_token, v_head;  // elements
@@ -60,8 +64,10 @@ struct DecodeCfg {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kDecStages * kStageBytes;
   static constexpr int kSmemBytes = kDecWarps * kWarpBytes;
-  // the join of the warps reuses the rings: 16 x D fp32 and 16 pairs per warp
-  static_assert(16 * D * 4 + 16 * 8 <= kWarpBytes, "join buffer");
+  // the join of the warps reuses the rings: 16 x D fp32 and 16 pairs per
+  // warp; in warp 0's, behind it, the CTA's result for the cluster's join
+  static constexpr int kResult = 16 * D * 4 + 16 * 8;
+  static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -91,6 +97,28 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A shared-memory address of CTA `rank` of the cluster, and loads through it.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+// All threads of the cluster's CTAs (a hardware barrier: they run together).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int D>
@@ -292,12 +320,42 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
     if (a.nsplit == 1) {
       *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);
       if (c == 0) a.lse[row] = l2 * 0.69314718055994530942f;
+    } else if (a.nsplit <= kDecMaxCluster) {
+      float* res = reinterpret_cast<float*>(smem + C::kResult);
+      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(o0 * inv, o1 * inv);
+      if (c == 0) res[16 * D + r] = l2;
     } else {
       const int64_t pr = row * a.nsplit + split;
       *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(o0 * inv, o1 * inv);
       if (c == 0) a.part_lse[pr] = l2;
     }
   }
+  if (a.nsplit == 1 || a.nsplit > kDecMaxCluster) return;
+  // The cluster's CTAs are the runs of one unit, in order: each joins its
+  // share of the unit's features.
+  cluster_sync();
+  const uint32_t res = smem_u32(smem) + C::kResult;
+  for (int i = split * kDecWarps * 32 + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kDecWarps * 32) {
+    const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+    float mm = -INFINITY;
+#pragma unroll 4
+    for (int s = 0; s < a.nsplit; ++s) mm = fmaxf(mm, cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)));
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < a.nsplit; ++s) {
+      const float w = ex2_approx(cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)) - base);
+      const float2 o = cluster_ld2(cluster_addr(res + (r * D + c) * 4, s));
+      ll += w;
+      o0 = fmaf(w, o.x, o0);
+      o1 = fmaf(w, o.y, o1);
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int64_t row = int64_t(bi) * a.hq + h0 + r;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);
+    if (c == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
+  }
+  cluster_sync();  // no CTA leaves while another still reads its results
 }
 
 // Joins the runs of a row: one warp per (sequence, query head).

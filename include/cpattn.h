@@ -491,9 +491,10 @@ int cpattn_bwd_window_varlen(const void* q, const void* k, const void* v, const 
  *             sequence's length is read.
  *   window:   0: every key; otherwise as above, with the first `sinks` keys.
  *   workspace: device, 16-byte aligned, at least
- *             cpattn_decode_workspace_bytes(...) bytes (of the current
- *             device; 0 for an unsupported shape or device), contents
- *             irrelevant. Calls that may overlap need one each.
+ *             cpattn_decode_workspace_bytes(...) bytes (on the current
+ *             device), contents irrelevant. Calls that may overlap need one
+ *             each. Mostly none is needed: 0 bytes, and NULL will do (0 too
+ *             for a shape or device that cpattn_decode refuses).
  * scale 0 selects 1/sqrt(d). d in {64, 128}. Deterministic. Errors: NULL_PTR,
  * INVALID_ARG, MISALIGNED, WORKSPACE_TOO_SMALL, UNSUPPORTED_ARCH,
  * LAUNCH_FAILED.

@@ -47,6 +47,8 @@ CASES = [
     ([700, 33], 700, 40, 1, 64, 0, 0, None),                             # 40 heads per group: three row tiles
     ([5000], 5003, 4, 2, 128, 0, 0, None),                               # one sequence over many runs
     ([5000, 1], 5003, 4, 2, 64, 4000, 4, None),                          # a sequence shorter than the runs
+    ([40000], 40001, 4, 1, 128, 0, 0, None),                             # more runs than a cluster has CTAs
+    ([36000, 0, 3], 40001, 4, 1, 64, 35000, 4, None),
     ([300, 300], 300, 2, 1, 128, 1, 0, None),                            # a window of the new token alone
     ([300, 2], 300, 2, 1, 128, 1, 500, None),                            # every key a first token
     ([777] * 90, 800, 16, 8, 64, 500, 1, None),                          # more sequences than places
@@ -104,11 +106,10 @@ def test_graph_replays_with_new_lengths():
     q, k, v = _randn(b, hq, d, seed=10), _randn(b, cap, hkv, d, seed=11), _randn(b, cap, hkv, d, seed=12)
     qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
     ln = torch.tensor([1, 500], dtype=torch.int32, device="cuda")
-    ws = torch.empty(pkg.cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, 64, 4), dtype=torch.uint8, device="cuda")
-    cpattn_decode(qd, kd, vd, ln, 64, 4, workspace=ws)
+    cpattn_decode(qd, kd, vd, ln, 64, 4)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        o, lse = cpattn_decode(qd, kd, vd, ln, 64, 4, workspace=ws)
+        o, lse = cpattn_decode(qd, kd, vd, ln, 64, 4)
     for lengths in ([1, 500], [64, 65], [0, 600]):
         ln.copy_(torch.tensor(lengths, dtype=torch.int32))
         g.replay()
@@ -138,7 +139,7 @@ def test_checked_build_is_silent_and_identical():
         o, lse = cpattn_decode(q, k, v, ln, window, sinks)
         o2, l2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
         n = lib.cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window, sinks)
-        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
         rc = lib.cpattn_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), ln.data_ptr(), o2.data_ptr(), l2.data_ptr(),
                                ws.data_ptr(), n, b, hq, hkv, d, cap, hq * d, cap * hkv * d, hkv * d, d, cap * hkv * d,
                                hkv * d, d, window, sinks, 0.0, None)
@@ -167,6 +168,7 @@ def test_refusals():
     with pytest.raises(TypeError):
         cpattn_decode(q, k.float(), k.float(), ln)
     need = pkg.cpattn_decode_workspace_bytes(1, 4, 2, 64, 100000)
+    assert need > 0  # a few long sequences: over 16 runs
     big = torch.zeros(1, 100000, 2, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(pkg.CpattnError):
         cpattn_decode(q[:1], big, big, ln[:1], workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))

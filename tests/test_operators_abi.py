@@ -91,7 +91,7 @@ def test_decode_arguments(lib):
           sinks=0, scale=0.0):
         return lib.cpattn_decode(*ptr, n, b, hq, hkv, d, cap, *strides, window, sinks, scale, None)
 
-    for i in range(7):
+    for i in range(6):
         assert f((P,) * i + (None,) + (P,) * (6 - i)) == NULL
     for bad in ({"b": 0}, {"hq": 3}, {"d": 80}, {"cap": 0}, {"cap": (1 << 30) + 1}, {"window": -1}, {"sinks": -1},
                 {"scale": -2.0}, {"strides": (256, 12800, 129, 64, 12800, 128, 64)},
