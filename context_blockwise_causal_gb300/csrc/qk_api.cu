@@ -18,8 +18,9 @@ constexpr double kTwoPi = 6.283185307179586476925;
 // Turns per position as a fraction of 2^64 (whole turns drop out).
 uint64_t turn_fraction(double radians) {
   double t = radians / kTwoPi;
-  t -= std::floor(t);
-  return uint64_t(std::ldexp(t, 32)) << 32 | uint64_t(std::ldexp(std::ldexp(t, 32) - std::floor(std::ldexp(t, 32)), 32));
+  t = (t - double(int64_t(t))) * 4294967296.0;  // exact: radians <= 1e6
+  const uint64_t hi = uint64_t(t);
+  return hi << 32 | uint64_t((t - double(hi)) * 4294967296.0);
 }
 
 // Checks the rotary plan for b x n tokens and fills the kernel's fields.
@@ -88,7 +89,7 @@ int launch_fwd(QkArgs& a, DeviceInfo* di, cudaStream_t st) {
   const int split = want < groups ? int(want) : groups;
   a.heads_per = (groups + split - 1) / split * kRows;
   a.split = (heads + a.heads_per - 1) / a.heads_per;
-  const int64_t ctas = (tokens * a.split + kWarps - 1) / kWarps, most = int64_t(di->num_sms) * 16;
+  const int64_t ctas = (tokens * a.split + kWarps - 1) / kWarps, most = int64_t(di->num_sms) * 2;  // resident at once
   cpattn_qk_fwd_kernel<D, kNorm, kInter><<<int(ctas < most ? ctas : most), kQkThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
 }
@@ -100,16 +101,19 @@ int dispatch_fwd(QkArgs& a, int d, int layout, DeviceInfo* di, cudaStream_t st) 
   return d == 128 ? launch_fwd<128, kNorm, false>(a, di, st) : launch_fwd<64, kNorm, false>(a, di, st);
 }
 
-// CTAs of the backward at most: two per SM of the largest chip of this kind.
+// CTAs of the backward at most (the workspace holds one row of sums for each).
 constexpr int kQkBwdMaxCtas = 512;
 
 template <int D>
 int launch_bwd(QkArgs& a, int layout, float* dwq, float* dwk, DeviceInfo* di, cudaStream_t st) {
   const int64_t tokens = int64_t(a.b) * a.n, per = kQkThreads / 32;
-  int64_t most = int64_t(di->num_sms) * 3;
+  int64_t most = int64_t(di->num_sms) * 2;  // resident at once
   if (most > kQkBwdMaxCtas) most = kQkBwdMaxCtas;
-  const int hq = a.t[0].h, hk = a.t[1].h;
-  int64_t kc = (most * hk + (hq + hk) / 2) / (hq + hk);
+  // A token costs its rows and, for its cosines, about as much as kCosRows
+  // groups of rows a warp works on at once.
+  constexpr int kRows = 32 / (D / 16), kCosRows = 1;
+  const int64_t cq = (a.t[0].h + kRows - 1) / kRows + kCosRows, ck = (a.t[1].h + kRows - 1) / kRows + kCosRows;
+  int64_t kc = (most * ck + (cq + ck) / 2) / (cq + ck);
   kc = kc < 1 ? 1 : (kc > most - 1 ? most - 1 : kc);
   const int64_t need = (tokens + per - 1) / per;
   const int64_t qc = most - kc < need ? most - kc : need;

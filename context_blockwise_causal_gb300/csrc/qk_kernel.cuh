@@ -152,18 +152,22 @@ __device__ __forceinline__ int qk_position(const QkArgs& a, int bi, int tok) {
   return a.positions ? a.positions[int64_t(bi) * a.pos_batch + tok] : rope_position(a, tok);
 }
 
-__device__ __forceinline__ void qk_weights(const void* w, int fp32, const QkLane& l, float (&out)[16]) {
-  if (fp32) {
-    const float* p = static_cast<const float*>(w);
+// The norm weights of both tensors as fp32 in shared memory (registers hold
+// the rows in flight instead).
+template <int D>
+__device__ __forceinline__ void qk_stage_weights(const QkArgs& a, float (&w)[2][D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += kQkThreads) {
+    const void* p = a.t[i / D].w;
+    w[i / D][i % D] = a.w_fp32 ? static_cast<const float*>(p)[i % D]
+                               : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i % D]);
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void qk_weights(const float* w, const QkLane& l, float (&out)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + (i < 8 ? l.fa + i : l.fb + i - 8));
-      out[i] = v.x; out[i + 1] = v.y; out[i + 2] = v.z; out[i + 3] = v.w;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(w);
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p + l.fa), out);
-    bf16x8_to_f32(*reinterpret_cast<const uint4*>(p + l.fb), out + 8);
+  for (int i = 0; i < 16; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(w + (i < 8 ? l.fa + i : l.fb + i - 8));
+    out[i] = v.x; out[i + 1] = v.y; out[i + 2] = v.z; out[i + 3] = v.w;
   }
 }
 
@@ -176,165 +180,215 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // ---------------------------------------------------------------- forward
-// Heads [h0, h1) of one token of tensor t, kRows rows of the warp at a time
-// and kU such groups in flight.
-template <int D, bool kNorm, bool kInter>
-__device__ __forceinline__ void qk_token(const QkArgs& a, const QkTensor& t, int bi, int tok, int h0, int h1, int sub,
-                                         const QkLane& l, const float (&cs)[8], const float (&sn)[8]) {
-  constexpr int kT = D / 16, kRows = 32 / kT, kU = 4;
-  const __nv_bfloat16* x = t.x + int64_t(bi) * t.x_batch + int64_t(tok) * t.x_token;
-  __nv_bfloat16* y = t.y + int64_t(bi) * t.y_batch + int64_t(tok) * t.y_token;
-  [[maybe_unused]] float w[16];
-  if constexpr (kNorm) qk_weights(t.w, a.w_fp32, l, w);
-  for (int h = h0; h < h1; h += kRows * kU) {
-    uint4 va[kU], vb[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int hh = h + u * kRows + sub;
-      if (hh < h1) {
-        va[u] = *reinterpret_cast<const uint4*>(x + hh * D + l.fa);
-        vb[u] = *reinterpret_cast<const uint4*>(x + hh * D + l.fb);
-      } else {
-        va[u] = vb[u] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int hh = h + u * kRows + sub;
-      if (h + u * kRows >= h1) break;  // uniform in the warp
-      float f[16];
-      bf16x8_to_f32(va[u], f);
-      bf16x8_to_f32(vb[u], f + 8);
-      if constexpr (kNorm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
-        ss = row_sum<kT>(ss);
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] *= r * w[i];
-      }
-      qk_rotate<kInter>(f, l, cs, sn);
-      if (hh < h1 && bounds_ok(bi < a.b && tok < a.n && hh < t.h, a.status)) {
-        *reinterpret_cast<uint4*>(y + hh * D + l.fa) = f32_to_bf16x8(f);
-        *reinterpret_cast<uint4*>(y + hh * D + l.fb) = f32_to_bf16x8(f + 8);
-      }
+// One unit of a warp: some heads of one token. The heads of both tensors
+// count as one run, queries first, so the keys' rows are addressed from the
+// queries' head 0.
+template <int D, bool kNorm>
+struct QkUnit {
+  int bi, tok, h0, h1, hq;
+  const __nv_bfloat16* xq;
+  const __nv_bfloat16* xk;
+  __device__ __forceinline__ void set(const QkArgs& a, int64_t idx) {
+    const int64_t bt = idx / a.split;
+    const int part = int(idx - bt * a.split);
+    hq = a.t[0].h;
+    const int heads = hq + (kNorm ? a.t[1].h : 0);
+    bi = int(bt / a.n);
+    tok = int(bt - int64_t(bi) * a.n);
+    h0 = part * a.heads_per;
+    h1 = h0 + a.heads_per < heads ? h0 + a.heads_per : heads;
+    xq = a.t[0].x + int64_t(bi) * a.t[0].x_batch + int64_t(tok) * a.t[0].x_token;
+    xk = xq;
+    if constexpr (kNorm)
+      xk = a.t[1].x + int64_t(bi) * a.t[1].x_batch + int64_t(tok) * a.t[1].x_token - int64_t(hq) * D;
+  }
+  __device__ __forceinline__ void fetch(int hh, const QkLane& l, uint4& va, uint4& vb) const {
+    va = vb = make_uint4(0u, 0u, 0u, 0u);
+    if (hh < h1) {
+      const __nv_bfloat16* x = (hh < hq ? xq : xk) + hh * D;
+      va = *reinterpret_cast<const uint4*>(x + l.fa);
+      vb = *reinterpret_cast<const uint4*>(x + l.fb);
     }
   }
-}
+};
 
+// A warp's rows are loaded one group ahead of the one it works on, across
+// units too, so that loads are in flight while cosines are formed.
 template <int D, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kQkThreads) cpattn_qk_fwd_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int kT = D / 16;
+__global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_fwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int kT = D / 16, kRows = 32 / kT, kU = 2, kGroup = kRows * kU;
+  __shared__ __align__(16) float w[kNorm ? 2 : 1][D];
+  if constexpr (kNorm) qk_stage_weights<D>(a, w);
   const int lane = threadIdx.x & 31;
   const QkLane l = qk_lane<D, kInter>(lane % kT, a.rot);
   const int sub = lane / kT;
   const int64_t units = int64_t(a.b) * a.n * a.split;
   const int64_t step = int64_t(gridDim.x) * (kQkThreads / 32);
-  for (int64_t idx = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5); idx < units; idx += step) {
-    const int64_t bt = idx / a.split;
-    const int part = int(idx - bt * a.split);
-    const int bi = int(bt / a.n), tok = int(bt - int64_t(bi) * a.n);
+  int64_t idx = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
+  if (idx >= units) return;
+  QkUnit<D, kNorm> U;
+  U.set(a, idx);
+  uint4 va[kU], vb[kU], na[kU], nb[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) U.fetch(U.h0 + u * kRows + sub, l, va[u], vb[u]);
+  while (true) {
+    const int bi = U.bi, tok = U.tok, h1 = U.h1, hq = U.hq;
+    __nv_bfloat16* yq = a.t[0].y + int64_t(bi) * a.t[0].y_batch + int64_t(tok) * a.t[0].y_token;
+    __nv_bfloat16* yk = yq;
+    if constexpr (kNorm) yk = a.t[1].y + int64_t(bi) * a.t[1].y_batch + int64_t(tok) * a.t[1].y_token - int64_t(hq) * D;
     float cs[8], sn[8];
     qk_cos_sin(a, l, qk_position(a, bi, tok), cs, sn);
-    const int h0 = part * a.heads_per, h1 = h0 + a.heads_per, hq = a.t[0].h;
-    if (h0 < hq) qk_token<D, kNorm, kInter>(a, a.t[0], bi, tok, h0, h1 < hq ? h1 : hq, sub, l, cs, sn);
-    if (kNorm && h1 > hq) {
-      const int k1 = h1 - hq < a.t[1].h ? h1 - hq : a.t[1].h;
-      qk_token<D, kNorm, kInter>(a, a.t[1], bi, tok, h0 > hq ? h0 - hq : 0, k1, sub, l, cs, sn);
+    idx += step;
+    for (int h = U.h0, last; ; h += kGroup) {
+      last = h + kGroup >= h1;
+      if (!last) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) U.fetch(h + kGroup + u * kRows + sub, l, na[u], nb[u]);
+      } else if (idx < units) {
+        U.set(a, idx);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) U.fetch(U.h0 + u * kRows + sub, l, na[u], nb[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int hh = h + u * kRows + sub;
+        if (h + u * kRows >= h1) break;  // uniform in the warp
+        float f[16];
+        bf16x8_to_f32(va[u], f);
+        bf16x8_to_f32(vb[u], f + 8);
+        if constexpr (kNorm) {
+          float ss = 0.f, wr[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ss = fmaf(f[i], f[i], ss);
+          ss = row_sum<kT>(ss);
+          const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+          qk_weights(w[hh < hq ? 0 : 1], l, wr);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] *= r * wr[i];
+        }
+        qk_rotate<kInter>(f, l, cs, sn);
+        if (hh < h1 && bounds_ok(bi < a.b && tok < a.n, a.status)) {
+          __nv_bfloat16* y = (hh < hq ? yq : yk) + hh * D;
+          *reinterpret_cast<uint4*>(y + l.fa) = f32_to_bf16x8(f);
+          *reinterpret_cast<uint4*>(y + l.fb) = f32_to_bf16x8(f + 8);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        va[u] = na[u];
+        vb[u] = nb[u];
+      }
+      if (last) break;
     }
+    if (idx >= units) break;
   }
 }
 
 // ---------------------------------------------------------------- backward
 // dx of every row and, per CTA, the sum over its rows of t * xh. The first
-// q_ctas CTAs take the queries, the others the keys, in proportion to their
-// rows, so that a thread keeps one set of 16 sums over all its rows; they are
-// added across the CTA in a fixed order at the end and across CTAs by
-// cpattn_qk_dw_kernel: no atomics, the same bits every time.
+// q_ctas CTAs take the queries, the others the keys, so that a thread keeps
+// one set of 16 sums over all its rows; they are added across the CTA in a
+// fixed order at the end and across CTAs by cpattn_qk_dw_kernel: no atomics,
+// the same bits every time. Rows are loaded one group ahead, as above.
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int kT = D / 16, kRows = 32 / kT, kWarps = kQkThreads / 32, kU = 2;
+  constexpr int kT = D / 16, kRows = 32 / kT, kWarps = kQkThreads / 32;
+  __shared__ __align__(16) float w[2][D];
   __shared__ float red[kWarps][D];
+  qk_stage_weights<D>(a, w);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const QkLane l = qk_lane<D, kInter>(lane % kT, a.rot);
   const int sub = lane / kT;
   const bool is_q = int(blockIdx.x) < a.q_ctas;
   const QkTensor& t = a.t[is_q ? 0 : 1];
+  const float* wt = w[is_q ? 0 : 1];
   const int cta = is_q ? blockIdx.x : blockIdx.x - a.q_ctas;
   const int ctas = is_q ? a.q_ctas : gridDim.x - a.q_ctas;
-  float w[16], dw[16];
-  qk_weights(t.w, a.w_fp32, l, w);
+  float dw[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) dw[i] = 0.f;
   const int64_t tokens = int64_t(a.b) * a.n;
-  for (int64_t bt = int64_t(cta) * kWarps + warp; bt < tokens; bt += int64_t(ctas) * kWarps) {
-    const int bi = int(bt / a.n), tok = int(bt - int64_t(bi) * a.n);
+  int64_t bt = int64_t(cta) * kWarps + warp;
+  int bi = 0, tok = 0;
+  const __nv_bfloat16* x = nullptr;
+  const __nv_bfloat16* dy = nullptr;
+  auto set = [&](int64_t at) {
+    bi = int(at / a.n);
+    tok = int(at - int64_t(bi) * a.n);
+    x = t.x + int64_t(bi) * t.x_batch + int64_t(tok) * t.x_token;
+    dy = t.dy + int64_t(bi) * t.dy_batch + int64_t(tok) * t.dy_token;
+  };
+  auto fetch = [&](int hh, uint4 (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
+    if (hh < t.h) {
+      v[0] = *reinterpret_cast<const uint4*>(x + hh * D + l.fa);
+      v[1] = *reinterpret_cast<const uint4*>(x + hh * D + l.fb);
+      v[2] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fa);
+      v[3] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fb);
+    }
+  };
+  uint4 v[4], nx[4];
+  if (bt < tokens) {
+    set(bt);
+    fetch(sub, v);
+  }
+  while (bt < tokens) {
+    __nv_bfloat16* y = t.y + int64_t(bi) * t.y_batch + int64_t(tok) * t.y_token;
     float cs[8], sn[8];
     qk_cos_sin(a, l, qk_position(a, bi, tok), cs, sn);
-    const __nv_bfloat16* x = t.x + int64_t(bi) * t.x_batch + int64_t(tok) * t.x_token;
-    const __nv_bfloat16* dy = t.dy + int64_t(bi) * t.dy_batch + int64_t(tok) * t.dy_token;
-    __nv_bfloat16* y = t.y + int64_t(bi) * t.y_batch + int64_t(tok) * t.y_token;
-    for (int h = 0; h < t.h; h += kRows * kU) {
-      uint4 xa[kU], xb[kU], ga[kU], gb[kU];
+    bt += int64_t(ctas) * kWarps;
+    for (int h = 0; h < t.h; h += kRows) {
+      const int hh = h + sub;
+      if (h + kRows < t.h) {
+        fetch(h + kRows + sub, nx);
+      } else if (bt < tokens) {
+        set(bt);
+        fetch(sub, nx);
+      }
+      float f[16], g[16];
+      bf16x8_to_f32(v[0], f);
+      bf16x8_to_f32(v[1], f + 8);
+      bf16x8_to_f32(v[2], g);
+      bf16x8_to_f32(v[3], g + 8);
+      qk_rotate<kInter>(g, l, cs, sn);  // a.inverse: turns back
+      float ss = 0.f, gx = 0.f, wr[16];
+      qk_weights(wt, l, wr);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int hh = h + u * kRows + sub;
-        if (hh < t.h) {
-          xa[u] = *reinterpret_cast<const uint4*>(x + hh * D + l.fa);
-          xb[u] = *reinterpret_cast<const uint4*>(x + hh * D + l.fb);
-          ga[u] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fa);
-          gb[u] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fb);
-        } else {
-          xa[u] = xb[u] = ga[u] = gb[u] = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < 16; ++i) {
+        ss = fmaf(f[i], f[i], ss);
+        gx = fmaf(g[i] * wr[i], f[i], gx);
+      }
+      ss = row_sum<kT>(ss);
+      gx = row_sum<kT>(gx);
+      const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+      const float c = gx * r * r * (1.0f / D);  // mean(t * w * xh) * r
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        dw[i] = fmaf(g[i], f[i] * r, dw[i]);  // a lane past the last head adds zero
+        f[i] = r * (g[i] * wr[i] - f[i] * c);
+      }
+      if (hh < t.h && bounds_ok(bi < a.b && tok < a.n, a.status)) {
+        *reinterpret_cast<uint4*>(y + hh * D + l.fa) = f32_to_bf16x8(f);
+        *reinterpret_cast<uint4*>(y + hh * D + l.fb) = f32_to_bf16x8(f + 8);
       }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int hh = h + u * kRows + sub;
-        if (h + u * kRows >= t.h) break;  // uniform in the warp
-        float f[16], g[16];
-        bf16x8_to_f32(xa[u], f);
-        bf16x8_to_f32(xb[u], f + 8);
-        bf16x8_to_f32(ga[u], g);
-        bf16x8_to_f32(gb[u], g + 8);
-        qk_rotate<kInter>(g, l, cs, sn);  // a.inverse: turns back
-        float ss = 0.f, gx = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          ss = fmaf(f[i], f[i], ss);
-          gx = fmaf(g[i] * w[i], f[i], gx);
-        }
-        ss = row_sum<kT>(ss);
-        gx = row_sum<kT>(gx);
-        const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-        const float c = gx * r * r * (1.0f / D);  // mean(t w * xh) * r
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          dw[i] = fmaf(g[i], f[i] * r, dw[i]);  // a lane past the last head adds zero
-          f[i] = r * (g[i] * w[i] - f[i] * c);
-        }
-        if (hh < t.h && bounds_ok(bi < a.b && tok < a.n, a.status)) {
-          *reinterpret_cast<uint4*>(y + hh * D + l.fa) = f32_to_bf16x8(f);
-          *reinterpret_cast<uint4*>(y + hh * D + l.fb) = f32_to_bf16x8(f + 8);
-        }
-      }
+      for (int i = 0; i < 4; ++i) v[i] = nx[i];
     }
   }
   // the warp's rows, then the CTA's warps
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float v = dw[i];
+    float s = dw[i];
 #pragma unroll
-    for (int o = kT; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (sub == 0) red[warp][(i < 8 ? l.fa + i : l.fb + i - 8)] = v;
+    for (int o = kT; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (sub == 0) red[warp][(i < 8 ? l.fa + i : l.fb + i - 8)] = s;
   }
   __syncthreads();
   for (int c = threadIdx.x; c < D; c += kQkThreads) {
-    float v = 0.f;
+    float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += red[i][c];
-    a.partial[int64_t(blockIdx.x) * D + c] = v;
+    for (int i = 0; i < kWarps; ++i) s += red[i][c];
+    a.partial[int64_t(blockIdx.x) * D + c] = s;
   }
 }
 
