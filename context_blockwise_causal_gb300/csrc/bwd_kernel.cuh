@@ -174,16 +174,6 @@ __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
 // region, each written by the warp that read the fp32 values there.
 __device__ __forceinline__ uint32_t half_split_col(int kk) { return kk < 4 ? kk * 8 : 64 + (kk - 4) * 8; }
 
-// Bits [lo, hi) of a 32-bit mask (lo, hi clipped to [0, 32]).
-__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
-  lo = lo < 0 ? 0 : (lo > 32 ? 32 : lo);
-  hi = hi < 0 ? 0 : (hi > 32 ? 32 : hi);
-  if (hi <= lo) return 0u;
-  const uint32_t upto_hi = hi >= 32 ? 0xffffffffu : ((1u << hi) - 1u);
-  const uint32_t below_lo = (1u << lo) - 1u;
-  return upto_hi & ~below_lo;
-}
-
 // ================================================================ dK / dV
 // P for one warp's 32 keys x 32 queries held in 16x256b fragments (see
 // tmem_ld16x256b_2x2): element 16u + 4r + 2e + j of rs is key row 16u + 8e +
@@ -243,6 +233,11 @@ __device__ __forceinline__ void ds_frag(const uint32_t (&pp)[16], const uint32_t
           pd[o] &= (bits & 1u ? 0x0000ffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
         }
       }
+}
+
+__device__ __forceinline__ void zero16(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = 0u;
 }
 
 // The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
@@ -709,18 +704,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         bool full = !dg && q_valid == kTile && U.k_valid == kTile;
         uint32_t valid[2][4];
         uint32_t pp[2][16];
+        [[maybe_unused]] int piece0 = kVisible, piece1 = kVisible;
         if constexpr (kWin) {
+          constexpr int no_from[4] = {0, 0, 0, 0};
+          constexpr uint32_t no_len[4] = {0, 0, 0, 0};
           full = q_valid == kTile && win_block_full(g, U.off + tile * kTile, U.k_t0);
           if (full) {
-            const int from[4] = {0, 0, 0, 0};
-            const uint32_t len[4] = {0, 0, 0, 0};
-            softmax_p_frag32<false>(ra, sl2, lv[0], from, len, pp[0]);
-            softmax_p_frag32<false>(rb, sl2, lv[1], from, len, pp[1]);
+            softmax_p_frag32<false>(ra, sl2, lv[0], no_from, no_len, pp[0]);
+            softmax_p_frag32<false>(rb, sl2, lv[1], no_from, no_len, pp[1]);
           } else {
             // A key row is seen by the block's queries from its own position
             // on, up to its window's last one unless it is a first token.
             // (Rows past the last key only reach their own rows of dK, dV,
-            // which are not stored.)
+            // which are not stored.) The warp's 32 keys and 32 queries at a
+            // time: a hidden piece is zero, a visible one needs no mask.
             const int pq = U.off + tile * kTile - U.k_t0;  // first query's position, from the first key
             int from[4];
             uint32_t len[4];
@@ -733,10 +730,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               from[f] = a0 - 64 * hf - 2 * c4;
               len[f] = a1 > a0 ? a1 - a0 : 0;
             }
-            softmax_p_frag32<true>(ra, sl2, lv[0], from, len, pp[0]);
+            const int q0 = U.off + tile * kTile + 64 * hf, k0 = U.k_t0 + wq * 32;
+            piece0 = win_piece(g, q0, k0);
+            piece1 = win_piece(g, q0 + 32, k0);
+            if (q_valid < kTile) {
+              piece0 = piece0 == kVisible ? kMixed : piece0;
+              piece1 = piece1 == kVisible ? kMixed : piece1;
+            }
+            if (piece0 == kMixed) softmax_p_frag32<true>(ra, sl2, lv[0], from, len, pp[0]);
+            else if (piece0 == kVisible) softmax_p_frag32<false>(ra, sl2, lv[0], no_from, no_len, pp[0]);
+            else zero16(pp[0]);
 #pragma unroll
             for (int f = 0; f < 4; ++f) from[f] -= 32;
-            softmax_p_frag32<true>(rb, sl2, lv[1], from, len, pp[1]);
+            if (piece1 == kMixed) softmax_p_frag32<true>(rb, sl2, lv[1], from, len, pp[1]);
+            else if (piece1 == kVisible) softmax_p_frag32<false>(rb, sl2, lv[1], no_from, no_len, pp[1]);
+            else zero16(pp[1]);
           }
         } else if (full) {
           softmax_p_frag<false>(ra, sl2, lv[0], none, c4, pp[0]);
@@ -774,19 +782,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(pt_full);
+          auto load_d = [&](int cb) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) dv[0][r] = *reinterpret_cast<const float2*>(Lq + kTile + 8 * r);
-          if (q_valid == kTile)
+            for (int r = 0; r < 4; ++r) dv[cb][r] = *reinterpret_cast<const float2*>(Lq + kTile + 32 * cb + 8 * r);
+          };
+          load_d(0);
+          if (full) {
             ds_frag32<false>(ra, rc, dv[0], pd[0]);
-          else
-            ds_frag32<true>(ra, rc, dv[0], pd[0]);
-          tmem_ld16x256b_x2(tP + 32, tP + kL16 + 32, rc);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) dv[1][r] = *reinterpret_cast<const float2*>(Lq + kTile + 32 + 8 * r);
-          if (q_valid == kTile)
+            tmem_ld16x256b_x2(tP + 32, tP + kL16 + 32, rc);
+            load_d(1);
             ds_frag32<false>(rb, rc, dv[1], pd[1]);
-          else
-            ds_frag32<true>(rb, rc, dv[1], pd[1]);
+          } else {
+            if (piece0 == kHidden) zero16(pd[0]);
+            else ds_frag32<true>(ra, rc, dv[0], pd[0]);
+            tmem_ld16x256b_x2(tP + 32, tP + kL16 + 32, rc);
+            load_d(1);
+            if (piece1 == kHidden) zero16(pd[1]);
+            else ds_frag32<true>(rb, rc, dv[1], pd[1]);
+          }
         } else {
           tmem_ld16x256b_2x2(tP, tP + kL16, tP + 32, tP + kL16 + 32, ra, rb);
           // P^T -> [64h, 64h+32) of the dP^T columns just read: dV may start
@@ -1131,6 +1144,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     {
       constexpr uint32_t idS = make_idesc_bf16(kTile, kTile, false, false);  // S, dP
       constexpr uint32_t idQ = make_idesc_bf16(kTile, D, false, true);       // dQ += dS K
+      constexpr uint32_t idSn = make_idesc_bf16(kTile, kSinkKeys, false, false);  // window form: first tokens
       const uint64_t dKV_km = make_sdesc_sw128(smem_u32(sKV), 16, 1024);
       const uint64_t dKV_mn = make_sdesc_sw128(smem_u32(sKV), 16384, 1024);
       const uint32_t tS = tbase + C::kColS, tdP = tbase + C::kColdP, tdQ = tbase + C::kColdQ;
@@ -1142,20 +1156,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++ncons;
       };
       // S = Q K^T and dP = dO V^T, A (Q, dO) from TMEM, B from the ring
-      auto issue_s = [&](uint32_t ks) {
+      auto issue_s = [&](uint32_t ks, uint32_t id) {
         const uint64_t kb = dKV_km + ((ks * C::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) >> 4;
-          umma_ts_w(tS, tQA + kk * 8, kb + off, idS, kk > 0);
+          umma_ts_w(tS, tQA + kk * 8, kb + off, id, kk > 0);
         }
       };
-      auto issue_dp = [&](uint32_t vs) {
+      auto issue_dp = [&](uint32_t vs, uint32_t id) {
         const uint64_t vb = dKV_km + ((vs * C::kTileBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) >> 4;
-          umma_ts_w(tdP, tdOA + kk * 8, vb + off, idS, kk > 0);
+          umma_ts_w(tdP, tdOA + kk * 8, vb + off, id, kk > 0);
         }
       };
       bool ok = true;
@@ -1178,10 +1192,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
              (jt == 0 || mbar_wait_warp_lean(s_free, (jt - 1) & 1, abort_flag, kWaitLimitNs));
         if (!ok) break;
         tc_fence_after();
-        issue_s(ks);
+        bool narrow = false;  // window form: the first tile's products are kSinkKeys keys wide
+        if constexpr (kWin) narrow = U.narrow;
+        issue_s(ks, narrow ? idSn : idS);
         umma_commit_w(s_full);
         if (!(ok = mbar_wait_warp_lean(&kv_full[vs], vp, abort_flag, kWaitLimitNs))) break;
-        issue_dp(vs);
+        issue_dp(vs, narrow ? idSn : idS);
         umma_commit_w(dp_full);
         umma_commit_w(&kv_empty[vs]);
         if (n == 1) umma_commit_w(qa_empty);
@@ -1196,7 +1212,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  mbar_wait_warp_lean(&kv_full[ks], kp, abort_flag, kWaitLimitNs);
             if (!ok) break;
             tc_fence_after();
-            issue_s(ks);
+            issue_s(ks, idS);
             umma_commit_w(s_full);
           }
           ok = mbar_wait_warp_lean(p_half, jt & 1, abort_flag, kWaitLimitNs) &&
@@ -1206,6 +1222,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // dQ += dS(jt) K_j   (dS from TMEM, K MN-major): first the K-steps of
           // each warp's first 32 keys (0, 1 and 4, 5), then the rest
           const uint64_t kmn = dKV_mn + ((cur_ks * C::kTileBytes) >> 4);
+          if (kWin && narrow && j == 0) {  // one K-step of 16 keys
+            umma_ts_w(tdQ, tdP, kmn, idQ, 0u);
+          } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int kk = (q & 1) + 4 * (q >> 1);
@@ -1218,12 +1237,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int kk = 2 + (q & 1) + 4 * (q >> 1);
             umma_ts_w(tdQ, tdP + half_split_col(kk), kmn + ((kk * 2048) >> 4), idQ, 1u);
           }
+          }
           umma_commit_w(&kv_empty[cur_ks]);
           if (j == n - 1) umma_commit_w(dq_full);
           if (j + 1 < n) {
             // dP(jt+1) over dS(jt), which the dQ MMAs just issued read first
             if (!(ok = mbar_wait_warp_lean(&kv_full[nvs], nvp, abort_flag, kWaitLimitNs))) break;
-            issue_dp(nvs);
+            issue_dp(nvs, idS);
             umma_commit_w(dp_full);
             umma_commit_w(&kv_empty[nvs]);
             if (j + 1 == n - 1) umma_commit_w(qa_empty);  // the unit's last reads of Q/dO in TMEM
@@ -1302,7 +1322,44 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // walk itself (as the forward's softmax warps do).
       const bool walkless = (U.c & (kTile - 1)) == 0;
       const int jdiag = g.causal ? (U.half ? U.tpc : 0) + U.u : -1;
-      for (int j = 0; j < U.n && ok; ++j, ++jt) {
+      int j0 = 0;
+      if constexpr (kWin) {
+        if (U.narrow) {
+          // the first tokens, all of them visible to every row of the unit:
+          // the warps of the lower half take the 16 keys, the others arrive
+          uint32_t r[kSinkKeys], rp[kSinkKeys], pd[kSinkKeys / 2];
+          if (!(ok = mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs))) break;
+          tc_fence_after();
+          if (hf == 0) {
+            tmem_ld16(tS, r);
+#pragma unroll
+            for (int i = 0; i < kSinkKeys; ++i)
+              r[i] = i < g.sinks ? __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i]), sl2, -l2))) : 0u;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          if (!(ok = mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))) break;
+          tc_fence_after();
+          if (hf == 0) {
+            tmem_ld16(tdP, rp);
+#pragma unroll
+            for (int i = 0; i < kSinkKeys; i += 2)
+              pd[i / 2] = pack_bf16x2(__uint_as_float(r[i]) * (__uint_as_float(rp[i]) - dd),
+                                      __uint_as_float(r[i + 1]) * (__uint_as_float(rp[i + 1]) - dd));
+            tmem_st8(tdP, pd);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(p_half);
+            mbar_arrive(p_full);
+          }
+          j0 = 1;
+          ++jt;
+        }
+      }
+      for (int j = j0; j < U.n && ok; ++j, ++jt) {
         int chunk = 0, tile = 0;
         bool dg = false;
         int n_valid = kTile;
@@ -1327,6 +1384,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         bool full;
         uint32_t v0 = 0u, v1 = 0u;  // bit c: key column c (of this warp's 64) is visible
         uint32_t pp0[16], pp1[16];
+        [[maybe_unused]] int piece0 = kVisible, piece1 = kVisible;  // of the warp's 32 rows and 32 keys each
         if constexpr (kWin) {
           const int p0 = U.off + U.q_t0, kb = win_tile(U, j) * kTile;
           full = win_block_full(g, p0, kb);
@@ -1334,13 +1392,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             p_row32_fp32<false>(r0, sl2, l2, 0, 0, 0);
             p_row32_fp32<false>(r1, sl2, l2, 0, 0, 0);
           } else {
+            piece0 = win_piece(g, p0 + wq * 32, kb + cb);
+            piece1 = win_piece(g, p0 + wq * 32, kb + cb + 32);
             // columns up to the row's own position, from its window's first
             // on or before the last first token
             const int hi = p0 + jr + 1 - kb - cb;
             const int from = hi - g.window;
             const int first = g.sinks - kb - cb < hi ? g.sinks - kb - cb : hi;
-            p_row32_fp32<true>(r0, sl2, l2, from, g.window, first);
-            p_row32_fp32<true>(r1, sl2, l2, from - 32, g.window, first - 32);
+            if (piece0 == kMixed) p_row32_fp32<true>(r0, sl2, l2, from, g.window, first);
+            else if (piece0 == kVisible) p_row32_fp32<false>(r0, sl2, l2, 0, 0, 0);
+            if (piece1 == kMixed) p_row32_fp32<true>(r1, sl2, l2, from - 32, g.window, first - 32);
+            else if (piece1 == kVisible) p_row32_fp32<false>(r1, sl2, l2, 0, 0, 0);
           }
         } else {
           full = !dg && n_valid == kTile;
@@ -1368,9 +1430,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         uint32_t pd0[16], pd1[16];
         // dS packed into [64h, 64h+32) of the dP columns (read above), its
         // first 32 keys published before the second are formed
-        if constexpr (kWin)
-          ds_row32_fp32(r0, s0, dd, pd0);
-        else if (full)
+        if constexpr (kWin) {
+          if (piece0 == kHidden)
+            zero16(pd0);
+          else
+            ds_row32_fp32(r0, s0, dd, pd0);
+        } else if (full)
           ds_row32<false>(pp0, r0, dd, 0u, pd0);
         else
           ds_row32<true>(pp0, r0, dd, v0, pd0);
@@ -1378,9 +1443,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_half);
-        if constexpr (kWin)
-          ds_row32_fp32(r1, s1, dd, pd1);
-        else if (full)
+        if constexpr (kWin) {
+          if (piece1 == kHidden)
+            zero16(pd1);
+          else
+            ds_row32_fp32(r1, s1, dd, pd1);
+        } else if (full)
           ds_row32<false>(pp1, r1, dd, 0u, pd1);
         else
           ds_row32<true>(pp1, r1, dd, v1, pd1);

@@ -108,6 +108,20 @@ enum FwdStatusBits : unsigned int {
   kStatusDrain = 1u << 3,  // copies or MMAs still in flight after the time limit
 };
 
+// Maximum of a row's scores: eight independent chains of 3-input maxima,
+// chain k over the scores k, k+8, ..., k+120.
+__device__ __forceinline__ float row_max(const float (&s)[kTile]) {
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float m = fmax3(s[k], s[k + 8], s[k + 16]);
+#pragma unroll
+    for (int i = 24; i + 8 < kTile; i += 16) m = fmax3(m, s[i + k], s[i + 8 + k]);
+    mx[k] = fmaxf(m, s[kTile - 8 + k]);
+  }
+  return fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+}
+
 // kStep = false: the fused forward (all CP steps, merged on chip, bf16 O).
 // kStep = true: one CP step `a.step` for every rank, unmerged: each query
 // row's softmax over that step's keys only, written as an fp32 partial O and
@@ -268,20 +282,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     {
       constexpr uint32_t idS = make_idesc_bf16(kTile, kTile, false, false);
       constexpr uint32_t idO = make_idesc_bf16(kTile, D, false, true);
+      constexpr uint32_t idSn = make_idesc_bf16(kTile, kSinkKeys, false, false);  // window form: first tokens
       const uint64_t dQ[2] = {make_sdesc_sw128(smem_u32(sQ), 16, 1024),
                               make_sdesc_sw128(smem_u32(sQ + C::kQBytes), 16, 1024)};
       const uint64_t dKV0 = make_sdesc_sw128(smem_u32(sKV), 16, 1024);
       const uint64_t dV0 = make_sdesc_sw128(smem_u32(sKV), 16384, 1024);
-      auto issue_S = [&](int sub, uint32_t slot) {
+      auto issue_S = [&](int sub, uint32_t slot, uint32_t id) {
         const uint64_t kb = dKV0 + ((slot * C::kKVBytes) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * (kTile * 128) + (kk % 4) * 32) >> 4;
-          umma_ss_w(tbase + sub * kTile, dQ[sub] + off, kb + off, idS, kk > 0);
+          umma_ss_w(tbase + sub * kTile, dQ[sub] + off, kb + off, id, kk > 0);
         }
       };
       // O += P V over keys [64*half, 64*half + 64) (K-steps 4*half .. +3)
-      auto issue_PV = [&](int sub, uint32_t slot, bool acc, int half) {
+      auto issue_PV = [&](int sub, uint32_t slot, bool acc, int half, bool one = false) {
+        if (kWin && one) {  // one K-step of 16 keys, with the first half
+          if (half == 0)
+            umma_ts_w(tbase + C::kColO + sub * D, tbase + sub * kTile, dV0 + ((slot * C::kKVBytes) >> 4), idO,
+                      acc ? 1u : 0u);
+          return;
+        }
         const uint64_t vb = dV0 + ((slot * C::kKVBytes) >> 4);
 #pragma unroll
         for (int q = 0; q < kTile / 32; ++q) {
@@ -318,12 +339,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // the MMA operand reads are both async-proxy operations ordered by
         // the transaction barrier
         if (!(ok = mbar_wait_warp(&kv_full[k0], k0p, abort_flag, kWaitLimitNs))) break;
-        issue_S(0, k0);
+        bool narrow = false;  // window form: the first tile's product is kSinkKeys keys wide
+        if constexpr (kWin) narrow = U.narrow;
+        issue_S(0, k0, narrow ? idSn : idS);
         umma_commit_w(&s_full[0]);
         if (!shared_kv) umma_commit_w(&kv_empty[k0]);
         if (n == 1) umma_commit_w(&q_empty[0]);
         if (!shared_kv && !(ok = mbar_wait_warp(&kv_full[k1], k1p, abort_flag, kWaitLimitNs))) break;
-        issue_S(1, k1);
+        issue_S(1, k1, narrow ? idSn : idS);
         umma_commit_w(&s_full[1]);
         umma_commit_w(&kv_empty[k1]);
         if (n == 1) umma_commit_w(&q_empty[1]);
@@ -338,11 +361,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                (j > 0 || ul == 0 || mbar_wait_warp(&o_empty[0], (ul - 1) & 1, abort_flag, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          issue_PV(0, v0, j > 0, 0);
+          issue_PV(0, v0, j > 0, 0, narrow && j == 0);
           if (!(ok = mbar_wait_warp(&p_full[0], pcnt[0] & 1, abort_flag, kWaitLimitNs))) break;
           ++pcnt[0];
           tc_fence_after();
-          issue_PV(0, v0, j > 0, 1);
+          issue_PV(0, v0, j > 0, 1, narrow && j == 0);
           if (!shared_kv) umma_commit_w(&kv_empty[v0]);
           if (j == n - 1) umma_commit_w(&o_full[0]);
           uint32_t nk0 = 0, nk0p = 0, nk1 = 0, nk1p = 0;
@@ -350,7 +373,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             take(nk0, nk0p);
             if (shared_kv) { nk1 = nk0; nk1p = nk0p; } else take(nk1, nk1p);
             if (!(ok = mbar_wait_warp(&kv_full[nk0], nk0p, abort_flag, kWaitLimitNs))) break;
-            issue_S(0, nk0);
+            issue_S(0, nk0, idS);
             umma_commit_w(&s_full[0]);
             if (!shared_kv) umma_commit_w(&kv_empty[nk0]);
             if (j + 1 == n - 1) umma_commit_w(&q_empty[0]);
@@ -361,16 +384,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                (j > 0 || ul == 0 || mbar_wait_warp(&o_empty[1], (ul - 1) & 1, abort_flag, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          issue_PV(1, v1, j > 0, 0);
+          issue_PV(1, v1, j > 0, 0, narrow && j == 0);
           if (!(ok = mbar_wait_warp(&p_full[1], pcnt[1] & 1, abort_flag, kWaitLimitNs))) break;
           ++pcnt[1];
           tc_fence_after();
-          issue_PV(1, v1, j > 0, 1);
+          issue_PV(1, v1, j > 0, 1, narrow && j == 0);
           umma_commit_w(&kv_empty[v1]);
           if (j == n - 1) umma_commit_w(&o_full[1]);
           if (j + 1 < n) {
             if (!shared_kv && !(ok = mbar_wait_warp(&kv_full[nk1], nk1p, abort_flag, kWaitLimitNs))) break;
-            issue_S(1, nk1);
+            issue_S(1, nk1, idS);
             umma_commit_w(&s_full[1]);
             umma_commit_w(&kv_empty[nk1]);
             if (j + 1 == n - 1) umma_commit_w(&q_empty[1]);
@@ -436,7 +459,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       // softmax warps then follow the positions without the walk itself.
       const bool walkless = !kStep && (U.c & (kTile - 1)) == 0;
       const int jdiag = g.causal ? (U.half ? U.tpc : 0) + U.u : -1;
-      for (int j = 0; j < n; ++j) {
+      int j0 = 0;
+      if constexpr (kWin) {
+        if (U.narrow) {
+          // the first tokens, all of them visible to every row of the unit
+          if (!(ok = mbar_wait_bounded(&s_full[sub], scnt & 1, abort_flag, kWaitLimitNs))) break;
+          ++scnt;
+          tc_fence_after();
+          uint32_t r[kSinkKeys], pk[kSinkKeys / 2];
+          tmem_ld16(tS, r);
+#pragma unroll
+          for (int i = 0; i < kSinkKeys; ++i) {
+            if (i >= g.sinks) r[i] = 0xff800000u;  // -inf
+            m_used = fmaxf(m_used, __uint_as_float(r[i]));
+          }
+          m_used *= sl2;
+          const float neg = m_used == -INFINITY ? 0.f : -m_used;
+#pragma unroll
+          for (int i = 0; i < kSinkKeys; i += 2) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(r[i]), sl2, neg));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(r[i + 1]), sl2, neg));
+            l += e0 + e1;
+            pk[i / 2] = pack_bf16x2(e0, e1);
+          }
+          tmem_st8(tS, pk);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&p_half[sub]);
+            mbar_arrive(&p_full[sub]);
+          }
+          j0 = 1;
+        }
+      }
+      for (int j = j0; j < n; ++j) {
         int chunk = 0, tile = 0;
         bool walk_dg = false, dg = false, dead = false;
         int n_valid = kTile;
@@ -478,32 +534,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // row max: from the load itself, except on a masked tile (the diagonal
         // or a ragged chunk end), where it is taken over the unmasked scores
         float m_raw = hw_max;
-        if (kWin ? !win_block_full(g, p0, kb) : (dg || dead || n_valid < kTile)) {
-          if constexpr (kWin) {
-            // this row sees keys lo .. lim of the tile, and those before `first`
+        if constexpr (kWin) {
+          // On a window's edge: bit i of a piece's word says whether this row
+          // sees key 32 c + i, lo .. lim of the tile and those before `first`;
+          // pieces that the warp's 32 rows see whole are left as they are.
+          if (!win_block_full(g, p0, kb)) {
             const int lim = p0 + row - kb;
             const int lo = lim - g.window + 1;
-            const int first = g.sinks - kb;
+            const int first = g.sinks - kb < lim + 1 ? g.sinks - kb : lim + 1;
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (i > lim || (i < lo && i >= first)) s[i] = -INFINITY;
-          } else {
-            const int lim = dead ? -1 : dg ? (row < n_valid - 1 ? row : n_valid - 1) : n_valid - 1;
+            for (int c = 0; c < 4; ++c) {
+              if (win_piece(g, p0 + wq * 32, kb + c * 32) == kVisible) continue;
+              const uint32_t see = bit_range(lo - 32 * c, lim + 1 - 32 * c) | bit_range(0, first - 32 * c);
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if (i > lim) s[i] = -INFINITY;
+              for (int i = 0; i < 32; ++i)
+                if (!(see & (1u << i))) s[c * 32 + i] = -INFINITY;
+            }
+            m_raw = row_max(s);
           }
-          // row max: eight independent chains of 3-input maxima, chain k over
-          // the scores k, k+8, ..., k+120
-          float mx[8];
+        } else if (dg || dead || n_valid < kTile) {
+          const int lim = dead ? -1 : dg ? (row < n_valid - 1 ? row : n_valid - 1) : n_valid - 1;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float m = fmax3(s[k], s[k + 8], s[k + 16]);
-#pragma unroll
-            for (int i = 24; i + 8 < kTile; i += 16) m = fmax3(m, s[i + k], s[i + 8 + k]);
-            mx[k] = fmaxf(m, s[kTile - 8 + k]);
-          }
-          m_raw = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], fmax3(mx[5], mx[6], mx[7])));
+          for (int i = 0; i < kTile; ++i)
+            if (i > lim) s[i] = -INFINITY;
+          m_raw = row_max(s);
         }
         const float m_new = m_raw * sl2;
         const bool upd = m_new > m_used + kRescaleThreshold;

@@ -48,7 +48,14 @@ struct WinUnit : FwdUnit {
   int kv0;      // first key row of the unit's sequence
   int off;      // position of its query row 0
   int ns, w0;   // tiles of first tokens visited, then tiles from w0 on
+  // The one tile of first tokens is visited for its first kSinkKeys keys only:
+  // all of the unit's queries see exactly the first `sinks` of them.
+  bool narrow;
 };
+
+// First tokens up to this many take a product of their own width instead of a
+// whole tile's (in the forward and dQ kernels).
+constexpr int kSinkKeys = 16;
 
 // Query tiles (kPairs: pairs of tiles) of a sequence of qlen queries.
 __host__ __device__ inline int win_unit_tiles(int qlen, bool pairs) {
@@ -83,6 +90,7 @@ __host__ __device__ inline void win_fill_walk(const CpGeom& g, WinUnit& U, int p
   U.w0 = lo > 0 ? lo / kTile : 0;
   const int st = (g.sinks + kTile - 1) / kTile;
   U.ns = st < U.w0 ? st : U.w0;
+  U.narrow = U.ns == 1 && g.sinks <= kSinkKeys;
   U.n = U.ns + p_last / kTile - U.w0 + 1;
 }
 
@@ -90,6 +98,15 @@ __host__ __device__ inline void win_fill_walk(const CpGeom& g, WinUnit& U, int p
 // visible as a whole.
 __host__ __device__ inline bool win_block_full(const CpGeom& g, int p0, int kb) {
   return kb + kTile - 1 <= p0 && (p0 + kTile - 1 - kb < g.window || kb + kTile <= g.sinks);
+}
+
+// What 32 queries from position p0 see of 32 keys from kb: none, all, or some.
+// The kernels' warps skip the exponentials of hidden pieces and mask only
+// mixed ones.
+enum WinPiece { kHidden = 0, kMixed = 1, kVisible = 2 };
+__host__ __device__ inline int win_piece(const CpGeom& g, int p0, int kb) {
+  if (kb > p0 + 31 || (kb + 31 <= p0 - g.window && kb >= g.sinks)) return kHidden;
+  return kb + 31 <= p0 && (p0 + 31 - kb < g.window || kb + 31 < g.sinks) ? kVisible : kMixed;
 }
 
 // Forward units per launch: a query tile for a pair of query heads of one KV
