@@ -28,6 +28,8 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "cp_schedule.cuh"
 #include "ptx.cuh"
 #include "win_schedule.cuh"
@@ -241,8 +243,8 @@ __device__ __forceinline__ void zero16(uint32_t (&r)[16]) {
 }
 
 // The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
-// to bf16 there too, as above, costs a third of the gradients' error (relative
-// L2 3.0e-3 against 2.4e-3, dK and dQ at a window of 300). A masked block zeroes P, and
+// to bf16 there too, as above, adds to the gradients' error (relative
+// L2 3.0e-3 against 2.5e-3, dK and dQ at a window of 300). A masked block zeroes P, and
 // dS = P (dP - D) with it, by testing query 8r + 2 c4 + j + c0 against the key
 // row's visible range [from, from + len) (an unsigned compare does both ends).
 template <bool kMasked>
@@ -918,10 +920,10 @@ __device__ __forceinline__ void ds_row32(const uint32_t (&pp)[16], const uint32_
   }
 }
 
-// The window form's versions, P kept in fp32 (see softmax_p_frag32): key c of
-// the 32 is visible when c lies in [from, from + len) or below first.
+// The window form's versions, P kept in fp32 (see softmax_p_frag32): bit c of
+// `see` keeps key c of the 32.
 template <bool kMasked>
-__device__ __forceinline__ void p_row32_fp32(uint32_t (&rs)[32], float sl2, float l2, int from, uint32_t len, int first) {
+__device__ __forceinline__ void p_row32_fp32(uint32_t (&rs)[32], float sl2, float l2, uint32_t see) {
   const uint64_t sl2x2 = f2_pack(sl2, sl2), nl2 = f2_pack(-l2, -l2);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
@@ -930,8 +932,8 @@ __device__ __forceinline__ void p_row32_fp32(uint32_t (&rs)[32], float sl2, floa
     x0 = ex2_approx(x0);
     x1 = ex2_approx(x1);
     if constexpr (kMasked) {
-      x0 = uint32_t(i - from) < len || i < first ? x0 : 0.f;
-      x1 = uint32_t(i + 1 - from) < len || i + 1 < first ? x1 : 0.f;
+      x0 = see & (1u << i) ? x0 : 0.f;
+      x1 = see & (2u << i) ? x1 : 0.f;
     }
     rs[i] = __float_as_uint(x0);
     rs[i + 1] = __float_as_uint(x1);
@@ -1269,6 +1271,169 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool ok = true;
     uint32_t jt = 0;
     int ul = 0;
+    if constexpr (kWin) {
+      // Window form. Units are short, so the next unit's Q and dO go into TMEM
+      // (whose last readers have finished by then) before this unit's dQ is
+      // stored, and its first products run meanwhile. P stays in fp32 (see
+      // softmax_p_frag32), so dP is taken 32 keys at a time.
+      float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
+      int rd = 0;
+      auto take_unit = [&](WinUnit& U, int u) -> bool {
+        const int idx = snake_unit(rd, blockIdx.x, grid);
+        if (idx >= num_units) return false;
+        ++rd;
+        U = win_dq_unit(g, idx);
+        // (padding rows of a ragged tile read arbitrary values; their dQ is never stored)
+        int64_t pos = int64_t(U.seq * g.hq + U.h0) * a.ntp + U.u * kTile + jr;
+        if (!bounds_ok(pos >= 0 && pos < a.vec_len, a.status)) pos = 0;  // stays inside the vectors
+        l2 = a.lvec[pos];
+        dd = a.dvec[pos];
+        ok = mbar_wait_lean(q_full, u & 1, abort_flag, kWaitLimitNs) &&
+             (u == 0 || mbar_wait_lean(qa_empty, (u - 1) & 1, abort_flag, kWaitLimitNs));
+        if (!ok) return false;
+        tc_fence_after();
+        // this row's columns hf*D/2 .. of the swizzled TMA tiles: 16-byte
+        // chunk c of row jr sits at chunk c ^ (jr & 7) of the row's 128 bytes
+        auto copy = [&](const uint8_t* tile, uint32_t dst) {
+          uint32_t r[D / 4];
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const int e0 = hf * (D / 2) + c * 8;
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + (e0 / 64) * (kTile * 128) + jr * 128 +
+                                                            ((((e0 % 64) / 8) ^ (jr & 7)) * 16));
+            r[4 * c] = v.x; r[4 * c + 1] = v.y; r[4 * c + 2] = v.z; r[4 * c + 3] = v.w;
+          }
+          if constexpr (D == 128) tmem_st32(dst, r);
+          else tmem_st16(dst, r);
+        };
+        copy(sQ, tbase + lane_off + C::kColQA + hf * (D / 4));
+        copy(sdO, tbase + lane_off + C::kColdOA + hf * (D / 4));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(qa_full);
+          mbar_arrive(q_empty);
+        }
+        return true;
+      };
+      WinUnit U;
+      bool have = take_unit(U, 0);
+      while (have && ok) {
+        const int krow = U.tok0 + U.q_t0 + jr;
+        const bool store = jr < U.q_valid && bounds_ok(krow < a.q_rows && U.h0 < g.hq, a.status);
+        __nv_bfloat16* dst = a.dq + (int64_t(krow) * g.hq + U.h0) * D + hf * (D / 2);
+        const int p0 = U.off + U.q_t0;  // position of the tile's row 0
+        int j = 0;
+        if (U.narrow) {
+          // the first tokens, all of them visible to every row of the unit:
+          // the warps of the lower half take the 16 keys, the others arrive
+          uint32_t r[kSinkKeys], rp[kSinkKeys], pd[kSinkKeys / 2];
+          if (!(ok = mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs))) break;
+          tc_fence_after();
+          if (hf == 0) {
+            tmem_ld16(tS, r);
+#pragma unroll
+            for (int i = 0; i < kSinkKeys; ++i)
+              r[i] = i < g.sinks ? __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i]), sl2, -l2))) : 0u;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          if (!(ok = mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))) break;
+          tc_fence_after();
+          if (hf == 0) {
+            tmem_ld16(tdP, rp);
+#pragma unroll
+            for (int i = 0; i < kSinkKeys; i += 2)
+              pd[i / 2] = pack_bf16x2(__uint_as_float(r[i]) * (__uint_as_float(rp[i]) - dd),
+                                      __uint_as_float(r[i + 1]) * (__uint_as_float(rp[i + 1]) - dd));
+            tmem_st8(tdP, pd);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(p_half);
+            mbar_arrive(p_full);
+          }
+          j = 1;
+          ++jt;
+        }
+        // One key tile; kEdge: one that the tile's rows do not see whole. Two
+        // bodies, so that the ordinary one has no masks to hold, and the edge's
+        // selects by one bit per key, which is cheaper than skipping its hidden
+        // pieces (644 against 664 us at b1 s32768 h32/8 window 1024: the
+        // branches spill).
+        auto key_tile = [&](auto edge) -> bool {
+          constexpr bool kEdge = decltype(edge)::value;
+          if (!mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs)) return false;
+          tc_fence_after();
+          uint32_t r0[32], r1[32];
+          tmem_ld32x2(tS, tS + 32, r0, r1);
+          // S(jt) is in registers: the MMA may compute S(jt+1) meanwhile
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+          if constexpr (kEdge) {
+            // columns up to the row's own position, from its window's first
+            // on or before the last first token
+            const int hi = p0 + jr + 1 - win_tile(U, j) * kTile - hf * 64;
+            const int lo = hi - g.window;
+            const int first = hi + g.sinks - (p0 + jr + 1) < hi ? hi + g.sinks - (p0 + jr + 1) : hi;
+            p_row32_fp32<true>(r0, sl2, l2, bit_range(lo, hi) | bit_range(0, first));
+            p_row32_fp32<true>(r1, sl2, l2, bit_range(lo - 32, hi - 32) | bit_range(0, first - 32));
+          } else {
+            p_row32_fp32<false>(r0, sl2, l2, 0u);
+            p_row32_fp32<false>(r1, sl2, l2, 0u);
+          }
+          if (!mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs)) return false;
+          tc_fence_after();
+          // dS packed into [64h, 64h+32) of the dP columns: the first 32
+          // keys' over columns read before, published before the others are formed
+          uint32_t rp[32], pd[16];
+          tmem_ld32(tdP, rp);
+          ds_row32_fp32(r0, rp, dd, pd);
+          tmem_st16(tdP, pd);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_half);
+          tmem_ld32(tdP + 32, rp);
+          ds_row32_fp32(r1, rp, dd, pd);
+          tmem_st16(tdP + 16, pd);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full);
+          return true;
+        };
+        for (; j < U.n && ok; ++j, ++jt)
+          ok = win_block_full(g, p0, win_tile(U, j) * kTile) ? key_tile(std::false_type()) : key_tile(std::true_type());
+        if (!ok) break;
+        have = take_unit(U, ul + 1);
+        if (!ok || !(ok = mbar_wait_lean(dq_full, ul & 1, abort_flag, kWaitLimitNs))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          uint32_t rq[32];
+          tmem_ld32(tbase + lane_off + C::kColdQ + hf * (D / 2) + c0, rq);
+          if (c0 + 32 >= D / 2) {  // all read: the MMA may start the next unit's dQ
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dq_empty);
+          }
+          if (store) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 pk;
+              pk.x = pack_bf16x2(__uint_as_float(rq[i]) * scale, __uint_as_float(rq[i + 1]) * scale);
+              pk.y = pack_bf16x2(__uint_as_float(rq[i + 2]) * scale, __uint_as_float(rq[i + 3]) * scale);
+              pk.z = pack_bf16x2(__uint_as_float(rq[i + 4]) * scale, __uint_as_float(rq[i + 5]) * scale);
+              pk.w = pack_bf16x2(__uint_as_float(rq[i + 6]) * scale, __uint_as_float(rq[i + 7]) * scale);
+              *reinterpret_cast<uint4*>(dst + c0 + i) = pk;
+            }
+          }
+        }
+        ++ul;
+      }
+    } else
     for (int rd = 0; ok; ++rd) {
       const int idx = snake_unit(rd, blockIdx.x, grid);
       if (idx >= num_units) break;
@@ -1322,55 +1487,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // walk itself (as the forward's softmax warps do).
       const bool walkless = (U.c & (kTile - 1)) == 0;
       const int jdiag = g.causal ? (U.half ? U.tpc : 0) + U.u : -1;
-      int j0 = 0;
-      if constexpr (kWin) {
-        if (U.narrow) {
-          // the first tokens, all of them visible to every row of the unit:
-          // the warps of the lower half take the 16 keys, the others arrive
-          uint32_t r[kSinkKeys], rp[kSinkKeys], pd[kSinkKeys / 2];
-          if (!(ok = mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs))) break;
-          tc_fence_after();
-          if (hf == 0) {
-            tmem_ld16(tS, r);
-#pragma unroll
-            for (int i = 0; i < kSinkKeys; ++i)
-              r[i] = i < g.sinks ? __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i]), sl2, -l2))) : 0u;
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_free);
-          if (!(ok = mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))) break;
-          tc_fence_after();
-          if (hf == 0) {
-            tmem_ld16(tdP, rp);
-#pragma unroll
-            for (int i = 0; i < kSinkKeys; i += 2)
-              pd[i / 2] = pack_bf16x2(__uint_as_float(r[i]) * (__uint_as_float(rp[i]) - dd),
-                                      __uint_as_float(r[i + 1]) * (__uint_as_float(rp[i + 1]) - dd));
-            tmem_st8(tdP, pd);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(p_half);
-            mbar_arrive(p_full);
-          }
-          j0 = 1;
-          ++jt;
-        }
-      }
-      for (int j = j0; j < U.n && ok; ++j, ++jt) {
+      for (int j = 0; j < U.n && ok; ++j, ++jt) {
         int chunk = 0, tile = 0;
         bool dg = false;
         int n_valid = kTile;
-        if constexpr (!kWin) {
-          if (walkless) {
-            dg = j == jdiag;
-          } else {
-            w.next(chunk, tile, dg);
-            const int rem = U.c - tile * kTile;
-            n_valid = rem < kTile ? rem : kTile;
-          }
+        if (walkless) {
+          dg = j == jdiag;
+        } else {
+          w.next(chunk, tile, dg);
+          const int rem = U.c - tile * kTile;
+          n_valid = rem < kTile ? rem : kTile;
         }
         if (!(ok = mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
@@ -1380,62 +1506,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
+        const bool full = !dg && n_valid == kTile;
+        // key column c (of this warp's 64) is valid when it is inside its
+        // chunk and (on the diagonal) c <= jr
         const int cb = hf * 64;
-        bool full;
-        uint32_t v0 = 0u, v1 = 0u;  // bit c: key column c (of this warp's 64) is visible
+        int hi = n_valid - cb;
+        if (dg && jr + 1 - cb < hi) hi = jr + 1 - cb;
+        const uint32_t v0 = full ? 0u : bit_range(0, hi), v1 = full ? 0u : bit_range(0, hi - 32);
         uint32_t pp0[16], pp1[16];
-        [[maybe_unused]] int piece0 = kVisible, piece1 = kVisible;  // of the warp's 32 rows and 32 keys each
-        if constexpr (kWin) {
-          const int p0 = U.off + U.q_t0, kb = win_tile(U, j) * kTile;
-          full = win_block_full(g, p0, kb);
-          if (full) {
-            p_row32_fp32<false>(r0, sl2, l2, 0, 0, 0);
-            p_row32_fp32<false>(r1, sl2, l2, 0, 0, 0);
-          } else {
-            piece0 = win_piece(g, p0 + wq * 32, kb + cb);
-            piece1 = win_piece(g, p0 + wq * 32, kb + cb + 32);
-            // columns up to the row's own position, from its window's first
-            // on or before the last first token
-            const int hi = p0 + jr + 1 - kb - cb;
-            const int from = hi - g.window;
-            const int first = g.sinks - kb - cb < hi ? g.sinks - kb - cb : hi;
-            if (piece0 == kMixed) p_row32_fp32<true>(r0, sl2, l2, from, g.window, first);
-            else if (piece0 == kVisible) p_row32_fp32<false>(r0, sl2, l2, 0, 0, 0);
-            if (piece1 == kMixed) p_row32_fp32<true>(r1, sl2, l2, from - 32, g.window, first - 32);
-            else if (piece1 == kVisible) p_row32_fp32<false>(r1, sl2, l2, 0, 0, 0);
-          }
+        if (full) {
+          p_row32<false>(r0, sl2, l2, 0u, pp0);
+          p_row32<false>(r1, sl2, l2, 0u, pp1);
         } else {
-          full = !dg && n_valid == kTile;
-          // key column c is valid when it is inside its chunk and (on the
-          // diagonal) c <= jr
-          int hi = n_valid - cb;
-          if (dg && jr + 1 - cb < hi) hi = jr + 1 - cb;
-          v0 = full ? 0u : bit_range(0, hi);
-          v1 = full ? 0u : bit_range(0, hi - 32);
-          if (full) {
-            p_row32<false>(r0, sl2, l2, 0u, pp0);
-            p_row32<false>(r1, sl2, l2, 0u, pp1);
-          } else {
-            p_row32<true>(r0, sl2, l2, v0, pp0);
-            p_row32<true>(r1, sl2, l2, v1, pp1);
-          }
+          p_row32<true>(r0, sl2, l2, v0, pp0);
+          p_row32<true>(r1, sl2, l2, v1, pp1);
         }
         if (!(ok = mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))) break;
         tc_fence_after();
-        [[maybe_unused]] uint32_t s0[32], s1[32];
-        if constexpr (kWin)
-          tmem_ld32x2(tdP, tdP + 32, s0, s1);
-        else
-          tmem_ld32x2(tdP, tdP + 32, r0, r1);
+        tmem_ld32x2(tdP, tdP + 32, r0, r1);
         uint32_t pd0[16], pd1[16];
         // dS packed into [64h, 64h+32) of the dP columns (read above), its
         // first 32 keys published before the second are formed
-        if constexpr (kWin) {
-          if (piece0 == kHidden)
-            zero16(pd0);
-          else
-            ds_row32_fp32(r0, s0, dd, pd0);
-        } else if (full)
+        if (full)
           ds_row32<false>(pp0, r0, dd, 0u, pd0);
         else
           ds_row32<true>(pp0, r0, dd, v0, pd0);
@@ -1443,12 +1535,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_half);
-        if constexpr (kWin) {
-          if (piece1 == kHidden)
-            zero16(pd1);
-          else
-            ds_row32_fp32(r1, s1, dd, pd1);
-        } else if (full)
+        if (full)
           ds_row32<false>(pp1, r1, dd, 0u, pd1);
         else
           ds_row32<true>(pp1, r1, dd, v1, pd1);
