@@ -24,6 +24,7 @@ struct DeviceInfo {
   std::atomic<bool> win_fwd_attr[4] = {};  // window form: [d == 128][tile pairs]
   std::atomic<bool> win_bwd_attr[2] = {};  // window form: [d == 128]
   std::atomic<bool> decode_attr[2] = {};   // [d == 128]
+  std::atomic<bool> qk_bwd_attr[4] = {};   // [d == 128][interleaved]
 };
 
 // State of the current device (CPATTN_ERR_UNSUPPORTED_ARCH unless sm_103).

@@ -25,26 +25,32 @@ int64_t max_keys(int cap, int window, int sinks) {
   return seen < cap ? seen : cap;
 }
 
-// Runs per (sequence, KV head): two CTAs fit an SM. With many keys four CTAs
-// per place level out different lengths (runs of 512 keys or more); with few
-// sequences a run goes down to one round of the warps, 64 keys. Runs of one
-// cluster are a power of two; only when 16 of them leave over half of the
-// chip idle, on runs of at least 2048 keys, are there more (device memory and
-// the second kernel).
+// Runs per (sequence, KV head group): two CTAs fit an SM.
+//  * As many as fill the places without a second wave, of 64 keys or more (one
+//    round of a CTA's warps), up to a cluster: 8 of one 1028-key sequence with
+//    8 KV heads take 6.7 us, 4 take 7.7; with 8 such sequences 4 take 9.6 us
+//    and 8, a second wave, 15.5.
+//  * Runs of 2048 keys or more may fill the places twice, which levels out
+//    different lengths: 16 sequences of 32K to 64K keys take 447 us in 4 runs,
+//    507 in 2 and 465 in 8.
+//  * Where a cluster's 8 leave half of the places empty, such long runs go up
+//    to all places through device memory (one 131K-key sequence, 8 KV heads:
+//    92 us in 38 runs with their join, 188 in 8). Clusters of 16 find too few
+//    places together (122 us there).
 int choose_split(int num_sms, int64_t units, int64_t keys) {
   const int64_t places = 2 * int64_t(num_sms);
-  int64_t s = (4 * places + units - 1) / units;
-  if (s > keys / 512) s = keys / 512;
-  int64_t fill = places / units;
-  if (fill > keys / 64) fill = keys / 64;
-  if (s < fill) s = fill;
-  if (s > kDecMaxCluster && 2 * kDecMaxCluster * units <= num_sms && keys / 2048 > kDecMaxCluster) {
-    s = keys / 2048 < s ? keys / 2048 : s;
-    return int(s < kDecMaxSplit ? s : kDecMaxSplit);
+  int64_t s = 1;
+  while (2 * s <= kDecMaxCluster) {
+    const int64_t ctas = 2 * s * units, run = keys / (2 * s);
+    if (!(ctas <= places ? run >= 64 : ctas <= 2 * places && run >= 2048)) break;
+    s *= 2;
   }
-  int p = 1;
-  while (2 * p <= s && 2 * p <= kDecMaxCluster) p *= 2;
-  return p;
+  if (s == kDecMaxCluster && 2 * s * units <= places) {
+    int64_t more = places / units;
+    if (more > keys / 2048) more = keys / 2048;
+    if (more > s) s = more < kDecMaxSplit ? more : kDecMaxSplit;
+  }
+  return int(s);
 }
 
 // Workspace bytes (0: none).
@@ -63,8 +69,7 @@ int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
   std::atomic<bool>& done = di->decode_attr[D == 128 ? 1 : 0];
   if (!done.load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(cpattn_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             DecodeCfg<D>::kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(cpattn_decode_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                             DecodeCfg<D>::kSmemBytes) != cudaSuccess)
       return CPATTN_ERR_CUDA;
     done.store(true, std::memory_order_release);
   }

@@ -22,7 +22,7 @@
 // until the end. Keys past the run are never read: their slots are filled
 // with zeros and their scores masked, whatever the cache holds there. Warps
 // and then runs are joined through their log-sum-exp in a fixed order. Up to
-// 16 runs are the CTAs of one cluster, which read one another's results from
+// 8 runs are the CTAs of one cluster, which read one another's results from
 // shared memory: one launch and no workspace. More runs (a few very long
 // sequences) go through device memory and a second kernel.
 #pragma once
@@ -37,7 +37,7 @@ namespace cpattn {
 constexpr int kDecWarps = 4;
 constexpr int kDecStages = 3;
 constexpr int kDecBlock = 16;  // keys per block
-constexpr int kDecMaxCluster = 16;
+constexpr int kDecMaxCluster = 8;  // the portable cluster size
 constexpr int kDecMaxSplit = 64;
 
 struct DecodeArgs {
@@ -70,15 +70,6 @@ struct DecodeCfg {
   static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int bytes = valid ? 16 : 0;  // 0: the 16 bytes are filled with zeros and src is not read
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -379,6 +370,7 @@ __global__ void __launch_bounds__(128) cpattn_decode_join_kernel(const DecodeArg
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 8
   for (int s = 0; s < a.nsplit; ++s) {
     const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
     const float* p = a.part_o + (row * a.nsplit + s) * D + lane * kPer;

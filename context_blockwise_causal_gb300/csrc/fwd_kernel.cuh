@@ -51,6 +51,7 @@ static_assert(2 * 128 * kFwdSoftmaxRegs + 128 * kFwdOtherRegs <= kFwdThreads * k
 // exceeds 1 and is rounded, which measured about twice the output error on
 // peaky rows (Q, K ~ N(0, 4)) for a 2-4% gain in speed.
 constexpr float kRescaleThreshold = 0.0f;  // log2 units
+
 // The window form lets the running max lag by up to this much: its walks are
 // a few tiles long, where some row of a warp meets a new maximum in almost
 // every tile and the rescale's TMEM round trip would be paid each time.
@@ -213,7 +214,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       uint32_t nload = 0;
       int ul = 0;
-      [[maybe_unused]] int nq0 = 0, nq1 = 0;  // window form: Q tiles issued of each sub-tile
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
@@ -224,22 +224,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           w.only_step(a.step);
           if (w.step_tiles(a.step) == 0) continue;  // no key tile at this step
         }
-        auto load_q = [&](int sub) {
+        if (ul > 0) {
+          ok = mbar_wait_bounded(&q_empty[0], (ul - 1) & 1, abort_flag, plimit) &&
+               mbar_wait_bounded(&q_empty[1], (ul - 1) & 1, abort_flag, plimit);
+          if (!ok) break;
+        }
+        for (int sub = 0; sub < 2; ++sub) {
           mbar_arrive_expect_tx(&q_full[sub], C::kQBytes);
           const int h = sub ? U.h1 : U.h0;
           const int qrow = U.tok0 + (sub ? U.q_t1 : U.q_t0);
           bounds_ok(qrow >= 0 && qrow < a.q_rows && h >= 0 && h < g.hq, a.status);
           for (int x = 0; x < D; x += 64)
             tma_load_3d(sQ + sub * C::kQBytes + (x / 64) * (kTile * 128), &tmq, &q_full[sub], x, h, qrow);
-        };
-        if constexpr (!kWin) {
-          if (ul > 0) {
-            ok = mbar_wait_bounded(&q_empty[0], (ul - 1) & 1, abort_flag, plimit) &&
-                 mbar_wait_bounded(&q_empty[1], (ul - 1) & 1, abort_flag, plimit);
-            if (!ok) break;
-          }
-          load_q(0);
-          load_q(1);
         }
         const bool shared_kv = U.g0 == U.g1;
         int chunk, tile;
@@ -258,16 +254,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           return true;
         };
         if constexpr (kWin) {
-          // each sub-tile's Q as soon as its buffer is free, the first K between them
-          if (ul > 0 && !(ok = mbar_wait_bounded(&q_empty[0], (ul - 1) & 1, abort_flag, plimit))) break;
-          load_q(0);
-          ++nq0;
-          if (!(ok = load(&tmk, U.g0, U.kv0 + win_tile(U, 0) * kTile))) break;
-          if (ul > 0 && !(ok = mbar_wait_bounded(&q_empty[1], (ul - 1) & 1, abort_flag, plimit))) break;
-          load_q(1);
-          ++nq1;
-          ok = load(&tmv, U.g0, U.kv0 + win_tile(U, 0) * kTile);
-          for (int j = 1; ok && j < U.n; ++j) {
+          for (int j = 0; ok && j < U.n; ++j) {
             const int row = U.kv0 + win_tile(U, j) * kTile;
             ok = load(&tmk, U.g0, row) && load(&tmv, U.g0, row);
           }
@@ -288,10 +275,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const uint32_t first = nload > (uint32_t)C::kSlots ? nload - C::kSlots : 0;
       for (uint32_t i = first; i < nload; ++i)
         drained &= mbar_wait_drain(&kv_full[i % C::kSlots], (i / C::kSlots) & 1, kWaitLimitNs);
-      if constexpr (kWin) {
-        if (nq0 > 0) drained &= mbar_wait_drain(&q_full[0], (nq0 - 1) & 1, kWaitLimitNs);
-        if (nq1 > 0) drained &= mbar_wait_drain(&q_full[1], (nq1 - 1) & 1, kWaitLimitNs);
-      } else if (ul > 0) {
+      if (ul > 0) {
         drained &= mbar_wait_drain(&q_full[0], (ul - 1) & 1, kWaitLimitNs);
         drained &= mbar_wait_drain(&q_full[1], (ul - 1) & 1, kWaitLimitNs);
       }
@@ -341,71 +325,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       bool ok = true;
       uint32_t pcnt[2] = {0, 0};
       int ul = 0;
-      if constexpr (kWin) {
-        // Units are short here (a window's tiles), so the alternation of the
-        // sub-tiles runs on across their borders: after a sub-tile's last P.V
-        // its first S of the next unit follows as any other S would.
-        int rd = 0;
-        auto next_unit = [&](int& n, bool& narrow) -> bool {
-          const int idx = snake_unit(rd, blockIdx.x, grid);
-          if (idx >= num_units) return false;
-          ++rd;
-          const auto U = fwd_unit_of<kTP, kWin>(g, idx);
-          n = U.n;
-          narrow = U.narrow;
-          return true;
-        };
-        int n = 0, n2 = 0;
-        bool narrow = false, narrow2 = false;
-        bool have = next_unit(n, narrow), have2 = false;
-        uint32_t k = 0, kp = 0;
-        // S of sub-tile `sub` against the K tile in slot k; `first`: a unit's
-        // first, which waits for its Q; `last`: its last, which frees Q
-        auto step_S = [&](int sub, bool first, bool nar, bool last, int u) -> bool {
-          if (first && !mbar_wait_warp(&q_full[sub], u & 1, abort_flag, kWaitLimitNs)) return false;
-          if (sub == 0 && !mbar_wait_warp(&kv_full[k], kp, abort_flag, kWaitLimitNs)) return false;
-          issue_S(sub, k, nar ? idSn : idS);
-          umma_commit_w(&s_full[sub]);
-          if (sub == 1) umma_commit_w(&kv_empty[k]);
-          if (last) umma_commit_w(&q_empty[sub]);
-          return true;
-        };
-        if (have) {
-          take(k, kp);
-          ok = step_S(0, true, narrow, n == 1, 0) && step_S(1, true, narrow, n == 1, 0);
-        }
-        while (have && ok) {
-          for (int j = 0; j < n && ok; ++j) {
-            uint32_t v, vp;
-            take(v, vp);
-            const bool end = j == n - 1, one = narrow && j == 0;
-            if (end) have2 = next_unit(n2, narrow2);
-            const bool more = !end || have2;
-            const bool nar = end && narrow2, lastS = end ? n2 == 1 : j + 1 == n - 1;
-            if (!(ok = mbar_wait_warp(&kv_full[v], vp, abort_flag, kWaitLimitNs))) break;
-            if (more) take(k, kp);
-#pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-              ok = mbar_wait_warp(&p_half[sub], pcnt[sub] & 1, abort_flag, kWaitLimitNs) &&
-                   (j > 0 || ul == 0 || mbar_wait_warp(&o_empty[sub], (ul - 1) & 1, abort_flag, kWaitLimitNs));
-              if (!ok) break;
-              tc_fence_after();
-              issue_PV(sub, v, j > 0, 0, one);
-              if (!(ok = mbar_wait_warp(&p_full[sub], pcnt[sub] & 1, abort_flag, kWaitLimitNs))) break;
-              ++pcnt[sub];
-              tc_fence_after();
-              issue_PV(sub, v, j > 0, 1, one);
-              if (sub == 1) umma_commit_w(&kv_empty[v]);
-              if (end) umma_commit_w(&o_full[sub]);
-              if (more && !(ok = step_S(sub, end, nar, lastS, ul + 1))) break;
-            }
-          }
-          n = n2;
-          narrow = narrow2;
-          have = have2;
-          ++ul;
-        }
-      } else
       for (int rd = 0; ok; ++rd) {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) break;
@@ -425,12 +344,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // the MMA operand reads are both async-proxy operations ordered by
         // the transaction barrier
         if (!(ok = mbar_wait_warp(&kv_full[k0], k0p, abort_flag, kWaitLimitNs))) break;
-        issue_S(0, k0, idS);
+        bool narrow = false;  // window form: the first tile's product is kSinkKeys keys wide
+        if constexpr (kWin) narrow = U.narrow;
+        issue_S(0, k0, narrow ? idSn : idS);
         umma_commit_w(&s_full[0]);
         if (!shared_kv) umma_commit_w(&kv_empty[k0]);
         if (n == 1) umma_commit_w(&q_empty[0]);
         if (!shared_kv && !(ok = mbar_wait_warp(&kv_full[k1], k1p, abort_flag, kWaitLimitNs))) break;
-        issue_S(1, k1, idS);
+        issue_S(1, k1, narrow ? idSn : idS);
         umma_commit_w(&s_full[1]);
         umma_commit_w(&kv_empty[k1]);
         if (n == 1) umma_commit_w(&q_empty[1]);
@@ -445,11 +366,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                (j > 0 || ul == 0 || mbar_wait_warp(&o_empty[0], (ul - 1) & 1, abort_flag, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          issue_PV(0, v0, j > 0, 0);
+          issue_PV(0, v0, j > 0, 0, narrow && j == 0);
           if (!(ok = mbar_wait_warp(&p_full[0], pcnt[0] & 1, abort_flag, kWaitLimitNs))) break;
           ++pcnt[0];
           tc_fence_after();
-          issue_PV(0, v0, j > 0, 1);
+          issue_PV(0, v0, j > 0, 1, narrow && j == 0);
           if (!shared_kv) umma_commit_w(&kv_empty[v0]);
           if (j == n - 1) umma_commit_w(&o_full[0]);
           uint32_t nk0 = 0, nk0p = 0, nk1 = 0, nk1p = 0;
@@ -468,11 +389,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                (j > 0 || ul == 0 || mbar_wait_warp(&o_empty[1], (ul - 1) & 1, abort_flag, kWaitLimitNs));
           if (!ok) break;
           tc_fence_after();
-          issue_PV(1, v1, j > 0, 0);
+          issue_PV(1, v1, j > 0, 0, narrow && j == 0);
           if (!(ok = mbar_wait_warp(&p_full[1], pcnt[1] & 1, abort_flag, kWaitLimitNs))) break;
           ++pcnt[1];
           tc_fence_after();
-          issue_PV(1, v1, j > 0, 1);
+          issue_PV(1, v1, j > 0, 1, narrow && j == 0);
           umma_commit_w(&kv_empty[v1]);
           if (j == n - 1) umma_commit_w(&o_full[1]);
           if (j + 1 < n) {

@@ -120,10 +120,14 @@ int launch_bwd(QkArgs& a, int layout, float* dwq, float* dwk, DeviceInfo* di, cu
   if (kc > need) kc = need;
   a.q_ctas = int(qc);
   const int ctas = int(qc + kc);
-  if (layout == CPATTN_ROPE_INTERLEAVED)
-    cpattn_qk_bwd_kernel<D, true><<<ctas, kQkThreads, 0, st>>>(a);
-  else
-    cpattn_qk_bwd_kernel<D, false><<<ctas, kQkThreads, 0, st>>>(a);
+  auto kernel = layout == CPATTN_ROPE_INTERLEAVED ? cpattn_qk_bwd_kernel<D, true> : cpattn_qk_bwd_kernel<D, false>;
+  std::atomic<bool>& done = di->qk_bwd_attr[(D == 128 ? 2 : 0) + (layout == CPATTN_ROPE_INTERLEAVED ? 1 : 0)];
+  if (!done.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQkBwdSmem) != cudaSuccess)
+      return CPATTN_ERR_CUDA;
+    done.store(true, std::memory_order_release);
+  }
+  kernel<<<ctas, kQkThreads, kQkBwdSmem, st>>>(a);
   cpattn_qk_dw_kernel<<<dim3(D / 8, 2), 256, 0, st>>>(a.partial, a.q_ctas, ctas, D, dwq, dwk);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
 }

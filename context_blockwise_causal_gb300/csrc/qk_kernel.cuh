@@ -289,12 +289,20 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_fwd_kernel(const __gr
 // q_ctas CTAs take the queries, the others the keys, so that a thread keeps
 // one set of 16 sums over all its rows; they are added across the CTA in a
 // fixed order at the end and across CTAs by cpattn_qk_dw_kernel: no atomics,
-// the same bits every time. Rows are loaded one group ahead, as above.
+// the same bits every time. A thread's pieces of the next three groups of rows
+// are on their way into its own slots of shared memory while it works on one
+// (held in registers one group ahead, as in the forward, the 16 warps an SM has
+// room for do not keep enough bytes in flight: 178 us against 163 at 32K
+// tokens, 32 + 8 heads).
+constexpr int kQkBwdStages = 4;
+constexpr int kQkBwdSmem = kQkBwdStages * kQkThreads * 4 * 16;
+
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __grid_constant__ QkArgs a) {
   constexpr int kT = D / 16, kRows = 32 / kT, kWarps = kQkThreads / 32;
   __shared__ __align__(16) float w[2][D];
   __shared__ float red[kWarps][D];
+  extern __shared__ __align__(16) uint8_t ring[];  // [stage][piece][thread] 16 bytes
   qk_stage_weights<D>(a, w);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const QkLane l = qk_lane<D, kInter>(lane % kT, a.rot);
@@ -307,49 +315,60 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __gr
   float dw[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-  const int64_t tokens = int64_t(a.b) * a.n;
-  int64_t bt = int64_t(cta) * kWarps + warp;
-  int bi = 0, tok = 0;
-  const __nv_bfloat16* x = nullptr;
-  const __nv_bfloat16* dy = nullptr;
-  auto set = [&](int64_t at) {
-    bi = int(at / a.n);
-    tok = int(at - int64_t(bi) * a.n);
-    x = t.x + int64_t(bi) * t.x_batch + int64_t(tok) * t.x_token;
-    dy = t.dy + int64_t(bi) * t.dy_batch + int64_t(tok) * t.dy_token;
+  const int64_t tokens = int64_t(a.b) * a.n, step = int64_t(ctas) * kWarps;
+  // the group of rows to be loaded next: heads h .. of token pt
+  int64_t pt = int64_t(cta) * kWarps + warp;
+  int ph = 0;
+  const __nv_bfloat16* px = nullptr;
+  const __nv_bfloat16* pdy = nullptr;
+  auto rows_of = [&](int64_t at) {
+    const int bi = int(at / a.n), tok = int(at - int64_t(bi) * a.n);
+    px = t.x + int64_t(bi) * t.x_batch + int64_t(tok) * t.x_token;
+    pdy = t.dy + int64_t(bi) * t.dy_batch + int64_t(tok) * t.dy_token;
   };
-  auto fetch = [&](int hh, uint4 (&v)[4]) {
-    v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
-    if (hh < t.h) {
-      v[0] = *reinterpret_cast<const uint4*>(x + hh * D + l.fa);
-      v[1] = *reinterpret_cast<const uint4*>(x + hh * D + l.fb);
-      v[2] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fa);
-      v[3] = *reinterpret_cast<const uint4*>(dy + hh * D + l.fb);
+  const uint32_t slot = smem_u32(ring) + threadIdx.x * 16;
+  auto load = [&](int stage) {  // a group is committed even when nothing is left
+    if (pt < tokens) {
+      const int hh = ph + sub;
+      const bool on = hh < t.h;
+      const int64_t o = on ? int64_t(hh) * D : 0;
+      const uint32_t dst = slot + stage * (kQkThreads * 64);
+      cp_async16(dst, px + o + l.fa, on);
+      cp_async16(dst + kQkThreads * 16, px + o + l.fb, on);
+      cp_async16(dst + kQkThreads * 32, pdy + o + l.fa, on);
+      cp_async16(dst + kQkThreads * 48, pdy + o + l.fb, on);
+      ph += kRows;
+      if (ph >= t.h) {
+        ph = 0;
+        pt += step;
+        if (pt < tokens) rows_of(pt);
+      }
     }
+    cp_async_commit();
   };
-  uint4 v[4], nx[4];
-  if (bt < tokens) {
-    set(bt);
-    fetch(sub, v);
-  }
-  while (bt < tokens) {
+  int64_t bt = pt;
+  if (pt < tokens) rows_of(pt);
+#pragma unroll
+  for (int s = 0; s < kQkBwdStages - 1; ++s) load(s);
+  int stage = 0;
+  for (; bt < tokens; bt += step) {
+    const int bi = int(bt / a.n), tok = int(bt - int64_t(bi) * a.n);
     __nv_bfloat16* y = t.y + int64_t(bi) * t.y_batch + int64_t(tok) * t.y_token;
     float cs[8], sn[8];
     qk_cos_sin(a, l, qk_position(a, bi, tok), cs, sn);
-    bt += int64_t(ctas) * kWarps;
     for (int h = 0; h < t.h; h += kRows) {
       const int hh = h + sub;
-      if (h + kRows < t.h) {
-        fetch(h + kRows + sub, nx);
-      } else if (bt < tokens) {
-        set(bt);
-        fetch(sub, nx);
-      }
+      cp_async_wait<kQkBwdStages - 2>();
       float f[16], g[16];
-      bf16x8_to_f32(v[0], f);
-      bf16x8_to_f32(v[1], f + 8);
-      bf16x8_to_f32(v[2], g);
-      bf16x8_to_f32(v[3], g + 8);
+      {
+        const uint4* v = reinterpret_cast<const uint4*>(ring + stage * (kQkThreads * 64)) + threadIdx.x;
+        bf16x8_to_f32(v[0], f);
+        bf16x8_to_f32(v[kQkThreads], f + 8);
+        bf16x8_to_f32(v[2 * kQkThreads], g);
+        bf16x8_to_f32(v[3 * kQkThreads], g + 8);
+      }
+      load((stage + kQkBwdStages - 1) % kQkBwdStages);
+      stage = (stage + 1) % kQkBwdStages;
       qk_rotate<kInter>(g, l, cs, sn);  // a.inverse: turns back
       float ss = 0.f, gx = 0.f, wr[16];
       qk_weights(wt, l, wr);
@@ -371,10 +390,9 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __gr
         *reinterpret_cast<uint4*>(y + hh * D + l.fa) = f32_to_bf16x8(f);
         *reinterpret_cast<uint4*>(y + hh * D + l.fb) = f32_to_bf16x8(f + 8);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = nx[i];
     }
   }
+  cp_async_wait<0>();
   // the warp's rows, then the CTA's warps
 #pragma unroll
   for (int i = 0; i < 16; ++i) {

@@ -219,6 +219,7 @@ struct BwdWinUnit : BwdUnit {
   int qlen;
   int qa;       // first query tile visited (nq of them; the walk comes down from the last)
   int slot;     // a part of a cut walk: index of its fp32 result; -1: the whole walk
+  int rows;     // key rows of the tile that the part's queries see (win_part_rows)
 };
 
 // Query tiles in which some query sees a key of tile kt: [qa, qa + nq).
@@ -233,6 +234,15 @@ __host__ __device__ inline void win_query_tiles(const CpGeom& g, const WinSeq& s
   }
   qa = lo / kTile;
   nq = hi < lo ? 0 : hi / kTile - qa + 1;
+}
+
+// Key rows of tile kt that query tiles from qa on see: all of them, or only
+// first tokens where the tiles lie beyond every row's window. The other rows'
+// results of such a part are zero: they are neither stored nor added.
+__host__ __device__ inline int win_part_rows(const CpGeom& g, const WinSeq& s, int kt, int qa) {
+  const int k0 = kt * kTile;
+  if (int64_t(s.off) + int64_t(qa) * kTile < int64_t(k0) + kTile - 1 + g.window) return kTile;
+  return g.sinks - k0 < kTile ? g.sinks - k0 : kTile;
 }
 
 // Parts of a cut walk: query tiles [qa + part * per, ...) with per =
@@ -290,6 +300,7 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   U.v = U.gt = kt;
   U.k_t0 = kt * kTile;
   U.qa = 0;
+  U.rows = kTile;
   // no such key tile, or an ordinary unit of a tile whose walk is cut
   if (U.k_t0 >= s.klen || (U.slot < 0 && kt < cut)) {
     U.k_t0 = U.k_valid = U.nq = U.items = 0;
@@ -304,21 +315,24 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
     U.qa += from;
     U.nq = left < 0 ? 0 : (left < g.part_tiles ? left : g.part_tiles);
     if (U.nq == 0) U.k_valid = 0;  // a part that the walk does not reach writes nothing
+    U.rows = win_part_rows(g, s, kt, U.qa);
   }
   U.items = U.nq * (g.hq / g.hkv);
   return U;
 }
 
 // Cuts the walks of the tiles that hold first tokens when the longest of them
-// is over twice an ordinary tile's: an ordinary tile is seen by about
-// window/128 + 1 query tiles, a cut part covers twice as many (at least 8).
+// is over twice an ordinary tile's (which is seen by about window/128 + 1
+// query tiles) into parts of an ordinary tile's work, at least 8 tiles. (Parts
+// of twice that left the last round of CTAs uneven: 852 us against 795 us for
+// the kernel at b1 s32768 h32/8 window 1024.)
 __host__ __device__ inline void win_set_parts(CpGeom& g) {
   g.sink_parts = 1;
   g.part_tiles = g.tpc > 0 ? g.tpc : 1;
   if (g.sinks == 0) return;
-  const int per = 2 * (g.window / kTile + 2);
+  const int per = g.window / kTile + 1;
   const int tiles = per > 8 ? per : 8;
-  if (g.tpc <= tiles) return;
+  if (g.tpc <= 2 * tiles) return;
   g.part_tiles = tiles;
   g.sink_parts = (g.tpc + tiles - 1) / tiles;
 }

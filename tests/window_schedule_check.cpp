@@ -132,6 +132,11 @@ static int backward(CpGeom g, long* dq_pairs, long* kv_pairs) {
       int qa, nq;
       win_query_tiles(g, s, U.v, qa, nq);
       CHECK(U.slot % g.sink_parts < win_parts(g, nq), "dkdv unit %ld: part beyond those joined", idx);
+      // rows past U.rows are neither stored nor joined: none of the part's queries sees them
+      CHECK(U.rows >= 1 && U.rows == win_part_rows(g, s, U.v, qa + (U.slot % g.sink_parts) * g.part_tiles), "rows");
+      for (int r = U.rows; r < U.k_valid; ++r)
+        for (int t = U.qa * kTile; t < (U.qa + U.nq) * kTile && t < s.qlen; ++t)
+          CHECK(!sees(g, s.off + t, U.k_t0 + r), "dkdv unit %ld: row %d is seen", idx, r);
     } else {
       for (int r = 0; r < U.k_valid; ++r) ++owner[size_t(U.g) * kvrows + U.kv0 + U.k_t0 + r];
     }
