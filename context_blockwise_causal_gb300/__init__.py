@@ -454,6 +454,22 @@ def _empty(shape, like, stream, dtype=_BF16):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _out_rows(name, t, b, n, h, d, like, stream):
+    """An output [b, n, h, d], given or new, and its cpattn_rows."""
+    if t is not None:
+        return t, _rows(name, t, (b, n, h, d))
+    t = _empty((b, n, h, d), like, stream)
+    return t, _ROWS(t.data_ptr(), n * h * d, h * d)
+
+
+def _out(name, t, shape, like, stream, dtype=_BF16):
+    """An output of a shape, given or new, and its address."""
+    if t is not None:
+        return t, _dense(name, t, dtype, shape)
+    t = _empty(shape, like, stream, dtype)
+    return t, t.data_ptr()
+
+
 def _dense(name, t, dtype, shape):
     """A contiguous tensor of a type and shape, beside ``_on``'s checks."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
@@ -550,12 +566,9 @@ def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, 
     ins, b, n, hq, hkv, d = _qk(q, k, q_weight, k_weight)
     plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
     handle = _on(stream, q, k, q_weight, k_weight, q_out, k_out, cu_seqlens, positions)
-    if q_out is None:
-        q_out = _empty((b, n, hq, d), q, stream)
-    if k_out is None:
-        k_out = _empty((b, n, hkv, d), k, stream)
-    rc = library().cpattn_qk_norm_rope(*ins, eps, _rows("q_out", q_out, q.shape), _rows("k_out", k_out, k.shape), b, n,
-                                       hq, hkv, d, plan, handle)
+    q_out, qo = _out_rows("q_out", q_out, b, n, hq, d, q, stream)
+    k_out, ko = _out_rows("k_out", k_out, b, n, hkv, d, k, stream)
+    rc = library().cpattn_qk_norm_rope(*ins, eps, qo, ko, b, n, hq, hkv, d, plan, handle)
     if rc:
         raise CpattnError(rc, "cpattn_qk_norm_rope")
     return q_out, k_out
@@ -571,20 +584,14 @@ def cpattn_qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, eps=1e-6, 
     plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
     handle = _on(stream, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, cu_seqlens,
                  positions)
-    if dq is None:
-        dq = _empty((b, n, hq, d), q, stream)
-    if dk is None:
-        dk = _empty((b, n, hkv, d), k, stream)
-    if dq_weight is None:
-        dq_weight = _empty((d,), q, stream, _F32)
-    if dk_weight is None:
-        dk_weight = _empty((d,), q, stream, _F32)
+    gq, gk = _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape)
+    dq, rq = _out_rows("dq", dq, b, n, hq, d, q, stream)
+    dk, rk = _out_rows("dk", dk, b, n, hkv, d, k, stream)
+    dq_weight, wq = _out("dq_weight", dq_weight, (d,), q, stream, _F32)
+    dk_weight, wk = _out("dk_weight", dk_weight, (d,), q, stream, _F32)
     ws, ws_bytes, workspace = _workspace(workspace, _qk_bwd_bytes(d), q, stream)
-    rc = library().cpattn_qk_norm_rope_bwd(*ins, eps, _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape),
-                                           _rows("dq", dq, q.shape), _rows("dk", dk, k.shape),
-                                           _dense("dq_weight", dq_weight, _F32, (d,)),
-                                           _dense("dk_weight", dk_weight, _F32, (d,)), ws, ws_bytes, b, n, hq, hkv, d,
-                                           plan, handle)
+    rc = library().cpattn_qk_norm_rope_bwd(*ins, eps, gq, gk, rq, rk, wq, wk, ws, ws_bytes, b, n, hq, hkv, d, plan,
+                                           handle)
     if rc:
         raise CpattnError(rc, "cpattn_qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
@@ -720,6 +727,11 @@ def cpattn_bwd(q, k, v, o, lse, do, cp, causal=True, dq=None, dk=None, dv=None, 
     return dq, dk, dv
 
 
+def _keys(n):
+    """A count of keys for the C call; any that int32 cannot hold is all of them."""
+    return n if n <= 0x7FFFFFFF else 0x7FFFFFFF
+
+
 def _window_dims(q, k, v):
     """Pointers and sizes b, sq, skv, hq, hkv, d of a window call."""
     if q.dim() != 4 or k.dim() != 4:
@@ -740,19 +752,17 @@ def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, st
     queries are the last sq positions. Returns (o like q, lse [b, hq, sq])."""
     ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
     handle = _on(stream, q, k, v, o, lse)
-    if o is None:
-        o = _empty((b, sq, hq, d), q, stream)
-    if lse is None:
-        lse = _empty((b, hq, sq), q, stream, _F32)
-    rc = library().cpattn_fwd_window(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (b, hq, sq)), b, sq,
-                                     skv, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
+    o, po = _out("o", o, (b, sq, hq, d), q, stream)
+    lse, pl = _out("lse", lse, (b, hq, sq), q, stream, _F32)
+    rc = library().cpattn_fwd_window(*ins, po, pl, b, sq, skv, hq, hkv, d, _keys(window), _keys(sinks),
+                                     0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_fwd_window")
     return o, lse
 
 
 def cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks=0):
-    return int(library().cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, int(window), int(sinks)))
+    return int(library().cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, _keys(window), _keys(sinks)))
 
 
 def cpattn_bwd_window(q, k, v, o, lse, do, window, sinks=0, scale=None, dq=None, dk=None, dv=None, workspace=None,
@@ -760,19 +770,15 @@ def cpattn_bwd_window(q, k, v, o, lse, do, window, sinks=0, scale=None, dq=None,
     """Backward of cpattn_fwd_window from its o and lse. Returns (dq, dk, dv)."""
     ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
     handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
-    if dq is None:
-        dq = _empty((b, sq, hq, d), q, stream)
-    if dk is None:
-        dk = _empty((b, skv, hkv, d), q, stream)
-    if dv is None:
-        dv = _empty((b, skv, hkv, d), q, stream)
+    dq, gq = _out("dq", dq, (b, sq, hq, d), q, stream)
+    dk, gk = _out("dk", dk, (b, skv, hkv, d), q, stream)
+    dv, gv = _out("dv", dv, (b, skv, hkv, d), q, stream)
     lib = library()
-    need = lib.cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks)
+    need = lib.cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, _keys(window), _keys(sinks))
     ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
     rc = lib.cpattn_bwd_window(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (b, hq, sq)),
-                               _dense("do", do, _BF16, q.shape), _dense("dq", dq, _BF16, q.shape),
-                               _dense("dk", dk, _BF16, k.shape), _dense("dv", dv, _BF16, k.shape), ws, ws_bytes, b, sq,
-                               skv, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
+                               _dense("do", do, _BF16, q.shape), gq, gk, gv, ws, ws_bytes, b, sq, skv, hq, hkv, d,
+                               _keys(window), _keys(sinks), 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_bwd_window")
     return dq, dk, dv
@@ -797,13 +803,10 @@ def cpattn_fwd_window_varlen(q, k, v, cu_seqlens, window, sinks=0, scale=None, o
     offsets (host list/tensor). Returns (o [total, hq, d], lse [hq, total])."""
     ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
     handle = _on(stream, q, k, v, o, lse)
-    if o is None:
-        o = _empty((total, hq, d), q, stream)
-    if lse is None:
-        lse = _empty((hq, total), q, stream, _F32)
-    rc = library().cpattn_fwd_window_varlen(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (hq, total)),
-                                            cu.buffer_info()[0], len(cu) - 1, hq, hkv, d, window, sinks,
-                                            0.0 if scale is None else scale, handle)
+    o, po = _out("o", o, (total, hq, d), q, stream)
+    lse, pl = _out("lse", lse, (hq, total), q, stream, _F32)
+    rc = library().cpattn_fwd_window_varlen(*ins, po, pl, cu.buffer_info()[0], len(cu) - 1, hq, hkv, d, _keys(window),
+                                            _keys(sinks), 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_fwd_window_varlen")
     return o, lse
@@ -814,19 +817,15 @@ def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, s
     """Backward of cpattn_fwd_window_varlen. Returns (dq, dk, dv)."""
     ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
     handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
-    if dq is None:
-        dq = _empty((total, hq, d), q, stream)
-    if dk is None:
-        dk = _empty((total, hkv, d), q, stream)
-    if dv is None:
-        dv = _empty((total, hkv, d), q, stream)
+    dq, gq = _out("dq", dq, (total, hq, d), q, stream)
+    dk, gk = _out("dk", dk, (total, hkv, d), q, stream)
+    dv, gv = _out("dv", dv, (total, hkv, d), q, stream)
     lib, cu_p, nseq = library(), cu.buffer_info()[0], len(cu) - 1
-    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, window, sinks)
+    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, _keys(window), _keys(sinks))
     ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
     rc = lib.cpattn_bwd_window_varlen(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (hq, total)),
-                                      _dense("do", do, _BF16, q.shape), _dense("dq", dq, _BF16, q.shape),
-                                      _dense("dk", dk, _BF16, k.shape), _dense("dv", dv, _BF16, k.shape), ws, ws_bytes,
-                                      cu_p, nseq, hq, hkv, d, window, sinks, 0.0 if scale is None else scale, handle)
+                                      _dense("do", do, _BF16, q.shape), gq, gk, gv, ws, ws_bytes, cu_p, nseq, hq, hkv, d,
+                                      _keys(window), _keys(sinks), 0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_bwd_window_varlen")
     return dq, dk, dv
@@ -834,7 +833,7 @@ def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, s
 
 def cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
     """Workspace bytes of cpattn_decode on the current device (0: none)."""
-    return int(library().cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, int(window), int(sinks)))
+    return int(library().cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, _keys(window), _keys(sinks)))
 
 
 def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o=None, lse=None, workspace=None,
@@ -868,15 +867,13 @@ def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o
         kh = vh = 0
     ln = _dense("lengths", lengths, _I32, (b,))
     handle = _on(stream, q, k_cache, v_cache, lengths, o, lse, workspace)
-    if o is None:
-        o = _empty((b, hq, d), q, stream)
-    if lse is None:
-        lse = _empty((b, hq), q, stream, _F32)
+    o, po = _out("o", o, (b, hq, d), q, stream)
+    lse, pl = _out("lse", lse, (b, hq), q, stream, _F32)
+    window, sinks = _keys(window), _keys(sinks)
     need = _decode_bytes(_device(), b, hq, hkv, d, cap, window, sinks)
     ws, ws_bytes, workspace = (None, 0, None) if need == 0 else _workspace(workspace, need, q, stream)
     rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ln,
-                                 _dense("o", o, _BF16, (b, hq, d)), _dense("lse", lse, _F32, (b, hq)), ws, ws_bytes, b,
-                                 hq, hkv, d, cap, qb, kb, kt, kh, vb, vt, vh, window, sinks,
+                                 po, pl, ws, ws_bytes, b, hq, hkv, d, cap, qb, kb, kt, kh, vb, vt, vh, window, sinks,
                                  0.0 if scale is None else scale, handle)
     if rc:
         raise CpattnError(rc, "cpattn_decode")

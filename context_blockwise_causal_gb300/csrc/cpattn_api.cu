@@ -971,4 +971,4 @@ extern "C" const char* cpattn_strerror(int code) {
   }
 }
 
-extern "C" int cpattn_version(void) { return 100; }
+extern "C" int cpattn_version(void) { return 200; }

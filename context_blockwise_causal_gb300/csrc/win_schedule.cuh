@@ -321,18 +321,29 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   return U;
 }
 
-// Cuts the walks of the tiles that hold first tokens when the longest of them
-// is over twice an ordinary tile's (which is seen by about window/128 + 1
-// query tiles) into parts of an ordinary tile's work, at least 8 tiles. (Parts
-// of twice that left the last round of CTAs uneven: 852 us against 795 us for
-// the kernel at b1 s32768 h32/8 window 1024.)
+// Cuts the walks of the tiles that hold first tokens into parts of an ordinary
+// tile's work (which is seen by about window/128 + 1 query tiles; at least 8
+// tiles, at most kMaxParts parts) when such a walk is over twice that and
+// longer than a quarter of what each of a full chip's CTAs has to do in all:
+// with many sequences or heads whole walks balance by themselves, and parts
+// would only cost workspace. (Parts of twice that size left the last round of
+// CTAs uneven: 852 us against 795 us for the kernel at b1 s32768 h32/8 window
+// 1024.)
+constexpr int kMaxParts = 64;
+constexpr int kWinChipCtas = 152;
 __host__ __device__ inline void win_set_parts(CpGeom& g) {
   g.sink_parts = 1;
   g.part_tiles = g.tpc > 0 ? g.tpc : 1;
   if (g.sinks == 0) return;
-  const int per = g.window / kTile + 1;
-  const int tiles = per > 8 ? per : 8;
+  const int ordinary = g.window / kTile + 1;
+  int tiles = ordinary > 8 ? ordinary : 8;
   if (g.tpc <= 2 * tiles) return;
+  const int64_t key_tiles = g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_key_tiles(g);
+  const int64_t long_walks = int64_t(num_seqs(g)) * ((g.sinks + kTile - 1) / kTile) * g.tpc;
+  const int64_t work = g.hkv * (key_tiles * ordinary + long_walks);  // query tiles visited
+  if (int64_t(g.tpc) * 4 * kWinChipCtas <= work) return;
+  const int least = (g.tpc + kMaxParts - 1) / kMaxParts;
+  if (tiles < least) tiles = least;
   g.part_tiles = tiles;
   g.sink_parts = (g.tpc + tiles - 1) / tiles;
 }

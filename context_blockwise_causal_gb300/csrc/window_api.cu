@@ -247,12 +247,13 @@ extern "C" int cpattn_fwd_window_varlen(const void* q, const void* k, const void
                                         float scale, void* stream) {
   const int64_t total = check_cu(cu_seqlens, nseq);
   if (total < 0) return int(total);
-  if (!q || !k || !v || !o || !lse) return CPATTN_ERR_NULL_PTR;
   const int rows = total > 0 ? int(total) : 1;
   int rc = check_shape(WinShape{1, rows, rows, hq, hkv, d, window, sinks});
   if (rc) return rc;
   double sc = 0.0;
   if ((rc = scale_of(scale, d, &sc))) return rc;
+  if (total == 0) return CPATTN_OK;
+  if (!q || !k || !v || !o || !lse) return CPATTN_ERR_NULL_PTR;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return CPATTN_ERR_MISALIGNED;
   return for_groups(cu_seqlens, nseq, [&](int start, int len, const int* cu, int n) {
     const size_t qo = size_t(start) * hq * d * 2, ko = size_t(start) * hkv * d * 2;
@@ -306,12 +307,13 @@ extern "C" int cpattn_bwd_window_varlen(const void* q, const void* k, const void
                                         int window, int sinks, float scale, void* stream) {
   const int64_t total = check_cu(cu_seqlens, nseq);
   if (total < 0) return int(total);
-  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace) return CPATTN_ERR_NULL_PTR;
   const int rows = total > 0 ? int(total) : 1;
   int rc = check_shape(WinShape{1, rows, rows, hq, hkv, d, window, sinks});
   if (rc) return rc;
   double sc = 0.0;
   if ((rc = scale_of(scale, d, &sc))) return rc;
+  if (total == 0) return CPATTN_OK;
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv || !workspace) return CPATTN_ERR_NULL_PTR;
   for (const void* p : {q, k, v, o, static_cast<const void*>(lse), dout, static_cast<const void*>(dq),
                         static_cast<const void*>(dk), static_cast<const void*>(dv), static_cast<const void*>(workspace)})
     if (!aligned16(p)) return CPATTN_ERR_MISALIGNED;

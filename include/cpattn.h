@@ -450,9 +450,12 @@ int cpattn_qk_norm_rope_bwd(const cpattn_rows* q, const cpattn_rows* k, const vo
  * chunk of a prompt attends to what was read before it. lse [b, hq, sq]. Any
  * lengths (no divisibility); other layouts, limits, pointers and errors as
  * cpattn_fwd; scale 0 selects 1/sqrt(d). b * skv < 2^31, skv <= 2^30.
- * Keys hidden from a query are masked after the product of whole 128-key
- * tiles: a non-finite value in a V row can reach queries within 127 positions
- * of those that see it.
+ * Hidden keys are masked inside products of whole 128-row tiles, where a zero
+ * weight times a non-finite value is NaN. So inputs must be finite: a
+ * non-finite row of v (in the backward of q, k, v or dout) can reach rows up to
+ * 127 positions from those that see it, and at a sequence's ragged end those
+ * of the sequence before it. (Non-finite scores alone are masked: k in the
+ * forward.)
  */
 int cpattn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int b, int sq, int skv, int hq,
                       int hkv, int d, int window, int sinks, float scale, void* stream);
@@ -467,7 +470,8 @@ int cpattn_bwd_window(const void* q, const void* k, const void* v, const void* o
 
 /* Packed samples, laid out as for cpattn_fwd_varlen (cu_seqlens: HOST int32
  * [nseq + 1], any sample lengths, 0 too); windows and first tokens are each
- * sample's own. Up to 512 samples run in one launch per kernel. */
+ * sample's own. Up to 512 samples run in one launch per kernel. No rows at
+ * all: nothing is done, and the other pointers may be NULL. */
 int cpattn_fwd_window_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_seqlens,
                              int nseq, int hq, int hkv, int d, int window, int sinks, float scale, void* stream);
 size_t cpattn_bwd_window_varlen_workspace_bytes(const int* cu_seqlens, int nseq, int hq, int hkv, int d, int window,

@@ -65,6 +65,13 @@ def test_window_arguments(lib):
     need = lib.cpattn_bwd_window_workspace_bytes(1, 8192, 8192, 4, 2, 64, 10, 1)
     assert need == 2 * 4 * 8192 * 4 + 2 * (2 * 8 * 128 * 64 * 4)
     assert lib.cpattn_bwd_window_workspace_bytes(1, 300, 200, 4, 2, 64, 10, 2) == 0
+    # parts cost workspace only where whole walks would not balance: not with
+    # many sequences, nor when every key is a first token
+    assert lib.cpattn_bwd_window_workspace_bytes(512, 8192, 8192, 4, 2, 64, 10, 1) == 512 * 2 * 4 * 8192 * 4
+    assert lib.cpattn_bwd_window_workspace_bytes(1, 32768, 32768, 32, 8, 128, 10, 32768) == 2 * 32 * 32768 * 4
+    # at most 64 parts of a walk
+    need = lib.cpattn_bwd_window_workspace_bytes(1, 1 << 20, 1 << 20, 4, 2, 64, 10, 1)
+    assert need == 2 * 4 * (1 << 20) * 4 + 2 * (2 * 64 * 128 * 64 * 4)
 
 
 def test_window_packed_arguments(lib):
@@ -79,6 +86,8 @@ def test_window_packed_arguments(lib):
     assert f(cu(0, 10, 5), 2) == ARG and f(cu(1, 10), 1) == ARG and f(cu(0, 10), 0) == ARG
     assert f(cu(0, 10), 1, window=0) == ARG and f(cu(0, 10), 1, hq=5) == ARG and f(cu(0, 0), 1, d=32) == ARG
     assert f(cu(0, 0), 1) == 0  # nothing to do
+    assert lib.cpattn_fwd_window_varlen(*(None,) * 5, cu(0, 0), 1, 4, 2, 64, 10, 2, 0.0, None) == 0
+    assert lib.cpattn_bwd_window_varlen(*(None,) * 10, 0, cu(0, 0), 1, 4, 2, 64, 10, 2, 0.0, None) == 0
     w = lib.cpattn_bwd_window_varlen_workspace_bytes
     # three samples of up to two tiles: L and D of 256 rows per sample and head
     assert w(cu(0, 100, 300, 301), 3, 4, 2, 64, 10, 2) == 2 * 3 * 4 * 256 * 4

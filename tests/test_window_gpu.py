@@ -15,6 +15,9 @@ u / 2^-17 = 512. LSE: scores off by up to 2^-17 sum |q k| scale, which is
 below 5e-5 for the inputs here (sum |q k| scale < 7): 1e-4.
 """
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -124,6 +127,49 @@ def test_packed_all_elements(lengths, hq, hkv, d, window, sinks):
              for a, e in zip(cu, cu[1:]) if e > a]
     r = {n: torch.cat([p[n] for p in parts], dim=1 if n == "lse" else 0) for n in parts[0]}
     _check(r, o, lse, grads)
+
+
+def test_no_rows_and_windows_beyond_int32():
+    q, k = (torch.empty(0, h, 64, dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    o, lse = cpattn_fwd_window_varlen(q, k, k, [0, 0, 0], 16)
+    grads = cpattn_bwd_window_varlen(q, k, k, o, lse, q, [0, 0, 0], 16)
+    assert o.shape == q.shape and lse.shape == (4, 0) and grads[1].shape == k.shape
+    x = [_randn(1, 200, h, 64, seed=15 + i).cuda() for i, h in enumerate((2, 1, 1))]
+    want = cpattn_fwd_window(*x, 200)
+    for window, sinks in ((2 ** 32 + 1, 0), (2 ** 40, 2 ** 33)):  # all keys, not what 32 bits leave of the number
+        got = cpattn_fwd_window(*x, window, sinks)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        got = cpattn_fwd_window_varlen(*(t[0] for t in x), [0, 200], window, sinks)
+        assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[1][0])
+
+
+def test_first_call_may_be_captured():
+    """The library's first call on a device inside a capture, in a fresh process."""
+    code = """
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import context_blockwise_causal_gb300 as pkg
+g = torch.Generator(device="cuda").manual_seed(1)
+q, k, v = (torch.randn(1, 300, h, 64, generator=g, device="cuda").bfloat16() for h in (2, 1, 1))
+n = torch.tensor([300], dtype=torch.int32, device="cuda")
+w = torch.ones(64, device="cuda")
+def step():
+    qn, kn = pkg.cpattn_qk_norm_rope(q, k, w, w)
+    o, lse = pkg.cpattn_fwd_window(qn, kn, v, 40, 2)
+    grads = pkg.cpattn_bwd_window(qn, kn, v, o, lse, q, 40, 2)
+    dx = pkg.cpattn_qk_norm_rope_bwd(q, k, w, w, grads[0], grads[1])
+    return (o, *grads, *dx, pkg.cpattn_decode(qn[:, -1], kn, v, n, 40, 2)[0])
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code, root], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-1500:]
 
 
 def test_packed_equals_the_samples_alone():

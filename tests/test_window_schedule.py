@@ -45,6 +45,7 @@ UNIFORM = [
     (1, 3500, 3500, 2, 2, 130, 4),      # walks of the first tile cut into parts
     (1, 2500, 3700, 2, 1, 64, 200),     # two cut tiles, queries from position 1200 on
     (3, 1300, 1500, 1, 1, 128, 128),
+    (8, 2300, 2300, 4, 4, 16, 4),       # as long walks, but enough of them to stay whole
 ]
 
 
