@@ -88,7 +88,7 @@ __device__ __forceinline__ int64_t ld_pos(const CpGeom& g, int ntp, int seq, int
 // rows (D/8 lanes x 16 bytes per row, so 32*16/(2D) rows per instruction),
 // the partial dot products are summed by xor shuffles inside each row's lane
 // group, and the lane that owns the row keeps its sum.
-template <int D, bool kWin = false>
+template <int D>
 __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
   constexpr int kLanesPerRow = D / 8;              // 16 (d = 128) or 8 (d = 64)
   constexpr int kRowsPerLoad = 32 / kLanesPerRow;  // rows one warp-wide load covers
@@ -154,16 +154,11 @@ __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
       seq = lo;
       tl = t - g.cu[lo];
     }
-    int64_t pos;
-    if constexpr (kWin) {
-      pos = int64_t(seq * g.hq + h) * a.ntp + tl;
-    } else {
-      const SeqGeom q = seq_geom(g, seq);
-      int chunk = tl / q.c;  // rank-local form: 0 or 1, the rank's first or second chunk
-      const int in = tl - chunk * q.c;
-      if (g.rank >= 0) chunk = chunk ? 2 * g.cp - 1 - g.rank : g.rank;
-      pos = ld_pos(g, a.ntp, seq, h, chunk, in / kTile, q.tpc, in % kTile);
-    }
+    const SeqGeom q = seq_geom(g, seq);
+    int chunk = tl / q.c;  // rank-local form: 0 or 1, the rank's first or second chunk
+    const int in = tl - chunk * q.c;
+    if (g.rank >= 0) chunk = chunk ? 2 * g.cp - 1 - g.rank : g.rank;
+    const int64_t pos = ld_pos(g, a.ntp, seq, h, chunk, in / kTile, q.tpc, in % kTile);
     const int64_t li = (int64_t(bi) * g.hq + h) * a.lse_stride + t;
     if (!bounds_ok(pos >= 0 && pos < a.vec_len && li < a.lse_len && idx < a.q_rows * g.hq, a.status)) continue;
     a.dvec[pos] = acc;
@@ -961,10 +956,11 @@ struct DqCfg {
   static constexpr int kOffKV = kOffdO + kTileBytes;
   static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
   // q_full q_empty qa_full qa_empty s_full s_free dp_full p_full dq_full
-  // dq_empty drain, kv_full[] kv_empty[], p_half
-  static constexpr int kNumBars = 12 + 2 * kSlots;
+  // dq_empty drain, kv_full[] kv_empty[], p_half, d_full (window form)
+  static constexpr int kNumBars = 13 + 2 * kSlots;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kLayoutBytes = kOffMisc + 16;
+  static constexpr int kOffRed = kOffMisc + 16;  // window form: each half-row's part of D, two units'
+  static constexpr int kLayoutBytes = kOffRed + 4 * kTile * 4;
   // The d=128 layout leaves no room for re-alignment: the dynamic shared
   // memory base must already be 1024-byte aligned (checked at run time).
   static constexpr bool kNeedAlignedBase = (kLayoutBytes + 1024 > 232448);
@@ -995,6 +991,25 @@ struct DqCfg {
 //   S(j+1) | dQ(j) | dP(j+1) | S(j+2) | ...
 // so the exponentials of tile j overlap dQ(j-1) and dP(j), and only the dS
 // step of each warp's first 32 keys lies on the tensor core's critical path.
+// Lane i of each four ends with piece i of the four lanes' rows: p[j] = piece
+// i of lane j.
+__device__ __forceinline__ void transpose4(uint4 (&p)[4], int lane) {
+  auto swap = [&](uint4& lo, uint4& hi, int bit) {
+    const bool up = lane & bit;
+    uint4 send = up ? lo : hi, got;
+    got.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+    got.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+    got.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+    got.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+    if (up) lo = got;
+    else hi = got;
+  };
+  swap(p[0], p[1], 1);
+  swap(p[2], p[3], 1);
+  swap(p[0], p[2], 2);
+  swap(p[1], p[3], 2);
+}
+
 template <bool kWin>
 __device__ __forceinline__ auto dq_unit_of(const CpGeom& g, int idx) {
   if constexpr (kWin)
@@ -1035,6 +1050,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* kv_full = bars + 11;
   uint64_t* kv_empty = bars + 11 + C::kSlots;
   uint64_t* p_half = bars + 11 + 2 * C::kSlots;
+  uint64_t* d_full = bars + 12 + 2 * C::kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
 
@@ -1058,6 +1074,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(dq_empty, 8);
     mbar_init(drain, 1);
     mbar_init(p_half, 8);
+    mbar_init(d_full, 8);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -1275,7 +1292,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // Window form. Units are short, so the next unit's Q and dO go into TMEM
       // (whose last readers have finished by then) before this unit's dQ is
       // stored, and its first products run meanwhile. P stays in fp32 (see
-      // softmax_p_frag32), so dP is taken 32 keys at a time.
+      // softmax_p_frag32), so dP is taken 32 keys at a time. Each row belongs
+      // to one unit, so L*log2e and D are formed here, from the dO that passes
+      // through the registers anyway, and written for the dK/dV kernel, which
+      // runs after this one: no pass of its own over O and dO (95 us for one
+      // at b1 s32768 h32 d128).
       float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
       int rd = 0;
       auto take_unit = [&](WinUnit& U, int u) -> bool {
@@ -1283,24 +1304,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (idx >= num_units) return false;
         ++rd;
         U = win_dq_unit(g, idx);
-        // (padding rows of a ragged tile read arbitrary values; their dQ is never stored)
-        int64_t pos = int64_t(U.seq * g.hq + U.h0) * a.ntp + U.u * kTile + jr;
-        if (!bounds_ok(pos >= 0 && pos < a.vec_len, a.status)) pos = 0;  // stays inside the vectors
-        l2 = a.lvec[pos];
-        dd = a.dvec[pos];
+        // O on its way, whole 128-byte lines (64-byte ones at d = 64): kL lanes
+        // take a half-row, the warp's rows 32 / kL at a time. (A lane per row
+        // touches 32 lines per load and took as long as a pass of its own.)
+        constexpr int kL = D / 16, kPer = 32 / kL;
+        const int r0 = wq * 32 + lane / kL, piece = lane % kL;
+        const bool real = jr < U.q_valid && bounds_ok(U.tok0 + U.q_t0 + jr < a.q_rows && U.h0 < g.hq, a.status);
+        uint4 ov[kL];
+#pragma unroll
+        for (int i = 0; i < kL; ++i) {
+          const int r = r0 + i * kPer;
+          ov[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < U.q_valid && bounds_ok(U.tok0 + U.q_t0 + r < a.q_rows, a.status))
+            ov[i] = *reinterpret_cast<const uint4*>(
+                a.o + (int64_t(U.tok0 + U.q_t0 + r) * g.hq + U.h0) * D + hf * (D / 2) + piece * 8);
+        }
+        const int64_t li = (int64_t(U.bi) * g.hq + U.h0) * a.lse_stride + U.lse_t0 + U.q_t0 + jr;
+        l2 = real && bounds_ok(li < a.lse_len, a.status) ? a.lse[li] * 1.4426950408889634f : 0.f;
         ok = mbar_wait_lean(q_full, u & 1, abort_flag, kWaitLimitNs) &&
              (u == 0 || mbar_wait_lean(qa_empty, (u - 1) & 1, abort_flag, kWaitLimitNs));
         if (!ok) return false;
         tc_fence_after();
-        // this row's columns hf*D/2 .. of the swizzled TMA tiles: 16-byte
-        // chunk c of row jr sits at chunk c ^ (jr & 7) of the row's 128 bytes
-        auto copy = [&](const uint8_t* tile, uint32_t dst) {
+        // 16-byte chunk c of row r of a swizzled TMA tile sits at chunk
+        // c ^ (r & 7) of the row's 128 bytes
+        auto chunk = [&](const uint8_t* tile, int r, int c) {
+          const int e0 = hf * (D / 2) + c * 8;
+          return *reinterpret_cast<const uint4*>(tile + (e0 / 64) * (kTile * 128) + r * 128 +
+                                                 ((((e0 % 64) / 8) ^ (r & 7)) * 16));
+        };
+        auto copy = [&](const uint8_t* tile, uint32_t dst) {  // this row's columns hf*D/2 ..
           uint32_t r[D / 4];
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
-            const int e0 = hf * (D / 2) + c * 8;
-            const uint4 v = *reinterpret_cast<const uint4*>(tile + (e0 / 64) * (kTile * 128) + jr * 128 +
-                                                            ((((e0 % 64) / 8) ^ (jr & 7)) * 16));
+            const uint4 v = chunk(tile, jr, c);
             r[4 * c] = v.x; r[4 * c + 1] = v.y; r[4 * c + 2] = v.z; r[4 * c + 3] = v.w;
           }
           if constexpr (D == 128) tmem_st32(dst, r);
@@ -1310,18 +1346,62 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         copy(sdO, tbase + lane_off + C::kColdOA + hf * (D / 4));
         tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(qa_full);
+        // D = rowsum(dO * O): both halves of the row, through shared memory
+        // (two units' worth of it: who writes unit u + 2's part has waited for
+        // every warp's part of u + 1, which it writes after reading unit u's)
+        float* red = reinterpret_cast<float*>(smem + C::kOffRed) + (u & 1) * (2 * kTile);
+#pragma unroll
+        for (int i = 0; i < kL; ++i) {
+          const uint4 v = chunk(sdO, r0 + i * kPer, piece);
+          const uint32_t d4[4] = {v.x, v.y, v.z, v.w}, o4[4] = {ov[i].x, ov[i].y, ov[i].z, ov[i].w};
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dot = fmaf(__uint_as_float(o4[e] << 16), __uint_as_float(d4[e] << 16), dot);
+            dot = fmaf(__uint_as_float(o4[e] & 0xffff0000u), __uint_as_float(d4[e] & 0xffff0000u), dot);
+          }
+#pragma unroll
+          for (int o = kL / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (piece == 0) red[hf * kTile + r0 + i * kPer] = dot;
+        }
+        __syncwarp();
         if (lane == 0) {
-          mbar_arrive(qa_full);
           mbar_arrive(q_empty);
+          mbar_arrive(d_full);
+        }
+        if (!(ok = mbar_wait_lean(d_full, u & 1, abort_flag, kWaitLimitNs))) return false;
+        dd = red[jr] + red[kTile + jr];
+        if (hf == 0 && real) {
+          const int64_t pos = int64_t(U.seq * g.hq + U.h0) * a.ntp + U.u * kTile + jr;
+          if (bounds_ok(pos < a.vec_len, a.status)) {
+            a.lvec[pos] = l2;
+            a.dvec[pos] = dd;
+          }
         }
         return true;
+      };
+      // Brings the next unit's O (a half-row per thread) into L2 a unit
+      // ahead, so that take_unit waits for L2, not for DRAM.
+      auto prefetch_unit = [&]() {
+        const int idx = snake_unit(rd, blockIdx.x, grid);
+        if (idx >= num_units) return;
+        const WinUnit N = win_dq_unit(g, idx);
+        const int row = N.tok0 + N.q_t0 + jr;
+        if (jr >= N.q_valid || !bounds_ok(row < a.q_rows && N.h0 < g.hq, a.status)) return;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.o + (int64_t(row) * g.hq + N.h0) * D + hf * (D / 2)));
       };
       WinUnit U;
       bool have = take_unit(U, 0);
       while (have && ok) {
-        const int krow = U.tok0 + U.q_t0 + jr;
-        const bool store = jr < U.q_valid && bounds_ok(krow < a.q_rows && U.h0 < g.hq, a.status);
-        __nv_bfloat16* dst = a.dq + (int64_t(krow) * g.hq + U.h0) * D + hf * (D / 2);
+        prefetch_unit();
+        // this lane's part of the stores: rows 4q .. 4q + 3 of the four lanes
+        // it exchanges pieces with (below)
+        const int r4 = jr & ~3;
+        const int rows_left = U.q_valid - r4;
+        __nv_bfloat16* dst =
+            a.dq + (int64_t(U.tok0 + U.q_t0 + r4) * g.hq + U.h0) * D + hf * (D / 2) + (lane & 3) * 8;
+        const int64_t left_in_dq = a.q_rows - (U.tok0 + U.q_t0 + r4);
         const int p0 = U.off + U.q_t0;  // position of the tile's row 0
         int j = 0;
         if (U.narrow) {
@@ -1419,17 +1499,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(dq_empty);
           }
-          if (store) {
+          uint4 pc[4];  // this row's four 16-byte pieces
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 pk;
-              pk.x = pack_bf16x2(__uint_as_float(rq[i]) * scale, __uint_as_float(rq[i + 1]) * scale);
-              pk.y = pack_bf16x2(__uint_as_float(rq[i + 2]) * scale, __uint_as_float(rq[i + 3]) * scale);
-              pk.z = pack_bf16x2(__uint_as_float(rq[i + 4]) * scale, __uint_as_float(rq[i + 5]) * scale);
-              pk.w = pack_bf16x2(__uint_as_float(rq[i + 6]) * scale, __uint_as_float(rq[i + 7]) * scale);
-              *reinterpret_cast<uint4*>(dst + c0 + i) = pk;
-            }
+          for (int i = 0; i < 4; ++i) {
+            pc[i].x = pack_bf16x2(__uint_as_float(rq[8 * i]) * scale, __uint_as_float(rq[8 * i + 1]) * scale);
+            pc[i].y = pack_bf16x2(__uint_as_float(rq[8 * i + 2]) * scale, __uint_as_float(rq[8 * i + 3]) * scale);
+            pc[i].z = pack_bf16x2(__uint_as_float(rq[8 * i + 4]) * scale, __uint_as_float(rq[8 * i + 5]) * scale);
+            pc[i].w = pack_bf16x2(__uint_as_float(rq[8 * i + 6]) * scale, __uint_as_float(rq[8 * i + 7]) * scale);
           }
+          // four lanes transpose their pieces, so that a store covers 64
+          // contiguous bytes of 8 rows instead of 16 bytes of 32
+          transpose4(pc, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < rows_left && bounds_ok(i < left_in_dq && U.h0 < g.hq, a.status))
+              *reinterpret_cast<uint4*>(dst + int64_t(i) * g.hq * D + c0) = pc[i];
         }
         ++ul;
       }

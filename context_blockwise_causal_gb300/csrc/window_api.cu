@@ -140,15 +140,13 @@ int launch_bwd(const CUtensorMap* maps, const BwdArgs& args, DeviceInfo* di, cud
     done.store(true, std::memory_order_release);
   }
   const CpGeom& g = args.g;
-  const int64_t rows = int64_t(g.b) * g.s * g.hq;
-  const int64_t pre = (rows + 255) / 256;
-  cpattn_bwd_pre_kernel<D, true><<<int(pre < di->num_sms * 16 ? pre : di->num_sms * 16), 256, 0, st>>>(args);
+  // dQ first: it forms the row vectors that dK/dV reads
+  dqk<<<persistent_grid(di, win_dq_units(g)), kBwdThreads, DqCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
+                                                                                       maps[3], args);
   dkdv<<<persistent_grid(di, win_dkdv_units(g)), kBwdThreads, DkdvCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
                                                                                             maps[3], args);
   const int64_t rows_cut = int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g) * kTile;
   if (rows_cut > 0) cpattn_window_join_kernel<D><<<int(rows_cut), 256, 0, st>>>(args);
-  dqk<<<persistent_grid(di, win_dq_units(g)), kBwdThreads, DqCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
-                                                                                       maps[3], args);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
 }
 
