@@ -166,6 +166,25 @@ __global__ void __launch_bounds__(256) cpattn_bwd_pre_kernel(const BwdArgs a) {
   }
 }
 
+// Lane i of each four ends with piece i of the four lanes' rows: p[j] = piece
+// i of lane j.
+__device__ __forceinline__ void transpose4(uint4 (&p)[4], int lane) {
+  auto swap = [&](uint4& lo, uint4& hi, int bit) {
+    const bool up = lane & bit;
+    uint4 send = up ? lo : hi, got;
+    got.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
+    got.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
+    got.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
+    got.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
+    if (up) lo = got;
+    else hi = got;
+  };
+  swap(p[0], p[1], 1);
+  swap(p[2], p[3], 1);
+  swap(p[0], p[2], 2);
+  swap(p[1], p[3], 2);
+}
+
 // Column of a packed bf16 operand tile for K-step kk (16 elements): the two
 // 64-element halves sit at columns [0,32) and [64,96) of their 128-column
 // region, each written by the warp that read the fp32 values there.
@@ -847,6 +866,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             continue;
           }
+          // as in dQ: four lanes transpose their 16-byte pieces, so that a
+          // store covers 64 contiguous bytes of 8 rows
+          uint4 pv[4], pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int q = 8 * i;
+            pv[i] = make_uint4(pack_bf16x2(__uint_as_float(rv[q]), __uint_as_float(rv[q + 1])),
+                               pack_bf16x2(__uint_as_float(rv[q + 2]), __uint_as_float(rv[q + 3])),
+                               pack_bf16x2(__uint_as_float(rv[q + 4]), __uint_as_float(rv[q + 5])),
+                               pack_bf16x2(__uint_as_float(rv[q + 6]), __uint_as_float(rv[q + 7])));
+            pk[i] = make_uint4(pack_bf16x2(__uint_as_float(rk[q]) * scale, __uint_as_float(rk[q + 1]) * scale),
+                               pack_bf16x2(__uint_as_float(rk[q + 2]) * scale, __uint_as_float(rk[q + 3]) * scale),
+                               pack_bf16x2(__uint_as_float(rk[q + 4]) * scale, __uint_as_float(rk[q + 5]) * scale),
+                               pack_bf16x2(__uint_as_float(rk[q + 6]) * scale, __uint_as_float(rk[q + 7]) * scale));
+          }
+          transpose4(pv, lane);
+          transpose4(pk, lane);
+          const int r4 = jr & ~3;
+          const int64_t o4 = (int64_t(krow - jr + r4) * g.hkv + U.g) * D + hf * (D / 2) + c0 + (lane & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (r4 + i < U.k_valid && bounds_ok(krow - jr + r4 + i < a.kv_rows && U.g < g.hkv, a.status)) {
+              *reinterpret_cast<uint4*>(a.dv + o4 + int64_t(i) * g.hkv * D) = pv[i];
+              *reinterpret_cast<uint4*>(a.dk + o4 + int64_t(i) * g.hkv * D) = pk[i];
+            }
+          }
+          continue;
         }
         if (key_ok && bounds_ok(krow < a.kv_rows && U.g < g.hkv, a.status)) {
 #pragma unroll
@@ -991,25 +1037,6 @@ struct DqCfg {
 //   S(j+1) | dQ(j) | dP(j+1) | S(j+2) | ...
 // so the exponentials of tile j overlap dQ(j-1) and dP(j), and only the dS
 // step of each warp's first 32 keys lies on the tensor core's critical path.
-// Lane i of each four ends with piece i of the four lanes' rows: p[j] = piece
-// i of lane j.
-__device__ __forceinline__ void transpose4(uint4 (&p)[4], int lane) {
-  auto swap = [&](uint4& lo, uint4& hi, int bit) {
-    const bool up = lane & bit;
-    uint4 send = up ? lo : hi, got;
-    got.x = __shfl_xor_sync(0xffffffffu, send.x, bit);
-    got.y = __shfl_xor_sync(0xffffffffu, send.y, bit);
-    got.z = __shfl_xor_sync(0xffffffffu, send.z, bit);
-    got.w = __shfl_xor_sync(0xffffffffu, send.w, bit);
-    if (up) lo = got;
-    else hi = got;
-  };
-  swap(p[0], p[1], 1);
-  swap(p[2], p[3], 1);
-  swap(p[0], p[2], 2);
-  swap(p[1], p[3], 2);
-}
-
 template <bool kWin>
 __device__ __forceinline__ auto dq_unit_of(const CpGeom& g, int idx) {
   if constexpr (kWin)
