@@ -108,8 +108,8 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
 }
 // All threads of the cluster's CTAs (a hardware barrier: they run together).
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 template <int D>
