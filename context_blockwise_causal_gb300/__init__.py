@@ -514,6 +514,8 @@ def _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, 
     if cu_seqlens is not None:
         if cu_seqlens.dtype is not _I32 or not cu_seqlens.is_contiguous():
             raise TypeError("cu_seqlens must be a contiguous int32 CUDA tensor")
+        if cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold nseq + 1 offsets, nseq >= 1")
         cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
     if positions is not None:
         if positions.dtype is not _I32:
@@ -728,8 +730,9 @@ def cpattn_bwd(q, k, v, o, lse, do, cp, causal=True, dq=None, dk=None, dv=None, 
 
 
 def _keys(n):
-    """A count of keys for the C call; any that int32 cannot hold is all of them."""
-    return n if n <= 0x7FFFFFFF else 0x7FFFFFFF
+    """A count of keys for the C call; any that int32 cannot hold is all of them
+    (and any negative one -1, which the call refuses)."""
+    return min(max(n, -1), 0x7FFFFFFF)
 
 
 def _window_dims(q, k, v):

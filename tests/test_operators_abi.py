@@ -185,3 +185,14 @@ def test_packed_structs_match_the_header():
     assert len(got) == ctypes.sizeof(Rotary)
     for name, _ in Rotary._fields_:
         assert getattr(Rotary.from_buffer_copy(got), name) == getattr(r, name), name
+
+
+def test_counts_and_offsets_that_the_call_cannot_take():
+    import context_blockwise_causal_gb300 as cp
+
+    # counts beyond int32 are every key, negative ones stay refusable
+    assert [cp._keys(n) for n in (0, 5, 1 << 40, -1, -(1 << 32) + 5)] == [0, 5, 0x7FFFFFFF, -1, -1]
+    # offsets without a sample are refused, not taken for no offsets
+    for n in (0, 1):
+        with pytest.raises(ValueError):
+            cp._rotary(1, 4, 64, 1e4, 1, None, None, torch.zeros(n, dtype=torch.int32), None, "half", None, None, 1.0)
