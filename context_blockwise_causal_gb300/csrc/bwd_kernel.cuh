@@ -258,7 +258,10 @@ __device__ __forceinline__ void zero16(uint32_t (&r)[16]) {
 
 // The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
 // to bf16 there too, as above, adds to the gradients' error (relative
-// L2 3.0e-3 against 2.5e-3, dK and dQ at a window of 300). A masked block zeroes P, and
+// L2 3.0e-3 against 2.5e-3, dK and dQ at a window of 300). Measured at b1
+// s32768 h32/8 d128 window 1024 with 4 first tokens: 792 us, the dK/dV kernel's
+// four products at 0.72 of the measured burst peak; its walks are 36 blocks,
+// 8 of them edges. A masked block zeroes P, and
 // dS = P (dP - D) with it, by testing query 8r + 2 c4 + j + c0 against the key
 // row's visible range [from, from + len) (an unsigned compare does both ends).
 template <bool kMasked>
@@ -1323,7 +1326,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // to one unit, so L*log2e and D are formed here, from the dO that passes
       // through the registers anyway, and written for the dK/dV kernel, which
       // runs after this one: no pass of its own over O and dO (95 us for one
-      // at b1 s32768 h32 d128).
+      // at b1 s32768 h32 d128). Measured there with h32/8, window 1024, 4 first
+      // tokens: 690 us, its three products at 0.62 of the measured burst peak.
       float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
       int rd = 0;
       auto take_unit = [&](WinUnit& U, int u) -> bool {
@@ -1468,8 +1472,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // One key tile; kEdge: one that the tile's rows do not see whole. Two
         // bodies, so that the ordinary one has no masks to hold, and the edge's
         // selects by one bit per key, which is cheaper than skipping its hidden
-        // pieces (644 against 664 us at b1 s32768 h32/8 window 1024: the
-        // branches spill).
+        // pieces (644 against 664 us at b1 s32768 h32/8 window 1024, with D
+        // still formed by a pass of its own: the branches spill).
         auto key_tile = [&](auto edge) -> bool {
           constexpr bool kEdge = decltype(edge)::value;
           if (!mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs)) return false;

@@ -25,6 +25,11 @@
 // 8 runs are the CTAs of one cluster, which read one another's results from
 // shared memory: one launch and no workspace. More runs (a few very long
 // sequences) go through device memory and a second kernel.
+//
+// Measured, d128: 64 sequences of up to 16384 tokens, h32/8, window 4096: 154
+// us; 16 of up to 65537, h64/8, whole: 447 to 488 us (both at the measured copy
+// bandwidth and a few percent above it, as reads alone may be); one sequence,
+// h32/8, window 1024: 6.9 us, a launch and three rounds of loads.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -54,7 +54,10 @@ constexpr float kRescaleThreshold = 0.0f;  // log2 units
 
 // The window form lets the running max lag by up to this much: its walks are
 // a few tiles long, where some row of a warp meets a new maximum in almost
-// every tile and the rescale's TMEM round trip would be paid each time.
+// every tile and the rescale's TMEM round trip would be paid each time (s16384
+// h64/8 window 4096: 1332 us with the lag, 1418 without; s32768 h32/8 window
+// 1024: 460 against 482). P then reaches 2^8 at most; rounding
+// P to bf16 is relative, so its error is the same, and the sums are fp32.
 constexpr float kWinRescaleThreshold = 8.0f;
 
 struct FwdArgs {
@@ -134,6 +137,13 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
 // rows that take no part in the step get O = 0, L = -inf.
 // kTP: units are tile pairs (a.g.tile_pairs), not head pairs.
 // kWin: sliding-window attention (win_schedule.cuh) instead of the CP steps.
+// Bound by the tensor cores and the exponentials beside them: 2 products of d
+// flops x 2 per visible pair, and whole tiles where a window's edges cut them
+// (9 tiles visited for 8 tiles' worth of keys at window 1024). Measured, d128
+// with 4 first tokens: 1283 us at s16384 h64/8 window 4096 (1500 TFLOP/s of
+// visible pairs, 0.79 of the measured burst peak), 460 us at s32768 h32/8
+// window 1024 (1180, 0.62: walks of 9 tiles, of which two have edges), 44 us
+// for four chunks of 333 queries over 8192 keys, h32/8 window 1024.
 // kShortWaits: the producer's waits for free buffers use a.producer_limit_ns
 // (the abort self-test) instead of the compile-time limit.
 template <bool kTP, bool kWin>

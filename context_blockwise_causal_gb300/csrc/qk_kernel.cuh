@@ -26,7 +26,10 @@
 // whatever the layout: cosines and sines are formed once per thread and token
 // and used for all of the warp's heads. A warp takes the heads of one token
 // (or, when tokens are few, some of them, so that single tokens spread over
-// the chip); rows of several tokens and heads are in flight at once.
+// the chip); rows of several tokens and heads are in flight at once. Measured
+// at 32K tokens, d128: rotation alone of 40 heads 103 us (0.97 of the measured
+// copy bandwidth), with the norms of 32 + 8 heads 105 us, the backward 160 us
+// (0.94); one token of 40 heads takes 2.6 us, a launch.
 #pragma once
 #include <cuda_bf16.h>
 

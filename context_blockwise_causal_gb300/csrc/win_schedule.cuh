@@ -11,8 +11,8 @@
 // tiles that hold visible first tokens, then the tiles its windows cover.
 // dK/dV units: a key tile visits the query tiles whose windows reach it; a
 // tile holding first tokens is seen by every later query, so its walk is cut
-// into parts of about two ordinary tiles' work, each a unit of its own, whose
-// fp32 results a second kernel adds in a fixed order.
+// into parts of about an ordinary tile's work, each a unit of its own, whose
+// fp32 results a second kernel adds in a fixed order (win_set_parts).
 //
 // Window units differ little in cost, so their order follows the data:
 // consecutive units are neighbouring tiles of one KV head, and the CTAs in

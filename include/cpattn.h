@@ -406,8 +406,8 @@ typedef struct cpattn_rotary {
 
 /*
  * y = x rotated by the plan ([b, n, h, d], d in {64, 128}); inverse != 0 turns
- * back (the gradient: dx from dy; the magnitude stays). Phases are exact to
- * far below fp32 at any int32 position. Errors: NULL_PTR, INVALID_ARG,
+ * back (the gradient: dx from dy; the magnitude stays). Phases are
+ * within fp32's own rounding at any int32 position. Errors: NULL_PTR, INVALID_ARG,
  * MISALIGNED, UNSUPPORTED_ARCH, LAUNCH_FAILED.
  */
 int cpattn_rope_ex(const cpattn_rows* x, const cpattn_rows* y, int b, int n, int h, int d,
@@ -455,7 +455,7 @@ int cpattn_qk_norm_rope_bwd(const cpattn_rows* q, const cpattn_rows* k, const vo
  * non-finite row of v (in the backward of q, k, v or dout) can reach rows up to
  * 127 positions from those that see it, and at a sequence's ragged end those
  * of the sequence before it. (Non-finite scores alone are masked: k in the
- * forward.)
+ * forward.) Outputs must not overlap inputs.
  */
 int cpattn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int b, int sq, int skv, int hq,
                       int hkv, int d, int window, int sinks, float scale, void* stream);
