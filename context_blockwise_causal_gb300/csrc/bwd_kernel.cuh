@@ -1705,59 +1705,77 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ================================================================ window form
 // dK and dV of the key tiles whose walks were cut (win_schedule.cuh): the
 // parts' fp32 results added in a fixed order, dK scaled, rounded once to bf16.
-// A CTA takes a key row, its warps every eighth part; rows past the first
-// tokens have one or two parts, so this kernel reads little and is bound by
-// its launch and one round of loads (a warp per row, parts one after another:
-// 13 us for 29 parts).
+// First tokens have a row in every part: a CTA each, its warps every eighth
+// part. Rows past them have one or two: a warp each. This kernel reads little
+// and is bound by its launch and one round of loads (first tokens by a warp
+// each, part after part: 13 us for 29 parts; every row by a CTA: 9 us for
+// seven packed samples of 8 heads).
+constexpr int kJoinWarps = 8;
+// CTAs per cut tile: one per first token, then the other rows eight at a time.
+__host__ __device__ inline int win_join_ctas(const CpGeom& g) {
+  return (g.sinks < kTile ? g.sinks : kTile) + kTile / kJoinWarps;
+}
 template <int D>
-__global__ void __launch_bounds__(256) cpattn_window_join_kernel(const BwdArgs a) {
-  constexpr int kWarps = 8, kPer = D / 32;  // features per lane
-  __shared__ float red[2][kWarps][D];
+__global__ void __launch_bounds__(kJoinWarps * 32) cpattn_window_join_kernel(const BwdArgs a) {
+  constexpr int kPer = D / 32;  // features per lane
+  __shared__ float red[2][kJoinWarps][D];
   const CpGeom& g = a.g;
-  const int cut = win_cut_tiles(g);
+  const int cut = win_cut_tiles(g), per = win_join_ctas(g), firsts = per - kTile / kJoinWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int x = blockIdx.x / kTile, jr = blockIdx.x % kTile;
+  const int x = blockIdx.x / per, i = blockIdx.x - x * per;
   const int y = g.fd_cut.div(x), kt = x - y * cut;
   const int seq = g.fd_hkv.div(y), h = y - seq * g.hkv;
   const WinSeq s = win_seq(g, seq);
-  if (kt * kTile + jr >= s.klen) return;
+  const bool whole = i < firsts;  // a row of the CTA's own
+  const int jr = whole ? i : (i - firsts) * kJoinWarps + warp;
+  if ((kt * kTile + jr < g.sinks) != whole || kt * kTile + jr >= s.klen) return;  // the whole CTA, or this warp
   int qa, nq;
   win_query_tiles(g, s, kt, qa, nq);
   const int np = win_parts(g, nq);
-  const bool first = kt * kTile + jr < g.sinks;  // in every part; other rows only in those that the windows reach
   float sk[kPer], sv[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sk[i] = sv[i] = 0.f;
+  for (int e = 0; e < kPer; ++e) sk[e] = sv[e] = 0.f;
+  const int step = whole ? kJoinWarps : 1;
 #pragma unroll 4
-  for (int p = warp; p < np; p += kWarps) {
-    if (!first && win_part_rows(g, s, kt, qa + p * g.part_tiles) < kTile) break;
+  for (int p = whole ? warp : 0; p < np; p += step) {
+    // rows past the first tokens only have a result in parts that the windows reach
+    if (!whole && win_part_rows(g, s, kt, qa + p * g.part_tiles) < kTile) break;
     const int64_t po = ((int64_t(x) * g.sink_parts + p) * kTile + jr) * D + lane * kPer;
     if (!bounds_ok(po + kPer <= a.part_len, a.status)) break;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      sk[i] += a.part_dk[po + i];
-      sv[i] += a.part_dv[po + i];
+    for (int e = 0; e < kPer; ++e) {
+      sk[e] += a.part_dk[po + e];
+      sv[e] += a.part_dv[po + e];
     }
   }
+  const int krow = s.kv0 + kt * kTile + jr;
+  const int64_t out = (int64_t(krow) * g.hkv + h) * D;
+  if (!whole) {
+    if (!bounds_ok(krow < a.kv_rows && h < g.hkv, a.status)) return;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    red[0][warp][lane * kPer + i] = sk[i];
-    red[1][warp][lane * kPer + i] = sv[i];
+    for (int e = 0; e < kPer; e += 2) {
+      *reinterpret_cast<uint32_t*>(a.dk + out + lane * kPer + e) = pack_bf16x2(sk[e] * a.scale, sk[e + 1] * a.scale);
+      *reinterpret_cast<uint32_t*>(a.dv + out + lane * kPer + e) = pack_bf16x2(sv[e], sv[e + 1]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    red[0][warp][lane * kPer + e] = sk[e];
+    red[1][warp][lane * kPer + e] = sv[e];
   }
   __syncthreads();
-  const int krow = s.kv0 + kt * kTile + jr;
   if (!bounds_ok(krow < a.kv_rows && h < g.hkv, a.status)) return;
   const int which = threadIdx.x / (D / 2), c = (threadIdx.x % (D / 2)) * 2;  // two features of dK or dV
   if (which < 2) {
     float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       v0 += red[which][w][c];
       v1 += red[which][w][c + 1];
     }
     const float f = which == 0 ? a.scale : 1.f;
-    *reinterpret_cast<uint32_t*>((which == 0 ? a.dk : a.dv) + (int64_t(krow) * g.hkv + h) * D + c) =
-        pack_bf16x2(v0 * f, v1 * f);
+    *reinterpret_cast<uint32_t*>((which == 0 ? a.dk : a.dv) + out + c) = pack_bf16x2(v0 * f, v1 * f);
   }
 }
 

@@ -145,8 +145,8 @@ int launch_bwd(const CUtensorMap* maps, const BwdArgs& args, DeviceInfo* di, cud
                                                                                        maps[3], args);
   dkdv<<<persistent_grid(di, win_dkdv_units(g)), kBwdThreads, DkdvCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
                                                                                             maps[3], args);
-  const int64_t rows_cut = int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g) * kTile;
-  if (rows_cut > 0) cpattn_window_join_kernel<D><<<int(rows_cut), 256, 0, st>>>(args);
+  const int64_t cut = int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g);
+  if (cut > 0) cpattn_window_join_kernel<D><<<int(cut * win_join_ctas(g)), kJoinWarps * 32, 0, st>>>(args);
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
 }
 
