@@ -9,13 +9,12 @@ library has not been built the calls raise.
 """
 import array
 import ctypes
-import functools
 import os
 import struct
 
 import torch
 
-from ._build import CHECKED_LIB_PATH, LIB_PATH, build  # noqa: F401
+from ._build import BINDING_PATH, CHECKED_LIB_PATH, LIB_PATH, build  # noqa: F401
 
 __all__ = [
     "CpattnError",
@@ -75,18 +74,12 @@ _i, _p, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
 _f, _i64 = ctypes.c_float, ctypes.c_int64
 
 
-# cpattn_rows (data, batch_stride, token_stride) and cpattn_rotary (layout,
-# rot_dim, magnitude, s, cp, rank, cu_seqlens, nseq, positions,
-# positions_batch, inv_freq) as the bytes of the C structs: packing them costs
-# a fraction of building ctypes structures, which counts in calls that run for
-# a few microseconds.
-_ROWS = struct.Struct("@Pqq").pack
-_PLAN = struct.Struct("@iifiiiPiPqP").pack
-# The current device and a device's current stream without the Python objects
-# around them, for the same reason.
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_BF16, _F32, _I32, _F64 = torch.bfloat16, torch.float32, torch.int32, torch.float64
+# The functions that the native half of the binding (csrc/binding.cpp) calls,
+# in its order.
+_CALLS = ("cpattn_rope_frequencies", "cpattn_rope_ex", "cpattn_qk_norm_rope", "cpattn_qk_norm_rope_bwd_workspace_bytes",
+          "cpattn_qk_norm_rope_bwd", "cpattn_fwd_window", "cpattn_bwd_window_workspace_bytes", "cpattn_bwd_window",
+          "cpattn_fwd_window_varlen", "cpattn_bwd_window_varlen_workspace_bytes", "cpattn_bwd_window_varlen",
+          "cpattn_decode_workspace_bytes", "cpattn_decode")
 
 
 _CHECKED = None
@@ -100,6 +93,21 @@ def library():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with context_blockwise_causal_gb300.build()")
         _LIB = _declare(ctypes.CDLL(LIB_PATH))
     return _LIB
+
+
+_BINDING = None
+
+
+def _native():
+    """The native half of the binding (once). Raises if it has not been built."""
+    global _BINDING
+    if _BINDING is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with context_blockwise_causal_gb300.build()")
+        from . import _binding as module
+
+        _BINDING = module
+    return _BINDING
 
 
 def checked_library():
@@ -203,6 +211,7 @@ def _declare(lib):
     lib.cpattn_checked_build.restype = _i
     lib.cpattn_selftest_bounds.argtypes = [_p] * 5 + [_i] * 6 + [_p]
     lib.cpattn_selftest_bounds.restype = _i
+    lib.calls = struct.pack(f"@{len(_CALLS)}P", *(ctypes.cast(getattr(lib, n), _p).value for n in _CALLS))
     return lib
 
 
@@ -384,8 +393,9 @@ def cpattn_rope(x, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None, inver
     """
     if (positions is not None or layout != "half" or rot_dim is not None or inv_freq is not None or magnitude != 1.0 or
             out is not None):
-        return _rope_ex(x, base, cp, rank, s, cu_seqlens, inverse, stream, positions, layout, rot_dim, inv_freq,
-                        magnitude, x if out is None else out)
+        return _done("cpattn_rope_ex", _native().rope(
+            library().calls, x, x if out is None else out, base, cp, rank, s, cu_seqlens, positions,
+            _ROPE_LAYOUTS.get(layout), rot_dim, inv_freq, magnitude, 1 if inverse else 0, stream))
     _check_act("x", x)
     if x.dim() != 4:
         raise ValueError("x must be [b, n, h, d]")
@@ -427,133 +437,12 @@ def cpattn_rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, ori
     return out
 
 
-def _on(stream, *tensors):
-    """The stream to launch on (the current one by default), as a handle; every
-    tensor given must be on the current device, and so must the stream."""
-    cur = _device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:
-            if not t.is_cuda:
-                raise TypeError("every tensor must be a CUDA tensor")
-            raise ValueError(f"a tensor is on {t.device} but the current CUDA device is cuda:{cur}; "
-                             f"call under torch.cuda.device({t.device})")
-    if stream is None:
-        return _raw_stream(cur)
-    if stream.device.index != cur:
-        raise ValueError(f"the stream belongs to {stream.device}, the current CUDA device is cuda:{cur}")
-    return stream.cuda_stream
-
-
-def _empty(shape, like, stream, dtype=_BF16):
-    """A new tensor beside ``like``, from the memory of the stream that the
-    call runs on: the caching allocator then hands it to nobody else before
-    that stream is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _out_rows(name, t, b, n, h, d, like, stream):
-    """An output [b, n, h, d], given or new, and its cpattn_rows."""
-    if t is not None:
-        return t, _rows(name, t, (b, n, h, d))
-    t = _empty((b, n, h, d), like, stream)
-    return t, _ROWS(t.data_ptr(), n * h * d, h * d)
-
-
-def _out(name, t, shape, like, stream, dtype=_BF16):
-    """An output of a shape, given or new, and its address."""
-    if t is not None:
-        return t, _dense(name, t, dtype, shape)
-    t = _empty(shape, like, stream, dtype)
-    return t, t.data_ptr()
-
-
-def _dense(name, t, dtype, shape):
-    """A contiguous tensor of a type and shape, beside ``_on``'s checks."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
-        raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows(name, t, shape=None):
-    """cpattn_rows of a bf16 tensor [b, n, h, d] with contiguous heads. A
-    stride of a dimension of one element means nothing and is not passed on."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16:
-        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must be [b, n, h, d]")
-    b, n, h, d = t.shape
-    sb, sn, sh, sd = t.stride()
-    if sd != 1 or (h > 1 and sh != d):
-        raise ValueError(f"{name} must have contiguous heads and features")
-    return _ROWS(t.data_ptr(), sb if b > 1 else 0, sn if n > 1 else h * d)
-
-
-def _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude):
-    """cpattn_rotary for b x n tokens, and inv_freq, which must outlive it."""
-    if layout not in _ROPE_LAYOUTS:
-        raise ValueError(f"layout must be one of {list(_ROPE_LAYOUTS)}")
-    if inv_freq is None:
-        inv_freq = cpattn_rope_frequencies(d if rot_dim is None else rot_dim, base)
-    elif inv_freq.dtype is not _F64 or inv_freq.is_cuda or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-        raise TypeError("inv_freq must be a contiguous fp64 host vector")
-    pairs = inv_freq.shape[0]
-    if rot_dim is not None and 2 * pairs != rot_dim:
-        raise ValueError(f"inv_freq has {pairs} values, rot_dim {rot_dim} needs {rot_dim // 2}")
-    if s is None:
-        s = n if rank is None else n * int(cp)
-    cu = nseq = pos = pos_batch = 0
-    if cu_seqlens is not None:
-        if cu_seqlens.dtype is not _I32 or not cu_seqlens.is_contiguous():
-            raise TypeError("cu_seqlens must be a contiguous int32 CUDA tensor")
-        if cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must hold nseq + 1 offsets, nseq >= 1")
-        cu, nseq = cu_seqlens.data_ptr(), cu_seqlens.numel() - 1
-    if positions is not None:
-        if positions.dtype is not _I32:
-            raise TypeError("positions must be an int32 CUDA tensor")
-        if positions.shape != (n,) and positions.shape != (b, n):
-            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(n,)} or {(b, n)}")
-        if n > 1 and positions.stride(-1) != 1:
-            raise ValueError("the positions of a sequence must be contiguous")
-        pos = positions.data_ptr()
-        pos_batch = positions.stride(0) if positions.dim() == 2 and b > 1 else 0
-    return _PLAN(_ROPE_LAYOUTS[layout], 2 * pairs, magnitude, s, cp, -1 if rank is None else rank, cu, nseq, pos,
-                 pos_batch, inv_freq.data_ptr()), inv_freq
-
-
-def _rope_ex(x, base, cp, rank, s, cu_seqlens, inverse, stream, positions, layout, rot_dim, inv_freq, magnitude, out):
-    xr = _rows("x", x)
-    outr = xr if out is x else _rows("out", out, x.shape)
-    b, n, h, d = x.shape
-    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
-    rc = library().cpattn_rope_ex(xr, outr, b, n, h, d, plan, 1 if inverse else 0,
-                                  _on(stream, x, out, cu_seqlens, positions))
-    if rc:
-        raise CpattnError(rc, "cpattn_rope_ex")
-    return out
-
-
-def _qk(q, k, q_weight, k_weight):
-    """Rows of q and k, weights and sizes of a q/k norm call."""
-    qr, kr = _rows("q", q), _rows("k", k)
-    b, n, hq, d = q.shape
-    hkv = k.shape[2]
-    if k.shape != (b, n, hkv, d):
-        raise ValueError("k must be [b, n, hkv, d] matching q")
-    wt = q_weight.dtype
-    if wt is not _F32 and wt is not _BF16:
-        raise TypeError("q_weight and k_weight must be bf16 or fp32 CUDA tensors")
-    return (qr, kr, _dense("q_weight", q_weight, wt, (d,)), _dense("k_weight", k_weight, wt, (d,)),
-            1 if wt is _F32 else 0), b, n, hq, hkv, d
+def _done(name, result):
+    """The result of a call of the native binding, which is an int when the
+    library returned an error code."""
+    if type(result) is int:
+        raise CpattnError(result, name)
+    return result
 
 
 def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, rank=None, s=None, cu_seqlens=None,
@@ -565,15 +454,9 @@ def cpattn_qk_norm_rope(q, k, q_weight, k_weight, eps=1e-6, base=10000.0, cp=1, 
     q, k and the outputs are bf16 and may be strided (e.g. parts of a fused
     projection); an output may be its input. Positions and rotation as for
     cpattn_rope. Returns (q_out, k_out), allocated contiguous when not given."""
-    ins, b, n, hq, hkv, d = _qk(q, k, q_weight, k_weight)
-    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
-    handle = _on(stream, q, k, q_weight, k_weight, q_out, k_out, cu_seqlens, positions)
-    q_out, qo = _out_rows("q_out", q_out, b, n, hq, d, q, stream)
-    k_out, ko = _out_rows("k_out", k_out, b, n, hkv, d, k, stream)
-    rc = library().cpattn_qk_norm_rope(*ins, eps, qo, ko, b, n, hq, hkv, d, plan, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_qk_norm_rope")
-    return q_out, k_out
+    return _done("cpattn_qk_norm_rope", _native().qk_norm_rope(
+        library().calls, q, k, q_weight, k_weight, eps, base, cp, rank, s, cu_seqlens, positions,
+        _ROPE_LAYOUTS.get(layout), rot_dim, inv_freq, magnitude, q_out, k_out, stream))
 
 
 def cpattn_qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, eps=1e-6, base=10000.0, cp=1, rank=None, s=None,
@@ -582,43 +465,9 @@ def cpattn_qk_norm_rope_bwd(q, k, q_weight, k_weight, dq_out, dk_out, eps=1e-6, 
     """Backward of cpattn_qk_norm_rope from its inputs q, k and the gradients
     of its outputs. Returns (dq, dk, dq_weight, dk_weight); the weights'
     gradients are fp32 [d], written (not accumulated)."""
-    ins, b, n, hq, hkv, d = _qk(q, k, q_weight, k_weight)
-    plan, freq = _rotary(b, n, d, base, cp, rank, s, cu_seqlens, positions, layout, rot_dim, inv_freq, magnitude)
-    handle = _on(stream, q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight, workspace, cu_seqlens,
-                 positions)
-    gq, gk = _rows("dq_out", dq_out, q.shape), _rows("dk_out", dk_out, k.shape)
-    dq, rq = _out_rows("dq", dq, b, n, hq, d, q, stream)
-    dk, rk = _out_rows("dk", dk, b, n, hkv, d, k, stream)
-    dq_weight, wq = _out("dq_weight", dq_weight, (d,), q, stream, _F32)
-    dk_weight, wk = _out("dk_weight", dk_weight, (d,), q, stream, _F32)
-    ws, ws_bytes, workspace = _workspace(workspace, _qk_bwd_bytes(d), q, stream)
-    rc = library().cpattn_qk_norm_rope_bwd(*ins, eps, gq, gk, rq, rk, wq, wk, ws, ws_bytes, b, n, hq, hkv, d, plan,
-                                           handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_qk_norm_rope_bwd")
-    return dq, dk, dq_weight, dk_weight
-
-
-# Workspace sizes by shape alone (and device, where it matters).
-@functools.lru_cache(maxsize=64)
-def _qk_bwd_bytes(d):
-    return int(library().cpattn_qk_norm_rope_bwd_workspace_bytes(d))
-
-
-@functools.lru_cache(maxsize=1024)
-def _decode_bytes(device, *shape):
-    return int(library().cpattn_decode_workspace_bytes(*shape))
-
-
-def _workspace(workspace, need, like, stream):
-    """Pointer and bytes of the workspace given, or of a new one."""
-    if workspace is None:
-        need = need if need > 16 else 16
-        workspace = _empty((need,), like, stream, torch.uint8)
-        return workspace.data_ptr(), need, workspace
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    return _done("cpattn_qk_norm_rope_bwd", _native().qk_norm_rope_bwd(
+        library().calls, q, k, q_weight, k_weight, dq_out, dk_out, eps, base, cp, rank, s, cu_seqlens, positions,
+        _ROPE_LAYOUTS.get(layout), rot_dim, inv_freq, magnitude, dq, dk, dq_weight, dk_weight, workspace, stream))
 
 
 def _cu_host(cu_seqlens):
@@ -735,16 +584,9 @@ def _keys(n):
     return min(max(n, -1), 0x7FFFFFFF)
 
 
-def _window_dims(q, k, v):
-    """Pointers and sizes b, sq, skv, hq, hkv, d of a window call."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q must be [b, sq, hq, d] and k, v [b, skv, hkv, d]")
-    b, sq, hq, d = q.shape
-    skv, hkv = k.shape[1], k.shape[2]
-    kv = (b, skv, hkv, d)
-    if k.shape != kv:
-        raise ValueError("q must be [b, sq, hq, d] and k, v [b, skv, hkv, d]")
-    return (_dense("q", q, _BF16, q.shape), _dense("k", k, _BF16, kv), _dense("v", v, _BF16, kv)), b, sq, skv, hq, hkv, d
+def _offsets(cu_seqlens):
+    """Sample offsets of a packed window call, as an int32 buffer."""
+    return array.array("i", cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
 
 
 def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, stream=None):
@@ -753,15 +595,7 @@ def cpattn_fwd_window(q, k, v, window, sinks=0, scale=None, o=None, lse=None, st
     The query at position p sees key j when j <= p and p - j < window or
     j < sinks. q [b, sq, hq, d]; k, v [b, skv, hkv, d] with skv >= sq: the
     queries are the last sq positions. Returns (o like q, lse [b, hq, sq])."""
-    ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
-    handle = _on(stream, q, k, v, o, lse)
-    o, po = _out("o", o, (b, sq, hq, d), q, stream)
-    lse, pl = _out("lse", lse, (b, hq, sq), q, stream, _F32)
-    rc = library().cpattn_fwd_window(*ins, po, pl, b, sq, skv, hq, hkv, d, _keys(window), _keys(sinks),
-                                     0.0 if scale is None else scale, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_fwd_window")
-    return o, lse
+    return _done("cpattn_fwd_window", _native().fwd_window(library().calls, q, k, v, window, sinks, scale, o, lse, stream))
 
 
 def cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks=0):
@@ -771,67 +605,23 @@ def cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, window, sinks=0):
 def cpattn_bwd_window(q, k, v, o, lse, do, window, sinks=0, scale=None, dq=None, dk=None, dv=None, workspace=None,
                       stream=None):
     """Backward of cpattn_fwd_window from its o and lse. Returns (dq, dk, dv)."""
-    ins, b, sq, skv, hq, hkv, d = _window_dims(q, k, v)
-    handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
-    dq, gq = _out("dq", dq, (b, sq, hq, d), q, stream)
-    dk, gk = _out("dk", dk, (b, skv, hkv, d), q, stream)
-    dv, gv = _out("dv", dv, (b, skv, hkv, d), q, stream)
-    lib = library()
-    need = lib.cpattn_bwd_window_workspace_bytes(b, sq, skv, hq, hkv, d, _keys(window), _keys(sinks))
-    ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
-    rc = lib.cpattn_bwd_window(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (b, hq, sq)),
-                               _dense("do", do, _BF16, q.shape), gq, gk, gv, ws, ws_bytes, b, sq, skv, hq, hkv, d,
-                               _keys(window), _keys(sinks), 0.0 if scale is None else scale, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_bwd_window")
-    return dq, dk, dv
-
-
-def _packed_window(q, k, v, cu_seqlens):
-    """Pointers, offsets (an int32 buffer) and sizes of a packed window call."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("packed q must be [total, hq, d] and k, v [total, hkv, d]")
-    total, hq, d = q.shape
-    hkv = k.shape[1]
-    kv = (total, hkv, d)
-    cu = array.array("i", cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else cu_seqlens)
-    if not cu or cu[-1] != total:
-        raise ValueError("cu_seqlens must end at the packed length")
-    return (_dense("q", q, _BF16, q.shape), _dense("k", k, _BF16, kv), _dense("v", v, _BF16, kv)), cu, total, hq, hkv, d
+    return _done("cpattn_bwd_window", _native().bwd_window(
+        library().calls, q, k, v, o, lse, do, window, sinks, scale, dq, dk, dv, workspace, stream))
 
 
 def cpattn_fwd_window_varlen(q, k, v, cu_seqlens, window, sinks=0, scale=None, o=None, lse=None, stream=None):
     """cpattn_fwd_window over packed samples, each with its own window and
     first tokens. q [total, hq, d], k/v [total, hkv, d]; cu_seqlens: sample
     offsets (host list/tensor). Returns (o [total, hq, d], lse [hq, total])."""
-    ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
-    handle = _on(stream, q, k, v, o, lse)
-    o, po = _out("o", o, (total, hq, d), q, stream)
-    lse, pl = _out("lse", lse, (hq, total), q, stream, _F32)
-    rc = library().cpattn_fwd_window_varlen(*ins, po, pl, cu.buffer_info()[0], len(cu) - 1, hq, hkv, d, _keys(window),
-                                            _keys(sinks), 0.0 if scale is None else scale, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_fwd_window_varlen")
-    return o, lse
+    return _done("cpattn_fwd_window_varlen", _native().fwd_window_varlen(
+        library().calls, q, k, v, _offsets(cu_seqlens), window, sinks, scale, o, lse, stream))
 
 
 def cpattn_bwd_window_varlen(q, k, v, o, lse, do, cu_seqlens, window, sinks=0, scale=None, dq=None, dk=None, dv=None,
                              workspace=None, stream=None):
     """Backward of cpattn_fwd_window_varlen. Returns (dq, dk, dv)."""
-    ins, cu, total, hq, hkv, d = _packed_window(q, k, v, cu_seqlens)
-    handle = _on(stream, q, k, v, o, lse, do, dq, dk, dv, workspace)
-    dq, gq = _out("dq", dq, (total, hq, d), q, stream)
-    dk, gk = _out("dk", dk, (total, hkv, d), q, stream)
-    dv, gv = _out("dv", dv, (total, hkv, d), q, stream)
-    lib, cu_p, nseq = library(), cu.buffer_info()[0], len(cu) - 1
-    need = lib.cpattn_bwd_window_varlen_workspace_bytes(cu_p, nseq, hq, hkv, d, _keys(window), _keys(sinks))
-    ws, ws_bytes, workspace = _workspace(workspace, need, q, stream)
-    rc = lib.cpattn_bwd_window_varlen(*ins, _dense("o", o, _BF16, q.shape), _dense("lse", lse, _F32, (hq, total)),
-                                      _dense("do", do, _BF16, q.shape), gq, gk, gv, ws, ws_bytes, cu_p, nseq, hq, hkv, d,
-                                      _keys(window), _keys(sinks), 0.0 if scale is None else scale, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_bwd_window_varlen")
-    return dq, dk, dv
+    return _done("cpattn_bwd_window_varlen", _native().bwd_window_varlen(
+        library().calls, q, k, v, o, lse, do, _offsets(cu_seqlens), window, sinks, scale, dq, dk, dv, workspace, stream))
 
 
 def cpattn_decode_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
@@ -848,39 +638,8 @@ def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o
     CUDA tensor [b]: tokens held of each sequence, the new one's key and value
     among them. window 0: every key; otherwise the last ``window`` keys and
     the first ``sinks``. Returns (o [b, hq, d], lse [b, hq])."""
-    if q.dtype is not _BF16 or k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16:
-        raise TypeError("q, k_cache and v_cache must be bfloat16 CUDA tensors")
-    if q.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("q must be [b, hq, d] and k_cache, v_cache [b, cap, hkv, d]")
-    b, hq, d = q.shape
-    _, cap, hkv, _ = k_cache.shape
-    if k_cache.shape != (b, cap, hkv, d) or v_cache.shape != (b, cap, hkv, d):
-        raise ValueError("k_cache and v_cache must be [b, cap, hkv, d] matching q")
-    qb, qh, q1 = q.stride()
-    kb, kt, kh, k1 = k_cache.stride()
-    vb, vt, vh, v1 = v_cache.stride()
-    if q1 != 1 or k1 != 1 or v1 != 1 or (hq > 1 and qh != d):
-        raise ValueError("q's heads and the features of q and of the cache must be contiguous")
-    # a stride of a dimension of one element means nothing
-    if b == 1:
-        qb = kb = vb = 0
-    if cap == 1:
-        kt = vt = 0
-    if hkv == 1:
-        kh = vh = 0
-    ln = _dense("lengths", lengths, _I32, (b,))
-    handle = _on(stream, q, k_cache, v_cache, lengths, o, lse, workspace)
-    o, po = _out("o", o, (b, hq, d), q, stream)
-    lse, pl = _out("lse", lse, (b, hq), q, stream, _F32)
-    window, sinks = _keys(window), _keys(sinks)
-    need = _decode_bytes(_device(), b, hq, hkv, d, cap, window, sinks)
-    ws, ws_bytes, workspace = (None, 0, None) if need == 0 else _workspace(workspace, need, q, stream)
-    rc = library().cpattn_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ln,
-                                 po, pl, ws, ws_bytes, b, hq, hkv, d, cap, qb, kb, kt, kh, vb, vt, vh, window, sinks,
-                                 0.0 if scale is None else scale, handle)
-    if rc:
-        raise CpattnError(rc, "cpattn_decode")
-    return o, lse
+    return _done("cpattn_decode", _native().decode(library().calls, q, k_cache, v_cache, lengths, window, sinks, scale,
+                                                    o, lse, workspace, stream))
 
 
 def _rank_dims(q, k, v, cp):

@@ -2,6 +2,8 @@
 attention, rotary and q/k norm calls: argument errors come before any device
 work (the pointers are never followed), sizes of workspaces, frequencies."""
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -174,25 +176,37 @@ def test_frequencies(lib):
         assert f(*bad, out) == ARG, bad
 
 
-def test_packed_structs_match_the_header():
-    """The binding packs cpattn_rows and cpattn_rotary as bytes: the same
-    layout as the C structs (checked against ctypes', field by field)."""
-    import context_blockwise_causal_gb300 as pkg
-
-    assert bytes(Rows(4096, 5, 6)) == pkg._ROWS(4096, 5, 6)
-    r = Rotary(1, 64, 1.5, 7, 2, -1, 4096, 3, 8192, 9, 12288)
-    got = pkg._PLAN(1, 64, 1.5, 7, 2, -1, 4096, 3, 8192, 9, 12288)
-    assert len(got) == ctypes.sizeof(Rotary)
-    for name, _ in Rotary._fields_:
-        assert getattr(Rotary.from_buffer_copy(got), name) == getattr(r, name), name
-
-
-def test_counts_and_offsets_that_the_call_cannot_take():
+def test_counts_that_the_call_cannot_take(lib):
     import context_blockwise_causal_gb300 as cp
 
     # counts beyond int32 are every key, negative ones stay refusable
     assert [cp._keys(n) for n in (0, 5, 1 << 40, -1, -(1 << 32) + 5)] == [0, 5, 0x7FFFFFFF, -1, -1]
-    # offsets without a sample are refused, not taken for no offsets
-    for n in (0, 1):
-        with pytest.raises(ValueError):
-            cp._rotary(1, 4, 64, 1e4, 1, None, None, torch.zeros(n, dtype=torch.int32), None, "half", None, None, 1.0)
+
+
+def test_binding_refuses_before_it_needs_a_device(lib):
+    import context_blockwise_causal_gb300 as cp
+
+    x, w = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.ones(64)
+    q, ln = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.ones(1, dtype=torch.int32)
+    for call in (lambda: cp.cpattn_rope(x, layout="interleaved"), lambda: cp.cpattn_rope(x.half(), rot_dim=32),
+                 lambda: cp.cpattn_rope(None, rot_dim=32), lambda: cp.cpattn_qk_norm_rope(x, x, w, w),
+                 lambda: cp.cpattn_qk_norm_rope_bwd(x, x, w, w, x, x), lambda: cp.cpattn_fwd_window(x, x, x, 4),
+                 lambda: cp.cpattn_fwd_window(x.half(), x, x, 4), lambda: cp.cpattn_fwd_window(5, x, x, 4),
+                 lambda: cp.cpattn_bwd_window(x, x, x, x, w, x, 4), lambda: cp.cpattn_decode(q, x, x, ln),
+                 lambda: cp.cpattn_decode(q, x, x, None), lambda: cp.cpattn_fwd_window_varlen(x[0], x[0], x[0], [0, 4], 4)):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        cp.cpattn_fwd_window(x[0], x, x, 4)
+    # the table of functions is checked, and so is the number of arguments
+    for bad in ((), (b"",), (cp.library().calls,), (cp.library().calls, x)):
+        with pytest.raises((SystemError, TypeError)):
+            cp._native().rope(*bad)
+
+
+def test_binding_table_names_the_structure_of_the_source():
+    import context_blockwise_causal_gb300 as cp
+
+    src = open(os.path.join(os.path.dirname(cp.__file__), "csrc", "binding.cpp")).read()
+    body = src[src.index("struct Calls {"):]
+    assert tuple(re.findall(r"decltype\(&(\w+)\)", body[:body.index("};")])) == cp._CALLS

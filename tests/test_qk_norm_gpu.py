@@ -353,3 +353,44 @@ def test_refusals():
             cpattn_rope_frequencies(64, **kw)
     with pytest.raises(ValueError):
         cpattn_rope_frequencies(64, scaling="other")
+
+
+def test_refusals_of_offsets_and_of_sizes_beyond_int32():
+    x = torch.zeros(1, 8, 3, 64, dtype=torch.bfloat16, device="cuda")
+    for n in (0, 1):
+        with pytest.raises(ValueError):  # offsets without a sample, not taken for none
+            cpattn_rope(x, rot_dim=32, cu_seqlens=torch.zeros(n, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        cpattn_rope(x, rot_dim=32, rank=0, cp=1 << 20, s=1 << 40)
+    with pytest.raises(ValueError):
+        cpattn_rope(x, rot_dim=32, rank=0, cp=1 << 30)  # s = n cp
+    with pytest.raises(pkg.CpattnError):
+        cpattn_rope(x[:, :1].expand(1, (1 << 32) + 1, 3, 64), rot_dim=32)
+    with pytest.raises(TypeError):
+        cpattn_rope(x, rot_dim=32, positions=[0] * 8)
+    with pytest.raises(TypeError):
+        cpattn_rope(x, rot_dim=32.5)
+    with pytest.raises(AttributeError):
+        cpattn_rope(x, rot_dim=32, stream=7)
+    assert torch.equal(x, torch.zeros_like(x))
+
+
+def test_given_outputs_are_returned_and_new_ones_are_kept_apart():
+    x = torch.randn(2, 5, 3, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    out = torch.empty_like(x)
+    q, k = cpattn_qk_norm_rope(x, x, w, w, q_out=out)
+    assert q is out and k is not out and torch.equal(q, k)
+    assert k.is_contiguous() and not k.requires_grad and k.data_ptr() != q.data_ptr()
+    assert cpattn_rope(x, rot_dim=32) is x
+    grads = cpattn_qk_norm_rope_bwd(x, x, w, w, x, x)
+    assert len({t.data_ptr() for t in grads}) == 4 and torch.equal(grads[0], grads[1])
+    with torch.cuda.stream(torch.cuda.Stream()):
+        s = torch.cuda.Stream()
+        before = torch.cuda.current_stream()
+        cpattn_qk_norm_rope(x, x, w, w, stream=s)
+        assert torch.cuda.current_stream() == before
+        with pytest.raises(pkg.CpattnError):
+            cpattn_qk_norm_rope(x, x, w, w, eps=-1.0, stream=s)
+        assert torch.cuda.current_stream() == before
+        s.synchronize()
