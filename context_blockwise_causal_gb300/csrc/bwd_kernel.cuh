@@ -1005,8 +1005,8 @@ struct DqCfg {
   static constexpr int kOffKV = kOffdO + kTileBytes;
   static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
   // q_full q_empty qa_full qa_empty s_full s_free dp_full p_full dq_full
-  // dq_empty drain, kv_full[] kv_empty[], p_half, d_full (window form)
-  static constexpr int kNumBars = 13 + 2 * kSlots;
+  // dq_empty drain, kv_full[] kv_empty[], p_half, d_full d_sole (window form)
+  static constexpr int kNumBars = 14 + 2 * kSlots;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRed = kOffMisc + 16;  // window form: each half-row's part of D, two units'
   static constexpr int kLayoutBytes = kOffRed + 4 * kTile * 4;
@@ -1081,6 +1081,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint64_t* kv_empty = bars + 11 + C::kSlots;
   uint64_t* p_half = bars + 11 + 2 * C::kSlots;
   uint64_t* d_full = bars + 12 + 2 * C::kSlots;
+  uint64_t* d_sole = bars + 13 + 2 * C::kSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
 
@@ -1105,6 +1106,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(drain, 1);
     mbar_init(p_half, 8);
     mbar_init(d_full, 8);
+    mbar_init(d_sole, 8);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
@@ -1329,7 +1331,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // at b1 s32768 h32 d128). Measured there with h32/8, window 1024, 4 first
       // tokens: 690 us, its three products at 0.62 of the measured burst peak.
       float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
-      int rd = 0;
+      int rd = 0, sole = 0;
       auto take_unit = [&](WinUnit& U, int u) -> bool {
         const int idx = snake_unit(rd, blockIdx.x, grid);
         if (idx >= num_units) return false;
@@ -1410,6 +1412,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             a.dvec[pos] = dd;
           }
         }
+        return true;
+      };
+      // Where one key tile is all that a unit's rows see, D = sum P dP is at
+      // hand without the rounding that O went through. It matters for rows of
+      // few keys, whose O is as large as V while dP - D is small: dQ and dK of
+      // 85 tokens are off by 2.4e-3 (relative L2) instead of 2.8e-3. `part` is
+      // the half-row's sum.
+      auto sole_d = [&](const WinUnit& U, float part) -> bool {
+        // every warp has read the D that take_unit left here, then every
+        // half-row's part is there (and read before the unit after next's)
+        float* red = reinterpret_cast<float*>(smem + C::kOffRed) + (ul & 1) * (2 * kTile);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_sole);
+        if (!mbar_wait_lean(d_sole, sole++ & 1, abort_flag, kWaitLimitNs)) return false;
+        red[hf * kTile + jr] = part;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_sole);
+        if (!mbar_wait_lean(d_sole, sole++ & 1, abort_flag, kWaitLimitNs)) return false;
+        dd = red[jr] + red[kTile + jr];
+        const int64_t pos = int64_t(U.seq * g.hq + U.h0) * a.ntp + U.u * kTile + jr;
+        if (hf == 0 && jr < U.q_valid && bounds_ok(pos < a.vec_len, a.status)) a.dvec[pos] = dd;
         return true;
       };
       // Brings the next unit's O (a half-row per thread) into L2 a unit
@@ -1501,6 +1524,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // dS packed into [64h, 64h+32) of the dP columns: the first 32
           // keys' over columns read before, published before the others are formed
           uint32_t rp[32], pd[16];
+          if constexpr (kEdge) {
+            if (U.n == 1) {
+              float part = 0.f;  // a hidden key's dP may be anything
+              tmem_ld32(tdP, rp);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                part = fmaf(__uint_as_float(r0[i]), r0[i] == 0u ? 0.f : __uint_as_float(rp[i]), part);
+              tmem_ld32(tdP + 32, rp);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                part = fmaf(__uint_as_float(r1[i]), r1[i] == 0u ? 0.f : __uint_as_float(rp[i]), part);
+              if (!sole_d(U, part)) return false;
+            }
+          }
           tmem_ld32(tdP, rp);
           ds_row32_fp32(r0, rp, dd, pd);
           tmem_st16(tdP, pd);
