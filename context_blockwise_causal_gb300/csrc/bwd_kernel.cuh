@@ -1329,7 +1329,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // through the registers anyway, and written for the dK/dV kernel, which
       // runs after this one: no pass of its own over O and dO (95 us for one
       // at b1 s32768 h32 d128). Measured there with h32/8, window 1024, 4 first
-      // tokens: 690 us, its three products at 0.62 of the measured burst peak.
+      // tokens: 704 us, its three products at 0.61 of the measured burst peak.
       float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
       int rd = 0, sole = 0;
       auto take_unit = [&](WinUnit& U, int u) -> bool {
@@ -1417,9 +1417,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // Where one key tile is all that a unit's rows see, D = sum P dP is at
       // hand without the rounding that O went through. It matters for rows of
       // few keys, whose O is as large as V while dP - D is small: dQ and dK of
-      // 85 tokens are off by 2.4e-3 (relative L2) instead of 2.8e-3. `part` is
-      // the half-row's sum.
-      auto sole_d = [&](const WinUnit& U, float part) -> bool {
+      // 85 tokens are off by 2.4e-3 (relative L2) instead of 2.8e-3. A pass of
+      // its own over S and dP: at b1 s32768 h32/8 window 1024, where few units
+      // take it, the kernel takes 692 us without it, 704 with it, 710 with it
+      // inside the edge tile's body and as much with the sum out of line
+      // (registers).
+      auto sole_d = [&](const WinUnit& U) -> bool {
+        if (!mbar_wait_lean(s_full, jt & 1, abort_flag, kWaitLimitNs) ||
+            !mbar_wait_lean(dp_full, jt & 1, abort_flag, kWaitLimitNs))
+          return false;
+        tc_fence_after();
+        float part = 0.f;
+        const int hi = U.off + U.q_t0 + jr + 1 - win_tile(U, 0) * kTile - hf * 64;
+        const int first = g.sinks - win_tile(U, 0) * kTile - hf * 64;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t rs[32], rp[32];
+          tmem_ld32(tS + c, rs);
+          tmem_ld32(tdP + c, rp);
+          p_row32_fp32<true>(rs, sl2, l2,
+                             bit_range(hi - g.window - c, hi - c) | bit_range(0, (first < hi ? first : hi) - c));
+#pragma unroll
+          for (int i = 0; i < 32; ++i)  // a hidden key's dP may be anything
+            part = fmaf(__uint_as_float(rs[i]), rs[i] == 0u ? 0.f : __uint_as_float(rp[i]), part);
+        }
         // every warp has read the D that take_unit left here, then every
         // half-row's part is there (and read before the unit after next's)
         float* red = reinterpret_cast<float*>(smem + C::kOffRed) + (ul & 1) * (2 * kTile);
@@ -1524,20 +1545,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           // dS packed into [64h, 64h+32) of the dP columns: the first 32
           // keys' over columns read before, published before the others are formed
           uint32_t rp[32], pd[16];
-          if constexpr (kEdge) {
-            if (U.n == 1) {
-              float part = 0.f;  // a hidden key's dP may be anything
-              tmem_ld32(tdP, rp);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                part = fmaf(__uint_as_float(r0[i]), r0[i] == 0u ? 0.f : __uint_as_float(rp[i]), part);
-              tmem_ld32(tdP + 32, rp);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                part = fmaf(__uint_as_float(r1[i]), r1[i] == 0u ? 0.f : __uint_as_float(rp[i]), part);
-              if (!sole_d(U, part)) return false;
-            }
-          }
           tmem_ld32(tdP, rp);
           ds_row32_fp32(r0, rp, dd, pd);
           tmem_st16(tdP, pd);
@@ -1552,6 +1559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (lane == 0) mbar_arrive(p_full);
           return true;
         };
+        if (U.n == 1 && !(ok = sole_d(U))) break;
         for (; j < U.n && ok; ++j, ++jt)
           ok = win_block_full(g, p0, win_tile(U, j) * kTile) ? key_tile(std::false_type()) : key_tile(std::true_type());
         if (!ok) break;
