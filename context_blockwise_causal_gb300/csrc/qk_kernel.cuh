@@ -23,13 +23,13 @@
 // HBM-bound: each feature is read once and written once (backward: read twice,
 // written once); 2 or 3 flops a byte. A row takes D/16 threads, each holding
 // two 16-byte pieces placed so that both features of a pair are in one thread,
-// whatever the layout: cosines and sines are formed once per thread and token
-// and used for all of the warp's heads. A warp takes the heads of one token
+// whatever the layout: a warp forms its token's cosines and sines once (see
+// QkTurns) for all of its heads. A warp takes the heads of one token
 // (or, when tokens are few, some of them, so that single tokens spread over
 // the chip); rows of several tokens and heads are in flight at once. Measured
 // at 32K tokens, d128: rotation alone of 40 heads 103 us (0.97 of the measured
 // copy bandwidth), with the norms of 32 + 8 heads 105 us, the backward 160 us
-// (0.94); one token of 40 heads takes 2.6 us, a launch.
+// (0.94); one token of 40 heads takes 2.3 us, a launch.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -138,18 +138,42 @@ __device__ __forceinline__ void qk_rotate(float (&f)[16], const QkLane& l, const
   }
 }
 
-// Cosines and sines, times the magnitude, of a thread's eight pairs.
-__device__ __forceinline__ void qk_cos_sin(const QkArgs& a, const QkLane& l, int pos, float (&cs)[8], float (&sn)[8]) {
-  const float sign = a.inverse ? -a.magnitude : a.magnitude;
+// Cosines and sines, times the magnitude, of a thread's eight pairs. The
+// threads at one place of a warp's 512/D rows need the same ones, so each of
+// them forms 1/(512/D) of them, of pairs that stay its own, and they exchange
+// (a whole warp works on one token). All eight formed by each: 5331 tokens of
+// 6 + 2 heads of 64 took 6.3 us forward and 11.9 backward, with this 5.2 and
+// 9.5; with 40 heads there is no difference.
+template <int D>
+struct QkTurns {
+  static constexpr int kT = D / 16, kRows = 32 / kT, kOwn = 8 / kRows;
+  uint64_t own[kOwn];  // turns of pairs sub, sub + kRows, ...
+  __device__ __forceinline__ QkTurns(const QkArgs& a, const QkLane& l, int sub) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const bool on = p < 4 ? l.ra : l.rb;
-    const uint64_t ph = uint64_t(int64_t(pos)) * a.turns[on ? (p < 4 ? l.pa + p : l.pb + p - 4) : 0];
-    sincospif(float(int32_t(ph >> 32)) * 4.656612873077393e-10f, &sn[p], &cs[p]);  // 2^-31 half turns
-    sn[p] *= sign;
-    cs[p] *= a.magnitude;
+    for (int i = 0; i < kOwn; ++i) {
+      const int p = sub + i * kRows;
+      const bool on = p < 4 ? l.ra : l.rb;
+      own[i] = a.turns[on ? (p < 4 ? l.pa + p : l.pb + p - 4) : 0];
+    }
   }
-}
+  __device__ __forceinline__ void cos_sin(const QkArgs& a, int pos, float (&cs)[8], float (&sn)[8]) const {
+    const float sign = a.inverse ? -a.magnitude : a.magnitude;
+    float c[kOwn], s[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const uint64_t ph = uint64_t(int64_t(pos)) * own[i];
+      sincospif(float(int32_t(ph >> 32)) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31 half turns
+      s[i] *= sign;
+      c[i] *= a.magnitude;
+    }
+    const int j = threadIdx.x & (kT - 1);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      cs[p] = __shfl_sync(0xffffffffu, c[p / kRows], (p % kRows) * kT + j);
+      sn[p] = __shfl_sync(0xffffffffu, s[p / kRows], (p % kRows) * kT + j);
+    }
+  }
+};
 
 __device__ __forceinline__ int qk_position(const QkArgs& a, int bi, int tok) {
   return a.positions ? a.positions[int64_t(bi) * a.pos_batch + tok] : rope_position(a, tok);
@@ -225,6 +249,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_fwd_kernel(const __gr
   const int lane = threadIdx.x & 31;
   const QkLane l = qk_lane<D, kInter>(lane % kT, a.rot);
   const int sub = lane / kT;
+  const QkTurns<D> turns(a, l, sub);
   const int64_t units = int64_t(a.b) * a.n * a.split;
   const int64_t step = int64_t(gridDim.x) * (kQkThreads / 32);
   int64_t idx = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
@@ -240,7 +265,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_fwd_kernel(const __gr
     __nv_bfloat16* yk = yq;
     if constexpr (kNorm) yk = a.t[1].y + int64_t(bi) * a.t[1].y_batch + int64_t(tok) * a.t[1].y_token - int64_t(hq) * D;
     float cs[8], sn[8];
-    qk_cos_sin(a, l, qk_position(a, bi, tok), cs, sn);
+    turns.cos_sin(a, qk_position(a, bi, tok), cs, sn);
     idx += step;
     for (int h = U.h0, last; ; h += kGroup) {
       last = h + kGroup >= h1;
@@ -310,6 +335,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __gr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const QkLane l = qk_lane<D, kInter>(lane % kT, a.rot);
   const int sub = lane / kT;
+  const QkTurns<D> turns(a, l, sub);
   const bool is_q = int(blockIdx.x) < a.q_ctas;
   const QkTensor& t = a.t[is_q ? 0 : 1];
   const float* wt = w[is_q ? 0 : 1];
@@ -358,7 +384,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __gr
     const int bi = int(bt / a.n), tok = int(bt - int64_t(bi) * a.n);
     __nv_bfloat16* y = t.y + int64_t(bi) * t.y_batch + int64_t(tok) * t.y_token;
     float cs[8], sn[8];
-    qk_cos_sin(a, l, qk_position(a, bi, tok), cs, sn);
+    turns.cos_sin(a, qk_position(a, bi, tok), cs, sn);
     for (int h = 0; h < t.h; h += kRows) {
       const int hh = h + sub;
       cp_async_wait<kQkBwdStages - 2>();
