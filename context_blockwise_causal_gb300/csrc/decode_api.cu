@@ -87,15 +87,10 @@ int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
     cfg.attrs = &cluster;
     cfg.numAttrs = 1;
   }
-  if (cudaLaunchKernelEx(&cfg, cpattn_decode_kernel<D>, a) != cudaSuccess) {
-    cudaGetLastError();
-    return CPATTN_ERR_LAUNCH_FAILED;
-  }
-  if (a.nsplit > kDecMaxCluster) {
-    const int64_t rows = int64_t(a.b) * a.hq;
-    cpattn_decode_join_kernel<D><<<int((rows + 3) / 4), 128, 0, st>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn_decode_kernel<D>, a);
+  if (e == cudaSuccess && a.nsplit > kDecMaxCluster)
+    e = launch_chained(cpattn_decode_join_kernel<D>, (int64_t(a.b) * a.hq + 3) / 4, 128, st, a);
+  return launched(e);
 }
 
 }  // namespace

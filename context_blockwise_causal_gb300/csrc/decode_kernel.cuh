@@ -119,6 +119,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 template <int D>
 __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const DecodeArgs a) {
+  if (a.nsplit > kDecMaxCluster) chain_next();
   using C = DecodeCfg<D>;
   constexpr int kPieces = D / 8;          // 16-byte pieces of a row
   constexpr int kSteps = D / 16;          // 16-feature steps
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
 // Joins the runs of a row: one warp per (sequence, query head).
 template <int D>
 __global__ void __launch_bounds__(128) cpattn_decode_join_kernel(const DecodeArgs a) {
+  chain_wait();
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (row >= int64_t(a.b) * a.hq) return;

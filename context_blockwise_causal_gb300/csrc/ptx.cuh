@@ -355,6 +355,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// A call's second kernel (launch_chained in api_common.h) may be placed once
+// every CTA of its first one has said so; each of its threads waits, before it
+// touches global memory, until the first one has finished and its writes are
+// visible.
+__device__ __forceinline__ void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 16-byte asynchronous copies global -> shared by ordinary threads, in groups
 // that the issuing thread waits for.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {

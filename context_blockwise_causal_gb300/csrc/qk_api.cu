@@ -91,7 +91,7 @@ int launch_fwd(QkArgs& a, DeviceInfo* di, cudaStream_t st) {
   a.split = (heads + a.heads_per - 1) / a.heads_per;
   const int64_t ctas = (tokens * a.split + kWarps - 1) / kWarps, most = int64_t(di->num_sms) * 2;  // resident at once
   cpattn_qk_fwd_kernel<D, kNorm, kInter><<<int(ctas < most ? ctas : most), kQkThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
+  return launched(cudaGetLastError());
 }
 
 template <bool kNorm>
@@ -128,8 +128,9 @@ int launch_bwd(QkArgs& a, int layout, float* dwq, float* dwk, DeviceInfo* di, cu
     done.store(true, std::memory_order_release);
   }
   kernel<<<ctas, kQkThreads, kQkBwdSmem, st>>>(a);
-  cpattn_qk_dw_kernel<<<dim3(D / 8, 2), 256, 0, st>>>(a.partial, a.q_ctas, ctas, D, dwq, dwk);
-  return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_chained(cpattn_qk_dw_kernel, D / 4, 256, st, a.partial, a.q_ctas, ctas, D, dwq, dwk);
+  return launched(e);
 }
 
 void set_tensor(QkTensor* t, const cpattn_rows* x, const cpattn_rows* dy, const cpattn_rows* y, const void* w, int h) {

@@ -327,6 +327,7 @@ constexpr int kQkBwdSmem = kQkBwdStages * kQkThreads * 4 * 16;
 
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __grid_constant__ QkArgs a) {
+  chain_next();
   constexpr int kT = D / 16, kRows = 32 / kT, kWarps = kQkThreads / 32;
   __shared__ __align__(16) float w[2][D];
   __shared__ float red[kWarps][D];
@@ -439,13 +440,15 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_bwd_kernel(const __gr
   }
 }
 
-// Adds the CTAs' sums: grid (D / 8, 2), 256 threads = 8 features x 32 strips
-// of CTAs. A few hundred KB at most: bound by its launch.
+// Adds the CTAs' sums: D / 8 CTAs for the queries' and as many for the keys',
+// 256 threads = 8 features x 32 strips of CTAs. A few hundred KB at most: bound by its launch.
 __global__ void __launch_bounds__(256) cpattn_qk_dw_kernel(const float* partial, int q_ctas, int ctas, int d,
                                                            float* dwq, float* dwk) {
+  chain_wait();
   __shared__ float red[32][8];
-  const int c = blockIdx.x * 8 + (threadIdx.x & 7), strip = threadIdx.x >> 3;
-  const int lo = blockIdx.y ? q_ctas : 0, hi = blockIdx.y ? ctas : q_ctas;
+  const bool keys = int(blockIdx.x) >= d / 8;
+  const int c = (blockIdx.x - (keys ? d / 8 : 0)) * 8 + (threadIdx.x & 7), strip = threadIdx.x >> 3;
+  const int lo = keys ? q_ctas : 0, hi = keys ? ctas : q_ctas;
   float v = 0.f;
   for (int i = lo + strip; i < hi; i += 32) v += partial[int64_t(i) * d + c];
   red[strip][threadIdx.x & 7] = v;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(256) cpattn_qk_dw_kernel(const float* partial,
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-    (blockIdx.y ? dwk : dwq)[c] = s;
+    (keys ? dwk : dwq)[c] = s;
   }
 }
 
