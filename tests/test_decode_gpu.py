@@ -172,3 +172,39 @@ def test_refusals():
     big = torch.zeros(1, 100000, 2, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(pkg.CpattnError):
         cpattn_decode(q[:1], big, big, ln[:1], workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+def test_long_decodes_one_after_another_eager_and_captured():
+    """More runs than a cluster has CTAs: two kernels a call, the second placed
+    while the first still runs. Each call here takes the one before's output as
+    its queries, and all of them one workspace."""
+    cap, hq, hkv, d = 40001, 4, 1, 64
+    k, v = _randn(1, cap, hkv, d, seed=50).cuda(), _randn(1, cap, hkv, d, seed=51).cuda()
+    q = _randn(1, hq, d, seed=52).cuda()
+    ln = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    need = pkg.cpattn_decode_workspace_bytes(1, hq, hkv, d, cap)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def chain(sync):
+        x, out = q, []
+        for i in range(6):
+            x, lse = cpattn_decode(x * 8, k, v, ln, workspace=ws)
+            out += [x, lse]
+            if sync:
+                torch.cuda.synchronize()
+        return out
+
+    want = chain(True)
+    for _ in range(20):
+        got = chain(False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(want, got))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain(False)
+    for new in (100, cap):
+        ln.fill_(new)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(chain(True), got))
