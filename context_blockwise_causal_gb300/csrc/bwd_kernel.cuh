@@ -259,8 +259,8 @@ __device__ __forceinline__ void zero16(uint32_t (&r)[16]) {
 // The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
 // to bf16 there too, as above, adds to the gradients' error (relative
 // L2 3.0e-3 against 2.5e-3, dK and dQ at a window of 300). Measured at b1
-// s32768 h32/8 d128 window 1024 with 4 first tokens: 792 us, the dK/dV kernel's
-// four products at 0.72 of the measured burst peak; its walks are 36 blocks,
+// s32768 h32/8 d128 window 1024 with 4 first tokens: 779 us, the dK/dV kernel's
+// four products at 0.73 of the measured burst peak; its walks are 36 blocks,
 // 8 of them edges. A masked block zeroes P, and
 // dS = P (dP - D) with it, by testing query 8r + 2 c4 + j + c0 against the key
 // row's visible range [from, from + len) (an unsigned compare does both ends).
@@ -682,9 +682,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // No query of this call sees the tile. A tile a shorter packed sample
         // does not have has no rows (k_valid == 0); a real one (rank-local
         // form: no query of the rank reaches it) gets a zero share.
-        const int krow = kv_first_row<kWin>(U) + U.k_t0 + jr;
+        const int64_t krow = int64_t(kv_first_row<kWin>(U)) + U.k_t0 + jr;
         if (key_ok && bounds_ok(krow < a.kv_rows && U.g < g.hkv, a.status)) {
-          const int64_t off = (int64_t(krow) * g.hkv + U.g) * D + hf * (D / 2);
+          const int64_t off = (krow * g.hkv + U.g) * D + hf * (D / 2);
 #pragma unroll
           for (int c0 = 0; c0 < D / 2; c0 += 8) {
             *reinterpret_cast<uint4*>(a.dv + off + c0) = make_uint4(0u, 0u, 0u, 0u);
@@ -844,8 +844,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // ---- dK, dV of the tile: TMEM -> bf16 -> global, 32 columns at a time
       if (!(ok = mbar_wait_lean(dkv_full, ul & 1, abort_flag, kWaitLimitNs))) break;
       tc_fence_after();
-      const int krow = kv_first_row<kWin>(U) + U.k_t0 + jr;
-      const int64_t off = (int64_t(krow) * g.hkv + U.g) * D + hf * (D / 2);
+      const int64_t krow = int64_t(kv_first_row<kWin>(U)) + U.k_t0 + jr;
+      const int64_t off = (krow * g.hkv + U.g) * D + hf * (D / 2);
 #pragma unroll
       for (int c0 = 0; c0 < D / 2; c0 += 32) {
         uint32_t rv[32], rk[32];
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           transpose4(pv, lane);
           transpose4(pk, lane);
           const int r4 = jr & ~3;
-          const int64_t o4 = (int64_t(krow - jr + r4) * g.hkv + U.g) * D + hf * (D / 2) + c0 + (lane & 3) * 8;
+          const int64_t o4 = ((krow - jr + r4) * g.hkv + U.g) * D + hf * (D / 2) + c0 + (lane & 3) * 8;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if (r4 + i < U.k_valid && bounds_ok(krow - jr + r4 + i < a.kv_rows && U.g < g.hkv, a.status)) {
@@ -996,7 +996,7 @@ __device__ __forceinline__ void ds_row32_fp32(const uint32_t (&ps)[32], const ui
   }
 }
 
-template <int D>
+template <int D, bool kWin = false>
 struct DqCfg {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kSlots = D == 128 ? 5 : 8;  // K/V ring
@@ -1005,11 +1005,11 @@ struct DqCfg {
   static constexpr int kOffKV = kOffdO + kTileBytes;
   static constexpr int kOffBar = kOffKV + kSlots * kTileBytes;
   // q_full q_empty qa_full qa_empty s_full s_free dp_full p_full dq_full
-  // dq_empty drain, kv_full[] kv_empty[], p_half, d_full d_sole (window form)
-  static constexpr int kNumBars = 14 + 2 * kSlots;
+  // dq_empty drain, kv_full[] kv_empty[], p_half; window form: d_full d_sole
+  static constexpr int kNumBars = (kWin ? 14 : 12) + 2 * kSlots;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRed = kOffMisc + 16;  // window form: each half-row's part of D, two units'
-  static constexpr int kLayoutBytes = kOffRed + 4 * kTile * 4;
+  static constexpr int kLayoutBytes = kOffRed + (kWin ? 4 * kTile * 4 : 0);
   // The d=128 layout leaves no room for re-alignment: the dynamic shared
   // memory base must already be 1024-byte aligned (checked at run time).
   static constexpr bool kNeedAlignedBase = (kLayoutBytes + 1024 > 232448);
@@ -1053,7 +1053,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     cpattn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
                          const BwdArgs a) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, kWin>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   if constexpr (!C::kNeedAlignedBase)
@@ -1105,8 +1105,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(dq_empty, 8);
     mbar_init(drain, 1);
     mbar_init(p_half, 8);
-    mbar_init(d_full, 8);
-    mbar_init(d_sole, 8);
+    if constexpr (kWin) {
+      mbar_init(d_full, 8);
+      mbar_init(d_sole, 8);
+    }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);

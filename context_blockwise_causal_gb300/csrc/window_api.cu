@@ -135,13 +135,13 @@ int launch_bwd(const CUtensorMap* maps, const BwdArgs& args, DeviceInfo* di, cud
   std::atomic<bool>& done = di->win_bwd_attr[D == 128 ? 1 : 0];
   if (!done.load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(dkdv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::kSmemBytes) != cudaSuccess ||
-        cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes) != cudaSuccess)
+        cudaFuncSetAttribute(dqk, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D, true>::kSmemBytes) != cudaSuccess)
       return CPATTN_ERR_CUDA;
     done.store(true, std::memory_order_release);
   }
   const CpGeom& g = args.g;
   // dQ first: it forms the row vectors that dK/dV reads
-  dqk<<<persistent_grid(di, win_dq_units(g)), kBwdThreads, DqCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
+  dqk<<<persistent_grid(di, win_dq_units(g)), kBwdThreads, DqCfg<D, true>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
                                                                                        maps[3], args);
   dkdv<<<persistent_grid(di, win_dkdv_units(g)), kBwdThreads, DkdvCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
                                                                                             maps[3], args);
