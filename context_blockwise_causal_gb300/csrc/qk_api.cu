@@ -61,12 +61,17 @@ int fill_rotary(const cpattn_rotary* r, int b, int n, int d, int inverse, QkArgs
   return CPATTN_OK;
 }
 
+// Features of a token, queries' and keys' heads together, stay below this: the
+// kernels count heads, and features from a token's first head, in 32 bits.
+constexpr int64_t kQkMaxFeatures = int64_t(1) << 31;
+
 // Strides of one tensor's rows [b, n, h, d]: 16-byte pieces, tokens apart by
 // at least their heads; for an output, batch elements apart by their tokens.
 int check_rows(const void* p, int64_t batch, int64_t token, int b, int n, int h, int d, bool output) {
   if (!p) return CPATTN_ERR_NULL_PTR;
   if (h < 1 || batch < 0 || token < 0 || batch % 8 != 0 || token % 8 != 0) return CPATTN_ERR_INVALID_ARG;
   const int64_t row = int64_t(h) * d;
+  if (row >= kQkMaxFeatures) return CPATTN_ERR_INVALID_ARG;
   if (n > 1 && token < row) return CPATTN_ERR_INVALID_ARG;
   const int64_t span = int64_t(n - 1) * token + row;  // elements of one batch element
   if (output && b > 1 && batch < span) {
@@ -217,6 +222,7 @@ extern "C" int cpattn_qk_norm_rope(const cpattn_rows* q, const cpattn_rows* k, c
   if ((rc = check_rows(q, b, n, hq, d, false)) || (rc = check_rows(k, b, n, hkv, d, false)) ||
       (rc = check_rows(q_out, b, n, hq, d, true)) || (rc = check_rows(k_out, b, n, hkv, d, true)))
     return rc;
+  if ((int64_t(hq) + hkv) * d >= kQkMaxFeatures) return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(q_weight) || !aligned16(k_weight)) return CPATTN_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
@@ -249,6 +255,7 @@ extern "C" int cpattn_qk_norm_rope_bwd(const cpattn_rows* q, const cpattn_rows* 
       (rc = check_rows(dq_out, b, n, hq, d, false)) || (rc = check_rows(dk_out, b, n, hkv, d, false)) ||
       (rc = check_rows(dq, b, n, hq, d, true)) || (rc = check_rows(dk, b, n, hkv, d, true)))
     return rc;
+  if ((int64_t(hq) + hkv) * d >= kQkMaxFeatures) return CPATTN_ERR_INVALID_ARG;
   if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(workspace) || !aligned4(dq_weight) ||
       !aligned4(dk_weight))
     return CPATTN_ERR_MISALIGNED;

@@ -232,7 +232,7 @@ struct QkUnit {
   __device__ __forceinline__ void fetch(int hh, const QkLane& l, uint4& va, uint4& vb) const {
     va = vb = make_uint4(0u, 0u, 0u, 0u);
     if (hh < h1) {
-      const __nv_bfloat16* x = (hh < hq ? xq : xk) + hh * D;
+      const __nv_bfloat16* x = (hh < hq ? xq : xk) + hh * D;  // below 2^31 (kQkMaxFeatures in qk_api.cu)
       va = *reinterpret_cast<const uint4*>(x + l.fa);
       vb = *reinterpret_cast<const uint4*>(x + l.fb);
     }
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_qk_fwd_kernel(const __gr
           for (int i = 0; i < 16; ++i) f[i] *= r * wr[i];
         }
         qk_rotate<kInter>(f, l, cs, sn);
-        if (hh < h1 && bounds_ok(bi < a.b && tok < a.n, a.status)) {
+        if (hh < h1 && bounds_ok(bi < a.b && tok < a.n && hh < hq + (kNorm ? a.t[1].h : 0), a.status)) {
           __nv_bfloat16* y = (hh < hq ? yq : yk) + hh * D;
           *reinterpret_cast<uint4*>(y + l.fa) = f32_to_bf16x8(f);
           *reinterpret_cast<uint4*>(y + l.fb) = f32_to_bf16x8(f + 8);

@@ -348,7 +348,8 @@ int cpattn_bwd_rank_stage(int stage, const void* q, const void* k_all, const voi
 /* Rows [b, n, h, d] of a tensor, bf16: features and heads contiguous, tokens
  * and batch elements any multiple of 8 elements apart (for instance q or k
  * inside the fused projection's rows). Tokens of a tensor must not overlap; an
- * output may be its own input (same data and strides), element for element. */
+ * output may be its own input (same data and strides), element for element. A
+ * token has fewer than 2^31 features (q's and k's together). */
 typedef struct cpattn_rows {
   void* data;           /* device, 16-byte aligned; inputs are not written */
   int64_t batch_stride; /* elements */

@@ -210,3 +210,28 @@ def test_binding_table_names_the_structure_of_the_source():
     src = open(os.path.join(os.path.dirname(cp.__file__), "csrc", "binding.cpp")).read()
     body = src[src.index("struct Calls {"):]
     assert tuple(re.findall(r"decltype\(&(\w+)\)", body[:body.index("};")])) == cp._CALLS
+
+
+def test_rows_of_a_token_stay_below_32_bits(lib):
+    """The kernels form a head's offset in 32 bits: a token of 2^31 features or
+    more (one tensor's, or q's and k's together) is refused before a launch."""
+    freq = torch.ones(64, dtype=torch.float64)
+
+    def f(h, d):
+        r = Rows(4096, 0, h * d)
+        plan = Rotary(layout=0, rot_dim=64, magnitude=1.0, s=1, cp=1, rank=-1, inv_freq=freq.data_ptr())
+        return lib.cpattn_rope_ex(r, r, 1, 1, h, d, plan, 0, None)
+
+    def g(hq, hkv, d):
+        q, k = Rows(4096, 0, hq * d), Rows(4096, 0, hkv * d)
+        plan = Rotary(layout=0, rot_dim=64, magnitude=1.0, s=1, cp=1, rank=-1, inv_freq=freq.data_ptr())
+        fwd = lib.cpattn_qk_norm_rope(q, k, P, P, 1, 1e-6, q, k, 1, 1, hq, hkv, d, plan, None)
+        bwd = lib.cpattn_qk_norm_rope_bwd(q, k, P, P, 1, 1e-6, q, k, q, k, P, P, P, 1 << 30, 1, 1, hq, hkv, d, plan, None)
+        assert fwd == bwd
+        return fwd
+
+    for h, d in ((1 << 24, 128), (1 << 25, 64), (2 ** 31 - 1, 64)):
+        assert f(h, d) == ARG and g(h, 1, d) == ARG and g(1, h, d) == ARG, (h, d)
+    assert g((1 << 24) - 1, 1, 128) == ARG and g(1, (1 << 25) - 1, 64) == ARG and g(1 << 23, 1 << 23, 128) == ARG
+    if not torch.cuda.is_available():  # shapes below it pass the checks (and would be launched on a GPU)
+        assert f((1 << 24) - 1, 128) not in (0, ARG) and g((1 << 24) - 2, 1, 128) not in (0, ARG)
