@@ -8,20 +8,13 @@
 #include "../../include/cpattn.h"
 #include "api_common.h"
 #include "qk_kernel.cuh"
+#include "rope_turns.h"
 
 using namespace cpattn;
 
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925;
-
-// Turns per position as a fraction of 2^64 (whole turns drop out).
-uint64_t turn_fraction(double radians) {
-  double t = radians / kTwoPi;
-  t = (t - double(int64_t(t))) * 4294967296.0;  // exact: radians <= 1e6
-  const uint64_t hi = uint64_t(t);
-  return hi << 32 | uint64_t((t - double(hi)) * 4294967296.0);
-}
 
 // Checks the rotary plan for b x n tokens and fills the kernel's fields.
 int fill_rotary(const cpattn_rotary* r, int b, int n, int d, int inverse, QkArgs* a) {

@@ -16,9 +16,10 @@
 //
 // Angle: positions reach 10^5 and beyond, where an fp32 product has lost the
 // phase. The host gives each pair's turns per position as a 64-bit fraction of
-// a turn, so pos * fraction modulo 2^64 is the phase itself, exact to 2^-64 *
-// pos turns, by integer multiplication, without this chip's slow fp64. The upper 32 bits, signed, are the
-// phase in [-1/2, 1/2) turn, which sincospi takes.
+// a turn (rope_turns.h), so pos * fraction modulo 2^64 is the phase, within
+// |pos| 2^-64 turns, by integer multiplication, without this chip's slow fp64.
+// The upper 32 bits, signed, are the phase in [-1/2, 1/2) turn, which sincospi
+// takes.
 //
 // HBM-bound: each feature is read once and written once (backward: read twice,
 // written once); 2 or 3 flops a byte. A row takes D/16 threads, each holding

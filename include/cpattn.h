@@ -408,8 +408,9 @@ typedef struct cpattn_rotary {
 /*
  * y = x rotated by the plan ([b, n, h, d], d in {64, 128}); inverse != 0 turns
  * back (the gradient: dx from dy; the magnitude stays). Phases are
- * within fp32's own rounding at any int32 position. Errors: NULL_PTR, INVALID_ARG,
- * MISALIGNED, UNSUPPORTED_ARCH, LAUNCH_FAILED.
+ * within 2^-25 turn, fp32's own rounding, for every frequency and int32
+ * position. Errors: NULL_PTR, INVALID_ARG, MISALIGNED, UNSUPPORTED_ARCH,
+ * LAUNCH_FAILED.
  */
 int cpattn_rope_ex(const cpattn_rows* x, const cpattn_rows* y, int b, int n, int h, int d,
                    const cpattn_rotary* rotary, int inverse, void* stream);
