@@ -49,16 +49,13 @@ static_assert(2 * 128 * kFwdSoftmaxRegs + 128 * kFwdOtherRegs <= kFwdThreads * k
 // raises it. The largest P of the row is then exactly 1, which bf16 holds
 // exactly; with a lagging max (FA4's thresholded rescale) that dominant P
 // exceeds 1 and is rounded, which measured about twice the output error on
-// peaky rows (Q, K ~ N(0, 4)) for a 2-4% gain in speed.
+// peaky rows (Q, K ~ N(0, 4)) for a 2-4% gain in speed. The window form's walks
+// are a few tiles long, and some row of a warp meets a new maximum in most of
+// them: a lag of 2^8 takes 1296 us there instead of 1371 at s16384 h64/8 window
+// 4096 and 466 instead of 499 at s32768 h32/8 window 1024, at the same cost in
+// error (a row that one key dominates is off by up to 2.4 half steps of bf16
+// instead of the output's own 1), so it is not taken either.
 constexpr float kRescaleThreshold = 0.0f;  // log2 units
-
-// The window form lets the running max lag by up to this much: its walks are
-// a few tiles long, where some row of a warp meets a new maximum in almost
-// every tile and the rescale's TMEM round trip would be paid each time (s16384
-// h64/8 window 4096: 1332 us with the lag, 1418 without; s32768 h32/8 window
-// 1024: 460 against 482). P then reaches 2^8 at most; rounding
-// P to bf16 is relative, so its error is the same, and the sums are fp32.
-constexpr float kWinRescaleThreshold = 8.0f;
 
 struct FwdArgs {
   CpGeom g;
@@ -140,10 +137,10 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
 // Bound by the tensor cores and the exponentials beside them: 2 products of d
 // flops x 2 per visible pair, and whole tiles where a window's edges cut them
 // (9 tiles visited for 8 tiles' worth of keys at window 1024). Measured, d128
-// with 4 first tokens: 1283 us at s16384 h64/8 window 4096 (1500 TFLOP/s of
-// visible pairs, 0.79 of the measured burst peak), 460 us at s32768 h32/8
-// window 1024 (1180, 0.62: walks of 9 tiles, of which two have edges), 44 us
-// for four chunks of 333 queries over 8192 keys, h32/8 window 1024.
+// with 4 first tokens, calls one after another: 1371 us at s16384 h64/8 window
+// 4096 (1404 TFLOP/s of visible pairs, 0.74 of the measured burst peak), 499 us
+// at s32768 h32/8 window 1024 (1088, 0.57: walks of 9 tiles, of which two have
+// edges), 50 us for four chunks of 333 queries over 8192 keys, h32/8 window 1024.
 // kShortWaits: the producer's waits for free buffers use a.producer_limit_ns
 // (the abort self-test) instead of the compile-time limit.
 template <bool kTP, bool kWin>
@@ -567,7 +564,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
             // the load's maximum, over hidden keys too, is a bound: the row's
             // own is needed only where that could move the running one
-            if (__any_sync(0xffffffffu, hw_max * sl2 > m_used + kWinRescaleThreshold)) m_raw = row_max(s);
+            if (__any_sync(0xffffffffu, hw_max * sl2 > m_used + kRescaleThreshold)) m_raw = row_max(s);
           }
         } else if (dg || dead || n_valid < kTile) {
           const int lim = dead ? -1 : dg ? (row < n_valid - 1 ? row : n_valid - 1) : n_valid - 1;
@@ -577,7 +574,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           m_raw = row_max(s);
         }
         const float m_new = m_raw * sl2;
-        const bool upd = m_new > m_used + (kWin ? kWinRescaleThreshold : kRescaleThreshold);
+        const bool upd = m_new > m_used + kRescaleThreshold;
         float alpha = 1.f;
         if (upd) {
           alpha = (m_used == -INFINITY) ? 0.f : ex2_approx(m_used - m_new);
