@@ -858,8 +858,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (lane == 0) mbar_arrive(dkv_empty);
         }
         if constexpr (kWin) {
-          if (U.slot >= 0) {  // a part of a cut walk: fp32, added up by cpattn_window_join_kernel
-            const int64_t po = (int64_t(U.slot) * kTile + jr) * D + hf * (D / 2) + c0;
+          if (U.place >= 0) {  // a part of a cut walk: fp32, added up by cpattn_window_join_kernel
+            const int64_t po = (int64_t(U.place) * kTile + jr) * D + hf * (D / 2) + c0;
             if (jr < U.rows && bounds_ok(po + 32 <= a.part_len, a.status)) {
 #pragma unroll
               for (int q = 0; q < 32; q += 4) {
@@ -1762,16 +1762,22 @@ constexpr int kJoinWarps = 8;
 __host__ __device__ inline int win_join_ctas(const CpGeom& g) {
   return (g.sinks < kTile ? g.sinks : kTile) + kTile / kJoinWarps;
 }
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) cpattn_window_join_kernel(const BwdArgs a) {
+struct JoinArgs : BwdArgs {
+  WinCuts cuts;
+};
+template <int D, bool kPacked>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    cpattn_window_join_kernel(const __grid_constant__ std::conditional_t<kPacked, JoinArgs, BwdArgs> a) {
   constexpr int kPer = D / 32;  // features per lane
   __shared__ float red[2][kJoinWarps][D];
   const CpGeom& g = a.g;
-  const int cut = win_cut_tiles(g), per = win_join_ctas(g), firsts = per - kTile / kJoinWarps;
+  const int per = win_join_ctas(g), firsts = per - kTile / kJoinWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = blockIdx.x / per, i = blockIdx.x - x * per;
-  const int y = g.fd_cut.div(x), kt = x - y * cut;
-  const int seq = g.fd_hkv.div(y), h = y - seq * g.hkv;
+  int seq, h, kt;
+  if constexpr (kPacked) win_cut_tile(g, a.cuts, x, seq, h, kt);
+  else win_cut_tile(g, x, seq, h, kt);
+  const int64_t part0 = win_first_part(g, seq, h, kt);
   const WinSeq s = win_seq(g, seq);
   const bool whole = i < firsts;  // a row of the CTA's own
   const int jr = whole ? i : (i - firsts) * kJoinWarps + warp;
@@ -1787,7 +1793,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cpattn_window_join_kernel(con
   for (int p = whole ? warp : 0; p < np; p += step) {
     // rows past the first tokens only have a result in parts that the windows reach
     if (!whole && win_part_rows(g, s, kt, qa + p * g.part_tiles) < kTile) break;
-    const int64_t po = ((int64_t(x) * g.sink_parts + p) * kTile + jr) * D + lane * kPer;
+    const int64_t po = ((part0 + p) * kTile + jr) * D + lane * kPer;
     if (!bounds_ok(po + kPer <= a.part_len, a.status)) break;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {

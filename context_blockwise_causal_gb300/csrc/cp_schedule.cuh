@@ -83,13 +83,16 @@ struct CpGeom {
   int window = 0;        // a query sees the last `window` keys up to its own ...
   int sinks = 0;         // ... and the first `sinks` keys
   int part_tiles = 0;    // dK/dV: query tiles per part of a cut walk
-  int sink_parts = 0;    // dK/dV: parts per cut walk (1: none is cut)
+  int sink_parts = 0;    // dK/dV: parts of the longest cut walk (1: none is cut)
+  int part_units = 0;    // dK/dV: units that are parts of cut walks
+  int cut_tiles = 0;     // dK/dV: first-token tiles of a sequence, whose walks may be cut (0: none is)
   FastDiv fd_per, fd_T, fd_kt, fd_parts, fd_cut;  // divisors of its unit decodes (win_set_divs)
   // divisors of the backward's unit decodes (set_fast_divs; set again
   // whenever b, hq, hkv or tpc change)
   FastDiv fd_hq, fd_hkv, fd_G, fd_tpc, fd_bhq, fd_bhkv;
   int cu[kMaxSeqs + 1];     // packed: sample offsets
   int tile0[kMaxSeqs + 1];  // packed: query tiles (2cp * tpc_i) of the samples before sample i
+  int part0[kMaxSeqs + 1];  // packed, window form, dK/dV: part units per KV head of the samples before sample i
 };
 
 __host__ __device__ inline void set_fast_divs(CpGeom& g) {

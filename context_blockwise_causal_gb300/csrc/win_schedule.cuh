@@ -218,8 +218,10 @@ struct BwdWinUnit : BwdUnit {
   int off;      // position of its query row 0
   int qlen;
   int qa;       // first query tile visited (nq of them; the walk comes down from the last)
-  int slot;     // a part of a cut walk: index of its fp32 result; -1: the whole walk
+  int place;    // a part of a cut walk: index of its fp32 result; -1: the whole walk
   int rows;     // key rows of the tile that the part's queries see (win_part_rows)
+  int64_t slot; // first-token tiles where any walk is cut: the part's number among all that the call's
+                // sequences could have, by which the schedule's check knows it; -1: another tile
 };
 
 // Query tiles in which some query sees a key of tile kt: [qa, qa + nq).
@@ -249,46 +251,107 @@ __host__ __device__ inline int win_part_rows(const CpGeom& g, const WinSeq& s, i
 // part_tiles; the number of parts that have any.
 __host__ __device__ inline int win_parts(const CpGeom& g, int nq) { return (nq + g.part_tiles - 1) / g.part_tiles; }
 
-// Tiles whose walk is cut, per sequence and KV head (0 when no walk is).
-__host__ __device__ inline int win_cut_tiles(const CpGeom& g) {
-  return g.sink_parts > 1 ? (g.sinks + kTile - 1) / kTile : 0;
-}
+// First-token tiles of a sequence, whose walks are cut where they are longer
+// than a part (0 when no sequence's are).
+__host__ __device__ inline int win_cut_tiles(const CpGeom& g) { return g.cut_tiles; }
+// Parts there would be if every sequence were as long as the longest.
 __host__ __device__ inline int64_t win_cut_units(const CpGeom& g) {
   return int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g) * g.sink_parts;
 }
+// Of a packed sample of `tiles` key tiles: those whose walks are cut (samples
+// shorter than a part keep theirs whole and need no fp32 result).
+__host__ __device__ inline int win_sample_cut(const CpGeom& g, int tiles) {
+  const int cut = win_cut_tiles(g);
+  return tiles > g.part_tiles ? (cut < tiles ? cut : tiles) : 0;
+}
+__host__ __device__ inline int win_sample_tiles(const CpGeom& g, int i) {
+  return win_unit_tiles(g.cu[i + 1] - g.cu[i], false);
+}
+// The first part of tile kt of KV head h of a sequence: part units come first,
+// so their number is also the place of their fp32 result. Every cut tile has as
+// many as the first of its sequence.
+__host__ __device__ inline int64_t win_first_part(const CpGeom& g, int seq, int h, int kt) {
+  if (g.nseq == 0) return ((int64_t(seq) * g.hkv + h) * win_cut_tiles(g) + kt) * g.sink_parts;
+  const int tiles = win_sample_tiles(g, seq);
+  return int64_t(g.part0[seq]) * g.hkv + (int64_t(h) * win_sample_cut(g, tiles) + kt) * win_parts(g, tiles);
+}
+// The sample i with first[i] <= p < first[i + 1] of a prefix sum over samples.
+__host__ __device__ inline int win_sample_of(const int* first, int n, int p) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= p) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+// The join's tiles: all cut ones, by sequence, KV head and tile. Packed
+// samples have as many as they are long for.
+__host__ __device__ inline void win_cut_tile(const CpGeom& g, int x, int& seq, int& h, int& kt) {
+  const int y = g.fd_cut.div(x);
+  kt = x - y * win_cut_tiles(g);
+  seq = g.fd_hkv.div(y);
+  h = y - seq * g.hkv;
+}
+struct WinCuts {
+  int first[kMaxSeqs + 1];  // cut tiles per KV head of the samples before sample i
+};
+inline void win_set_cuts(const CpGeom& g, WinCuts& c) {
+  c.first[0] = 0;
+  for (int i = 0; i < g.nseq; ++i) c.first[i + 1] = c.first[i] + win_sample_cut(g, win_sample_tiles(g, i));
+}
+__host__ __device__ inline void win_cut_tile(const CpGeom& g, const WinCuts& c, int x, int& seq, int& h, int& kt) {
+  seq = win_sample_of(c.first, g.nseq, g.fd_hkv.div(x));
+  const int n = c.first[seq + 1] - c.first[seq];
+  x -= c.first[seq] * g.hkv;
+  h = x / n;
+  kt = x - h * n;
+}
 __host__ __device__ inline int win_key_tiles(const CpGeom& g) { return (g.kv_s + kTile - 1) / kTile; }
 __host__ __device__ inline int64_t win_dkdv_units(const CpGeom& g) {
-  return win_cut_units(g) + int64_t(g.hkv) * (g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_key_tiles(g));
+  return g.part_units + int64_t(g.hkv) * (g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_key_tiles(g));
 }
 
 __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   BwdWinUnit U;
   const int cut = win_cut_tiles(g);
-  const int ncut = int(win_cut_units(g));
   int kt, part = 0;
-  U.slot = -1;
-  if (idx < ncut) {
-    U.slot = idx;
-    const int x = g.fd_parts.div(idx);
-    part = idx - x * g.sink_parts;
-    const int y = g.fd_cut.div(x);
-    kt = x - y * cut;
-    U.seq = g.fd_hkv.div(y);
-    U.g = y - U.seq * g.hkv;
+  bool elsewhere = false;  // an ordinary unit of a tile whose walk is cut
+  U.place = -1;
+  if (idx < g.part_units) {
+    U.place = idx;
+    if (g.nseq > 0) {
+      U.seq = win_sample_of(g.part0, g.nseq, g.fd_hkv.div(idx));
+      const int tiles = win_sample_tiles(g, U.seq), np = win_parts(g, tiles), nc = win_sample_cut(g, tiles);
+      idx -= g.part0[U.seq] * g.hkv;
+      U.g = idx / (nc * np);
+      idx -= U.g * (nc * np);
+      kt = idx / np;
+      part = idx - kt * np;
+    } else {
+      const int x = g.fd_parts.div(idx);
+      part = idx - x * g.sink_parts;
+      const int y = g.fd_cut.div(x);
+      kt = x - y * cut;
+      U.seq = g.fd_hkv.div(y);
+      U.g = y - U.seq * g.hkv;
+    }
   } else {
-    idx -= ncut;
+    idx -= g.part_units;
     if (g.nseq > 0) {
       const int p = idx / g.hkv;
       U.g = idx - p * g.hkv;
       U.seq = packed_sample_of(g, p, kt);
+      elsewhere = kt < win_sample_cut(g, g.tile0[U.seq + 1] - g.tile0[U.seq]);
     } else {
       const int T = win_key_tiles(g);
       const int y = g.fd_kt.div(idx);
       kt = idx - y * T;
       U.seq = g.fd_hkv.div(y);
       U.g = y - U.seq * g.hkv;
+      elsewhere = kt < cut;
     }
   }
+  U.slot = kt < cut ? ((int64_t(U.seq) * g.hkv + U.g) * cut + kt) * g.sink_parts + part : -1;
   const WinSeq s = win_seq(g, U.seq);
   U.bi = g.nseq > 0 ? 0 : U.seq;
   U.tok0 = s.q0;
@@ -301,15 +364,14 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   U.k_t0 = kt * kTile;
   U.qa = 0;
   U.rows = kTile;
-  // no such key tile, or an ordinary unit of a tile whose walk is cut
-  if (U.k_t0 >= s.klen || (U.slot < 0 && kt < cut)) {
+  if (U.k_t0 >= s.klen || elsewhere) {  // no such key tile, or one whose parts are units
     U.k_t0 = U.k_valid = U.nq = U.items = 0;
     return U;
   }
   const int rem = s.klen - U.k_t0;
   U.k_valid = rem < kTile ? rem : kTile;
   win_query_tiles(g, s, kt, U.qa, U.nq);
-  if (U.slot >= 0) {
+  if (U.place >= 0) {
     const int from = part * g.part_tiles;
     const int left = U.nq - from;
     U.qa += from;
@@ -333,7 +395,9 @@ constexpr int kMaxParts = 64;
 constexpr int kWinChipCtas = 152;
 __host__ __device__ inline void win_set_parts(CpGeom& g) {
   g.sink_parts = 1;
+  g.part_units = g.cut_tiles = 0;
   g.part_tiles = g.tpc > 0 ? g.tpc : 1;
+  for (int i = 0; i <= g.nseq; ++i) g.part0[i] = 0;
   if (g.sinks == 0) return;
   const int ordinary = g.window / kTile + 1;
   int tiles = ordinary > 8 ? ordinary : 8;
@@ -346,6 +410,12 @@ __host__ __device__ inline void win_set_parts(CpGeom& g) {
   if (tiles < least) tiles = least;
   g.part_tiles = tiles;
   g.sink_parts = (g.tpc + tiles - 1) / tiles;
+  g.cut_tiles = (g.sinks + kTile - 1) / kTile;
+  for (int i = 0; i < g.nseq; ++i) {
+    const int t = win_sample_tiles(g, i);
+    g.part0[i + 1] = g.part0[i] + win_sample_cut(g, t) * win_parts(g, t);
+  }
+  g.part_units = int(g.nseq > 0 ? int64_t(g.hkv) * g.part0[g.nseq] : win_cut_units(g));
 }
 
 // The divisors of the decodes above; after win_finish and win_set_parts.

@@ -120,7 +120,7 @@ WinBwdLayout bwd_layout(const CpGeom& g, int d) {
   WinBwdLayout L;
   L.ntp = g.tpc * kTile;
   L.vec_len = int64_t(num_seqs(g)) * g.hq * L.ntp;
-  L.part_len = win_cut_units(g) * kTile * d;
+  L.part_len = int64_t(g.part_units) * kTile * d;
   L.dvec = align256(size_t(L.vec_len) * 4);
   L.part_dk = L.dvec + align256(size_t(L.vec_len) * 4);
   L.part_dv = L.part_dk + align256(size_t(L.part_len) * 4);
@@ -145,8 +145,16 @@ int launch_bwd(const CUtensorMap* maps, const BwdArgs& args, DeviceInfo* di, cud
                                                                                        maps[3], args);
   dkdv<<<persistent_grid(di, win_dkdv_units(g)), kBwdThreads, DkdvCfg<D>::kSmemBytes, st>>>(maps[0], maps[1], maps[2],
                                                                                             maps[3], args);
-  const int64_t cut = int64_t(num_seqs(g)) * g.hkv * win_cut_tiles(g);
-  if (cut > 0) cpattn_window_join_kernel<D><<<int(cut * win_join_ctas(g)), kJoinWarps * 32, 0, st>>>(args);
+  const int64_t per = win_join_ctas(g);
+  if (g.part_units > 0 && g.nseq > 0) {
+    JoinArgs join{args, {}};
+    win_set_cuts(g, join.cuts);
+    const int64_t tiles = int64_t(g.hkv) * join.cuts.first[g.nseq];
+    cpattn_window_join_kernel<D, true><<<unsigned(tiles * per), kJoinWarps * 32, 0, st>>>(join);
+  } else if (g.part_units > 0) {
+    const int64_t tiles = int64_t(g.b) * g.hkv * win_cut_tiles(g);
+    cpattn_window_join_kernel<D, false><<<unsigned(tiles * per), kJoinWarps * 32, 0, st>>>(args);
+  }
   return cudaGetLastError() == cudaSuccess ? CPATTN_OK : CPATTN_ERR_LAUNCH_FAILED;
 }
 
