@@ -408,14 +408,28 @@ __host__ __device__ inline void win_set_parts(CpGeom& g) {
   if (int64_t(g.tpc) * 4 * kWinChipCtas <= work) return;
   const int least = (g.tpc + kMaxParts - 1) / kMaxParts;
   if (tiles < least) tiles = least;
-  g.part_tiles = tiles;
-  g.sink_parts = (g.tpc + tiles - 1) / tiles;
-  g.cut_tiles = (g.sinks + kTile - 1) / kTile;
-  for (int i = 0; i < g.nseq; ++i) {
-    const int t = win_sample_tiles(g, i);
-    g.part0[i + 1] = g.part0[i] + win_sample_cut(g, t) * win_parts(g, t);
+  // The parts' fp32 dK and dV may take four times the bytes of dk and dv, no
+  // more: two parts per key tile. (Only hundreds of first tokens reach it, and
+  // two parts of every walk always fit.)
+  for (;; tiles += tiles / 8 + 1) {
+    g.part_tiles = tiles;
+    g.sink_parts = (g.tpc + tiles - 1) / tiles;
+    g.cut_tiles = g.sink_parts > 1 ? (g.sinks + kTile - 1) / kTile : 0;
+    int64_t parts = int64_t(g.b) * g.cut_tiles * g.sink_parts;  // per KV head
+    if (g.nseq > 0) {
+      parts = 0;
+      for (int i = 0; i < g.nseq; ++i) {
+        const int t = win_sample_tiles(g, i);
+        g.part0[i] = int(parts);
+        parts += int64_t(win_sample_cut(g, t)) * win_parts(g, t);
+      }
+      g.part0[g.nseq] = int(parts);
+    }
+    if (parts <= 2 * key_tiles) {
+      g.part_units = int(parts * g.hkv);
+      return;
+    }
   }
-  g.part_units = int(g.nseq > 0 ? int64_t(g.hkv) * g.part0[g.nseq] : win_cut_units(g));
 }
 
 // The divisors of the decodes above; after win_finish and win_set_parts.

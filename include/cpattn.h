@@ -464,7 +464,10 @@ int cpattn_fwd_window(const void* q, const void* k, const void* v, void* o, floa
 
 /* Backward from the saved o and lse; workspace as cpattn_bwd's. The keys that
  * later queries all see (the first tokens) are summed in parts in a fixed
- * order: deterministic. */
+ * order: deterministic. The workspace holds two fp32 vectors [b, hq, sq] (of
+ * packed samples: [nseq, hq, the longest one]), their rows rounded up to whole
+ * 128, and the parts' fp32 results: at most four times the bytes of dk and dv,
+ * whose rows are rounded up likewise. */
 size_t cpattn_bwd_window_workspace_bytes(int b, int sq, int skv, int hq, int hkv, int d, int window, int sinks);
 int cpattn_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                       void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes, int b, int sq, int skv,

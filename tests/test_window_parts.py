@@ -76,3 +76,32 @@ def test_shorter_samples_take_the_parts_they_have(check):
     c = check("packed", 8, 8, 300, 1, *lengths)
     tiles = [-(-n // 128) for n in lengths]
     assert c.parts in (0, 8 * sum(-(-t // 8) for t in tiles if t > 8))
+
+
+@pytest.mark.parametrize("case", [
+    # b, sq, skv, hq, hkv, d, window, sinks
+    (1, 65536, 65536, 1, 1, 128, 128, 65536),    # every key a first token
+    (1, 65536, 65536, 4, 4, 128, 128, 16384),
+    (1, 12800, 12800, 1, 1, 64, 16, 6400),
+    (2, 9000, 30000, 2, 1, 64, 100, 20000),
+    (1, 32768, 32768, 32, 8, 128, 1024, 4),
+    (1, 1 << 20, 1 << 20, 4, 2, 64, 10, 100),
+])
+def test_the_results_of_parts_are_bounded(check, lib, case):
+    """At most four times the bytes of dk and dv, in whole tiles; walks are
+    still cut where whole ones do not balance."""
+    b, sq, skv, hq, hkv, d, window, sinks = case
+    need = lib.cpattn_bwd_window_workspace_bytes(*case) - 2 * b * hq * (-(-sq // 128) * 128) * 4
+    grads = 2 * b * hkv * (-(-skv // 128) * 128) * d * 2
+    assert 0 <= need <= 4 * grads
+    if skv <= 65536:
+        c = check(b, sq, skv, hq, hkv, window, sinks)
+        assert need == c.parts * 2 * 128 * d * 4
+        assert c.longest <= max(c.blocks / 152, 9 * hq // hkv)
+
+
+def test_the_results_of_packed_parts_are_bounded(check, lib):
+    for lengths, hkv, sinks in (([20000, 5000, 4000, 100], 1, 3000), ([9000] * 7 + [3] * 100, 2, 5000), ([30000, 2000], 1, 1)):
+        need = _packed_bytes(lib, lengths, hkv, hkv, 64, 64, sinks) - 2 * len(lengths) * hkv * (-(-max(lengths) // 128) * 128) * 4
+        assert 0 <= need <= 4 * 2 * hkv * sum(-(-n // 128) * 128 for n in lengths) * 64 * 2
+        assert need == check("packed", hkv, hkv, 64, sinks, *lengths).parts * 2 * 128 * 64 * 4
