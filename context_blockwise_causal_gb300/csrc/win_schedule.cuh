@@ -383,6 +383,15 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
   return U;
 }
 
+// Query tiles that the key tiles with first tokens visit in a sequence of
+// `tiles` query tiles, the first at position off.
+__host__ __device__ inline int64_t win_first_walks(const CpGeom& g, int tiles, int off) {
+  const int64_t keys = win_unit_tiles(off, false) + int64_t(tiles);  // no key tile past the last query's
+  const int64_t firsts = (g.sinks + kTile - 1) / kTile, n = firsts < keys ? firsts : keys;
+  const int64_t later = n > win_unit_tiles(off, false) ? n - win_unit_tiles(off, false) : 0;  // a query tile less each
+  return n * tiles - later * (later - 1) / 2;
+}
+
 // Cuts the walks of the tiles that hold first tokens into parts of an ordinary
 // tile's work (which is seen by about window/128 + 1 query tiles; at least 8
 // tiles, at most kMaxParts parts) when such a walk is over twice that and
@@ -391,6 +400,10 @@ __host__ __device__ inline BwdWinUnit win_dkdv_unit(const CpGeom& g, int idx) {
 // would only cost workspace. (Parts of twice that size left the last round of
 // CTAs uneven: 852 us against 795 us for the kernel at b1 s32768 h32/8 window
 // 1024.)
+//
+// Every sample counts with its own length: taken to be as long as the longest,
+// 64 samples of 64 tokens beside one of 32768 kept that one's walk whole, and
+// the backward took 3100 us instead of 1680 (h32/8 d128 window 1024).
 constexpr int kMaxParts = 64;
 constexpr int kWinChipCtas = 152;
 __host__ __device__ inline void win_set_parts(CpGeom& g) {
@@ -403,7 +416,11 @@ __host__ __device__ inline void win_set_parts(CpGeom& g) {
   int tiles = ordinary > 8 ? ordinary : 8;
   if (g.tpc <= 2 * tiles) return;
   const int64_t key_tiles = g.nseq > 0 ? g.tile0[g.nseq] : int64_t(g.b) * win_key_tiles(g);
-  const int64_t long_walks = int64_t(num_seqs(g)) * ((g.sinks + kTile - 1) / kTile) * g.tpc;
+  int64_t long_walks = 0;
+  if (g.nseq > 0)
+    for (int i = 0; i < g.nseq; ++i) long_walks += win_first_walks(g, win_sample_tiles(g, i), 0);
+  else
+    long_walks = g.b * win_first_walks(g, g.tpc, g.kv_s - g.s);
   const int64_t work = g.hkv * (key_tiles * ordinary + long_walks);  // query tiles visited
   if (int64_t(g.tpc) * 4 * kWinChipCtas <= work) return;
   const int least = (g.tpc + kMaxParts - 1) / kMaxParts;

@@ -105,3 +105,36 @@ def test_the_results_of_packed_parts_are_bounded(check, lib):
         need = _packed_bytes(lib, lengths, hkv, hkv, 64, 64, sinks) - 2 * len(lengths) * hkv * (-(-max(lengths) // 128) * 128) * 4
         assert 0 <= need <= 4 * 2 * hkv * sum(-(-n // 128) * 128 for n in lengths) * 64 * 2
         assert need == check("packed", hkv, hkv, 64, sinks, *lengths).parts * 2 * 128 * 64 * 4
+
+
+@pytest.mark.parametrize("extra", [0, 32, 64, 200, 480])
+def test_short_samples_leave_the_long_walk_cut(check, extra):
+    """Work balances by the samples' own lengths: the longest unit stays under
+    a quarter of a CTA's even share, and the busiest CTA near it."""
+    c = check("packed", 32, 8, 1024, 4, 32768, *[64] * extra)
+    assert 4 * c.longest <= c.blocks / 152
+    assert c.busiest <= 1.1 * c.blocks / 152
+
+
+@pytest.mark.parametrize("b,sq,skv,hkv,sinks", [(1, 2000, 2000, 1, 4), (2, 700, 3000, 2, 1500), (1, 3000, 3000, 1, 3000),
+                                                (1, 1000, 5000, 1, 4500), (3, 129, 500, 1, 400), (1, 1, 1, 1, 1)])
+def test_walks_of_the_first_tokens_are_counted(tmp_path, b, sq, skv, hkv, sinks):
+    """win_first_walks against the units' own walks."""
+    src = tmp_path / "walks.cpp"
+    src.write_text('#include <cstdio>\n#include "%s"\n' % os.path.join(
+        os.path.dirname(HERE), "context_blockwise_causal_gb300", "csrc", "win_schedule.cuh") + """
+int main() {
+  using namespace cpattn;
+  CpGeom g{};
+  g.b = %d; g.s = %d; g.kv_s = %d; g.hq = g.hkv = %d; g.sinks = %d; g.cp = g.causal = g.window = 1;
+  win_finish(g, false);
+  const WinSeq s = win_seq(g, 0);
+  long n = 0;
+  for (int kt = 0; kt * kTile < g.sinks; ++kt) { int qa, nq; win_query_tiles(g, s, kt, qa, nq); n += nq; }
+  std::printf("%%ld %%ld", n, long(win_first_walks(g, g.tpc, s.off)));
+}
+""" % (b, sq, skv, hkv, sinks))
+    exe = str(tmp_path / "walks")
+    subprocess.run(["g++", "-std=c++17", "-O1", str(src), "-o", exe], check=True)
+    want, got = subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()
+    assert want == got
