@@ -103,7 +103,8 @@ def _native():
     global _BINDING
     if _BINDING is None:
         if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is missing: build it with context_blockwise_causal_gb300.build()")
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with context_blockwise_causal_gb300.build() (it needs "
+                               "g++ and the C++ headers of Python and PyTorch)")
         from . import _binding as module
 
         _BINDING = module
