@@ -14,7 +14,7 @@ import struct
 
 import torch
 
-from ._build import BINDING_PATH, CHECKED_LIB_PATH, LIB_PATH, build  # noqa: F401
+from ._build import CHECKED_LIB_PATH, LIB_PATH, build, check_binding  # noqa: F401
 
 __all__ = [
     "CpattnError",
@@ -99,12 +99,11 @@ _BINDING = None
 
 
 def _native():
-    """The native half of the binding (once). Raises if it has not been built."""
+    """The native half of the binding (once). Raises if it has not been built for
+    this PyTorch and Python."""
     global _BINDING
     if _BINDING is None:
-        if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is missing: build it with context_blockwise_causal_gb300.build() (it needs "
-                               "g++ and the C++ headers of Python and PyTorch)")
+        check_binding()
         from . import _binding as module
 
         _BINDING = module

@@ -36,6 +36,8 @@ def is_stale():
     outs = (LIB_PATH, CHECKED_LIB_PATH) + (() if _binding_lacks() else (BINDING_PATH,))
     if not all(os.path.exists(p) for p in outs):
         return True
+    if BINDING_PATH in outs and binding_made_for() != _made_for():
+        return True
     built = min(os.path.getmtime(p) for p in outs)
     inc = os.path.join(os.path.dirname(PKG_DIR), "include")
     for d in (CSRC, inc):
@@ -43,6 +45,34 @@ def is_stale():
             if os.path.getmtime(os.path.join(d, f)) > built:
                 return True
     return False
+
+
+def _made_for():
+    """What the binding's machine code depends on: it uses PyTorch's and Python's
+    own C++ interfaces, which change with every version."""
+    import torch
+
+    return f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_made_for():
+    """The versions that the binding was built for ("" when not recorded)."""
+    try:
+        with open(BINDING_PATH + ".txt") as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def check_binding():
+    """Raises where the binding is missing or made for another PyTorch or
+    Python than the ones that run."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: build it with context_blockwise_causal_gb300.build() (it needs "
+                           "g++ and the C++ headers of Python and PyTorch)")
+    if binding_made_for() != _made_for():
+        raise RuntimeError(f"{BINDING_PATH} was built for '{binding_made_for()}' and this is '{_made_for()}': build it "
+                           "again with context_blockwise_causal_gb300.build()")
 
 
 def _start(cmds, verbose):
@@ -126,6 +156,8 @@ def build(verbose=False):
               "rotations, norms, windows and decoding need it", file=sys.stderr)
         return LIB_PATH
     _wait(binding)
+    with open(BINDING_PATH + ".txt", "w") as f:
+        f.write(_made_for())
     os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 

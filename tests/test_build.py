@@ -69,3 +69,26 @@ def test_nothing_is_replaced_where_the_library_fails(tree, monkeypatch):
 
 def test_this_machine_has_what_the_binding_needs():
     assert _build._binding_lacks() is None
+
+
+def test_a_binding_for_another_pytorch_is_stale(tree, monkeypatch):
+    """The binding uses PyTorch's C++ interface: under another version it is
+    built again, and refused where it is not."""
+    import torch
+
+    monkeypatch.setattr(_build, "_binding_lacks", lambda: None)
+    _build.build()
+    _build.check_binding()
+    assert not _build.is_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.0.0")
+        assert _build.is_stale()
+        with pytest.raises(RuntimeError, match="2.0.0"):
+            _build.check_binding()
+        _build.build()
+        _build.check_binding()
+    with pytest.raises(RuntimeError, match="2.0.0"):
+        _build.check_binding()
+    os.remove(tree / "_binding.so")
+    with pytest.raises(RuntimeError, match="missing"):
+        _build.check_binding()
