@@ -1478,7 +1478,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int rows_left = U.q_valid - r4;
         __nv_bfloat16* dst =
             a.dq + (int64_t(U.tok0 + U.q_t0 + r4) * g.hq + U.h0) * D + hf * (D / 2) + (lane & 3) * 8;
-        const int64_t left_in_dq = a.q_rows - (U.tok0 + U.q_t0 + r4);
+        // (checked builds; take_unit below makes U the next unit)
+        const int64_t left_in_dq = bounds_ok(U.h0 < g.hq, a.status) ? a.q_rows - (U.tok0 + U.q_t0 + r4) : 0;
         const int p0 = U.off + U.q_t0;  // position of the tile's row 0
         int j = 0;
         if (U.narrow) {
@@ -1590,7 +1591,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           transpose4(pc, lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < rows_left && bounds_ok(i < left_in_dq && U.h0 < g.hq, a.status))
+            if (i < rows_left && bounds_ok(i < left_in_dq, a.status))
               *reinterpret_cast<uint4*>(dst + int64_t(i) * g.hq * D + c0) = pc[i];
         }
         ++ul;
