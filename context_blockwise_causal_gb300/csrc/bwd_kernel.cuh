@@ -259,9 +259,11 @@ __device__ __forceinline__ void zero16(uint32_t (&r)[16]) {
 // The window form's versions keep P in fp32 for dS (rs becomes P): rounding P
 // to bf16 there too, as above, adds to the gradients' error (relative
 // L2 3.0e-3 against 2.5e-3, dK and dQ at a window of 300). Measured at b1
-// s32768 h32/8 d128 window 1024 with 4 first tokens: 779 us, the dK/dV kernel's
-// four products at 0.73 of the measured burst peak; its walks are 36 blocks,
-// 8 of them edges. A masked block zeroes P, and
+// s32768 h32/8 d128 window 1024 with 4 first tokens: 803 us, the dK/dV kernel's
+// four products at 0.71 of the measured burst peak; its walks are 36 blocks,
+// 8 of them edges. (For milliseconds at 2070 MHz; for seconds on end the
+// board's power cap holds 1850 MHz and the whole backward takes 1610 us instead
+// of 1510.) A masked block zeroes P, and
 // dS = P (dP - D) with it, by testing query 8r + 2 c4 + j + c0 against the key
 // row's visible range [from, from + len) (an unsigned compare does both ends).
 template <bool kMasked>
@@ -1331,7 +1333,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // through the registers anyway, and written for the dK/dV kernel, which
       // runs after this one: no pass of its own over O and dO (95 us for one
       // at b1 s32768 h32 d128). Measured there with h32/8, window 1024, 4 first
-      // tokens: 704 us, its three products at 0.61 of the measured burst peak.
+      // tokens: 719 us, its three products at 0.60 of the measured burst peak.
       float l2 = 0.f, dd = 0.f;  // this row's L*log2e and D
       int rd = 0, sole = 0;
       auto take_unit = [&](WinUnit& U, int u) -> bool {

@@ -137,10 +137,12 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
 // Bound by the tensor cores and the exponentials beside them: 2 products of d
 // flops x 2 per visible pair, and whole tiles where a window's edges cut them
 // (9 tiles visited for 8 tiles' worth of keys at window 1024). Measured, d128
-// with 4 first tokens, calls one after another: 1371 us at s16384 h64/8 window
-// 4096 (1404 TFLOP/s of visible pairs, 0.74 of the measured burst peak), 499 us
-// at s32768 h32/8 window 1024 (1088, 0.57: walks of 9 tiles, of which two have
-// edges), 50 us for four chunks of 333 queries over 8192 keys, h32/8 window 1024.
+// with 4 first tokens, for milliseconds after an idle moment (2070 MHz): 1365 us
+// at s16384 h64/8 window 4096 (1410 TFLOP/s of visible pairs, 0.74 of the
+// measured burst peak), 503 us at s32768 h32/8 window 1024 (1080, 0.57: walks of
+// 9 tiles, of which two have edges), 47 us for four chunks of 333 queries over
+// 8192 keys, h32/8 window 1024. For seconds on end the board's power cap lowers
+// the clock (1.36 kW, 1970 to 2000 MHz): 1434 and 510 us.
 // kShortWaits: the producer's waits for free buffers use a.producer_limit_ns
 // (the abort self-test) instead of the compile-time limit.
 template <bool kTP, bool kWin>
