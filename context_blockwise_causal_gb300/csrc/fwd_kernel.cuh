@@ -47,7 +47,7 @@ static_assert(2 * 128 * kFwdSoftmaxRegs + 128 * kFwdOtherRegs <= kFwdThreads * k
               "register split exceeds the launch budget");
 // A row's running max is moved (and O, l rescaled) as soon as a key tile
 // raises it. The largest P of the row is then exactly 1, which bf16 holds
-// exactly; with a lagging max (FA4's thresholded rescale) that dominant P
+// exactly; with a lagging max (a rescale past a threshold only) that dominant P
 // exceeds 1 and is rounded, which measured about twice the output error on
 // peaky rows (Q, K ~ N(0, 4)) for a 2-4% gain in speed. The window form's walks
 // are a few tiles long, and some row of a warp meets a new maximum in most of
