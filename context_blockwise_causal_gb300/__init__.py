@@ -35,6 +35,11 @@ __all__ = [
     "cpattn_bwd_window_varlen",
     "cpattn_decode",
     "cpattn_decode_workspace_bytes",
+    "cpattn_append_paged",
+    "cpattn_decode_paged",
+    "cpattn_decode_paged_workspace_bytes",
+    "cpattn_decode_shared",
+    "cpattn_decode_shared_workspace_bytes",
     "cpattn_fwd_varlen",
     "cpattn_bwd_varlen",
     "cpattn_bwd",
@@ -79,7 +84,8 @@ _f, _i64 = ctypes.c_float, ctypes.c_int64
 _CALLS = ("cpattn_rope_frequencies", "cpattn_rope_ex", "cpattn_qk_norm_rope", "cpattn_qk_norm_rope_bwd_workspace_bytes",
           "cpattn_qk_norm_rope_bwd", "cpattn_fwd_window", "cpattn_bwd_window_workspace_bytes", "cpattn_bwd_window",
           "cpattn_fwd_window_varlen", "cpattn_bwd_window_varlen_workspace_bytes", "cpattn_bwd_window_varlen",
-          "cpattn_decode_workspace_bytes", "cpattn_decode")
+          "cpattn_decode_workspace_bytes", "cpattn_decode", "cpattn_append_paged", "cpattn_decode_paged_workspace_bytes",
+          "cpattn_decode_paged", "cpattn_decode_shared_workspace_bytes", "cpattn_decode_shared")
 
 
 _CHECKED = None
@@ -195,6 +201,16 @@ def _declare(lib):
     lib.cpattn_decode_workspace_bytes.restype = _sz
     lib.cpattn_decode.argtypes = [_p] * 7 + [_sz] + [_i] * 5 + [_i64] * 7 + [_i, _i, _f, _p]
     lib.cpattn_decode.restype = _i
+    lib.cpattn_append_paged.argtypes = [_p] * 5 + [_i] + [_p] * 2 + [_i] * 5 + [_p, _p]
+    lib.cpattn_append_paged.restype = _i
+    lib.cpattn_decode_paged_workspace_bytes.argtypes = [_i] * 7
+    lib.cpattn_decode_paged_workspace_bytes.restype = _sz
+    lib.cpattn_decode_paged.argtypes = [_p] * 6 + [_sz] + [_i] * 4 + [_i64, _i, _i, _f, _p]
+    lib.cpattn_decode_paged.restype = _i
+    lib.cpattn_decode_shared_workspace_bytes.argtypes = [_i] * 6
+    lib.cpattn_decode_shared_workspace_bytes.restype = _sz
+    lib.cpattn_decode_shared.argtypes = [_p] * 5 + [_i, _i] + [_p] * 3 + [_sz] + [_i] * 4 + [_i64, _f, _p]
+    lib.cpattn_decode_shared.restype = _i
     lib.cpattn_zigzag_index.argtypes = [_i, _i, _p]
     lib.cpattn_zigzag_index.restype = _i
     lib.cpattn_device_status.argtypes = [_p, ctypes.POINTER(_i)]
@@ -640,6 +656,68 @@ def cpattn_decode(q, k_cache, v_cache, lengths, window=0, sinks=0, scale=None, o
     the first ``sinks``. Returns (o [b, hq, d], lse [b, hq])."""
     return _done("cpattn_decode", _native().decode(library().calls, q, k_cache, v_cache, lengths, window, sinks, scale,
                                                     o, lse, workspace, stream))
+
+
+def cpattn_append_paged(k, v, k_pages, v_pages, tables, lengths, cu_tokens=None, q=None, rotate=True, base=10000.0,
+                        positions=None, layout="half", rot_dim=None, inv_freq=None, magnitude=1.0, q_out=None,
+                        stream=None):
+    """Puts new tokens' keys and values into the pages of their sequences, the
+    keys rotated to their positions, and rotates the queries beside them.
+
+    k, v [b, n, hkv, d] bf16, strided as for cpattn_qk_norm_rope: the last n
+    tokens of each of b sequences; with ``cu_tokens`` (int32 CUDA tensor
+    [seqs + 1]) k, v [1, n, hkv, d] hold those of seqs sequences one after
+    another. k_pages, v_pages [pages, page_size, hkv, d] of any strides with
+    contiguous features (a transposed [pages, hkv, page_size, d] too),
+    page_size a multiple of 16; tables int32 CUDA tensor [seqs, columns]: the
+    pages of each sequence in order; lengths int32 CUDA tensor [seqs]: tokens
+    held with the new ones. Token j of the m new ones goes to place
+    lengths - m + j, and its position is that place or given in ``positions``;
+    tokens without a place (a length of 0 and one padded row) are left out.
+    ``q`` [b, n, hq, d] is rotated into ``q_out`` (new when not given; may be
+    q). Rotation as for cpattn_rope; ``rotate=False`` copies. Returns q_out, or
+    None without q."""
+    return _done("cpattn_append_paged", _native().append_paged(
+        library().calls, k, v, k_pages, v_pages, tables, lengths, cu_tokens, q, 1 if rotate else 0, base, 1, None, None,
+        None, positions, _ROPE_LAYOUTS.get(layout), rot_dim, inv_freq, magnitude, q_out, stream))
+
+
+def cpattn_decode_paged_workspace_bytes(b, hq, hkv, d, cap, window=0, sinks=0):
+    """Workspace bytes of cpattn_decode_paged on the current device (0: none);
+    cap: tokens that a sequence's table has room for."""
+    return int(library().cpattn_decode_paged_workspace_bytes(b, hq, hkv, d, cap, _keys(window), _keys(sinks)))
+
+
+def cpattn_decode_paged(q, k_pages, v_pages, tables, lengths, window=0, sinks=0, scale=None, o=None, lse=None,
+                        workspace=None, stream=None):
+    """cpattn_decode over a cache in pages, which are given as to
+    cpattn_append_paged. Table entries that no visible token needs may hold
+    anything. Returns (o [b, hq, d], lse [b, hq])."""
+    return _done("cpattn_decode_paged", _native().decode_paged(
+        library().calls, q, k_pages, v_pages, tables, lengths, window, sinks, scale, o, lse, workspace, stream))
+
+
+def cpattn_decode_shared_workspace_bytes(b, hq, hkv, d, groups=1, max_group=None):
+    """Workspace bytes of cpattn_decode_shared on the current device."""
+    return int(library().cpattn_decode_shared_workspace_bytes(b, hq, hkv, d, groups, b if max_group is None else max_group))
+
+
+def cpattn_decode_shared(q, k_pages, v_pages, tables, lengths, shared, group_offsets=None, max_group=None, scale=None,
+                         o=None, lse=None, workspace=None, stream=None):
+    """cpattn_decode_paged over every key, for groups of sequences that begin
+    with the same tokens, whose keys and values are read once for the group.
+
+    shared int32 CUDA tensor [groups]: tokens that a group's members have in
+    common (their tables begin with the same pages, or with copies);
+    group_offsets int32 CUDA tensor [groups + 1]: group g is sequences
+    group_offsets[g] to group_offsets[g + 1] - 1 (None: one group, the whole
+    batch); ``max_group`` (default b): members of the largest group, which
+    bounds the workspace. A sequence outside of every group, behind max_group
+    others or with fewer tokens than its group shares is computed by itself.
+    Returns (o [b, hq, d], lse [b, hq])."""
+    return _done("cpattn_decode_shared", _native().decode_shared(
+        library().calls, q, k_pages, v_pages, tables, lengths, shared, group_offsets, max_group, scale, o, lse, workspace,
+        stream))
 
 
 def _rank_dims(q, k, v, cp):

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libcpattn.so")
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libcpattn_checked.so")
 BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
-SOURCES = ["cpattn_api.cu", "window_api.cu", "qk_api.cu", "decode_api.cu"]
+SOURCES = ["cpattn_api.cu", "window_api.cu", "qk_api.cu", "decode_api.cu", "paged_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 
@@ -153,7 +153,7 @@ def build(verbose=False):
             proc.wait()
     if lacks:
         print(f"{BINDING_PATH} is not built ({lacks} is missing): the C library is complete, the Python calls for "
-              "rotations, norms, windows and decoding need it", file=sys.stderr)
+              "rotations, norms, windows, decoding and pages need it", file=sys.stderr)
         return LIB_PATH
     _wait(binding)
     with open(BINDING_PATH + ".txt", "w") as f:

@@ -1,5 +1,5 @@
-// Native half of the Python entry points of the rotary, q/k norm, window and
-// decode calls: checks of the tensors, outputs and workspaces that were not
+// Native half of the Python entry points of the rotary, q/k norm, window,
+// decode and paged calls: checks of the tensors, outputs and workspaces that were not
 // given, and the call into the library, which is passed in as a table of its
 // functions (so that the checked build is reached the same way).
 //
@@ -44,6 +44,11 @@ struct Calls {
   decltype(&cpattn_bwd_window_varlen) bwd_window_varlen;
   decltype(&cpattn_decode_workspace_bytes) decode_bytes;
   decltype(&cpattn_decode) decode;
+  decltype(&cpattn_append_paged) append_paged;
+  decltype(&cpattn_decode_paged_workspace_bytes) decode_paged_bytes;
+  decltype(&cpattn_decode_paged) decode_paged;
+  decltype(&cpattn_decode_shared_workspace_bytes) decode_shared_bytes;
+  decltype(&cpattn_decode_shared) decode_shared;
 };
 
 // ---------------------------------------------------------------- refusals
@@ -575,6 +580,9 @@ PyObject* bwd_window_any(Args& a, bool packed) {
 PyObject* bwd_window(Args& a) { return bwd_window_any(a, false); }
 PyObject* bwd_window_varlen(Args& a) { return bwd_window_any(a, true); }
 
+// A stride of a dimension of one element means nothing.
+int64_t used(int64_t size, int64_t stride) { return size > 1 ? stride : 0; }
+
 PyObject* decode(Args& a) {
   const Calls& calls = a.calls();
   Place place;
@@ -602,13 +610,188 @@ PyObject* decode(Args& a) {
   make(o, q.sizes(), at::kBFloat16, place);
   make(lse, {b, hq}, at::kFloat, place);
   if (!given) ws.make(calls.decode_bytes(int(b), int(hq), int(hkv), int(d), int(cap), window, sinks), place);
-  // a stride of a dimension of one element means nothing
-  const auto used = [](int64_t size, int64_t stride) { return size > 1 ? stride : 0; };
   launch([&] {
     return calls.decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), static_cast<const int*>(lengths), o.data(),
                         static_cast<float*>(lse.data()), ws.data, ws.bytes, int(b), int(hq), int(hkv), int(d), int(cap),
                         used(b, qs[0]), used(b, ks[0]), used(cap, ks[1]), used(hkv, ks[2]), used(b, vs[0]),
                         used(cap, vs[1]), used(hkv, vs[2]), window, sinks, scale, place.handle());
+  });
+  return results({&o, &lse});
+}
+
+// Arguments k_pages, v_pages, tables: a cache in pages of heads of d features
+// (cpattn_pages), with its KV heads and the tables' rows.
+struct Pages {
+  cpattn_pages p{};
+  int64_t hkv = 0, rows = 0, cap = 0;
+};
+Pages read_pages(Args& a, int64_t d, Place& place) {
+  Pages r;
+  const at::Tensor& k = place.on(tensor("k_pages", a.next(), at::kBFloat16));
+  const at::Tensor& v = place.on(tensor("v_pages", a.next(), at::kBFloat16));
+  const at::Tensor& t = place.on(tensor("tables", a.next(), at::kInt));
+  if (k.dim() != 4 || k.size(3) != d || v.sizes() != k.sizes())
+    value_error(text("k_pages and v_pages must be [pages, page_size, hkv, ", d, "]"));
+  const auto ks = k.strides(), vs = v.strides();
+  if (ks[3] != 1 || vs[3] != 1) value_error("the features of the pages must be contiguous");
+  if (t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
+    value_error("tables must be [sequences, columns] with contiguous rows");
+  sizes_fit(k);
+  sizes_fit(t);
+  r.hkv = k.size(2);
+  r.rows = t.size(0);
+  r.cap = t.size(1) * k.size(1);
+  r.p.k = k.data_ptr();
+  r.p.v = v.data_ptr();
+  r.p.pages = int(k.size(0));
+  r.p.page_size = int(k.size(1));
+  r.p.table_cols = int(t.size(1));
+  r.p.tables = t.const_data_ptr<int>();
+  r.p.tables_row = used(t.size(0), t.stride(0));
+  r.p.k_page = used(k.size(0), ks[0]);
+  r.p.k_token = ks[1];
+  r.p.k_head = used(k.size(2), ks[2]);
+  r.p.v_page = used(k.size(0), vs[0]);
+  r.p.v_token = vs[1];
+  r.p.v_head = used(k.size(2), vs[2]);
+  return r;
+}
+
+PyObject* append_paged(Args& a) {
+  const Calls& calls = a.calls();
+  Place place;
+  PyObject* ko = a.next();
+  PyObject* vo = a.next();
+  const cpattn_rows k = rows("k", ko, place);
+  const auto size = THPVariable_Unpack(ko).sizes();
+  const cpattn_rows v = rows("v", vo, size, place);
+  const int64_t b = size[0], n = size[1], hkv = size[2], d = size[3];
+  const Pages pages = read_pages(a, d, place);
+  if (pages.hkv != hkv) value_error(text("the pages hold ", pages.hkv, " KV heads, k has ", hkv));
+  PyObject* lo = a.next();
+  PyObject* cuo = a.next_or_none();
+  int64_t seqs = b;
+  const int* cu = nullptr;
+  if (cuo) {
+    const at::Tensor& t = dense("cu_tokens", cuo, at::kInt, place);
+    if (t.dim() != 1 || t.size(0) < 2 || t.size(0) > INT_MAX) value_error("cu_tokens must hold seqs + 1 offsets, seqs >= 1");
+    if (b != 1) value_error("with cu_tokens, k and v must be [1, n, hkv, d]");
+    cu = t.const_data_ptr<int>();
+    seqs = t.size(0) - 1;
+  }
+  const int* lengths = static_cast<const int*>(dense("lengths", lo, at::kInt, {seqs}, place).data_ptr());
+  if (pages.rows != seqs) value_error(text("tables has ", pages.rows, " rows for ", seqs, " sequences"));
+  PyObject* qo = a.next_or_none();
+  cpattn_rows q{nullptr, 0, 0};
+  std::vector<int64_t> q_size;
+  if (qo) {
+    q = rows("q", qo, place);
+    q_size = THPVariable_Unpack(qo).sizes().vec();
+    if (q_size[0] != b || q_size[1] != n || q_size[3] != d) value_error("q must be [b, n, hq, d] matching k");
+  }
+  const bool rotate = a.integer("rotate") != 0;
+  Plan plan;
+  read_plan(plan, a, calls, b, n, d, place);
+  PyObject* outo = a.next_or_none();
+  if (outo && !qo) value_error("q_out goes with q");
+  Out out = out_rows("q_out", outo, q_size, place);
+  place.stream(a.next_or_none());
+  if (qo) make(out, q_size, at::kBFloat16, place);
+  launch([&] {
+    return calls.append_paged(&k, &v, &pages.p, lengths, cu, int(seqs), qo ? &q : nullptr, qo ? &out.at : nullptr, int(b),
+                              int(n), qo ? int(q_size[2]) : 0, int(hkv), int(d), rotate ? &plan.r : nullptr,
+                              place.handle());
+  });
+  if (qo) return out.take();
+  Py_RETURN_NONE;
+}
+
+// q [b, hq, d] and the pages of its sequences.
+struct PagedInputs {
+  const void* q;
+  const int* lengths;
+  at::IntArrayRef q_size;
+  int b, hq, hkv, d;
+  int64_t q_batch;
+  Pages pages;
+};
+PagedInputs read_paged(Args& a, Place& place) {
+  PagedInputs r;
+  const at::Tensor& q = place.on(tensor("q", a.next(), at::kBFloat16));
+  if (q.dim() != 3) value_error("q must be [b, hq, d]");
+  sizes_fit(q);
+  r.q_size = q.sizes();
+  const auto qs = q.strides();
+  if (qs[2] != 1 || (q.size(1) > 1 && qs[1] != q.size(2))) value_error("q's heads and features must be contiguous");
+  r.q = q.data_ptr();
+  r.b = int(q.size(0));
+  r.hq = int(q.size(1));
+  r.d = int(q.size(2));
+  r.q_batch = used(q.size(0), qs[0]);
+  r.pages = read_pages(a, r.d, place);
+  r.hkv = int(r.pages.hkv);
+  r.lengths = static_cast<const int*>(dense("lengths", a.next(), at::kInt, {r.b}, place).data_ptr());
+  if (r.pages.rows != r.b) value_error(text("tables has ", r.pages.rows, " rows for ", r.b, " sequences"));
+  return r;
+}
+
+PyObject* decode_paged(Args& a) {
+  const Calls& calls = a.calls();
+  Place place;
+  const PagedInputs in = read_paged(a, place);
+  const int window = a.keys(), sinks = a.keys();
+  const float scale = a.scale();
+  Out o = out_dense("o", a.next_or_none(), in.q_size, at::kBFloat16, place);
+  Out lse = out_dense("lse", a.next_or_none(), {in.b, in.hq}, at::kFloat, place);
+  Workspace ws;
+  PyObject* given = a.next_or_none();
+  if (given) ws.given(given, place);
+  place.stream(a.next_or_none());
+  make(o, in.q_size, at::kBFloat16, place);
+  make(lse, {in.b, in.hq}, at::kFloat, place);
+  // a shape that the call refuses needs none
+  if (!given && in.pages.cap <= INT_MAX)
+    ws.make(calls.decode_paged_bytes(in.b, in.hq, in.hkv, in.d, int(in.pages.cap), window, sinks), place);
+  launch([&] {
+    return calls.decode_paged(in.q, &in.pages.p, in.lengths, o.data(), static_cast<float*>(lse.data()), ws.data, ws.bytes,
+                              in.b, in.hq, in.hkv, in.d, in.q_batch, window, sinks, scale, place.handle());
+  });
+  return results({&o, &lse});
+}
+
+PyObject* decode_shared(Args& a) {
+  const Calls& calls = a.calls();
+  Place place;
+  const PagedInputs in = read_paged(a, place);
+  const at::Tensor& shared = dense("shared", a.next(), at::kInt, place);
+  if (shared.dim() != 1 || shared.size(0) < 1 || shared.size(0) > INT_MAX) value_error("shared must hold a count for each group");
+  const int groups = int(shared.size(0));
+  PyObject* offo = a.next_or_none();
+  const int* offsets = nullptr;
+  if (offo)
+    offsets = static_cast<const int*>(dense("group_offsets", offo, at::kInt, {int64_t(groups) + 1}, place).data_ptr());
+  else if (groups != 1)
+    value_error(text("shared holds ", groups, " counts; without group_offsets the batch is one group"));
+  PyObject* most = a.next_or_none();
+  const int max_group = most ? int(Args::integer_of(most, "max_group")) : in.b;
+  const float scale = a.scale();
+  Out o = out_dense("o", a.next_or_none(), in.q_size, at::kBFloat16, place);
+  Out lse = out_dense("lse", a.next_or_none(), {in.b, in.hq}, at::kFloat, place);
+  Workspace ws;
+  PyObject* given = a.next_or_none();
+  if (given) ws.given(given, place);
+  place.stream(a.next_or_none());
+  make(o, in.q_size, at::kBFloat16, place);
+  make(lse, {in.b, in.hq}, at::kFloat, place);
+  if (!given) {
+    // a shape that the call refuses needs none
+    const size_t need = calls.decode_shared_bytes(in.b, in.hq, in.hkv, in.d, groups, max_group);
+    ws.make(need > 0 ? need : 16, place);
+  }
+  launch([&] {
+    return calls.decode_shared(in.q, &in.pages.p, in.lengths, shared.const_data_ptr<int>(), offsets, groups, max_group,
+                               o.data(), static_cast<float*>(lse.data()), ws.data, ws.bytes, in.b, in.hq, in.hkv, in.d,
+                               in.q_batch, scale, place.handle());
   });
   return results({&o, &lse});
 }
@@ -646,6 +829,9 @@ PyMODINIT_FUNC PyInit__binding() {
                                   {"bwd_window", method<bwd_window>(), METH_FASTCALL, nullptr},
                                   {"bwd_window_varlen", method<bwd_window_varlen>(), METH_FASTCALL, nullptr},
                                   {"decode", method<decode>(), METH_FASTCALL, nullptr},
+                                  {"append_paged", method<append_paged>(), METH_FASTCALL, nullptr},
+                                  {"decode_paged", method<decode_paged>(), METH_FASTCALL, nullptr},
+                                  {"decode_shared", method<decode_shared>(), METH_FASTCALL, nullptr},
                                   {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr,
                                nullptr};

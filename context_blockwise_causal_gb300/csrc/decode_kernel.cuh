@@ -26,6 +26,14 @@
 // shared memory: one launch and no workspace. More runs (a few very long
 // sequences) go through device memory and a second kernel.
 //
+// Paged caches (DecodeKind) differ in where a key lies. A page holds a multiple
+// of 16 keys, so blocks that start at whole 16s of a sequence's own numbering
+// lie in one page each: a block costs one look into the table, read a block
+// ahead of the copies that need it, and its first and last keys are masked
+// where the visible ones begin or end inside it. kShared leaves out the keys
+// that a group of sequences has in common (prefix_kernel.cuh) and joins their
+// results in its epilogue, which is all that waits for that kernel.
+//
 // Measured, d128: 64 sequences of up to 16384 tokens, h32/8, window 4096: 154
 // us; 16 of up to 65537, h64/8, whole: 447 to 488 us (both at the measured copy
 // bandwidth and a few percent above it, as reads alone may be); one sequence,
@@ -35,6 +43,7 @@
 
 #include <cstdint>
 
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -44,6 +53,8 @@ constexpr int kDecStages = 3;
 constexpr int kDecBlock = 16;  // keys per block
 constexpr int kDecMaxCluster = 8;  // the portable cluster size
 constexpr int kDecMaxSplit = 64;
+
+enum class DecodeKind { kDense, kPaged, kShared };
 
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [b, hq, D], batch stride q_batch
@@ -61,6 +72,8 @@ struct DecodeArgs {
   int nsplit;
   float scale_log2;
   unsigned int* status;
+  PagedPlace pg;   // kPaged, kShared
+  SharedPlan sh;   // kShared
 };
 
 template <int D>
@@ -117,8 +130,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const DecodeArgs a) {
+template <int D, DecodeKind kKind = DecodeKind::kDense>
+__global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr bool kPaged = kKind != DecodeKind::kDense, kShared = kKind == DecodeKind::kShared;
   if (a.nsplit > kDecMaxCluster) chain_next();
   using C = DecodeCfg<D>;
   constexpr int kPieces = D / 8;          // 16-byte pieces of a row
@@ -139,9 +153,17 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
 
   int n = a.lengths[bi];
   n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
-  const int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
-  const int ns = a.sinks < lo ? a.sinks : lo;
-  const int nk = ns + (n - lo);  // visible keys
+  int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
+  [[maybe_unused]] SharedSeq mate;
+  if constexpr (kShared) {
+    mate = shared_seq(a.sh, bi, n);
+    lo = mate.keys;  // those before it are the prefix kernel's
+  }
+  const int ns = kShared ? 0 : (a.sinks < lo ? a.sinks : lo);
+  // visible keys; paged: 16 times the blocks that hold them, first tokens' and the window's
+  const int sink_blocks = (ns + kDecBlock - 1) / kDecBlock, lo_block = lo / kDecBlock;
+  const int nk = kPaged ? (sink_blocks + (n > lo ? (n + kDecBlock - 1) / kDecBlock - lo_block : 0)) * kDecBlock
+                        : ns + (n - lo);
   // this CTA's run: whole rounds of the warps' blocks
   constexpr int kRound = kDecWarps * kDecBlock;
   const int per = ((nk + a.nsplit - 1) / a.nsplit + kRound - 1) / kRound * kRound;
@@ -158,30 +180,76 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
   // Copies block i of this warp into its stage: lane -> piece lane % kPieces
   // of row lane / kPieces (+ 32 / kPieces per step); piece p of row r sits at
   // p ^ (r & 7), so ldmatrix's eight rows fall into different banks.
-  auto load = [&](int i) {
+  constexpr int kRowsPerStep = 32 / kPieces;
+  // Paged: the block's first key, the keys [from, to) of it that are seen, and its page.
+  auto place = [&](int i, int& from, int& to) {
+    const int vb = begin / kDecBlock + warp + i * kDecWarps;
+    const bool early = vb < sink_blocks;
+    const int key0 = (early ? vb : lo_block + (vb - sink_blocks)) * kDecBlock;
+    from = early || lo < key0 ? 0 : lo - key0;
+    to = (early ? ns : n) - key0;
+    return key0;
+  };
+  [[maybe_unused]] const int* table = nullptr;
+  if constexpr (kPaged) table = a.pg.tables + int64_t(bi) * a.pg.tables_row;
+  auto page_of = [&](int i) {
+    int from, to;
+    return i < mine ? table[unsigned(place(i, from, to)) / unsigned(a.pg.page_size)] : 0;
+  };
+  auto load = [&](int i, [[maybe_unused]] int page) {
     const int v0 = begin + (warp + i * kDecWarps) * kDecBlock;
     const uint32_t dst = ring + (i % kDecStages) * C::kStageBytes;
-    constexpr int kRowsPerStep = 32 / kPieces;
     const int p = lane % kPieces;
+    if constexpr (kPaged) {
+      int from, to;
+      const int key0 = place(i, from, to);
+      const bool held = page_ok(page, a.pg, a.status);
+      const int slot = int(unsigned(key0) % unsigned(a.pg.page_size)) + lane / kPieces;
+      const __nv_bfloat16* ks = kp + (held ? page : 0) * a.pg.k_page + slot * a.k_token + p * 8;
+      const __nv_bfloat16* vs = vp + (held ? page : 0) * a.pg.v_page + slot * a.v_token + p * 8;
 #pragma unroll
-    for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
-      const int r = s * kRowsPerStep + lane / kPieces;
-      const int vis = v0 + r;
-      const bool valid = vis < end;
-      int key = vis < ns ? vis : lo + (vis - ns);
-      if (!valid) key = 0;
-      bounds_ok(key >= 0 && key < a.cap, a.status);
-      const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
-      cp_async16(dst + off, kp + int64_t(key) * a.k_token + p * 8, valid);
-      cp_async16(dst + C::kTileBytes + off, vp + int64_t(key) * a.v_token + p * 8, valid);
+      for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
+        const int r = s * kRowsPerStep + lane / kPieces;
+        const bool valid = held && r >= from && r < to;
+        bounds_ok(!valid || (key0 + r < a.cap && slot + s * kRowsPerStep < a.pg.page_size), a.status);
+        const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
+        cp_async16(dst + off, ks + s * (kRowsPerStep * a.k_token), valid);
+        cp_async16(dst + C::kTileBytes + off, vs + s * (kRowsPerStep * a.v_token), valid);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
+        const int r = s * kRowsPerStep + lane / kPieces;
+        const int vis = v0 + r;
+        const bool valid = vis < end;
+        int key = vis < ns ? vis : lo + (vis - ns);
+        if (!valid) key = 0;
+        bounds_ok(key >= 0 && key < a.cap, a.status);
+        const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
+        cp_async16(dst + off, kp + int64_t(key) * a.k_token + p * 8, valid);
+        cp_async16(dst + C::kTileBytes + off, vp + int64_t(key) * a.v_token + p * 8, valid);
+      }
     }
   };
   // (a group is committed even when there is nothing left to load, so that
   // the wait counts blocks)
+  [[maybe_unused]] int page = 0;
+  if constexpr (kPaged) {
+    int first[kDecStages - 1];
 #pragma unroll
-  for (int i = 0; i < kDecStages - 1; ++i) {
-    if (i < mine) load(i);
-    cp_async_commit();
+    for (int i = 0; i < kDecStages - 1; ++i) first[i] = page_of(i);
+    page = page_of(kDecStages - 1);
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) {
+      if (i < mine) load(i, first[i]);
+      cp_async_commit();
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) {
+      if (i < mine) load(i, 0);
+      cp_async_commit();
+    }
   }
 
   // Q fragments (A operand): rows g4 and g4 + 8; rows past the group's heads are zero
@@ -204,8 +272,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<kDecStages - 2>();
     __syncwarp();  // every lane's copies of block i have landed; stage (i - 1) has been read by all
-    if (i + kDecStages - 1 < mine) load(i + kDecStages - 1);
+    if (i + kDecStages - 1 < mine) load(i + kDecStages - 1, page);
     cp_async_commit();
+    if constexpr (kPaged) page = page_of(i + kDecStages);
     const uint32_t sk = ring + (i % kDecStages) * C::kStageBytes, sv = sk + C::kTileBytes;
     // S = Q K^T: two 8-key column tiles. ldmatrix: lanes 0-7 and 8-15 address
     // keys 0-7 at features +0 and +8, lanes 16-31 keys 8-15.
@@ -223,12 +292,13 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
       }
     }
     // columns 2*c4, +1 (s0: keys 0-7, s1: keys 8-15); [0], [1]: row g4, [2], [3]: row g4 + 8
-    const int left = end - (begin + (warp + i * kDecWarps) * kDecBlock);
+    int from = 0, left = end - (begin + (warp + i * kDecWarps) * kDecBlock);
+    if constexpr (kPaged) place(i, from, left);
     float sc[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int col = 2 * c4 + (e & 1) + ((e >> 1) & 1) * 8;
-      sc[e] = col < left ? sc[e] * a.scale_log2 : -INFINITY;
+      sc[e] = (!kPaged || col >= from) && col < left ? sc[e] * a.scale_log2 : -INFINITY;
     }
     float alpha[2];
 #pragma unroll
@@ -293,6 +363,11 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
     jm[16 + g4] = l[0];
     jm[16 + g4 + 8] = l[1];
   }
+  // the group's common keys (every thread waits: the call is over only when both kernels are)
+  if constexpr (kShared) {
+    chain_wait();
+    if (mate.keys > 0) shared_runs(a.sh, mate);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (D / 2); i += kDecWarps * 32) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
@@ -309,6 +384,9 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
       ll = fmaf(f, p[16 * D + 16 + r], ll);
       o0 = fmaf(f, p[r * D + c], o0);
       o1 = fmaf(f, p[r * D + c + 1], o1);
+    }
+    if constexpr (kShared) {
+      if (a.nsplit == 1) shared_join<D>(a.sh, mate, kvh, (rg * 16 + r), c, a.status, mm, ll, o0, o1);
     }
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
@@ -347,6 +425,7 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
       o0 = fmaf(w, o.x, o0);
       o1 = fmaf(w, o.y, o1);
     }
+    if constexpr (kShared) shared_join<D>(a.sh, mate, kvh, (rg * 16 + r), c, a.status, mm, ll, o0, o1);
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
     *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);

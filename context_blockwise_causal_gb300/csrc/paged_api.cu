@@ -1,0 +1,319 @@
+// C-ABI entry points of the paged cache (include/cpattn.h): new tokens into
+// it, single-token attention over it, and the same for sequences that begin
+// alike.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <numeric>
+
+#include "../../include/cpattn.h"
+#include "api_common.h"
+#include "append_kernel.cuh"
+#include "decode_host.h"
+#include "prefix_kernel.cuh"
+#include "qk_host.h"
+#include "tmap.h"
+
+using namespace cpattn;
+
+namespace {
+
+// Strides of a pool [pages, page_size, hkv, d]: 16-byte pieces, no two
+// elements in one place, and extents that 64-bit offsets and tensor copies hold.
+bool pool_strides_ok(const cpattn_pages* p, int hkv, int d, int64_t page, int64_t token, int64_t head) {
+  struct Dim {
+    int64_t stride, size;
+  } dims[3] = {{page, p->pages}, {token, p->page_size}, {head, hkv}};
+  std::sort(dims, dims + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t span = d;
+  for (const Dim& x : dims) {
+    if (x.size == 1) continue;
+    if (x.stride % 8 != 0 || x.stride < span || x.stride >= int64_t(1) << 38) return false;
+    if (x.size - 1 > ((int64_t(1) << 46) - span) / x.stride) return false;
+    span += x.stride * (x.size - 1);
+  }
+  return true;
+}
+
+int64_t capacity(const cpattn_pages* p) { return int64_t(p->table_cols) * p->page_size; }
+
+int check_pages(const cpattn_pages* p, int hkv, int d) {
+  if (!p || !p->k || !p->v || !p->tables) return CPATTN_ERR_NULL_PTR;
+  if (hkv < 1 || (d != 64 && d != 128)) return CPATTN_ERR_INVALID_ARG;
+  if (p->pages < 1 || p->page_size < 16 || p->page_size % 16 != 0 || p->table_cols < 1 || p->tables_row < 0)
+    return CPATTN_ERR_INVALID_ARG;
+  if (p->page_size > (1 << 30) || capacity(p) > (1 << 30)) return CPATTN_ERR_INVALID_ARG;
+  if (!pool_strides_ok(p, hkv, d, p->k_page, p->k_token, p->k_head) ||
+      !pool_strides_ok(p, hkv, d, p->v_page, p->v_token, p->v_head))
+    return CPATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->k) || !aligned16(p->v) || !aligned4(p->tables)) return CPATTN_ERR_MISALIGNED;
+  return CPATTN_OK;
+}
+
+PagedPlace place_of(const cpattn_pages* p) {
+  PagedPlace r;
+  r.tables = p->tables;
+  r.tables_row = p->tables_row;
+  r.k_page = p->k_page;
+  r.v_page = p->v_page;
+  r.pages = p->pages;
+  r.page_size = p->page_size;
+  return r;
+}
+
+// Shapes of a decode over pages; b * hq * kDecMaxSplit rows fit 32 bits.
+int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int window, int sinks) {
+  if (b < 1 || hq < 1 || hkv < 1 || window < 0 || sinks < 0 || hq % hkv != 0) return CPATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return CPATTN_ERR_INVALID_ARG;
+  if (int64_t(b) * hq * kDecMaxSplit >= (int64_t(1) << 31)) return CPATTN_ERR_INVALID_ARG;
+  return p ? check_pages(p, hkv, d) : CPATTN_OK;
+}
+
+// What the calls' DecodeArgs have in common; o and lse as cpattn_decode.
+void fill_decode(DecodeArgs* a, const void* q, const cpattn_pages* p, const int* lengths, void* o, float* lse, int b,
+                 int hq, int hkv, int d, int64_t q_batch, float scale, DeviceInfo* di) {
+  *a = DecodeArgs{};
+  a->q = static_cast<const __nv_bfloat16*>(q);
+  a->k = static_cast<const __nv_bfloat16*>(p->k);
+  a->v = static_cast<const __nv_bfloat16*>(p->v);
+  a->lengths = lengths;
+  a->o = static_cast<__nv_bfloat16*>(o);
+  a->lse = lse;
+  a->q_batch = q_batch;
+  a->k_token = p->k_token;
+  a->k_head = p->k_head;
+  a->v_token = p->v_token;
+  a->v_head = p->v_head;
+  a->b = b;
+  a->hq = hq;
+  a->hkv = hkv;
+  a->G = hq / hkv;
+  a->cap = int(capacity(p));
+  a->row_groups = (a->G + 15) / 16;
+  a->scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
+  a->status = di->status;
+  a->pg = place_of(p);
+}
+
+int check_pointers(const void* q, const int* lengths, const void* o, const float* lse, const void* workspace,
+                   int64_t q_batch, float scale) {
+  if (!q || !lengths || !o || !lse) return CPATTN_ERR_NULL_PTR;
+  if (!(scale == 0.f || valid_scale(scale)) || q_batch < 0 || q_batch % 8 != 0) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(lengths) || !aligned16(workspace))
+    return CPATTN_ERR_MISALIGNED;
+  return CPATTN_OK;
+}
+
+// Runs of the common keys and where their results go.
+struct SharedShape {
+  int64_t ctas;
+  int part_rows;
+  size_t runs_bytes, lse_bytes, o_bytes;
+  size_t bytes() const { return runs_bytes + lse_bytes + o_bytes; }
+};
+
+// One run per SM, or as many as it takes for the units to be at most half of
+// them (so that runs of about the same length exist, whatever the groups'
+// lengths turn out to be).
+bool shared_shape(SharedShape* s, int num_sms, int hq, int hkv, int d, int groups, int max_group) {
+  const int64_t rows = int64_t(max_group) * (hq / hkv);
+  if (rows >= int64_t(1) << 30) return false;
+  const int64_t units = (rows + kSharedRows - 1) / kSharedRows * hkv * groups;
+  s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
+  if (units >= int64_t(1) << 30 || s->ctas >= int64_t(1) << 31) return false;
+  s->part_rows = rows < kSharedRows ? int((rows + 15) / 16 * 16) : kSharedRows;
+  const size_t parts = size_t(s->ctas) * s->part_rows;
+  s->runs_bytes = align256(size_t(groups) * sizeof(GroupRuns));
+  s->lse_bytes = align256(parts * 4);
+  s->o_bytes = align256(parts * d * 4);
+  return true;
+}
+
+int check_groups(int b, int groups, int max_group) {
+  return groups < 1 || groups > b || max_group < 1 || max_group > b ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
+}
+
+// CTAs per unit of a member's own keys: as for any decode of up to cap keys,
+// within a cluster, whose join also takes in the group's results.
+int own_split(int num_sms, int64_t units, int64_t cap) {
+  const int s = choose_split(num_sms, units, cap);
+  return s < kDecMaxCluster ? s : kDecMaxCluster;
+}
+
+template <int D>
+int launch_prefix(const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!encode_bf16_pages(&tk, p->k, p->pages, p->page_size, a.sh.hkv, D, p->k_page, p->k_token, p->k_head, a.box) ||
+      !encode_bf16_pages(&tv, p->v, p->pages, p->page_size, a.sh.hkv, D, p->v_page, p->v_token, p->v_head, a.box))
+    return CPATTN_ERR_CUDA;
+  std::atomic<bool>& done = di->prefix_attr[D == 128 ? 1 : 0];
+  if (!done.load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(cpattn_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             PrefixCfg<D>::kSmemBytes) != cudaSuccess)
+      return CPATTN_ERR_CUDA;
+    done.store(true, std::memory_order_release);
+  }
+  cpattn_prefix_kernel<D><<<unsigned(a.sh.ctas), kFwdThreads, PrefixCfg<D>::kSmemBytes, st>>>(tk, tv, a);
+  return launched(cudaGetLastError());
+}
+
+template <int D, bool kInter>
+int launch_append(AppendArgs& a, DeviceInfo* di, cudaStream_t st) {
+  constexpr int kRows = 32 / (D / 16), kWarps = kQkThreads / 32;
+  const int64_t heads = int64_t(a.qk.t[0].h) + 2 * int64_t(a.qk.t[1].h);
+  const int64_t groups = (heads + kRows - 1) / kRows;
+  const int64_t tokens = int64_t(a.qk.b) * a.qk.n;
+  // A token's heads stay with one warp (one set of cosines, one look-up) unless
+  // that leaves fewer than eight warps per SM; then they spread over more.
+  const int64_t want = (int64_t(di->num_sms) * 8 + tokens - 1) / tokens;
+  const int64_t split = want < groups ? want : groups;
+  a.qk.heads_per = int((groups + split - 1) / split * kRows);
+  a.qk.split = int((heads + a.qk.heads_per - 1) / a.qk.heads_per);
+  const int64_t ctas = (tokens * a.qk.split + kWarps - 1) / kWarps, most = int64_t(di->num_sms) * 2;  // resident at once
+  cpattn_append_kernel<D, kInter><<<int(ctas < most ? ctas : most), kQkThreads, 0, st>>>(a);
+  return launched(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" int cpattn_append_paged(const cpattn_rows* k, const cpattn_rows* v, const cpattn_pages* pages,
+                                   const int* lengths, const int* cu_tokens, int seqs, const cpattn_rows* q,
+                                   const cpattn_rows* q_out, int b, int n, int hq, int hkv, int d,
+                                   const cpattn_rotary* rotary, void* stream) {
+  if (!k || !v || !lengths || (!q) != (!q_out)) return CPATTN_ERR_NULL_PTR;
+  AppendArgs a = {};
+  int rc;
+  if ((rc = check_pages(pages, hkv, d))) return rc;
+  if (b < 1 || n < 1 || seqs < 1 || hq < 0 || (hq == 0) != (!q)) return CPATTN_ERR_INVALID_ARG;
+  if (cu_tokens ? b != 1 : seqs != b) return CPATTN_ERR_INVALID_ARG;
+  if (seqs > 1 && pages->tables_row < pages->table_cols) return CPATTN_ERR_INVALID_ARG;
+  if (rotary) {
+    // positions: the given ones, or each token's place in its sequence
+    if (rotary->rank >= 0 || rotary->cu_seqlens) return CPATTN_ERR_INVALID_ARG;
+    cpattn_rotary plan = *rotary;
+    plan.s = n;
+    if ((rc = fill_rotary(&plan, b, n, d, 0, &a.qk))) return rc;
+  } else {
+    a.qk.b = b;
+    a.qk.n = n;
+    a.qk.magnitude = 1.f;
+  }
+  if ((rc = check_rows(k, b, n, hkv, d, false)) || (rc = check_rows(v, b, n, hkv, d, false))) return rc;
+  if (q && ((rc = check_rows(q, b, n, hq, d, false)) || (rc = check_rows(q_out, b, n, hq, d, true)))) return rc;
+  if ((int64_t(hq) + 2 * int64_t(hkv)) * d >= kQkMaxFeatures) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned4(lengths) || !aligned4(cu_tokens)) return CPATTN_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  if (q) set_tensor(&a.qk.t[0], q, nullptr, q_out, nullptr, hq);
+  set_tensor(&a.qk.t[1], k, nullptr, k, nullptr, hkv);
+  a.qk.status = di->status;
+  a.v = static_cast<const __nv_bfloat16*>(v->data);
+  a.v_batch = v->batch_stride;
+  a.v_row = v->token_stride;
+  a.k_pool = static_cast<__nv_bfloat16*>(pages->k);
+  a.v_pool = static_cast<__nv_bfloat16*>(pages->v);
+  a.pg = place_of(pages);
+  a.k_token = pages->k_token;
+  a.k_head = pages->k_head;
+  a.v_token = pages->v_token;
+  a.v_head = pages->v_head;
+  a.lengths = lengths;
+  a.cu = cu_tokens;
+  a.seqs = seqs;
+  a.cap = int(capacity(pages));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rotary && rotary->layout == CPATTN_ROPE_INTERLEAVED)
+    return d == 128 ? launch_append<128, true>(a, di, st) : launch_append<64, true>(a, di, st);
+  return d == 128 ? launch_append<128, false>(a, di, st) : launch_append<64, false>(a, di, st);
+}
+
+extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
+  if (check_decode(nullptr, b, hq, hkv, d, window, sinks) || cap < 1 || cap > (1 << 30)) return 0;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di)) return 0;
+  const int64_t units = int64_t(b) * hkv * ((hq / hkv + 15) / 16);
+  return workspace_for(b, hq, d, choose_split(di->num_sms, units, max_keys(cap, window, sinks)));
+}
+
+extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse,
+                                   void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d,
+                                   int64_t q_batch, int window, int sinks, float scale, void* stream) {
+  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
+  if (rc) return rc;
+  if (!pages) return CPATTN_ERR_NULL_PTR;
+  if ((rc = check_decode(pages, b, hq, hkv, d, window, sinks))) return rc;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  DecodeArgs a;
+  fill_decode(&a, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.nsplit = choose_split(di->num_sms, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
+  const size_t need = workspace_for(b, hq, d, a.nsplit);
+  if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
+  if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_decode<128, DecodeKind::kPaged>(a, di, st) : launch_decode<64, DecodeKind::kPaged>(a, di, st);
+}
+
+extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group) {
+  if (check_decode(nullptr, b, hq, hkv, d, 0, 0) || check_groups(b, groups, max_group)) return 0;
+  DeviceInfo* di = nullptr;
+  SharedShape s;
+  if (device_info(&di) || !shared_shape(&s, di->num_sms, hq, hkv, d, groups, max_group)) return 0;
+  return s.bytes();
+}
+
+extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
+                                    const int* group_offsets, int groups, int max_group, void* o, float* lse,
+                                    void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d,
+                                    int64_t q_batch, float scale, void* stream) {
+  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
+  if (rc) return rc;
+  if (!pages || !shared || !workspace) return CPATTN_ERR_NULL_PTR;
+  if ((rc = check_decode(pages, b, hq, hkv, d, 0, 0)) || (rc = check_groups(b, groups, max_group))) return rc;
+  if (!group_offsets && groups != 1) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned4(shared) || !aligned4(group_offsets)) return CPATTN_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  SharedShape shape;
+  if (!shared_shape(&shape, di->num_sms, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < shape.bytes()) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  DecodeArgs a;
+  fill_decode(&a, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  a.nsplit = own_split(di->num_sms, int64_t(b) * hkv * a.row_groups, a.cap);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.sh.lengths = lengths;
+  a.sh.shared = shared;
+  a.sh.offsets = group_offsets;
+  a.sh.groups = groups;
+  a.sh.max_group = max_group;
+  a.sh.b = b;
+  a.sh.hkv = hkv;
+  a.sh.G = a.G;
+  a.sh.cap = a.cap;
+  a.sh.ctas = int(shape.ctas);
+  a.sh.part_rows = shape.part_rows;
+  a.sh.runs = reinterpret_cast<GroupRuns*>(ws);
+  a.sh.part_lse = reinterpret_cast<float*>(ws + shape.runs_bytes);
+  a.sh.part_o = reinterpret_cast<float*>(ws + shape.runs_bytes + shape.lse_bytes);
+  PrefixArgs p;
+  p.sh = a.sh;
+  p.pg = a.pg;
+  p.q = a.q;
+  p.q_batch = q_batch;
+  p.hq = hq;
+  p.box = std::gcd(pages->page_size, kTile);
+  p.scale_log2 = a.scale_log2;
+  p.status = di->status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 128) {
+    if ((rc = launch_prefix<128>(p, pages, di, st))) return rc;
+    return launch_decode<128, DecodeKind::kShared>(a, di, st);
+  }
+  if ((rc = launch_prefix<64>(p, pages, di, st))) return rc;
+  return launch_decode<64, DecodeKind::kShared>(a, di, st);
+}

@@ -515,6 +515,98 @@ int cpattn_decode(const void* q, const void* k_cache, const void* v_cache, const
                   int window, int sinks, float scale, void* stream);
 
 /*
+ * ---- A cache in pages ----
+ *
+ * A page holds page_size tokens (a multiple of 16) of every KV head of one
+ * layer. The pools k and v hold `pages` of them; slot t of KV head h of page g is
+ * at g * page + t * token + h * head elements (strides multiples of 8, no two
+ * rows in one place, so [pages, page_size, hkv, d] and [pages, hkv, page_size,
+ * d] both fit; a stride of a dimension of one element is not looked at).
+ * tables: device int32 [b, table_cols], rows tables_row elements apart: token
+ * t of sequence i is slot t % page_size of page tables[i][t / page_size]. Pages
+ * lie in any order, and sequences may share them. An entry that a call does not
+ * need is not read as a page (a sequence's entries past its length, or of pages
+ * that have left its window, may hold anything). One that it does need and that
+ * names no page of the pools is not followed: its tokens count as zeros, or are
+ * not written, and bit 17 of the device status word is set.
+ * table_cols * page_size, the tokens that a sequence can hold, is 2^30 at most.
+ */
+typedef struct cpattn_pages {
+  void* k;
+  void* v;
+  int pages, page_size, table_cols;
+  const int* tables;
+  int64_t tables_row;
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+} cpattn_pages;
+
+/*
+ * Puts new tokens' keys and values into the pages, the keys rotated, and
+ * rotates the queries beside them.
+ *   k, v:     rows [b, n, hkv, d]: the last n tokens of each of seqs = b
+ *             sequences; or, with cu_tokens, b = 1 and the new tokens of seqs
+ *             sequences one after another, those of sequence i from row
+ *             cu_tokens[i] to cu_tokens[i + 1] - 1 (device int32 [seqs + 1], not
+ *             decreasing; rows before the first and behind the last are left
+ *             out).
+ *   lengths:  device int32 [seqs], tokens held of each sequence with the new
+ *             ones, as for cpattn_decode. Token j of the m new ones of a
+ *             sequence goes to place lengths - m + j; a place below 0 or past the
+ *             table is left out (a length of 0 skips a padded row).
+ *   q, q_out: rows [b, n, hq, d], or both NULL and hq = 0; q_out may be q.
+ *             Every row that belongs to a sequence is rotated, whether or not its
+ *             key had a place; the others are left as they were.
+ *   rotary:   NULL: nothing turns. Otherwise a plan with rank < 0 and no
+ *             cu_seqlens: the given positions, or the tokens' places (s is not
+ *             looked at).
+ * Tokens are written in no order: two new tokens in one place, which tables
+ * that share a page being written can ask for, leave pieces of either there.
+ * Everything else in the pools stays as it was. q, k and v may be parts of
+ * one projection; they may not overlap the pools, nor q_out k or v. Errors as
+ * cpattn_rope_ex.
+ */
+int cpattn_append_paged(const cpattn_rows* k, const cpattn_rows* v, const cpattn_pages* pages, const int* lengths,
+                        const int* cu_tokens, int seqs, const cpattn_rows* q, const cpattn_rows* q_out, int b, int n,
+                        int hq, int hkv, int d, const cpattn_rotary* rotary, void* stream);
+
+/*
+ * cpattn_decode over pages: q, lengths, o, lse, window, sinks, scale and the
+ * workspace as there, with cap = table_cols * page_size. Deterministic.
+ */
+size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, int d, int cap, int window, int sinks);
+int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d, int64_t q_batch,
+                        int window, int sinks, float scale, void* stream);
+
+/*
+ * The same, over every key, for groups of sequences that begin with the same
+ * tokens: a group's common keys are read once for all of its queries.
+ *   shared:   device int32 [groups], tokens that the members of each group have
+ *             in common: those of every member's first pages hold the same keys
+ *             and values (the same pages, or copies). Any counts, 0 too.
+ *   group_offsets: device int32 [groups + 1], not decreasing: group g is
+ *             sequences group_offsets[g] to group_offsets[g + 1] - 1; sequences
+ *             in no group share nothing. NULL with groups = 1: the whole batch
+ *             is one group.
+ *   max_group: members of the largest group (1 to b). A member behind so many
+ *             others of its group, or one that holds fewer tokens than the group
+ *             has in common (a finished sequence's length of 0), shares nothing;
+ *             it is computed as by cpattn_decode_paged, but in few runs.
+ *   workspace: at least cpattn_decode_shared_workspace_bytes(...) bytes (on the
+ *             current device; 0 for a shape or device that is refused), 16-byte
+ *             aligned, contents irrelevant. Calls that may overlap need one each.
+ * shared and group_offsets are read on the device, so a captured call follows
+ * them. Deterministic; bits depend on how the group's keys are cut into runs,
+ * which follows from the counts and the number of SMs. Errors as cpattn_decode,
+ * CUDA where the pools cannot be described to the copy engine.
+ */
+size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group);
+int cpattn_decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
+                         const int* group_offsets, int groups, int max_group, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, int b, int hq, int hkv, int d, int64_t q_batch, float scale,
+                         void* stream);
+
+/*
  * Host helper: the zigzag index map. Fills global_of_local (HOST memory,
  * cp * 2c int64 values, row-major [cp][2c]) with the global token position
  * of virtual rank r's local position u: chunk r then chunk 2cp-1-r, each in
@@ -530,7 +622,7 @@ int cpattn_zigzag_index(int s, int cp, int64_t* global_of_local);
  * forward copies or MMAs still in flight at the end after the time limit (3);
  * the same for the backward kernels (8, 9, 10; 12); a backward kernel's
  * shared memory base not 1024-byte aligned (11); the timeout self-test (16);
- * a bounds test of a checked build failed (20).
+ * a page table named a page outside of the pools (17); a bounds test of a checked build failed (20).
  * A role that gives up makes the others leave too, but every role first waits
  * for the copies and MMAs it already issued, so no kernel frees memory that
  * asynchronous work still writes.

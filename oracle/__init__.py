@@ -41,3 +41,4 @@ from .rope import rope_angles, rope_apply, natural_positions, rank_local_positio
 from .varlen import varlen_attention_forward, varlen_attention_backward  # noqa: F401
 from .window import window_mask, window_attention, decode_attention  # noqa: F401
 from .qk_norm import scaled_frequencies, rotate, norm_rotate, norm_rotate_backward  # noqa: F401
+from .paged import held_tokens, append_tokens  # noqa: F401
