@@ -18,6 +18,16 @@ int check_shape(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
   return CPATTN_OK;
 }
 
+template <int D>
+int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
+  if (!allow_smem(di->decode_attr[D == 128 ? 1 : 0], cpattn_decode_kernel<D>, DecodeCfg<D>::kSmemBytes)) return CPATTN_ERR_CUDA;
+  cudaError_t e = launch_runs(cpattn_decode_kernel<D>, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, a.nsplit,
+                              DecodeCfg<D>::kSmemBytes, false, st, a);
+  if (e == cudaSuccess && a.nsplit > kDecMaxCluster)
+    e = launch_chained(cpattn_decode_join_kernel<D>, (int64_t(a.b) * a.hq + 3) / 4, 128, st, a);
+  return launched(e);
+}
+
 }  // namespace
 
 extern "C" size_t cpattn_decode_workspace_bytes(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
@@ -44,7 +54,7 @@ extern "C" int cpattn_decode(const void* q, const void* k_cache, const void* v_c
     return CPATTN_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
-  DecodeArgs a = {};
+  DecodeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k = static_cast<const __nv_bfloat16*>(k_cache);
   a.v = static_cast<const __nv_bfloat16*>(v_cache);
@@ -76,5 +86,5 @@ extern "C" int cpattn_decode(const void* q, const void* k_cache, const void* v_c
   a.scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
   a.status = di->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_decode<128, DecodeKind::kDense>(a, di, st) : launch_decode<64, DecodeKind::kDense>(a, di, st);
+  return d == 128 ? launch<128>(a, di, st) : launch<64>(a, di, st);
 }

@@ -56,39 +56,39 @@ inline bool strides_ok(int64_t batch, int64_t token, int64_t head) {
   return batch >= 0 && token >= 0 && head >= 0 && batch % 8 == 0 && token % 8 == 0 && head % 8 == 0;
 }
 
-// kShared runs behind the prefix kernel, as launch_chained's second kernels do.
-template <int D, DecodeKind kKind>
-int launch_decode(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
-  std::atomic<bool>& done = di->decode_attr[2 * int(kKind) + (D == 128 ? 1 : 0)];
-  if (!done.load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(cpattn_decode_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             DecodeCfg<D>::kSmemBytes) != cudaSuccess)
-      return CPATTN_ERR_CUDA;
-    done.store(true, std::memory_order_release);
-  }
-  const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
+// A kernel of one CTA per run: clusters of up to 8 runs; `chained`: as
+// launch_chained's second kernels.
+template <class... P, class... A>
+cudaError_t launch_runs(void (*kernel)(P...), int64_t ctas, int nsplit, int smem_bytes, bool chained, cudaStream_t st,
+                        A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kDecWarps * 32);
-  cfg.dynamicSmemBytes = DecodeCfg<D>::kSmemBytes;
+  cfg.dynamicSmemBytes = size_t(smem_bytes);
   cfg.stream = st;
   cudaLaunchAttribute attrs[2];
   cfg.attrs = attrs;
-  if (a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
+  if (nsplit > 1 && nsplit <= kDecMaxCluster) {
     cudaLaunchAttribute& cluster = attrs[cfg.numAttrs++];
     cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = unsigned(a.nsplit);
+    cluster.val.clusterDim.x = unsigned(nsplit);
     cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   }
-  if (kKind == DecodeKind::kShared) {
-    cudaLaunchAttribute& chained = attrs[cfg.numAttrs++];
-    chained.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    chained.val.programmaticStreamSerializationAllowed = 1;
+  if (chained) {
+    cudaLaunchAttribute& behind = attrs[cfg.numAttrs++];
+    behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    behind.val.programmaticStreamSerializationAllowed = 1;
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, cpattn_decode_kernel<D, kKind>, a);
-  if (e == cudaSuccess && a.nsplit > kDecMaxCluster)
-    e = launch_chained(cpattn_decode_join_kernel<D>, (int64_t(a.b) * a.hq + 3) / 4, 128, st, a);
-  return launched(e);
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+// Dynamic shared memory of a kernel, set once per device.
+template <class K>
+bool allow_smem(std::atomic<bool>& done, K kernel, int bytes) {
+  if (done.load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.store(true, std::memory_order_release);
+  return true;
 }
 
 }  // namespace cpattn

@@ -26,14 +26,6 @@
 // shared memory: one launch and no workspace. More runs (a few very long
 // sequences) go through device memory and a second kernel.
 //
-// Paged caches (DecodeKind) differ in where a key lies. A page holds a multiple
-// of 16 keys, so blocks that start at whole 16s of a sequence's own numbering
-// lie in one page each: a block costs one look into the table, read a block
-// ahead of the copies that need it, and its first and last keys are masked
-// where the visible ones begin or end inside it. kShared leaves out the keys
-// that a group of sequences has in common (prefix_kernel.cuh) and joins their
-// results in its epilogue, which is all that waits for that kernel.
-//
 // Measured, d128: 64 sequences of up to 16384 tokens, h32/8, window 4096: 154
 // us; 16 of up to 65537, h64/8, whole: 447 to 488 us (both at the measured copy
 // bandwidth and a few percent above it, as reads alone may be); one sequence,
@@ -43,7 +35,6 @@
 
 #include <cstdint>
 
-#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -53,8 +44,6 @@ constexpr int kDecStages = 3;
 constexpr int kDecBlock = 16;  // keys per block
 constexpr int kDecMaxCluster = 8;  // the portable cluster size
 constexpr int kDecMaxSplit = 64;
-
-enum class DecodeKind { kDense, kPaged, kShared };
 
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [b, hq, D], batch stride q_batch
@@ -72,8 +61,6 @@ struct DecodeArgs {
   int nsplit;
   float scale_log2;
   unsigned int* status;
-  PagedPlace pg;   // kPaged, kShared
-  SharedPlan sh;   // kShared
 };
 
 template <int D>
@@ -130,132 +117,19 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <int D, DecodeKind kKind = DecodeKind::kDense>
-__global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr bool kPaged = kKind != DecodeKind::kDense, kShared = kKind == DecodeKind::kShared;
-  if (a.nsplit > kDecMaxCluster) chain_next();
-  using C = DecodeCfg<D>;
-  constexpr int kPieces = D / 8;          // 16-byte pieces of a row
-  constexpr int kSteps = D / 16;          // 16-feature steps
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g4 = lane >> 2, c4 = lane & 3;
-  // unit: (batch, KV head, group of 16 query rows), then the run of keys
-  int x = blockIdx.x;
-  const int split = x % a.nsplit;
-  x /= a.nsplit;
-  const int rg = x % a.row_groups;
-  x /= a.row_groups;
-  const int kvh = x % a.hkv;
-  const int bi = x / a.hkv;
-  const int rows = a.G - rg * 16 < 16 ? a.G - rg * 16 : 16;  // query heads of this CTA
-  const int h0 = kvh * a.G + rg * 16;
-
-  int n = a.lengths[bi];
-  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
-  int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
-  [[maybe_unused]] SharedSeq mate;
-  if constexpr (kShared) {
-    mate = shared_seq(a.sh, bi, n);
-    lo = mate.keys;  // those before it are the prefix kernel's
-  }
-  const int ns = kShared ? 0 : (a.sinks < lo ? a.sinks : lo);
-  // visible keys; paged: 16 times the blocks that hold them, first tokens' and the window's
-  const int sink_blocks = (ns + kDecBlock - 1) / kDecBlock, lo_block = lo / kDecBlock;
-  const int nk = kPaged ? (sink_blocks + (n > lo ? (n + kDecBlock - 1) / kDecBlock - lo_block : 0)) * kDecBlock
-                        : ns + (n - lo);
-  // this CTA's run: whole rounds of the warps' blocks
-  constexpr int kRound = kDecWarps * kDecBlock;
-  const int per = ((nk + a.nsplit - 1) / a.nsplit + kRound - 1) / kRound * kRound;
-  const int64_t begin64 = int64_t(split) * per;
-  const int begin = begin64 < nk ? int(begin64) : nk;
-  const int end = nk - begin < per ? nk : begin + per;
-  const int blocks = (end - begin + kDecBlock - 1) / kDecBlock;
-  const int mine = blocks > warp ? (blocks - warp + kDecWarps - 1) / kDecWarps : 0;  // blocks of this warp
-
-  const __nv_bfloat16* kp = a.k + int64_t(bi) * a.k_batch + int64_t(kvh) * a.k_head;
-  const __nv_bfloat16* vp = a.v + int64_t(bi) * a.v_batch + int64_t(kvh) * a.v_head;
-  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-
-  // Copies block i of this warp into its stage: lane -> piece lane % kPieces
-  // of row lane / kPieces (+ 32 / kPieces per step); piece p of row r sits at
-  // p ^ (r & 7), so ldmatrix's eight rows fall into different banks.
-  constexpr int kRowsPerStep = 32 / kPieces;
-  // Paged: the block's first key, the keys [from, to) of it that are seen, and its page.
-  auto place = [&](int i, int& from, int& to) {
-    const int vb = begin / kDecBlock + warp + i * kDecWarps;
-    const bool early = vb < sink_blocks;
-    const int key0 = (early ? vb : lo_block + (vb - sink_blocks)) * kDecBlock;
-    from = early || lo < key0 ? 0 : lo - key0;
-    to = (early ? ns : n) - key0;
-    return key0;
-  };
-  [[maybe_unused]] const int* table = nullptr;
-  if constexpr (kPaged) table = a.pg.tables + int64_t(bi) * a.pg.tables_row;
-  auto page_of = [&](int i) {
-    int from, to;
-    return i < mine ? table[unsigned(place(i, from, to)) / unsigned(a.pg.page_size)] : 0;
-  };
-  auto load = [&](int i, [[maybe_unused]] int page) {
-    const int v0 = begin + (warp + i * kDecWarps) * kDecBlock;
-    const uint32_t dst = ring + (i % kDecStages) * C::kStageBytes;
-    const int p = lane % kPieces;
-    if constexpr (kPaged) {
-      int from, to;
-      const int key0 = place(i, from, to);
-      const bool held = page_ok(page, a.pg, a.status);
-      const int slot = int(unsigned(key0) % unsigned(a.pg.page_size)) + lane / kPieces;
-      const __nv_bfloat16* ks = kp + (held ? page : 0) * a.pg.k_page + slot * a.k_token + p * 8;
-      const __nv_bfloat16* vs = vp + (held ? page : 0) * a.pg.v_page + slot * a.v_token + p * 8;
-#pragma unroll
-      for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
-        const int r = s * kRowsPerStep + lane / kPieces;
-        const bool valid = held && r >= from && r < to;
-        bounds_ok(!valid || (key0 + r < a.cap && slot + s * kRowsPerStep < a.pg.page_size), a.status);
-        const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
-        cp_async16(dst + off, ks + s * (kRowsPerStep * a.k_token), valid);
-        cp_async16(dst + C::kTileBytes + off, vs + s * (kRowsPerStep * a.v_token), valid);
-      }
-    } else {
-#pragma unroll
-      for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
-        const int r = s * kRowsPerStep + lane / kPieces;
-        const int vis = v0 + r;
-        const bool valid = vis < end;
-        int key = vis < ns ? vis : lo + (vis - ns);
-        if (!valid) key = 0;
-        bounds_ok(key >= 0 && key < a.cap, a.status);
-        const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
-        cp_async16(dst + off, kp + int64_t(key) * a.k_token + p * 8, valid);
-        cp_async16(dst + C::kTileBytes + off, vp + int64_t(key) * a.v_token + p * 8, valid);
-      }
-    }
-  };
-  // (a group is committed even when there is nothing left to load, so that
-  // the wait counts blocks)
-  [[maybe_unused]] int page = 0;
-  if constexpr (kPaged) {
-    int first[kDecStages - 1];
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) first[i] = page_of(i);
-    page = page_of(kDecStages - 1);
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) {
-      if (i < mine) load(i, first[i]);
-      cp_async_commit();
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) {
-      if (i < mine) load(i, 0);
-      cp_async_commit();
-    }
-  }
-
-  // Q fragments (A operand): rows g4 and g4 + 8; rows past the group's heads are zero
+// A warp's part of a unit: up to 16 query heads as the rows of matrix tiles,
+// their running maximum and sum (rows g4 and g4 + 8 of the lane, the sum of its
+// own columns), and O.
+template <int D>
+struct DecodeRows {
+  static constexpr int kSteps = D / 16;  // 16-feature steps
   uint32_t qf[kSteps][4];
-  {
-    const __nv_bfloat16* qp = a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D;
+  float acc[D / 8][4];
+  float m[2], l[2];
+
+  // Q fragments (A operand) of `rows` heads from `qp`; the rows past them are zero.
+  __device__ __forceinline__ void load(const __nv_bfloat16* qp, int rows) {
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -263,42 +137,36 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const __g
         const int r = g4 + (e & 1) * 8, c = s * 16 + (e >> 1) * 8 + 2 * c4;
         qf[s][e] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + int64_t(r) * D + c) : 0u;
       }
-  }
-  float acc[D / 8][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4, g4 + 8 (l: this thread's columns)
+    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
 
-  for (int i = 0; i < mine; ++i) {
-    cp_async_wait<kDecStages - 2>();
-    __syncwarp();  // every lane's copies of block i have landed; stage (i - 1) has been read by all
-    if (i + kDecStages - 1 < mine) load(i + kDecStages - 1, page);
-    cp_async_commit();
-    if constexpr (kPaged) page = page_of(i + kDecStages);
-    const uint32_t sk = ring + (i % kDecStages) * C::kStageBytes, sv = sk + C::kTileBytes;
+  // One block of 16 keys, those in [from, to) of it visible. kat(r, p), vat(r, p):
+  // shared-memory address of 16-byte piece p of key r.
+  template <class K, class V>
+  __device__ __forceinline__ void block(K kat, V vat, int from, int to, float scale_log2) {
+    const int lane = threadIdx.x & 31, c4 = lane & 3;
     // S = Q K^T: two 8-key column tiles. ldmatrix: lanes 0-7 and 8-15 address
     // keys 0-7 at features +0 and +8, lanes 16-31 keys 8-15.
     float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const int r = (lane & 7) + ((lane >> 4) << 3);
-      const uint32_t row = sk + r * D * 2;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int p = 2 * s + ((lane >> 3) & 1);
         uint32_t kb[4];
-        ldmatrix4(row + ((p ^ (r & 7)) * 16), kb);
+        ldmatrix4(kat(r, 2 * s + ((lane >> 3) & 1)), kb);
         mma_16x8x16(s0, qf[s], kb[0], kb[1]);
         mma_16x8x16(s1, qf[s], kb[2], kb[3]);
       }
     }
     // columns 2*c4, +1 (s0: keys 0-7, s1: keys 8-15); [0], [1]: row g4, [2], [3]: row g4 + 8
-    int from = 0, left = end - (begin + (warp + i * kDecWarps) * kDecBlock);
-    if constexpr (kPaged) place(i, from, left);
     float sc[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int col = 2 * c4 + (e & 1) + ((e >> 1) & 1) * 8;
-      sc[e] = (!kPaged || col >= from) && col < left ? sc[e] * a.scale_log2 : -INFINITY;
+      sc[e] = col >= from && col < to ? sc[e] * scale_log2 : -INFINITY;
     }
     float alpha[2];
 #pragma unroll
@@ -324,12 +192,10 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const __g
     // address the 16 keys at features +0, lanes 16-31 at +8
     {
       const int r = lane & 15;
-      const uint32_t row = sv + r * D * 2;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int p = 2 * s + (lane >> 4);
         uint32_t vb[4];
-        ldmatrix4_trans(row + ((p ^ (r & 7)) * 16), vb);
+        ldmatrix4_trans(vat(r, 2 * s + (lane >> 4)), vb);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           float(&c)[4] = acc[2 * s + t];
@@ -341,95 +207,191 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const __g
         }
       }
     }
+  }
+
+  // For the join of the CTA's warps: O [16][D], then m[16] and l[16], at jo.
+  __device__ __forceinline__ void store(float* jo) {
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    float* jm = jo + 16 * D;
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) {
+      *reinterpret_cast<float2*>(jo + g4 * D + t * 8 + 2 * c4) = make_float2(acc[t][0], acc[t][1]);
+      *reinterpret_cast<float2*>(jo + (g4 + 8) * D + t * 8 + 2 * c4) = make_float2(acc[t][2], acc[t][3]);
+    }
+    if (c4 == 0) {
+      jm[g4] = m[0];
+      jm[g4 + 8] = m[1];
+      jm[16 + g4] = l[0];
+      jm[16 + g4 + 8] = l[1];
+    }
+  }
+};
+
+// A row's result in two features: values, and their log-sum-exp in base 2.
+struct DecodeResult {
+  float o0, o1, l2;
+};
+// Joins the warps' parts of row r at features c, c + 1; those of warp w lie at
+// smem + w * warp_bytes.
+template <int D>
+__device__ __forceinline__ DecodeResult decode_join_warps(const uint8_t* smem, int warp_bytes, int r, int c) {
+  float mm = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w)
+    mm = fmaxf(mm, reinterpret_cast<const float*>(smem + w * warp_bytes)[16 * D + r]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    const float* p = reinterpret_cast<const float*>(smem + w * warp_bytes);
+    const float f = ex2_approx(p[16 * D + r] - base);
+    ll = fmaf(f, p[16 * D + 16 + r], ll);
+    o0 = fmaf(f, p[r * D + c], o0);
+    o1 = fmaf(f, p[r * D + c + 1], o1);
+  }
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  return {o0 * inv, o1 * inv, ll == 0.f ? -INFINITY : mm + log2f(ll)};
+}
+// Joins the results of a cluster's n CTAs, each at shared-memory address res: O [16][D], then the 16 l2.
+template <int D>
+__device__ __forceinline__ DecodeResult decode_join_cluster(uint32_t res, int n, int r, int c) {
+  float mm = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) mm = fmaxf(mm, cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float w = ex2_approx(cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)) - base);
+    const float2 o = cluster_ld2(cluster_addr(res + (r * D + c) * 4, s));
+    ll += w;
+    o0 = fmaf(w, o.x, o0);
+    o1 = fmaf(w, o.y, o1);
+  }
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  return {o0 * inv, o1 * inv, ll == 0.f ? -INFINITY : mm + log2f(ll)};
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D>
+__global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const DecodeArgs a) {
+  if (a.nsplit > kDecMaxCluster) chain_next();
+  using C = DecodeCfg<D>;
+  constexpr int kPieces = D / 8;          // 16-byte pieces of a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // unit: (batch, KV head, group of 16 query rows), then the run of keys
+  int x = blockIdx.x;
+  const int split = x % a.nsplit;
+  x /= a.nsplit;
+  const int rg = x % a.row_groups;
+  x /= a.row_groups;
+  const int kvh = x % a.hkv;
+  const int bi = x / a.hkv;
+  const int rows = a.G - rg * 16 < 16 ? a.G - rg * 16 : 16;  // query heads of this CTA
+  const int h0 = kvh * a.G + rg * 16;
+
+  int n = a.lengths[bi];
+  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+  const int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
+  const int ns = a.sinks < lo ? a.sinks : lo;
+  const int nk = ns + (n - lo);  // visible keys
+  // this CTA's run: whole rounds of the warps' blocks
+  constexpr int kRound = kDecWarps * kDecBlock;
+  const int per = ((nk + a.nsplit - 1) / a.nsplit + kRound - 1) / kRound * kRound;
+  const int64_t begin64 = int64_t(split) * per;
+  const int begin = begin64 < nk ? int(begin64) : nk;
+  const int end = nk - begin < per ? nk : begin + per;
+  const int blocks = (end - begin + kDecBlock - 1) / kDecBlock;
+  const int mine = blocks > warp ? (blocks - warp + kDecWarps - 1) / kDecWarps : 0;  // blocks of this warp
+
+  const __nv_bfloat16* kp = a.k + int64_t(bi) * a.k_batch + int64_t(kvh) * a.k_head;
+  const __nv_bfloat16* vp = a.v + int64_t(bi) * a.v_batch + int64_t(kvh) * a.v_head;
+  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
+
+  // Copies block i of this warp into its stage: lane -> piece lane % kPieces
+  // of row lane / kPieces (+ 32 / kPieces per step); piece p of row r sits at
+  // p ^ (r & 7), so ldmatrix's eight rows fall into different banks.
+  auto load = [&](int i) {
+    const int v0 = begin + (warp + i * kDecWarps) * kDecBlock;
+    const uint32_t dst = ring + (i % kDecStages) * C::kStageBytes;
+    constexpr int kRowsPerStep = 32 / kPieces;
+    const int p = lane % kPieces;
+#pragma unroll
+    for (int s = 0; s < kDecBlock / kRowsPerStep; ++s) {
+      const int r = s * kRowsPerStep + lane / kPieces;
+      const int vis = v0 + r;
+      const bool valid = vis < end;
+      int key = vis < ns ? vis : lo + (vis - ns);
+      if (!valid) key = 0;
+      bounds_ok(key >= 0 && key < a.cap, a.status);
+      const uint32_t off = uint32_t(r * D * 2 + ((p ^ (r & 7)) * 16));
+      cp_async16(dst + off, kp + int64_t(key) * a.k_token + p * 8, valid);
+      cp_async16(dst + C::kTileBytes + off, vp + int64_t(key) * a.v_token + p * 8, valid);
+    }
+  };
+  // (a group is committed even when there is nothing left to load, so that
+  // the wait counts blocks)
+#pragma unroll
+  for (int i = 0; i < kDecStages - 1; ++i) {
+    if (i < mine) load(i);
+    cp_async_commit();
+  }
+
+  DecodeRows<D> rows_of;
+  rows_of.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
+
+  for (int i = 0; i < mine; ++i) {
+    cp_async_wait<kDecStages - 2>();
+    __syncwarp();  // every lane's copies of block i have landed; stage (i - 1) has been read by all
+    if (i + kDecStages - 1 < mine) load(i + kDecStages - 1);
+    cp_async_commit();
+    const uint32_t sk = ring + (i % kDecStages) * C::kStageBytes, sv = sk + C::kTileBytes;
+    const int left = end - (begin + (warp + i * kDecWarps) * kDecBlock);
+    const auto at = [](uint32_t tile) {
+      return [tile](int r, int p) { return tile + r * D * 2 + ((p ^ (r & 7)) * 16); };
+    };
+    rows_of.block(at(sk), at(sv), 0, left, a.scale_log2);
     __syncwarp();  // all lanes have read the stage before the next turn refills it
   }
   cp_async_wait<0>();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-  }
   __syncthreads();  // the rings are idle: reuse them for the join
-  float* jo = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);  // [16][D], then m[16], l[16]
-  float* jm = jo + 16 * D;
-#pragma unroll
-  for (int t = 0; t < D / 8; ++t) {
-    *reinterpret_cast<float2*>(jo + g4 * D + t * 8 + 2 * c4) = make_float2(acc[t][0], acc[t][1]);
-    *reinterpret_cast<float2*>(jo + (g4 + 8) * D + t * 8 + 2 * c4) = make_float2(acc[t][2], acc[t][3]);
-  }
-  if (c4 == 0) {
-    jm[g4] = m[0];
-    jm[g4 + 8] = m[1];
-    jm[16 + g4] = l[0];
-    jm[16 + g4 + 8] = l[1];
-  }
-  // the group's common keys (every thread waits: the call is over only when both kernels are)
-  if constexpr (kShared) {
-    chain_wait();
-    if (mate.keys > 0) shared_runs(a.sh, mate);
-  }
+  rows_of.store(reinterpret_cast<float*>(smem + warp * C::kWarpBytes));
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (D / 2); i += kDecWarps * 32) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w)
-      mm = fmaxf(mm, reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[16 * D + r]);
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float* p = reinterpret_cast<const float*>(smem + w * C::kWarpBytes);
-      const float f = ex2_approx(p[16 * D + r] - base);
-      ll = fmaf(f, p[16 * D + 16 + r], ll);
-      o0 = fmaf(f, p[r * D + c], o0);
-      o1 = fmaf(f, p[r * D + c + 1], o1);
-    }
-    if constexpr (kShared) {
-      if (a.nsplit == 1) shared_join<D>(a.sh, mate, kvh, (rg * 16 + r), c, a.status, mm, ll, o0, o1);
-    }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const DecodeResult x = decode_join_warps<D>(smem, C::kWarpBytes, r, c);
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
-    const float l2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
     if (!bounds_ok(bi < a.b && h0 + r < a.hq, a.status)) continue;
     if (a.nsplit == 1) {
-      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);
-      if (c == 0) a.lse[row] = l2 * 0.69314718055994530942f;
+      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(x.o0, x.o1);
+      if (c == 0) a.lse[row] = x.l2 * kLn2;
     } else if (a.nsplit <= kDecMaxCluster) {
       float* res = reinterpret_cast<float*>(smem + C::kResult);
-      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(o0 * inv, o1 * inv);
-      if (c == 0) res[16 * D + r] = l2;
+      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(x.o0, x.o1);
+      if (c == 0) res[16 * D + r] = x.l2;
     } else {
       const int64_t pr = row * a.nsplit + split;
-      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(o0 * inv, o1 * inv);
-      if (c == 0) a.part_lse[pr] = l2;
+      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(x.o0, x.o1);
+      if (c == 0) a.part_lse[pr] = x.l2;
     }
   }
   if (a.nsplit == 1 || a.nsplit > kDecMaxCluster) return;
   // The cluster's CTAs are the runs of one unit, in order: each joins its
   // share of the unit's features.
   cluster_sync();
-  const uint32_t res = smem_u32(smem) + C::kResult;
   for (int i = split * kDecWarps * 32 + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kDecWarps * 32) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    float mm = -INFINITY;
-#pragma unroll 4
-    for (int s = 0; s < a.nsplit; ++s) mm = fmaxf(mm, cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)));
-    const float base = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < a.nsplit; ++s) {
-      const float w = ex2_approx(cluster_ld(cluster_addr(res + (16 * D + r) * 4, s)) - base);
-      const float2 o = cluster_ld2(cluster_addr(res + (r * D + c) * 4, s));
-      ll += w;
-      o0 = fmaf(w, o.x, o0);
-      o1 = fmaf(w, o.y, o1);
-    }
-    if constexpr (kShared) shared_join<D>(a.sh, mate, kvh, (rg * 16 + r), c, a.status, mm, ll, o0, o1);
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const DecodeResult x = decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c);
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
-    *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);
-    if (c == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(x.o0, x.o1);
+    if (c == 0) a.lse[row] = x.l2 * kLn2;
   }
   cluster_sync();  // no CTA leaves while another still reads its results
 }
@@ -467,7 +429,7 @@ __global__ void __launch_bounds__(128) cpattn_decode_join_kernel(const DecodeArg
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
     *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
+  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 }  // namespace cpattn

@@ -47,6 +47,7 @@ struct SharedPlan {
   const int* offsets;  // nullptr: the whole batch is one group
   int groups, max_group;
   int b, hkv, G, cap;
+  float token_bytes;  // of a token's key and value in one KV head
   int ctas;       // runs at most
   int part_rows;  // rows kept of each CTA
   GroupRuns* runs;
@@ -107,36 +108,12 @@ __device__ __forceinline__ void shared_runs(const SharedPlan& s, SharedSeq& r) {
   r.at = {v.x, v.y};
 }
 
-// Joins the group's results to a row's own: mm, ll and two features c, c + 1
-// of the sum that belongs to them (ll 0: none). `head`: query head within the
-// KV head's.
-template <int D>
-__device__ __forceinline__ void shared_join(const SharedPlan& s, const SharedSeq& r, int kvh, int head, int c,
-                                            unsigned int* status, float& mm, float& ll, float& o0, float& o1) {
-  if (r.keys == 0) return;
+// Where the first run's result of a row stands (those of the other runs part_rows
+// apart). `head`: query head within the KV head's.
+__device__ __forceinline__ int64_t shared_at(const SharedPlan& s, const SharedSeq& r, int kvh, int head) {
   const int row = r.member * s.G + head;
   const int64_t cta = r.at.first + int64_t(kvh * r.units + row / kSharedRows) * r.at.runs;
-  if (!bounds_ok(cta + r.at.runs <= s.ctas && row % kSharedRows < s.part_rows, status)) return;
-  const int64_t at = cta * s.part_rows + row % kSharedRows;
-  const float* pl = s.part_lse + at;
-  const float* po = s.part_o + at * D + c;
-  float m2 = mm;
-#pragma unroll 4
-  for (int i = 0; i < r.at.runs; ++i) m2 = fmaxf(m2, __ldcg(pl + int64_t(i) * s.part_rows));
-  const float base = m2 == -INFINITY ? 0.f : m2;
-  const float own = ex2_approx(mm - base);
-  ll *= own;
-  o0 *= own;
-  o1 *= own;
-#pragma unroll 4
-  for (int i = 0; i < r.at.runs; ++i) {
-    const float w = ex2_approx(__ldcg(pl + int64_t(i) * s.part_rows) - base);
-    const float2 o = __ldcg(reinterpret_cast<const float2*>(po + int64_t(i) * s.part_rows * D));
-    ll += w;
-    o0 = fmaf(w, o.x, o0);
-    o1 = fmaf(w, o.y, o1);
-  }
-  mm = m2;
+  return cta * s.part_rows + row % kSharedRows;
 }
 
 }  // namespace cpattn

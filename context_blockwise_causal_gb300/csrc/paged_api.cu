@@ -11,6 +11,7 @@
 #include "api_common.h"
 #include "append_kernel.cuh"
 #include "decode_host.h"
+#include "paged_kernel.cuh"
 #include "prefix_kernel.cuh"
 #include "qk_host.h"
 #include "tmap.h"
@@ -70,21 +71,16 @@ int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int windo
   return p ? check_pages(p, hkv, d) : CPATTN_OK;
 }
 
-// What the calls' DecodeArgs have in common; o and lse as cpattn_decode.
-void fill_decode(DecodeArgs* a, const void* q, const cpattn_pages* p, const int* lengths, void* o, float* lse, int b,
+// What the calls' arguments have in common; o and lse as cpattn_decode.
+void fill_decode(PagedArgs* pa, const void* q, const cpattn_pages* p, const int* lengths, void* o, float* lse, int b,
                  int hq, int hkv, int d, int64_t q_batch, float scale, DeviceInfo* di) {
-  *a = DecodeArgs{};
+  *pa = PagedArgs{};
+  DecodeArgs* a = &pa->d;
   a->q = static_cast<const __nv_bfloat16*>(q);
-  a->k = static_cast<const __nv_bfloat16*>(p->k);
-  a->v = static_cast<const __nv_bfloat16*>(p->v);
   a->lengths = lengths;
   a->o = static_cast<__nv_bfloat16*>(o);
   a->lse = lse;
   a->q_batch = q_batch;
-  a->k_token = p->k_token;
-  a->k_head = p->k_head;
-  a->v_token = p->v_token;
-  a->v_head = p->v_head;
   a->b = b;
   a->hq = hq;
   a->hkv = hkv;
@@ -93,7 +89,7 @@ void fill_decode(DecodeArgs* a, const void* q, const cpattn_pages* p, const int*
   a->row_groups = (a->G + 15) / 16;
   a->scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
   a->status = di->status;
-  a->pg = place_of(p);
+  pa->pg = place_of(p);
 }
 
 int check_pointers(const void* q, const int* lengths, const void* o, const float* lse, const void* workspace,
@@ -109,14 +105,15 @@ int check_pointers(const void* q, const int* lengths, const void* o, const float
 struct SharedShape {
   int64_t ctas;
   int part_rows;
-  size_t runs_bytes, lse_bytes, o_bytes;
-  size_t bytes() const { return runs_bytes + lse_bytes + o_bytes; }
+  size_t runs_bytes, lse_bytes, o_bytes, own_lse_bytes, own_o_bytes;
+  // (results are stored in whole sectors, so the parts begin at the first multiple of 256)
+  size_t bytes() const { return 256 + runs_bytes + lse_bytes + o_bytes + own_lse_bytes + own_o_bytes; }
 };
 
 // One run per SM, or as many as it takes for the units to be at most half of
 // them (so that runs of about the same length exist, whatever the groups'
 // lengths turn out to be).
-bool shared_shape(SharedShape* s, int num_sms, int hq, int hkv, int d, int groups, int max_group) {
+bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
   const int64_t rows = int64_t(max_group) * (hq / hkv);
   if (rows >= int64_t(1) << 30) return false;
   const int64_t units = (rows + kSharedRows - 1) / kSharedRows * hkv * groups;
@@ -127,6 +124,8 @@ bool shared_shape(SharedShape* s, int num_sms, int hq, int hkv, int d, int group
   s->runs_bytes = align256(size_t(groups) * sizeof(GroupRuns));
   s->lse_bytes = align256(parts * 4);
   s->o_bytes = align256(parts * d * 4);
+  s->own_lse_bytes = align256(size_t(b) * hq * 4);
+  s->own_o_bytes = align256(size_t(b) * hq * d * 4);
   return true;
 }
 
@@ -141,21 +140,38 @@ int own_split(int num_sms, int64_t units, int64_t cap) {
   return s < kDecMaxCluster ? s : kDecMaxCluster;
 }
 
-template <int D>
-int launch_prefix(const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+// Descriptors of the pools for copies of `box` tokens.
+bool encode_pools(CUtensorMap* tk, CUtensorMap* tv, const cpattn_pages* p, int hkv, int d, int box) {
+  return encode_bf16_pages(tk, p->k, p->pages, p->page_size, hkv, d, p->k_page, p->k_token, p->k_head, box) &&
+         encode_bf16_pages(tv, p->v, p->pages, p->page_size, hkv, d, p->v_page, p->v_token, p->v_head, box);
+}
+
+template <int D, bool kOwn>
+int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  const DecodeArgs& a = pa.d;
+  const auto kernel = cpattn_decode_paged_kernel<D, kOwn>;
   CUtensorMap tk, tv;
-  if (!encode_bf16_pages(&tk, p->k, p->pages, p->page_size, a.sh.hkv, D, p->k_page, p->k_token, p->k_head, a.box) ||
-      !encode_bf16_pages(&tv, p->v, p->pages, p->page_size, a.sh.hkv, D, p->v_page, p->v_token, p->v_head, a.box))
+  if (!encode_pools(&tk, &tv, p, a.hkv, D, kDecBlock) ||
+      !allow_smem(di->paged_attr[(kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel, PagedCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
-  std::atomic<bool>& done = di->prefix_attr[D == 128 ? 1 : 0];
-  if (!done.load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(cpattn_prefix_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             PrefixCfg<D>::kSmemBytes) != cudaSuccess)
-      return CPATTN_ERR_CUDA;
-    done.store(true, std::memory_order_release);
-  }
+  cudaError_t e = launch_runs(kernel, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, a.nsplit, PagedCfg<D>::kSmemBytes,
+                              kOwn, st, tk, tv, pa);
+  const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
+  if (e == cudaSuccess && kOwn) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
+  if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
+    e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
+  return launched(e);
+}
+
+template <int D>
+int launch_shared(const PagedArgs& pa, const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  CUtensorMap tk, tv;
+  if (!encode_pools(&tk, &tv, p, a.sh.hkv, D, a.box) ||
+      !allow_smem(di->prefix_attr[D == 128 ? 1 : 0], cpattn_prefix_kernel<D>, PrefixCfg<D>::kSmemBytes))
+    return CPATTN_ERR_CUDA;
   cpattn_prefix_kernel<D><<<unsigned(a.sh.ctas), kFwdThreads, PrefixCfg<D>::kSmemBytes, st>>>(tk, tv, a);
-  return launched(cudaGetLastError());
+  const int rc = launched(cudaGetLastError());
+  return rc ? rc : launch_paged<D, true>(pa, p, di, st);
 }
 
 template <int D, bool kInter>
@@ -245,8 +261,9 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   if ((rc = check_decode(pages, b, hq, hkv, d, window, sinks))) return rc;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
-  DecodeArgs a;
-  fill_decode(&a, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  PagedArgs pa;
+  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  DecodeArgs& a = pa.d;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
   a.nsplit = choose_split(di->num_sms, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
@@ -256,14 +273,14 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_decode<128, DecodeKind::kPaged>(a, di, st) : launch_decode<64, DecodeKind::kPaged>(a, di, st);
+  return d == 128 ? launch_paged<128, false>(pa, pages, di, st) : launch_paged<64, false>(pa, pages, di, st);
 }
 
 extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group) {
   if (check_decode(nullptr, b, hq, hkv, d, 0, 0) || check_groups(b, groups, max_group)) return 0;
   DeviceInfo* di = nullptr;
   SharedShape s;
-  if (device_info(&di) || !shared_shape(&s, di->num_sms, hq, hkv, d, groups, max_group)) return 0;
+  if (device_info(&di) || !shared_shape(&s, di->num_sms, b, hq, hkv, d, groups, max_group)) return 0;
   return s.bytes();
 }
 
@@ -280,40 +297,46 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
   SharedShape shape;
-  if (!shared_shape(&shape, di->num_sms, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
+  if (!shared_shape(&shape, di->num_sms, b, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
   if (workspace_bytes < shape.bytes()) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
-  DecodeArgs a;
-  fill_decode(&a, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  PagedArgs pa;
+  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  DecodeArgs& a = pa.d;
   a.nsplit = own_split(di->num_sms, int64_t(b) * hkv * a.row_groups, a.cap);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.sh.lengths = lengths;
-  a.sh.shared = shared;
-  a.sh.offsets = group_offsets;
-  a.sh.groups = groups;
-  a.sh.max_group = max_group;
-  a.sh.b = b;
-  a.sh.hkv = hkv;
-  a.sh.G = a.G;
-  a.sh.cap = a.cap;
-  a.sh.ctas = int(shape.ctas);
-  a.sh.part_rows = shape.part_rows;
-  a.sh.runs = reinterpret_cast<GroupRuns*>(ws);
-  a.sh.part_lse = reinterpret_cast<float*>(ws + shape.runs_bytes);
-  a.sh.part_o = reinterpret_cast<float*>(ws + shape.runs_bytes + shape.lse_bytes);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
+  const auto take = [&ws](size_t bytes) {
+    uint8_t* at = ws;
+    ws += bytes;
+    return at;
+  };
+  SharedPlan& sh = pa.sh;
+  sh.lengths = lengths;
+  sh.shared = shared;
+  sh.offsets = group_offsets;
+  sh.groups = groups;
+  sh.max_group = max_group;
+  sh.b = b;
+  sh.hkv = hkv;
+  sh.G = a.G;
+  sh.cap = a.cap;
+  sh.token_bytes = float(4 * d);
+  sh.ctas = int(shape.ctas);
+  sh.part_rows = shape.part_rows;
+  sh.runs = reinterpret_cast<GroupRuns*>(take(shape.runs_bytes));
+  sh.part_lse = reinterpret_cast<float*>(take(shape.lse_bytes));
+  sh.part_o = reinterpret_cast<float*>(take(shape.o_bytes));
+  pa.own_lse = reinterpret_cast<float*>(take(shape.own_lse_bytes));
+  pa.own_o = reinterpret_cast<float*>(take(shape.own_o_bytes));
   PrefixArgs p;
-  p.sh = a.sh;
-  p.pg = a.pg;
+  p.sh = sh;
+  p.pg = pa.pg;
   p.q = a.q;
   p.q_batch = q_batch;
   p.hq = hq;
+  p.sms = di->num_sms;
   p.box = std::gcd(pages->page_size, kTile);
   p.scale_log2 = a.scale_log2;
   p.status = di->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 128) {
-    if ((rc = launch_prefix<128>(p, pages, di, st))) return rc;
-    return launch_decode<128, DecodeKind::kShared>(a, di, st);
-  }
-  if ((rc = launch_prefix<64>(p, pages, di, st))) return rc;
-  return launch_decode<64, DecodeKind::kShared>(a, di, st);
+  return d == 128 ? launch_shared<128>(pa, p, pages, di, st) : launch_shared<64>(pa, p, pages, di, st);
 }

@@ -1,0 +1,274 @@
+// Single-token attention over a cache in pages (paged.cuh), whole or with a
+// sliding window and visible first tokens; and the same over the keys that a
+// sequence does not share with its group (prefix_kernel.cuh), with the join of
+// the two.
+//
+// Mathematics, tiles and joins are those of decode_kernel.cuh; what differs is
+// how keys come. A page holds a multiple of 16 tokens, so a block of 16 that
+// starts at a whole 16 of the sequence's own numbering lies in one page: a
+// block is a few boxes (16 tokens x 64 features) that one lane asks the copy
+// engine for, instead of 16 addresses and copies by each of 32 lanes, and the
+// table is looked up once per block, a block ahead of the copy that needs it.
+// The first and last keys of what is visible are masked inside their blocks:
+// scores by the mask, and values, whose product with a weight of zero would
+// still be NaN if they are not finite, by zeros written over them.
+#pragma once
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "decode_kernel.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace cpattn {
+
+constexpr unsigned int kStatusCopies = 1u << 4;  // copies of a paged decode did not arrive in time
+
+struct PagedArgs {
+  DecodeArgs d;  // k and v are not used (the copies' descriptors name the pools)
+  PagedPlace pg;
+  SharedPlan sh;  // kOwn
+  float* own_o;   // kOwn: [b, hq, D] normalised
+  float* own_lse; // [b, hq], base 2
+};
+
+template <int D>
+struct PagedCfg {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kBoxBytes = kDecBlock * 128;  // 64 features
+  static constexpr int kTileBytes = kDecBlock * D * 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kOffBar = kDecWarps * kWarpBytes;
+  static constexpr int kOffFlag = kOffBar + kDecWarps * kStages * 8;
+  static constexpr int kSmemBytes = kOffFlag + 16 + 1024;  // + alignment slack
+  static constexpr int kResult = 16 * D * 4 + 16 * 8;      // as DecodeCfg
+  static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
+};
+
+template <int D, bool kOwn>
+__global__ void __launch_bounds__(kDecWarps * 32)
+    cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                               const __grid_constant__ PagedArgs pa) {
+  const DecodeArgs& a = pa.d;
+  if (kOwn || a.nsplit > kDecMaxCluster) chain_next();
+  using C = PagedCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag) + warp;  // warps wait for their own copies only
+  if (lane == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+    fence_mbar_init();
+  }
+  // unit: (batch, KV head, group of 16 query rows), then the run of keys
+  int x = blockIdx.x;
+  const int split = x % a.nsplit;
+  x /= a.nsplit;
+  const int rg = x % a.row_groups;
+  x /= a.row_groups;
+  const int kvh = x % a.hkv;
+  const int bi = x / a.hkv;
+  const int rows = a.G - rg * 16 < 16 ? a.G - rg * 16 : 16;  // query heads of this CTA
+  const int h0 = kvh * a.G + rg * 16;
+
+  int n = a.lengths[bi];
+  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+  int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
+  if constexpr (kOwn) lo = shared_seq(pa.sh, bi, n).keys;    // those before it are the prefix kernel's
+  const int ns = kOwn ? 0 : (a.sinks < lo ? a.sinks : lo);
+  // blocks that hold visible keys: the first tokens', then the window's
+  const int sink_blocks = (ns + kDecBlock - 1) / kDecBlock, lo_block = lo / kDecBlock;
+  const int all = sink_blocks + (n > lo ? (n + kDecBlock - 1) / kDecBlock - lo_block : 0);
+  // this CTA's run: whole rounds of the warps
+  const int per = ((all + a.nsplit - 1) / a.nsplit + kDecWarps - 1) / kDecWarps * kDecWarps;
+  const int64_t begin64 = int64_t(split) * per;
+  const int begin = begin64 < all ? int(begin64) : all;
+  const int blocks = all - begin < per ? all - begin : per;
+  const int mine = blocks > warp ? (blocks - warp + kDecWarps - 1) / kDecWarps : 0;  // blocks of this warp
+
+  uint8_t* ring = smem + warp * C::kWarpBytes;
+  const int* table = pa.pg.tables + int64_t(bi) * pa.pg.tables_row;
+  // Block i of this warp: its first key, and the keys [from, to) of it that are seen.
+  const auto place = [&](int i, int& from, int& to) {
+    const int vb = begin + warp + i * kDecWarps;
+    const bool early = vb < sink_blocks;
+    const int key0 = (early ? vb : lo_block + (vb - sink_blocks)) * kDecBlock;
+    from = early || lo < key0 ? 0 : lo - key0;
+    to = (early ? ns : n) - key0;
+    return key0;
+  };
+  const auto page_of = [&](int i) {
+    int from, to;
+    return i < mine ? table[unsigned(place(i, from, to)) / unsigned(pa.pg.page_size)] : 0;
+  };
+  const auto load = [&](int i, int page) {
+    int from, to;
+    const int key0 = place(i, from, to);
+    const int at = int(unsigned(key0) % unsigned(pa.pg.page_size));
+    if (lane == 0) {
+      page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
+      bounds_ok(key0 >= 0 && key0 < a.cap && at + kDecBlock <= pa.pg.page_size && kvh < a.hkv, a.status);
+      uint64_t* bar = &full[i % C::kStages];
+      uint8_t* dst = ring + (i % C::kStages) * C::kStageBytes;
+      mbar_arrive_expect_tx(bar, C::kStageBytes);
+#pragma unroll
+      for (int f = 0; f < D; f += 64) {
+        tma_load_4d(dst + (f / 64) * C::kBoxBytes, &tmk, bar, f, kvh, at, page);
+        tma_load_4d(dst + C::kTileBytes + (f / 64) * C::kBoxBytes, &tmv, bar, f, kvh, at, page);
+      }
+    }
+  };
+  __syncwarp();  // the warp's barriers are ready
+  int issued = mine < C::kStages - 1 ? mine : C::kStages - 1;
+  int page[C::kStages];
+#pragma unroll
+  for (int i = 0; i < C::kStages; ++i) page[i] = page_of(i);
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i)
+    if (i < mine) load(i, page[i]);
+  int next = page[C::kStages - 1];
+
+  DecodeRows<D> part;
+  part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
+
+  int done = 0;
+  for (; done < mine; ++done) {
+    if (issued < mine) {  // the stage of the last block, which every lane has read
+      load(issued, next);
+      ++issued;
+      next = page_of(issued);
+    }
+    if (!mbar_wait_warp_lean(&full[done % C::kStages], (done / C::kStages) & 1, abort_flag, kWaitLimitNs)) break;
+    uint8_t* sk = ring + (done % C::kStages) * C::kStageBytes;
+    int from, to;
+    place(done, from, to);
+    if (from > 0 || to < kDecBlock) {
+      uint8_t* sv = sk + C::kTileBytes;
+      for (int i = lane; i < kDecBlock * 8; i += 32)
+        if (i / 8 < from || i / 8 >= to)
+#pragma unroll
+          for (int f = 0; f < D; f += 64)
+            *reinterpret_cast<uint4*>(sv + (f / 64) * C::kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();  // before the copy that takes the stage next
+      __syncwarp();
+    }
+    const auto at = [](uint32_t tile) {
+      return [tile](int r, int p) { return tile + (p / 8) * C::kBoxBytes + r * 128 + (((p % 8) ^ (r & 7)) * 16); };
+    };
+    const uint32_t tile = smem_u32(sk);
+    part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
+    __syncwarp();  // all lanes have read the stage before it is filled again
+  }
+  if (done < mine) {  // gave up: what was asked for arrives before the shared memory is used otherwise
+    if (lane == 0) atomicOr(a.status, kStatusCopies);
+    for (int i = done; i < issued; ++i) mbar_wait_drain_warp(&full[i % C::kStages], (i / C::kStages) & 1, kWaitLimitNs);
+  }
+  __syncthreads();  // the rings are idle: reuse them for the join
+  part.store(reinterpret_cast<float*>(ring));
+  __syncthreads();
+  const auto put = [&](int64_t row, int c, const DecodeResult& r) {
+    if constexpr (kOwn) {
+      *reinterpret_cast<float2*>(pa.own_o + row * D + c) = make_float2(r.o0, r.o1);
+      if (c == 0) pa.own_lse[row] = r.l2;
+    } else {
+      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(r.o0, r.o1);
+      if (c == 0) a.lse[row] = r.l2 * kLn2;
+    }
+  };
+  for (int i = threadIdx.x; i < rows * (D / 2); i += kDecWarps * 32) {
+    const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+    const DecodeResult v = decode_join_warps<D>(smem, C::kWarpBytes, r, c);
+    const int64_t row = int64_t(bi) * a.hq + h0 + r;
+    if (!bounds_ok(bi < a.b && h0 + r < a.hq, a.status)) continue;
+    if (a.nsplit == 1) {
+      put(row, c, v);
+    } else if (a.nsplit <= kDecMaxCluster) {
+      float* res = reinterpret_cast<float*>(smem + C::kResult);
+      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(v.o0, v.o1);
+      if (c == 0) res[16 * D + r] = v.l2;
+    } else {
+      const int64_t pr = row * a.nsplit + split;
+      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(v.o0, v.o1);
+      if (c == 0) a.part_lse[pr] = v.l2;
+    }
+  }
+  if (a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
+    // the cluster's CTAs are the runs of one unit: each joins its share of the features
+    cluster_sync();
+    for (int i = split * kDecWarps * 32 + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kDecWarps * 32) {
+      const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+      put(int64_t(bi) * a.hq + h0 + r, c, decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c));
+    }
+    cluster_sync();  // no CTA leaves while another still reads its results
+  }
+  // This kernel is over only when the prefix kernel is, beside which it may run: the join waits for this one.
+  if (kOwn && blockIdx.x == gridDim.x - 1) chain_wait();
+}
+
+// Joins a row's own keys and its group's: one warp per (sequence, query head).
+template <int D>
+__global__ void __launch_bounds__(128) cpattn_shared_join_kernel(const __grid_constant__ PagedArgs pa) {
+  const DecodeArgs& a = pa.d;
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= int64_t(a.b) * a.hq) return;
+  const int bi = int(row / a.hq), h = int(row - int64_t(bi) * a.hq);
+  const int kvh = h / a.G;
+  int n = a.lengths[bi];
+  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+  SharedSeq mate = shared_seq(pa.sh, bi, n);
+  chain_wait();
+  const float own = __ldcg(pa.own_lse + row);
+  float o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = __ldcg(pa.own_o + row * D + lane * kPer + i);
+  int64_t at = 0;
+  if (mate.keys > 0) {
+    shared_runs(pa.sh, mate);
+    at = shared_at(pa.sh, mate, kvh, h - kvh * a.G);
+    if (!bounds_ok(at + int64_t(mate.at.runs - 1) * pa.sh.part_rows < int64_t(pa.sh.ctas) * pa.sh.part_rows, a.status)) return;
+  }
+  const float* pl = pa.sh.part_lse + at;
+  const float* po = pa.sh.part_o + at * D + lane * kPer;
+  const int64_t step = pa.sh.part_rows;
+  float mm = own;
+  for (int s = lane; s < mate.at.runs; s += 32) mm = fmaxf(mm, __ldcg(pl + s * step));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float ll = ex2_approx(own - base);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] *= ll;
+  for (int s0 = 0; s0 < mate.at.runs; s0 += 32) {
+    const float mine = s0 + lane < mate.at.runs ? ex2_approx(__ldcg(pl + (s0 + lane) * step) - base) : 0.f;
+    const int count = mate.at.runs - s0 < 32 ? mate.at.runs - s0 : 32;
+#pragma unroll 8
+    for (int s = 0; s < count; ++s) {
+      const float w = __shfl_sync(0xffffffffu, mine, s);
+      const float* p = po + (s0 + s) * step * D;
+      float v[kPer];
+      if constexpr (kPer == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
+        v[0] = f.x, v[1] = f.y;
+      }
+      ll += w;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] = fmaf(w, v[i], o[i]);
+    }
+  }
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+}  // namespace cpattn

@@ -44,6 +44,7 @@ struct PrefixArgs {
   int64_t q_batch;
   int hq;
   int box;  // tokens of a box: gcd(page_size, 128)
+  int sms;
   float scale_log2;
   unsigned int* status;
 };
@@ -59,8 +60,8 @@ struct PrefixCfg {
   static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + alignment slack
   static constexpr uint32_t kColO = 256;
   static_assert(kSmemBytes <= 232448, "shared memory per block");
-  // the results of both sub-tiles are staged where the keys were
-  static_assert(2 * kTile * D * 4 <= (kSlots - 2) * kTileBytes, "staging");
+  // a sub-tile's results are left where the keys were
+  static_assert(kTile * D * 4 <= (kSlots - 2) * kTileBytes, "join");
 };
 
 constexpr int kPrefixMinTiles = 2;  // tiles of a run at least (where there are as many)
@@ -75,80 +76,114 @@ struct PrefixRun {
   int table;         // the sequence whose table names the pages
 };
 
+// How many of the CTAs take runs. While they do, the members' own keys are read
+// by the other SMs (paged_kernel.cuh runs beside this kernel), so each of the
+// two gets the SMs that let both end together: with tp and to the times that
+// they would take by themselves on all SMs, and kOwnShare the part of the SMs
+// that reads at the chip's full bandwidth, tp / x = to kOwnShare / (1 - x).
+template <int D>
+constexpr float kRowTileNs = D == 128 ? 875.f : 600.f;  // of an SM for 128 rows and a key tile, as measured
+constexpr float kOwnBytesPerNs = 6700.f;                // measured copy bandwidth
+constexpr float kOwnShare = 0.5f;
+__device__ __forceinline__ float prefix_share(float tile_ns, float own_bytes, int sms) {
+  const float tp = tile_ns / sms, to = own_bytes / kOwnBytesPerNs;
+  return tp / (tp + to * kOwnShare);
+}
+
 // Finds the CTA's run. One whole warp; CTA 0 also writes every group's place.
-__device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta) {
+// (The number of groups is seldom above 32; up to there a lane keeps its group
+// in registers.)
+__device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, int sms, float row_tile_ns) {
   const int lane = threadIdx.x & 31;
   PrefixRun r = {};
-  const auto of = [&](int g, int& tiles, int& units) {
-    tiles = units = 0;
-    if (g >= s.groups) return;
-    int first, size;
-    shared_group(s, g, first, size);
-    tiles = (shared_count(s, g) + kTile - 1) / kTile;
-    units = shared_units(s, size) * s.hkv;
-    if (units == 0) tiles = 0;
+  struct Group {
+    int first, size, keys, tiles, units;
   };
-  const auto sum = [](int64_t v) {
+  const auto of = [&](int g) {
+    Group x = {};
+    if (g < s.groups) {
+      shared_group(s, g, x.first, x.size);
+      x.keys = shared_count(s, g);
+      x.units = shared_units(s, x.size) * s.hkv;
+      x.tiles = x.units > 0 ? (x.keys + kTile - 1) / kTile : 0;
+    }
+    return x;
+  };
+  const auto sum = [](float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
-  int64_t total = 0;
+  const Group mine = of(lane);
+  // work of all groups, in tiles and in time; bytes of the own keys (as if every member shared)
+  float held = 0.f;
+  for (int i = lane; i < s.b; i += 32) held += float(s.lengths[i] < s.cap ? s.lengths[i] : s.cap);
+  float total = 0.f, rows = 0.f, common = 0.f;
   for (int g0 = 0; g0 < s.groups; g0 += 32) {
-    int tiles, units;
-    of(g0 + lane, tiles, units);
-    total += sum(int64_t(tiles) * units);
+    const Group x = g0 == 0 ? mine : of(g0 + lane);
+    total += float(x.tiles) * float(x.units);
+    rows += float(x.tiles) * float((x.size * s.G + kTile - 1) / kTile) * float(s.hkv);
+    common += float(x.keys) * float(x.size);
   }
-  int64_t len = (total + s.ctas - 1) / s.ctas;
+  total = sum(total);
+  int ctas = s.ctas;
+  if (ctas == sms) {
+    rows = sum(rows);
+    const float own = fmaxf(sum(held - common), 0.f) * float(s.hkv) * s.token_bytes;
+    int units = 0;
+    for (int g0 = 0; g0 < s.groups; g0 += 32) units += int(__reduce_add_sync(0xffffffffu, unsigned((g0 == 0 ? mine : of(g0 + lane)).units)));
+    ctas = int(prefix_share(rows * row_tile_ns, own, sms) * float(sms));
+    ctas = ctas < 2 * units ? 2 * units : ctas;
+    ctas = ctas < s.ctas ? ctas : s.ctas;
+  }
+  int len = int(total / float(ctas));
   if (len < kPrefixMinTiles) len = kPrefixMinTiles;
   // units take at most half of the CTAs, so this ends: at the latest when no unit is cut
   while (true) {
-    int64_t runs = 0;
+    unsigned runs = 0;
     for (int g0 = 0; g0 < s.groups; g0 += 32) {
-      int tiles, units;
-      of(g0 + lane, tiles, units);
-      runs += sum(((tiles + len - 1) / len) * units);
+      const Group x = g0 == 0 ? mine : of(g0 + lane);
+      const unsigned long long v = (unsigned long long)(unsigned(x.tiles + len - 1) / unsigned(len)) * unsigned(x.units);
+      const unsigned most = 1u << 26;  // over any number of CTAs that the host admits; 32 of them fit a word
+      const unsigned add = __reduce_add_sync(0xffffffffu, v < most ? unsigned(v) : most);
+      runs = runs + add < (1u << 31) ? runs + add : (1u << 31);
     }
-    if (runs <= s.ctas) break;
+    if (runs <= unsigned(ctas)) break;
     len += len >= 16 ? len / 16 : 1;
   }
   int base = 0;
   for (int g0 = 0; g0 < s.groups; g0 += 32) {
-    const int g = g0 + lane;
-    int tiles, units;
-    of(g, tiles, units);
-    const int runs = int((tiles + len - 1) / len), mine = runs * units;
-    int up = mine;  // inclusive sum over the lanes
+    const Group x = g0 == 0 ? mine : of(g0 + lane);
+    const int runs = int(unsigned(x.tiles + len - 1) / unsigned(len)), count = runs * x.units;
+    int up = count;  // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += v;
     }
-    const int from = base + up - mine;
-    if (cta == 0 && g < s.groups) s.runs[g] = {from, runs};
-    const unsigned hit = __ballot_sync(0xffffffffu, cta >= from && cta < from + mine);
+    const int from = base + up - count;
+    if (cta == 0 && g0 + lane < s.groups) s.runs[g0 + lane] = {from, runs};
+    const unsigned hit = __ballot_sync(0xffffffffu, cta >= from && cta < from + count);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      const int gg = g0 + l;
-      const int gruns = __shfl_sync(0xffffffffu, runs, l), gtiles = __shfl_sync(0xffffffffu, tiles, l);
-      const int local = cta - __shfl_sync(0xffffffffu, from, l);
-      int first, size;
-      shared_group(s, gg, first, size);
+      const auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
+      const int first = get(x.first), size = get(x.size), tiles = get(x.tiles), gruns = get(runs);
+      const int local = cta - get(from);
       const int unit = local / gruns, run = local % gruns, row_units = shared_units(s, size);
       r.first = first;
+      r.keys = get(x.keys);
       r.kvh = unit / row_units;
       r.row0 = (unit % row_units) * kSharedRows;
       r.rows = size * s.G - r.row0 < kSharedRows ? size * s.G - r.row0 : kSharedRows;
-      r.keys = shared_count(s, gg);
-      const int per = (gtiles + gruns - 1) / gruns;  // no run is empty: per <= len
+      const int per = (tiles + gruns - 1) / gruns;  // no run is empty: per <= len
       r.tile0 = run * per;
-      r.tiles = gtiles - r.tile0 < per ? gtiles - r.tile0 : per;
+      r.tiles = tiles - r.tile0 < per ? tiles - r.tile0 : per;
       // the first member that holds all of the common tokens names their pages
       for (int m0 = 0; m0 < size; m0 += 32) {
         const int m = m0 + lane;
-        const unsigned held = __ballot_sync(0xffffffffu, m < size && s.lengths[first + m] >= r.keys);
-        if (held) {
-          r.table = first + m0 + __ffs(held) - 1;
+        const unsigned full = __ballot_sync(0xffffffffu, m < size && s.lengths[first + m] >= r.keys);
+        if (full) {
+          r.table = first + m0 + __ffs(full) - 1;
           r.go = 1;
           break;
         }
@@ -184,7 +219,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (warp == 0) {
-    const PrefixRun r = prefix_plan(a.sh, blockIdx.x);
+    const PrefixRun r = prefix_plan(a.sh, blockIdx.x, a.sms, kRowTileNs<D>);
     if (lane == 0) *run = r;
   }
   if (warp == 8 && lane == 0) {
@@ -205,8 +240,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     fence_mbar_init();
   }
-  __syncthreads();
-  if (!run->go) return;
   if (warp == 9) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -215,6 +248,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  if (!run->go) {
+    if (warp == 9) tmem_dealloc(tbase, 512);
+    return;
+  }
 
   const int n = run->tiles;
   const bool pair = run->rows > kTile;  // two row tiles, or one whose key tiles the sub-tiles take in turn
@@ -390,27 +427,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const int unit_row = (pair ? sub * kTile : 0) + row;  // row within the unit
-    // Queries: 16-byte pieces, swizzled as TMA would (piece p of row r of a 128-byte
-    // column block at p ^ (r & 7)); rows past the unit's are zeros.
+    // Queries: 16-byte pieces, all on their way at once, swizzled as TMA would
+    // (piece p of row r of a 128-byte column block at p ^ (r & 7)); rows past the
+    // unit's are zeros.
     {
       constexpr int kPieces = D / 8, kPerStep = 32 / kPieces;
       const int rows_each = pair ? 32 : 16;
-      const int r0 = pair ? wq * 32 : warp * 16;  // rows of this warp in its tile
-      uint8_t* dst = smem + (pair ? sub * C::kTileBytes : 0);
+      const int r0 = (pair ? wq * 32 : warp * 16) + lane / kPieces;  // this lane's first row of its tile
+      const int ur0 = (pair ? sub * kTile : 0) + r0;
       const int p = lane % kPieces;
-#pragma unroll 8
+      const uint32_t dst = smem_u32(smem) + (pair ? sub * C::kTileBytes : 0) + (p / 8) * (kTile * 128);
+      int seq = (run->row0 + ur0) / a.sh.G, head = run->row0 + ur0 - seq * a.sh.G;
+      const __nv_bfloat16* q0 = a.q + int64_t(run->first) * a.q_batch + int64_t(run->kvh * a.sh.G) * D + p * 8;
       for (int s = 0; s < rows_each; s += kPerStep) {
-        const int r = r0 + s + lane / kPieces;
-        const int ur = (pair ? sub * kTile : 0) + r;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (ur < run->rows) {
-          const int gr = run->row0 + ur, seq = gr / a.sh.G, head = gr - seq * a.sh.G;
-          bounds_ok(run->first + seq < a.sh.b && run->kvh * a.sh.G + head < a.hq, a.status);
-          x = *reinterpret_cast<const uint4*>(a.q + int64_t(run->first + seq) * a.q_batch +
-                                              int64_t(run->kvh * a.sh.G + head) * D + p * 8);
+        const int r = r0 + s;
+        const bool valid = ur0 + s < run->rows;
+        bounds_ok(!valid || (run->first + seq < a.sh.b && run->kvh * a.sh.G + head < a.hq), a.status);
+        cp_async16(dst + r * 128 + (((p % 8) ^ (r & 7)) * 16), valid ? q0 + seq * a.q_batch + head * D : a.q, valid);
+        head += kPerStep;
+        while (head >= a.sh.G) {
+          head -= a.sh.G;
+          ++seq;
         }
-        *reinterpret_cast<uint4*>(dst + (p / 8) * (kTile * 128) + r * 128 + (((p % 8) ^ (r & 7)) * 16)) = x;
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -491,38 +532,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
       l = l * alpha + (a0 + a1);
     }
-    // ---- epilogue. Results are staged where the keys were, once no product
-    // reads them any more: chunk c of 16 bytes of row r at c ^ r (modulo the
-    // row's chunks), so that neither rows nor chunks meet in a bank.
+    // ---- epilogue: O / l as it is, and its log-sum-exp. Two sub-tiles of the
+    // same rows are joined first: sub-tile 1 leaves its O where the keys were,
+    // once no product reads them any more (chunk c of 16 bytes of row r at
+    // c ^ r, modulo the row's chunks: no two rows meet in a bank), and its m and l
+    // where the queries were.
     constexpr int kChunks = D / 4;
-    for (int i = 0; ok && i < 2; ++i)
-      if (i < n || pair) ok = mbar_wait_bounded(&o_full[i], 0, abort_flag, kWaitLimitNs);
-    tc_fence_after();
-    const auto spot = [&](int tile, int r, int c) {
-      return reinterpret_cast<float4*>(sKV) + (tile * kTile + r) * kChunks + (c ^ (r & (kChunks - 1)));
+    const auto spot = [&](int c) {
+      return reinterpret_cast<float4*>(sKV) + row * kChunks + (c ^ (row & (kChunks - 1)));
     };
-    float2* sML = reinterpret_cast<float2*>(smem);  // where the queries were: m and l of sub-tile 1's rows
+    float2* sML = reinterpret_cast<float2*>(smem);
+    if (ok && mine > 0) ok = mbar_wait_bounded(&o_full[sub], 0, abort_flag, kWaitLimitNs);
     if (!pair) {
-      if (sub == 1 && ok) {
-        if (mine > 0) {
+      if (ok && n > 1) ok = mbar_wait_bounded(&o_full[1 - sub], 0, abort_flag, kWaitLimitNs);
+      tc_fence_after();
+      if (sub == 1 && ok && mine > 0) {  // (with one tile the queries may still be read)
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t r[32];
-            tmem_ld32(tO + c0, r);
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32(tO + c0, r);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *spot(1, row, (c0 + i) / 4) = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
-                                                        __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
-          }
+          for (int i = 0; i < 32; i += 4)
+            *spot((c0 + i) / 4) = make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]),
+                                              __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
         }
         sML[row] = make_float2(m_used, l);
       }
       // every softmax warp comes here, whether or not a role gave up
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
+    tc_fence_after();
     if (ok && !*abort_flag && (pair || sub == 0)) {
       float w0 = 1.f, w1 = 0.f;
-      if (!pair) {
+      const bool other = !pair && n > 1;
+      if (other) {
         const float2 o = sML[row];
         const float m = fmaxf(m_used, o.x);
         const float base = m == -INFINITY ? 0.f : m;
@@ -531,40 +574,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         l = l * w0 + o.y * w1;
         m_used = m;
       }
-      const bool other = !pair && n > 1;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       w0 *= inv;
       w1 *= inv;
+      const int64_t out = int64_t(blockIdx.x) * a.sh.part_rows + unit_row;
+      const bool store = unit_row < run->rows && bounds_ok(unit_row < a.sh.part_rows && blockIdx.x < a.sh.ctas, a.status);
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         uint32_t r[32];
         tmem_ld32(tO + c0, r);
+        float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float4 x = make_float4(__uint_as_float(r[i]) * w0, __uint_as_float(r[i + 1]) * w0,
-                                 __uint_as_float(r[i + 2]) * w0, __uint_as_float(r[i + 3]) * w0);
-          if (other) {
-            const float4 y = *spot(1, row, (c0 + i) / 4);
-            x.x = fmaf(y.x, w1, x.x);
-            x.y = fmaf(y.y, w1, x.y);
-            x.z = fmaf(y.z, w1, x.z);
-            x.w = fmaf(y.w, w1, x.w);
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]) * w0;
+        if (other) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 y = *spot((c0 + i) / 4);
+            x[i] = fmaf(y.x, w1, x[i]);
+            x[i + 1] = fmaf(y.y, w1, x[i + 1]);
+            x[i + 2] = fmaf(y.z, w1, x[i + 2]);
+            x[i + 3] = fmaf(y.w, w1, x[i + 3]);
           }
-          *spot(sub, row, (c0 + i) / 4) = x;
         }
+        // whole 32-byte sectors
+        if (store)
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) store_sector(a.sh.part_o + out * D + c0 + i, x + i);
       }
-      __syncwarp();
-      // whole lines: the warp's rows one (d = 64: two) at a time
-      const int64_t out = int64_t(blockIdx.x) * a.sh.part_rows;
-      const int u0 = (pair ? sub * kTile : 0) + wq * 32;
-#pragma unroll 4
-      for (int i = lane; i < 32 * kChunks; i += 32) {
-        const int r = i / kChunks, c = i % kChunks;
-        if (u0 + r < run->rows && bounds_ok(u0 + r < a.sh.part_rows && blockIdx.x < a.sh.ctas, a.status))
-          reinterpret_cast<float4*>(a.sh.part_o)[(out + u0 + r) * kChunks + c] = *spot(sub, wq * 32 + r, c);
-      }
-      if (unit_row < run->rows && unit_row < a.sh.part_rows)
-        a.sh.part_lse[out + unit_row] = l == 0.f ? -INFINITY : m_used + log2f(l);
+      if (store) a.sh.part_lse[out] = l == 0.f ? -INFINITY : m_used + log2f(l);
     }
     if (!ok && lane == 0) atomicOr(a.status, kStatusSoftmax);
   }

@@ -427,6 +427,13 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Eight fp32 values, a whole sector, to a 32-byte aligned global address.
+__device__ __forceinline__ void store_sector(float* gaddr, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(gaddr), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+
 // Scalar fp32 atomic add (no return).
 __device__ __forceinline__ void red_add_f32(float* gaddr, float v) {
   asm volatile("red.global.add.f32 [%0], %1;" ::"l"(gaddr), "f"(v) : "memory");

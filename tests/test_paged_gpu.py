@@ -361,7 +361,7 @@ def test_shared_all_elements_and_what_is_not_seen(groups, prefix, own, size, hq,
     _check(q, k, v, tables, lengths, 0, 0, scale, o, lse)
     # again, with a workspace full of NaN and the queries in wider rows: the same bits
     need = pkg.cpattn_decode_shared_workspace_bytes(b, hq, hkv, d, len(groups), max(groups))
-    ws = torch.full((need // 4,), NAN, device="cuda")
+    ws = torch.full((need // 4 + 4,), NAN, device="cuda")[4:]  # 16-byte aligned, no more
     wide = torch.zeros(b, hq + 3, d, dtype=torch.bfloat16, device="cuda")
     wide[:, :hq] = q.cuda()
     o2, l2 = cpattn_decode_shared(wide[:, :hq], kd, vd, tables.cuda(), ln, sh, group_offsets=off, max_group=max(groups),
