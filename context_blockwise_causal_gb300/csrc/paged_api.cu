@@ -146,13 +146,14 @@ bool encode_pools(CUtensorMap* tk, CUtensorMap* tv, const cpattn_pages* p, int h
          encode_bf16_pages(tv, p->v, p->pages, p->page_size, hkv, d, p->v_page, p->v_token, p->v_head, box);
 }
 
-template <int D, bool kOwn>
-int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+template <int D, bool kOwn, int kHeads>
+int launch_paged_as(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
   const DecodeArgs& a = pa.d;
-  const auto kernel = cpattn_decode_paged_kernel<D, kOwn>;
+  const auto kernel = cpattn_decode_paged_kernel<D, kOwn, kHeads>;
   CUtensorMap tk, tv;
   if (!encode_pools(&tk, &tv, p, a.hkv, D, kDecBlock) ||
-      !allow_smem(di->paged_attr[(kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel, PagedCfg<D>::kSmemBytes))
+      !allow_smem(di->paged_attr[(kHeads == 8 ? 4 : 0) + (kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel,
+                  PagedCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
   cudaError_t e = launch_runs(kernel, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, a.nsplit, PagedCfg<D>::kSmemBytes,
                               kOwn, st, tk, tv, pa);
@@ -161,6 +162,14 @@ int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cud
   if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
     e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
   return launched(e);
+}
+
+// Query heads of a unit: 8 where they suffice (half of the work), or 16.
+int unit_heads(int G) { return G <= 8 ? 8 : 16; }
+
+template <int D, bool kOwn>
+int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  return unit_heads(pa.d.G) == 8 ? launch_paged_as<D, kOwn, 8>(pa, p, di, st) : launch_paged_as<D, kOwn, 16>(pa, p, di, st);
 }
 
 template <int D>

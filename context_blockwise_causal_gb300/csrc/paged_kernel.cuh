@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "decode_kernel.cuh"
 #include "paged.cuh"
@@ -47,7 +48,122 @@ struct PagedCfg {
   static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
 };
 
-template <int D, bool kOwn>
+// An 8x8 matrix of 16-bit elements, turned over (as ldmatrix lays them out).
+__device__ __forceinline__ uint32_t turn_8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// A warp's part of a unit of up to 8 query heads. Where decode_kernel.cuh has
+// the heads as the rows of the matrix tiles, which come in sixteens, here they
+// are the columns, which come in eights: S^T = K Q^T and O^T = V^T P^T, half of
+// the products, exponentials and registers. Lane: heads 2 c4 and 2 c4 + 1; of S^T
+// keys g4 and g4 + 8, of O^T features g4 and g4 + 8 of each 16.
+template <int D>
+struct DecodeCols {
+  static constexpr int kHeads = 8, kSteps = D / 16;
+  uint32_t qf[kSteps][2];
+  float acc[kSteps][4];
+  float m[2], l[2];  // l: this lane's keys
+
+  __device__ __forceinline__ void load(const __nv_bfloat16* qp, int rows) {
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qf[s][e] = g4 < rows ? *reinterpret_cast<const uint32_t*>(qp + int64_t(g4) * D + s * 16 + e * 8 + 2 * c4) : 0u;
+      acc[s][0] = acc[s][1] = acc[s][2] = acc[s][3] = 0.f;
+    }
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // As DecodeRows::block.
+  template <class K, class V>
+  __device__ __forceinline__ void block(K kat, V vat, int from, int to, float scale_log2) {
+    const int lane = threadIdx.x & 31, g4 = lane >> 2;
+    // two chains of products, which are added: half as long
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t kb[4];
+        ldmatrix4(kat(r, 2 * s + (lane >> 4)), kb);
+        mma_16x8x16(s & 1 ? s1 : s0, kb, qf[s][0], qf[s][1]);
+      }
+    }
+    float x[4];  // [key g4, g4 + 8][head]
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = g4 + (e >> 1) * 8;
+      x[e] = key >= from && key < to ? (s0[e] + s1[e]) * scale_log2 : -INFINITY;
+    }
+    float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, alpha[2];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+    }
+    const bool moved = mx[0] > m[0] || mx[1] > m[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float mn = fmaxf(m[h], mx[h]);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      alpha[h] = ex2_approx(m[h] - base);
+      m[h] = mn;
+      x[h] = ex2_approx(x[h] - base);
+      x[2 + h] = ex2_approx(x[2 + h] - base);
+      l[h] = l[h] * alpha[h] + (x[h] + x[2 + h]);
+    }
+    const uint32_t p0 = turn_8x8(pack_bf16x2(x[0], x[1])), p1 = turn_8x8(pack_bf16x2(x[2], x[3]));
+    if (__any_sync(0xffffffffu, moved)) {  // seldom, after a few blocks
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        acc[s][0] *= alpha[0];
+        acc[s][1] *= alpha[1];
+        acc[s][2] *= alpha[0];
+        acc[s][3] *= alpha[1];
+      }
+    }
+    {
+      const int r = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t vb[4];
+        ldmatrix4_trans(vat(r, 2 * s + ((lane >> 3) & 1)), vb);
+        mma_16x8x16(acc[s], vb, p0, p1);
+      }
+    }
+  }
+
+  // As DecodeRows::store (8 rows of the 16).
+  __device__ __forceinline__ void store(float* jo) {
+    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) jo[(2 * c4 + (e & 1)) * D + s * 16 + g4 + (e >> 1) * 8] = acc[s][e];
+    if (g4 == 0) {
+      float* jm = jo + 16 * D;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        jm[2 * c4 + h] = m[h];
+        jm[16 + 2 * c4 + h] = l[h];
+      }
+    }
+  }
+};
+
+// kHeads: query heads of a unit, 8 (DecodeCols) or 16 (DecodeRows).
+template <int D, bool kOwn, int kHeads>
 __global__ void __launch_bounds__(kDecWarps * 32)
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
@@ -64,7 +180,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
-  // unit: (batch, KV head, group of 16 query rows), then the run of keys
+  // unit: (batch, KV head, group of kHeads query heads), then the run of keys
   int x = blockIdx.x;
   const int split = x % a.nsplit;
   x /= a.nsplit;
@@ -72,8 +188,8 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   x /= a.row_groups;
   const int kvh = x % a.hkv;
   const int bi = x / a.hkv;
-  const int rows = a.G - rg * 16 < 16 ? a.G - rg * 16 : 16;  // query heads of this CTA
-  const int h0 = kvh * a.G + rg * 16;
+  const int rows = a.G - rg * kHeads < kHeads ? a.G - rg * kHeads : kHeads;  // query heads of this CTA
+  const int h0 = kvh * a.G + rg * kHeads;
 
   int n = a.lengths[bi];
   n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
@@ -132,7 +248,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     if (i < mine) load(i, page[i]);
   int next = page[C::kStages - 1];
 
-  DecodeRows<D> part;
+  std::conditional_t<kHeads == 8, DecodeCols<D>, DecodeRows<D>> part;
   part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
 
   int done = 0;

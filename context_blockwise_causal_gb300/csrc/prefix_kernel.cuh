@@ -127,18 +127,21 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
   }
   total = sum(total);
   int ctas = s.ctas;
-  if (ctas == sms) {
+  if (ctas == sms) {  // (units take at most half of them)
     rows = sum(rows);
     const float own = fmaxf(sum(held - common), 0.f) * float(s.hkv) * s.token_bytes;
     int units = 0;
-    for (int g0 = 0; g0 < s.groups; g0 += 32) units += int(__reduce_add_sync(0xffffffffu, unsigned((g0 == 0 ? mine : of(g0 + lane)).units)));
+    for (int g0 = 0; g0 < s.groups; g0 += 32) {
+      const Group x = g0 == 0 ? mine : of(g0 + lane);
+      units += int(__reduce_add_sync(0xffffffffu, unsigned(x.tiles > 0 ? x.units : 0)));
+    }
     ctas = int(prefix_share(rows * row_tile_ns, own, sms) * float(sms));
-    ctas = ctas < 2 * units ? 2 * units : ctas;
+    ctas = ctas < units ? units : ctas;
     ctas = ctas < s.ctas ? ctas : s.ctas;
   }
   int len = int(total / float(ctas));
   if (len < kPrefixMinTiles) len = kPrefixMinTiles;
-  // units take at most half of the CTAs, so this ends: at the latest when no unit is cut
+  // there are as many CTAs as units, so this ends: at the latest when no unit is cut
   while (true) {
     unsigned runs = 0;
     for (int g0 = 0; g0 < s.groups; g0 += 32) {
