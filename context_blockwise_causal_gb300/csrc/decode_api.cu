@@ -21,8 +21,8 @@ int check_shape(int b, int hq, int hkv, int d, int cap, int window, int sinks) {
 template <int D>
 int launch(const DecodeArgs& a, DeviceInfo* di, cudaStream_t st) {
   if (!allow_smem(di->decode_attr[D == 128 ? 1 : 0], cpattn_decode_kernel<D>, DecodeCfg<D>::kSmemBytes)) return CPATTN_ERR_CUDA;
-  cudaError_t e = launch_runs(cpattn_decode_kernel<D>, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, a.nsplit,
-                              DecodeCfg<D>::kSmemBytes, false, st, a);
+  cudaError_t e = launch_runs(cpattn_decode_kernel<D>, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, kDecWarps * 32,
+                              a.nsplit, DecodeCfg<D>::kSmemBytes, false, st, a);
   if (e == cudaSuccess && a.nsplit > kDecMaxCluster)
     e = launch_chained(cpattn_decode_join_kernel<D>, (int64_t(a.b) * a.hq + 3) / 4, 128, st, a);
   return launched(e);

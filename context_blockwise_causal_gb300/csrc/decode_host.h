@@ -59,11 +59,11 @@ inline bool strides_ok(int64_t batch, int64_t token, int64_t head) {
 // A kernel of one CTA per run: clusters of up to 8 runs; `chained`: as
 // launch_chained's second kernels.
 template <class... P, class... A>
-cudaError_t launch_runs(void (*kernel)(P...), int64_t ctas, int nsplit, int smem_bytes, bool chained, cudaStream_t st,
-                        A&&... args) {
+cudaError_t launch_runs(void (*kernel)(P...), int64_t ctas, int threads, int nsplit, int smem_bytes, bool chained,
+                        cudaStream_t st, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = size_t(smem_bytes);
   cfg.stream = st;
   cudaLaunchAttribute attrs[2];

@@ -71,6 +71,9 @@ int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int windo
   return p ? check_pages(p, hkv, d) : CPATTN_OK;
 }
 
+// Query heads of a unit: 8 where they suffice (half of the work), or 16.
+int unit_heads(int G) { return G <= 8 ? 8 : 16; }
+
 // What the calls' arguments have in common; o and lse as cpattn_decode.
 void fill_decode(PagedArgs* pa, const void* q, const cpattn_pages* p, const int* lengths, void* o, float* lse, int b,
                  int hq, int hkv, int d, int64_t q_batch, float scale, DeviceInfo* di) {
@@ -86,7 +89,7 @@ void fill_decode(PagedArgs* pa, const void* q, const cpattn_pages* p, const int*
   a->hkv = hkv;
   a->G = hq / hkv;
   a->cap = int(capacity(p));
-  a->row_groups = (a->G + 15) / 16;
+  a->row_groups = (a->G + unit_heads(a->G) - 1) / unit_heads(a->G);
   a->scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
   a->status = di->status;
   pa->pg = place_of(p);
@@ -155,17 +158,14 @@ int launch_paged_as(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, 
       !allow_smem(di->paged_attr[(kHeads == 8 ? 4 : 0) + (kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel,
                   PagedCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
-  cudaError_t e = launch_runs(kernel, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, a.nsplit, PagedCfg<D>::kSmemBytes,
-                              kOwn, st, tk, tv, pa);
+  cudaError_t e = launch_runs(kernel, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, kPagedThreads, a.nsplit,
+                              PagedCfg<D>::kSmemBytes, kOwn, st, tk, tv, pa);
   const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
   if (e == cudaSuccess && kOwn) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
   if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
     e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
   return launched(e);
 }
-
-// Query heads of a unit: 8 where they suffice (half of the work), or 16.
-int unit_heads(int G) { return G <= 8 ? 8 : 16; }
 
 template <int D, bool kOwn>
 int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
@@ -257,7 +257,8 @@ extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, in
   if (check_decode(nullptr, b, hq, hkv, d, window, sinks) || cap < 1 || cap > (1 << 30)) return 0;
   DeviceInfo* di = nullptr;
   if (device_info(&di)) return 0;
-  const int64_t units = int64_t(b) * hkv * ((hq / hkv + 15) / 16);
+  const int G = hq / hkv;
+  const int64_t units = int64_t(b) * hkv * ((G + unit_heads(G) - 1) / unit_heads(G));
   return workspace_for(b, hq, d, choose_split(di->num_sms, units, max_keys(cap, window, sinks)));
 }
 

@@ -5,10 +5,13 @@
 //
 // Mathematics, tiles and joins are those of decode_kernel.cuh; what differs is
 // how keys come. A page holds a multiple of 16 tokens, so a block of 16 that
-// starts at a whole 16 of the sequence's own numbering lies in one page: a
-// block is a few boxes (16 tokens x 64 features) that one lane asks the copy
-// engine for, instead of 16 addresses and copies by each of 32 lanes, and the
-// table is looked up once per block, a block ahead of the copy that needs it.
+// starts at a whole 16 of the sequence's own numbering lies in one page and is
+// a few boxes (16 tokens x 64 features) for the copy engine. A warp of its own
+// asks for the boxes of four blocks at a time, one for each of the warps that
+// compute, a lane for each box; the table is looked up a round ahead. (When the
+// computing warps asked for their own, looking up, dividing by the page size and
+// issuing took longer than the products: 0.47 of 0.9 us a block, and 16
+// sequences of 32K to 64K keys took 491 us.)
 // The first and last keys of what is visible are masked inside their blocks:
 // scores by the mask, and values, whose product with a weight of zero would
 // still be NaN if they are not finite, by zeros written over them.
@@ -25,6 +28,7 @@
 namespace cpattn {
 
 constexpr unsigned int kStatusCopies = 1u << 4;  // copies of a paged decode did not arrive in time
+constexpr int kPagedThreads = (kDecWarps + 1) * 32;
 
 struct PagedArgs {
   DecodeArgs d;  // k and v are not used (the copies' descriptors name the pools)
@@ -42,7 +46,8 @@ struct PagedCfg {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kOffBar = kDecWarps * kWarpBytes;
-  static constexpr int kOffFlag = kOffBar + kDecWarps * kStages * 8;
+  static constexpr int kOffFlag = kOffBar + 2 * kDecWarps * kStages * 8;  // full and empty, per warp and stage
+  static constexpr int kBoxes = 2 * D / 64;  // of a block
   static constexpr int kSmemBytes = kOffFlag + 16 + 1024;  // + alignment slack
   static constexpr int kResult = 16 * D * 4 + 16 * 8;      // as DecodeCfg
   static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
@@ -164,7 +169,7 @@ struct DecodeCols {
 
 // kHeads: query heads of a unit, 8 (DecodeCols) or 16 (DecodeRows).
 template <int D, bool kOwn, int kHeads>
-__global__ void __launch_bounds__(kDecWarps * 32)
+__global__ void __launch_bounds__(kPagedThreads)
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
   const DecodeArgs& a = pa.d;
@@ -173,13 +178,15 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + warp * C::kStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag) + warp;  // warps wait for their own copies only
-  if (lane == 0) {
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [warp][stage]
+  uint64_t* empty = full + kDecWarps * C::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
+  if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2 * kDecWarps * C::kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
+  __syncthreads();
   // unit: (batch, KV head, group of kHeads query heads), then the run of keys
   int x = blockIdx.x;
   const int split = x % a.nsplit;
@@ -204,87 +211,96 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   const int64_t begin64 = int64_t(split) * per;
   const int begin = begin64 < all ? int(begin64) : all;
   const int blocks = all - begin < per ? all - begin : per;
-  const int mine = blocks > warp ? (blocks - warp + kDecWarps - 1) / kDecWarps : 0;  // blocks of this warp
-
-  uint8_t* ring = smem + warp * C::kWarpBytes;
-  const int* table = pa.pg.tables + int64_t(bi) * pa.pg.tables_row;
-  // Block i of this warp: its first key, and the keys [from, to) of it that are seen.
+  // Block i of the run: its first key, and the keys [from, to) of it that are seen.
   const auto place = [&](int i, int& from, int& to) {
-    const int vb = begin + warp + i * kDecWarps;
+    const int vb = begin + i;
     const bool early = vb < sink_blocks;
     const int key0 = (early ? vb : lo_block + (vb - sink_blocks)) * kDecBlock;
     from = early || lo < key0 ? 0 : lo - key0;
     to = (early ? ns : n) - key0;
     return key0;
   };
-  const auto page_of = [&](int i) {
-    int from, to;
-    return i < mine ? table[unsigned(place(i, from, to)) / unsigned(pa.pg.page_size)] : 0;
-  };
-  const auto load = [&](int i, int page) {
-    int from, to;
-    const int key0 = place(i, from, to);
-    const int at = int(unsigned(key0) % unsigned(pa.pg.page_size));
-    if (lane == 0) {
-      page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
-      bounds_ok(key0 >= 0 && key0 < a.cap && at + kDecBlock <= pa.pg.page_size && kvh < a.hkv, a.status);
-      uint64_t* bar = &full[i % C::kStages];
-      uint8_t* dst = ring + (i % C::kStages) * C::kStageBytes;
-      mbar_arrive_expect_tx(bar, C::kStageBytes);
-#pragma unroll
-      for (int f = 0; f < D; f += 64) {
-        tma_load_4d(dst + (f / 64) * C::kBoxBytes, &tmk, bar, f, kvh, at, page);
-        tma_load_4d(dst + C::kTileBytes + (f / 64) * C::kBoxBytes, &tmv, bar, f, kvh, at, page);
-      }
-    }
-  };
-  __syncwarp();  // the warp's barriers are ready
-  int issued = mine < C::kStages - 1 ? mine : C::kStages - 1;
-  int page[C::kStages];
-#pragma unroll
-  for (int i = 0; i < C::kStages; ++i) page[i] = page_of(i);
-#pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i)
-    if (i < mine) load(i, page[i]);
-  int next = page[C::kStages - 1];
-
   std::conditional_t<kHeads == 8, DecodeCols<D>, DecodeRows<D>> part;
-  part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
-
-  int done = 0;
-  for (; done < mine; ++done) {
-    if (issued < mine) {  // the stage of the last block, which every lane has read
-      load(issued, next);
-      ++issued;
-      next = page_of(issued);
-    }
-    if (!mbar_wait_warp_lean(&full[done % C::kStages], (done / C::kStages) & 1, abort_flag, kWaitLimitNs)) break;
-    uint8_t* sk = ring + (done % C::kStages) * C::kStageBytes;
-    int from, to;
-    place(done, from, to);
-    if (from > 0 || to < kDecBlock) {
-      uint8_t* sv = sk + C::kTileBytes;
-      for (int i = lane; i < kDecBlock * 8; i += 32)
-        if (i / 8 < from || i / 8 >= to)
-#pragma unroll
-          for (int f = 0; f < D; f += 64)
-            *reinterpret_cast<uint4*>(sv + (f / 64) * C::kBoxBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-      fence_proxy_async_smem();  // before the copy that takes the stage next
-      __syncwarp();
-    }
-    const auto at = [](uint32_t tile) {
-      return [tile](int r, int p) { return tile + (p / 8) * C::kBoxBytes + r * 128 + (((p % 8) ^ (r & 7)) * 16); };
+  if (warp == kDecWarps) {
+    // ------------------------------------------------------------ copies
+    // Round t: block 4 t + w for each warp w, lane kBoxes w + box.
+    const int w = lane / C::kBoxes, box = lane % C::kBoxes;
+    const int* table = pa.pg.tables + int64_t(bi) * pa.pg.tables_row;
+    const int rounds = (blocks + kDecWarps - 1) / kDecWarps;
+    const CUtensorMap* map = box < C::kBoxes / 2 ? &tmk : &tmv;
+    const int feature = (box % (C::kBoxes / 2)) * 64;
+    uint8_t* dst = smem + w * C::kWarpBytes + box * C::kBoxBytes;
+    // the slot in its page, and the page, of this lane's block of a round
+    const auto look = [&](int t, int& slot, int& page) {
+      const int i = t * kDecWarps + w;
+      if (w >= kDecWarps || i >= blocks) return;
+      int from, to;
+      const int key0 = place(i, from, to);
+      const int column = int(unsigned(key0) / unsigned(pa.pg.page_size));
+      slot = key0 - column * pa.pg.page_size;
+      bounds_ok(key0 >= 0 && key0 < a.cap && slot + kDecBlock <= pa.pg.page_size && kvh < a.hkv, a.status);
+      page = table[column];
     };
-    const uint32_t tile = smem_u32(sk);
-    part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
-    __syncwarp();  // all lanes have read the stage before it is filled again
-  }
-  if (done < mine) {  // gave up: what was asked for arrives before the shared memory is used otherwise
-    if (lane == 0) atomicOr(a.status, kStatusCopies);
-    for (int i = done; i < issued; ++i) mbar_wait_drain_warp(&full[i % C::kStages], (i / C::kStages) & 1, kWaitLimitNs);
+    int slot = 0, page = 0;
+    look(0, slot, page);
+    bool ok = true;
+    int t = 0;
+    for (; t < rounds; ++t) {
+      int next_slot = 0, next_page = 0;
+      look(t + 1, next_slot, next_page);
+      const bool on = w < kDecWarps && t * kDecWarps + w < blocks;
+      const int at = w * C::kStages + t % C::kStages;
+      if (on && t >= C::kStages) ok = mbar_wait_lean(&empty[at], (t / C::kStages - 1) & 1, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (on && box == 0) {
+        page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
+        mbar_arrive_expect_tx(&full[at], C::kStageBytes);
+      }
+      __syncwarp();
+      if (on) tma_load_4d(dst + (t % C::kStages) * C::kStageBytes, map, &full[at], feature, kvh, slot, page);
+      slot = next_slot;
+      page = next_page;
+    }
+    if (t < rounds) {  // gave up: what was asked for arrives before the shared memory is used otherwise
+      if (lane == 0) atomicOr(a.status, kStatusCopies);
+      for (int u = t > C::kStages ? t - C::kStages : 0; u < t; ++u)
+        if (w < kDecWarps && box == 0 && u * kDecWarps + w < blocks)
+          mbar_wait_drain(&full[w * C::kStages + u % C::kStages], (u / C::kStages) & 1, kWaitLimitNs);
+    }
+  } else {
+    // ------------------------------------------------------------ products
+    part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
+    uint8_t* ring = smem + warp * C::kWarpBytes;
+    for (int t = 0, i = warp; i < blocks; ++t, i += kDecWarps) {
+      const int stage = t % C::kStages;
+      if (!mbar_wait_warp_lean(&full[warp * C::kStages + stage], (t / C::kStages) & 1, abort_flag, kWaitLimitNs)) {
+        if (lane == 0) atomicOr(a.status, kStatusCopies);
+        break;
+      }
+      uint8_t* sk = ring + stage * C::kStageBytes;
+      int from, to;
+      place(i, from, to);
+      if (from > 0 || to < kDecBlock) {
+        uint8_t* sv = sk + C::kTileBytes;
+        for (int x = lane; x < kDecBlock * 8; x += 32)
+          if (x / 8 < from || x / 8 >= to)
+#pragma unroll
+            for (int f = 0; f < D; f += 64)
+              *reinterpret_cast<uint4*>(sv + (f / 64) * C::kBoxBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();  // before the copy that takes the stage next
+        __syncwarp();
+      }
+      const auto at = [](uint32_t tile) {
+        return [tile](int r, int p) { return tile + (p / 8) * C::kBoxBytes + r * 128 + (((p % 8) ^ (r & 7)) * 16); };
+      };
+      const uint32_t tile = smem_u32(sk);
+      part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
+      __syncwarp();  // all lanes have read the stage
+      if (lane == 0) mbar_arrive(&empty[warp * C::kStages + stage]);
+    }
   }
   __syncthreads();  // the rings are idle: reuse them for the join
-  part.store(reinterpret_cast<float*>(ring));
+  if (warp < kDecWarps) part.store(reinterpret_cast<float*>(smem + warp * C::kWarpBytes));
   __syncthreads();
   const auto put = [&](int64_t row, int c, const DecodeResult& r) {
     if constexpr (kOwn) {
@@ -295,7 +311,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       if (c == 0) a.lse[row] = r.l2 * kLn2;
     }
   };
-  for (int i = threadIdx.x; i < rows * (D / 2); i += kDecWarps * 32) {
+  for (int i = threadIdx.x; i < rows * (D / 2); i += kPagedThreads) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
     const DecodeResult v = decode_join_warps<D>(smem, C::kWarpBytes, r, c);
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   if (a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
     // the cluster's CTAs are the runs of one unit: each joins its share of the features
     cluster_sync();
-    for (int i = split * kDecWarps * 32 + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kDecWarps * 32) {
+    for (int i = split * kPagedThreads + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kPagedThreads) {
       const int r = i / (D / 2), c = (i % (D / 2)) * 2;
       put(int64_t(bi) * a.hq + h0 + r, c, decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c));
     }
