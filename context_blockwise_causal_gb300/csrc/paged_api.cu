@@ -143,23 +143,27 @@ int own_split(int num_sms, int64_t units, int64_t cap) {
   return s < kDecMaxCluster ? s : kDecMaxCluster;
 }
 
-// Descriptors of the pools for copies of `box` tokens.
-bool encode_pools(CUtensorMap* tk, CUtensorMap* tv, const cpattn_pages* p, int hkv, int d, int box) {
-  return encode_bf16_pages(tk, p->k, p->pages, p->page_size, hkv, d, p->k_page, p->k_token, p->k_head, box) &&
-         encode_bf16_pages(tv, p->v, p->pages, p->page_size, hkv, d, p->v_page, p->v_token, p->v_head, box);
+// Descriptors of the pools for copies of `box` tokens and 64 `cols` features.
+bool encode_pools(CUtensorMap* tk, CUtensorMap* tv, const cpattn_pages* p, int hkv, int d, int box, int cols) {
+  return encode_bf16_pages(tk, p->k, p->pages, p->page_size, hkv, d, p->k_page, p->k_token, p->k_head, box, cols) &&
+         encode_bf16_pages(tv, p->v, p->pages, p->page_size, hkv, d, p->v_page, p->v_token, p->v_head, box, cols);
 }
 
 template <int D, bool kOwn, int kHeads>
-int launch_paged_as(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  using C = PagedCfg<D>;
   const DecodeArgs& a = pa.d;
+  const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
+  pa.stages = ctas <= di->num_sms ? C::kMaxStages : C::kStages;
   const auto kernel = cpattn_decode_paged_kernel<D, kOwn, kHeads>;
   CUtensorMap tk, tv;
-  if (!encode_pools(&tk, &tv, p, a.hkv, D, kDecBlock) ||
+  pa.box = std::gcd(p->page_size, 2 * kDecBlock);
+  if (!encode_pools(&tk, &tv, p, a.hkv, D, pa.box, D / 64) ||
       !allow_smem(di->paged_attr[(kHeads == 8 ? 4 : 0) + (kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel,
-                  PagedCfg<D>::kSmemBytes))
+                  C::smem_bytes(C::kMaxStages)))
     return CPATTN_ERR_CUDA;
-  cudaError_t e = launch_runs(kernel, int64_t(a.b) * a.hkv * a.row_groups * a.nsplit, kPagedThreads, a.nsplit,
-                              PagedCfg<D>::kSmemBytes, kOwn, st, tk, tv, pa);
+  cudaError_t e =
+      launch_runs(kernel, ctas, kPagedThreads, a.nsplit, C::smem_bytes(pa.stages), kOwn, st, tk, tv, pa);
   const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
   if (e == cudaSuccess && kOwn) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
   if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
@@ -168,14 +172,14 @@ int launch_paged_as(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, 
 }
 
 template <int D, bool kOwn>
-int launch_paged(const PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+int launch_paged(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
   return unit_heads(pa.d.G) == 8 ? launch_paged_as<D, kOwn, 8>(pa, p, di, st) : launch_paged_as<D, kOwn, 16>(pa, p, di, st);
 }
 
 template <int D>
-int launch_shared(const PagedArgs& pa, const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+int launch_shared(PagedArgs& pa, const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
   CUtensorMap tk, tv;
-  if (!encode_pools(&tk, &tv, p, a.sh.hkv, D, a.box) ||
+  if (!encode_pools(&tk, &tv, p, a.sh.hkv, D, a.box, a.box == kTile ? D / 64 : 1) ||
       !allow_smem(di->prefix_attr[D == 128 ? 1 : 0], cpattn_prefix_kernel<D>, PrefixCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
   cpattn_prefix_kernel<D><<<unsigned(a.sh.ctas), kFwdThreads, PrefixCfg<D>::kSmemBytes, st>>>(tk, tv, a);

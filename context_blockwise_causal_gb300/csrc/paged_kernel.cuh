@@ -4,14 +4,14 @@
 // the two.
 //
 // Mathematics, tiles and joins are those of decode_kernel.cuh; what differs is
-// how keys come. A page holds a multiple of 16 tokens, so a block of 16 that
-// starts at a whole 16 of the sequence's own numbering lies in one page and is
-// a few boxes (16 tokens x 64 features) for the copy engine. A warp of its own
-// asks for the boxes of four blocks at a time, one for each of the warps that
-// compute, a lane for each box; the table is looked up a round ahead. (When the
-// computing warps asked for their own, looking up, dividing by the page size and
-// issuing took longer than the products: 0.47 of 0.9 us a block, and 16
-// sequences of 32K to 64K keys took 491 us.)
+// how keys come. What is visible is cut into rounds of 64 keys, each starting at
+// a whole 64 of the sequence's own numbering, 16 keys for each of the four
+// warps that compute. A warp of its own asks the copy engine for them: a box of
+// 32 or 16 tokens (the page size is a multiple of it) and all features for a
+// lane, whose page it has looked up a round ahead. Asking is not cheap, some tens
+// of cycles a box: when every warp asked for its own 16 keys in boxes of 64
+// features, that took longer than the products (0.47 of 0.9 us for 16 keys, and
+// 16 sequences of 32K to 64K keys took 491 us).
 // The first and last keys of what is visible are masked inside their blocks:
 // scores by the mask, and values, whose product with a weight of zero would
 // still be NaN if they are not finite, by zeros written over them.
@@ -36,21 +36,28 @@ struct PagedArgs {
   SharedPlan sh;  // kOwn
   float* own_o;   // kOwn: [b, hq, D] normalised
   float* own_lse; // [b, hq], base 2
+  int stages;
+  int box;  // tokens of a copy: gcd(page_size, 32)
 };
+
+constexpr int kPagedRound = kDecWarps * kDecBlock;  // keys of a round
 
 template <int D>
 struct PagedCfg {
-  static constexpr int kStages = D == 128 ? 3 : 6;
-  static constexpr int kBoxBytes = kDecBlock * 128;  // 64 features
-  static constexpr int kTileBytes = kDecBlock * D * 2;
+  static constexpr int kTileBytes = kPagedRound * D * 2;  // keys or values of a round
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kWarpBytes = kStages * kStageBytes;
-  static constexpr int kOffBar = kDecWarps * kWarpBytes;
-  static constexpr int kOffFlag = kOffBar + 2 * kDecWarps * kStages * 8;  // full and empty, per warp and stage
-  static constexpr int kBoxes = 2 * D / 64;  // of a block
-  static constexpr int kSmemBytes = kOffFlag + 16 + 1024;  // + alignment slack
-  static constexpr int kResult = 16 * D * 4 + 16 * 8;      // as DecodeCfg
-  static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
+  // Two CTAs fit an SM with kStages, one has it to itself with kMaxStages. Where
+  // there is no more than one CTA per SM, the deeper ring keeps twice as much on
+  // its way.
+  static constexpr int kStages = D == 128 ? 3 : 6, kMaxStages = 2 * kStages;
+  // barriers (full and empty per stage) and the flag come first, the ring (1024-byte aligned) behind them
+  static constexpr int kOffFlag = 2 * kMaxStages * 8;
+  static constexpr int kOffRing = 1024;
+  static constexpr int smem_bytes(int stages) { return kOffRing + stages * kStageBytes + 1024; }  // + alignment slack
+  // the join of the warps reuses the ring, kJoinBytes for each: O and pairs, as in DecodeCfg, and the CTA's result
+  static constexpr int kResult = 16 * D * 4 + 16 * 8;
+  static constexpr int kJoinBytes = kStages * kStageBytes / kDecWarps;
+  static_assert(kResult + 16 * D * 4 + 16 * 4 <= kJoinBytes, "join buffers");
 };
 
 // An 8x8 matrix of 16-bit elements, turned over (as ldmatrix lays them out).
@@ -178,15 +185,17 @@ __global__ void __launch_bounds__(kPagedThreads)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [warp][stage]
-  uint64_t* empty = full + kDecWarps * C::kStages;
+  const int stages = pa.stages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + stages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < 2 * kDecWarps * C::kStages; ++i) mbar_init(&full[i], 1);
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (threadIdx.x < 2 * stages) {
+    mbar_init(&full[threadIdx.x], threadIdx.x < stages ? 1 : kDecWarps);
     fence_mbar_init();
   }
   __syncthreads();
+  smem += C::kOffRing;
   // unit: (batch, KV head, group of kHeads query heads), then the run of keys
   int x = blockIdx.x;
   const int split = x % a.nsplit;
@@ -203,19 +212,19 @@ __global__ void __launch_bounds__(kPagedThreads)
   int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
   if constexpr (kOwn) lo = shared_seq(pa.sh, bi, n).keys;    // those before it are the prefix kernel's
   const int ns = kOwn ? 0 : (a.sinks < lo ? a.sinks : lo);
-  // blocks that hold visible keys: the first tokens', then the window's
-  const int sink_blocks = (ns + kDecBlock - 1) / kDecBlock, lo_block = lo / kDecBlock;
-  const int all = sink_blocks + (n > lo ? (n + kDecBlock - 1) / kDecBlock - lo_block : 0);
-  // this CTA's run: whole rounds of the warps
-  const int per = ((all + a.nsplit - 1) / a.nsplit + kDecWarps - 1) / kDecWarps * kDecWarps;
+  // rounds that hold visible keys: the first tokens', then the window's
+  const int sink_rounds = (ns + kPagedRound - 1) / kPagedRound, lo_round = lo / kPagedRound;
+  const int all = sink_rounds + (n > lo ? (n + kPagedRound - 1) / kPagedRound - lo_round : 0);
+  // this CTA's run
+  const int per = (all + a.nsplit - 1) / a.nsplit;
   const int64_t begin64 = int64_t(split) * per;
   const int begin = begin64 < all ? int(begin64) : all;
-  const int blocks = all - begin < per ? all - begin : per;
-  // Block i of the run: its first key, and the keys [from, to) of it that are seen.
-  const auto place = [&](int i, int& from, int& to) {
-    const int vb = begin + i;
-    const bool early = vb < sink_blocks;
-    const int key0 = (early ? vb : lo_block + (vb - sink_blocks)) * kDecBlock;
+  const int rounds = all - begin < per ? all - begin : per;
+  // Round t of the run: its first key, and the keys [from, to) of it that are seen.
+  const auto place = [&](int t, int& from, int& to) {
+    const int v = begin + t;
+    const bool early = v < sink_rounds;
+    const int key0 = (early ? v : lo_round + (v - sink_rounds)) * kPagedRound;
     from = early || lo < key0 ? 0 : lo - key0;
     to = (early ? ns : n) - key0;
     return key0;
@@ -223,84 +232,99 @@ __global__ void __launch_bounds__(kPagedThreads)
   std::conditional_t<kHeads == 8, DecodeCols<D>, DecodeRows<D>> part;
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ copies
-    // Round t: block 4 t + w for each warp w, lane kBoxes w + box.
-    const int w = lane / C::kBoxes, box = lane % C::kBoxes;
+    // lane: its box of the keys or of the values
+    const int boxes = kPagedRound / pa.box, box = lane % boxes;
+    const bool mine = lane < 2 * boxes, values = lane >= boxes;
+    const int box_bytes = pa.box * (D * 2);
     const int* table = pa.pg.tables + int64_t(bi) * pa.pg.tables_row;
-    const int rounds = (blocks + kDecWarps - 1) / kDecWarps;
-    const CUtensorMap* map = box < C::kBoxes / 2 ? &tmk : &tmv;
-    const int feature = (box % (C::kBoxes / 2)) * 64;
-    uint8_t* dst = smem + w * C::kWarpBytes + box * C::kBoxBytes;
-    // the slot in its page, and the page, of this lane's block of a round
+    const CUtensorMap* map = values ? &tmv : &tmk;
+    uint8_t* dst = smem + (values ? C::kTileBytes : 0) + box * box_bytes;
+    // whether this lane's box of a round holds visible keys, its slot in its page, and the page
     const auto look = [&](int t, int& slot, int& page) {
-      const int i = t * kDecWarps + w;
-      if (w >= kDecWarps || i >= blocks) return;
+      if (!mine || t >= rounds) return false;
       int from, to;
-      const int key0 = place(i, from, to);
+      const int key0 = place(t, from, to) + box * pa.box;
+      if (to <= box * pa.box || from >= (box + 1) * pa.box) return false;
       const int column = int(unsigned(key0) / unsigned(pa.pg.page_size));
       slot = key0 - column * pa.pg.page_size;
-      bounds_ok(key0 >= 0 && key0 < a.cap && slot + kDecBlock <= pa.pg.page_size && kvh < a.hkv, a.status);
+      bounds_ok(key0 >= 0 && key0 < a.cap && slot + pa.box <= pa.pg.page_size && kvh < a.hkv, a.status);
       page = table[column];
+      return true;
     };
     int slot = 0, page = 0;
-    look(0, slot, page);
+    bool on = look(0, slot, page);
     bool ok = true;
-    int t = 0;
+    int t = 0, stage = 0;
+    uint32_t turn = 0;  // of the ring
     for (; t < rounds; ++t) {
       int next_slot = 0, next_page = 0;
-      look(t + 1, next_slot, next_page);
-      const bool on = w < kDecWarps && t * kDecWarps + w < blocks;
-      const int at = w * C::kStages + t % C::kStages;
-      if (on && t >= C::kStages) ok = mbar_wait_lean(&empty[at], (t / C::kStages - 1) & 1, abort_flag, kWaitLimitNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (on && box == 0) {
-        page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
-        mbar_arrive_expect_tx(&full[at], C::kStageBytes);
-      }
+      const bool next_on = look(t + 1, next_slot, next_page);
+      if (turn > 0 && !(ok = mbar_wait_warp_lean(&empty[stage], (turn - 1) & 1, abort_flag, kWaitLimitNs))) break;
+      if (on) page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
+      const int count = __popc(__ballot_sync(0xffffffffu, on));
+      if (lane == 0) mbar_arrive_expect_tx(&full[stage], uint32_t(count * box_bytes));
       __syncwarp();
-      if (on) tma_load_4d(dst + (t % C::kStages) * C::kStageBytes, map, &full[at], feature, kvh, slot, page);
+      if (on) tma_load_5d(dst + stage * C::kStageBytes, map, &full[stage], 0, slot, 0, kvh, page);
+      on = next_on;
       slot = next_slot;
       page = next_page;
+      if (++stage == stages) {
+        stage = 0;
+        ++turn;
+      }
     }
-    if (t < rounds) {  // gave up: what was asked for arrives before the shared memory is used otherwise
+    if (!ok) {  // gave up: what was asked for arrives before the shared memory is used otherwise
       if (lane == 0) atomicOr(a.status, kStatusCopies);
-      for (int u = t > C::kStages ? t - C::kStages : 0; u < t; ++u)
-        if (w < kDecWarps && box == 0 && u * kDecWarps + w < blocks)
-          mbar_wait_drain(&full[w * C::kStages + u % C::kStages], (u / C::kStages) & 1, kWaitLimitNs);
+      for (int u = t > stages ? t - stages : 0; u < t; ++u)
+        mbar_wait_drain_warp(&full[u % stages], (u / stages) & 1, kWaitLimitNs);
     }
   } else {
     // ------------------------------------------------------------ products
     part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
-    uint8_t* ring = smem + warp * C::kWarpBytes;
-    for (int t = 0, i = warp; i < blocks; ++t, i += kDecWarps) {
-      const int stage = t % C::kStages;
-      if (!mbar_wait_warp_lean(&full[warp * C::kStages + stage], (t / C::kStages) & 1, abort_flag, kWaitLimitNs)) {
+    // this warp's 16 keys of a round: in a box, whose features come 64 at a time
+    const int half_bytes = pa.box * 128;
+    const int mine = (warp * kDecBlock / pa.box) * pa.box * (D * 2) + (warp * kDecBlock % pa.box) * 128;
+    int stage = 0;
+    uint32_t turn = 0;
+    for (int t = 0; t < rounds; ++t) {
+      if (!mbar_wait_warp_lean(&full[stage], turn & 1, abort_flag, kWaitLimitNs)) {
         if (lane == 0) atomicOr(a.status, kStatusCopies);
         break;
       }
-      uint8_t* sk = ring + stage * C::kStageBytes;
+      uint8_t* sk = smem + stage * C::kStageBytes + mine;
       int from, to;
-      place(i, from, to);
-      if (from > 0 || to < kDecBlock) {
-        uint8_t* sv = sk + C::kTileBytes;
-        for (int x = lane; x < kDecBlock * 8; x += 32)
-          if (x / 8 < from || x / 8 >= to)
+      place(t, from, to);
+      from -= warp * kDecBlock;
+      to -= warp * kDecBlock;
+      if (from < kDecBlock && to > 0) {
+        if (from > 0 || to < kDecBlock) {
+          uint8_t* sv = sk + C::kTileBytes;
+          for (int x = lane; x < kDecBlock * 8; x += 32)
+            if (x / 8 < from || x / 8 >= to)
 #pragma unroll
-            for (int f = 0; f < D; f += 64)
-              *reinterpret_cast<uint4*>(sv + (f / 64) * C::kBoxBytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();  // before the copy that takes the stage next
-        __syncwarp();
+              for (int f = 0; f < D / 64; ++f)
+                *reinterpret_cast<uint4*>(sv + f * half_bytes + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();  // before the copy that takes the stage next
+          __syncwarp();
+        }
+        const auto at = [half_bytes](uint32_t tile) {
+          return [tile, half_bytes](int r, int p) {
+            return tile + (p / 8) * half_bytes + r * 128 + (((p % 8) ^ (r & 7)) * 16);
+          };
+        };
+        const uint32_t tile = smem_u32(sk);
+        part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
+        __syncwarp();  // all lanes have read the stage
       }
-      const auto at = [](uint32_t tile) {
-        return [tile](int r, int p) { return tile + (p / 8) * C::kBoxBytes + r * 128 + (((p % 8) ^ (r & 7)) * 16); };
-      };
-      const uint32_t tile = smem_u32(sk);
-      part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
-      __syncwarp();  // all lanes have read the stage
-      if (lane == 0) mbar_arrive(&empty[warp * C::kStages + stage]);
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == stages) {
+        stage = 0;
+        ++turn;
+      }
     }
   }
-  __syncthreads();  // the rings are idle: reuse them for the join
-  if (warp < kDecWarps) part.store(reinterpret_cast<float*>(smem + warp * C::kWarpBytes));
+  __syncthreads();  // the ring is idle: the join reuses it
+  if (warp < kDecWarps) part.store(reinterpret_cast<float*>(smem + warp * C::kJoinBytes));
   __syncthreads();
   const auto put = [&](int64_t row, int c, const DecodeResult& r) {
     if constexpr (kOwn) {
@@ -313,7 +337,7 @@ __global__ void __launch_bounds__(kPagedThreads)
   };
   for (int i = threadIdx.x; i < rows * (D / 2); i += kPagedThreads) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    const DecodeResult v = decode_join_warps<D>(smem, C::kWarpBytes, r, c);
+    const DecodeResult v = decode_join_warps<D>(smem, C::kJoinBytes, r, c);
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
     if (!bounds_ok(bi < a.b && h0 + r < a.hq, a.status)) continue;
     if (a.nsplit == 1) {

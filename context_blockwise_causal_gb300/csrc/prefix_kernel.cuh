@@ -17,9 +17,9 @@
 // and, with one tile of queries, more room for keys on their way; their two
 // results are joined at the end in shared memory.
 //
-// Keys come by TMA, a box per page and 64 features (page_size and 128 have a
-// common divisor of 16 or more tokens), each lane of the producer warp one
-// page's boxes. Boxes past the common keys are not read. Where the last tile
+// Keys come by TMA, in boxes of as many tokens as page_size and 128 have as
+// their common divisor (16 or more), a lane of the producer warp for each of
+// a tile's boxes. Boxes past the common keys are not read. Where the last tile
 // ends inside a box, what the page holds beyond is masked in the scores, and
 // its values are overwritten with zeros in shared memory, so that nothing there,
 // infinities and NaN included, reaches a sum.
@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == 8) {
       // ------------------------------------------------------------ producer
       const int boxes = kTile / a.box;  // of a whole tile; lane: its box
+      const int cols = boxes == 1 ? 1 : D / 64;  // copies of a box: a whole tile is one
       const int* table = a.pg.tables + int64_t(run->table) * a.pg.tables_row;
       const int key0 = run->tile0 * kTile + lane * a.box;  // first key of this lane's box in the run's first tile
       const auto page_of = [&](int t) {
@@ -290,9 +291,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const int at = int(unsigned(key) % unsigned(a.pg.page_size));
           bounds_ok(key < a.sh.cap && at + a.box <= a.pg.page_size, a.status);
           uint8_t* dst = sKV + slot * C::kTileBytes + lane * a.box * 128;
-#pragma unroll
-          for (int x = 0; x < D; x += 64)
-            tma_load_4d(dst + (x / 64) * (kTile * 128), map, &kv_full[slot], x, run->kvh, at, page);
+          for (int c = 0; c < cols; ++c)
+            tma_load_5d(dst + c * (kTile * 128), map, &kv_full[slot], 0, at, c, run->kvh, page);
         }
         __syncwarp();
         ++nload;
