@@ -17,7 +17,7 @@ inline int64_t max_keys(int cap, int window, int sinks) {
   return seen < cap ? seen : cap;
 }
 
-// Runs per (sequence, KV head group): two CTAs fit an SM.
+// Runs per (sequence, KV head group), for places CTAs at once: two fit an SM.
 //  * As many as fill the places without a second wave, of 64 keys or more (one
 //    round of a CTA's warps), up to a cluster: 8 of one 1028-key sequence with
 //    8 KV heads take 6.7 us, 4 take 7.7; with 8 such sequences 4 take 9.6 us
@@ -29,8 +29,7 @@ inline int64_t max_keys(int cap, int window, int sinks) {
 //    to all places through device memory (one 131K-key sequence, 8 KV heads:
 //    92 us in 38 runs with their join, 188 in 8). Clusters of 16 find too few
 //    places together (122 us there).
-inline int choose_split(int num_sms, int64_t units, int64_t keys) {
-  const int64_t places = 2 * int64_t(num_sms);
+inline int choose_split(int64_t places, int64_t units, int64_t keys, int64_t long_runs) {
   int64_t s = 1;
   while (2 * s <= kDecMaxCluster) {
     const int64_t ctas = 2 * s * units, run = keys / (2 * s);
@@ -39,10 +38,13 @@ inline int choose_split(int num_sms, int64_t units, int64_t keys) {
   }
   if (s == kDecMaxCluster && 2 * s * units <= places) {
     int64_t more = places / units;
-    if (more > keys / 2048) more = keys / 2048;
+    if (more > long_runs) more = long_runs;
     if (more > s) s = more < kDecMaxSplit ? more : kDecMaxSplit;
   }
   return int(s);
+}
+inline int choose_split(int num_sms, int64_t units, int64_t keys) {
+  return choose_split(2 * int64_t(num_sms), units, keys, keys / 2048);
 }
 
 // Workspace bytes (0: none).

@@ -74,6 +74,15 @@ int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int windo
 // Query heads of a unit: 8 where they suffice (half of the work), or 16.
 int unit_heads(int G) { return G <= 8 ? 8 : 16; }
 
+// Runs over pages: the same rule, with twice the places at d = 64, and 16 runs
+// rather than a cluster's 8 from 8192 keys on, where the second kernel that
+// joins them costs less than it saves (one sequence of 8192 keys, 2 KV heads, d
+// 64: 11.4 us in 8 runs, 9.3 in 16; 8 KV heads of 128: 14.4 and 13.9; at 4096 keys 10.5 and 10.7).
+int paged_split(int num_sms, int d, int64_t units, int64_t keys) {
+  const int64_t places = int64_t(d == 128 ? PagedCfg<128>::kPerSm : PagedCfg<64>::kPerSm) * num_sms;
+  return choose_split(places, units, keys, keys < 8192 ? 0 : std::max<int64_t>(16, keys / 2048));
+}
+
 // What the calls' arguments have in common; o and lse as cpattn_decode.
 void fill_decode(PagedArgs* pa, const void* q, const cpattn_pages* p, const int* lengths, void* o, float* lse, int b,
                  int hq, int hkv, int d, int64_t q_batch, float scale, DeviceInfo* di) {
@@ -138,8 +147,8 @@ int check_groups(int b, int groups, int max_group) {
 
 // CTAs per unit of a member's own keys: as for any decode of up to cap keys,
 // within a cluster, whose join also takes in the group's results.
-int own_split(int num_sms, int64_t units, int64_t cap) {
-  const int s = choose_split(num_sms, units, cap);
+int own_split(int num_sms, int d, int64_t units, int64_t cap) {
+  const int s = paged_split(num_sms, d, units, cap);
   return s < kDecMaxCluster ? s : kDecMaxCluster;
 }
 
@@ -154,16 +163,15 @@ int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaSt
   using C = PagedCfg<D>;
   const DecodeArgs& a = pa.d;
   const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
-  pa.stages = ctas <= di->num_sms ? C::kMaxStages : C::kStages;
   const auto kernel = cpattn_decode_paged_kernel<D, kOwn, kHeads>;
   CUtensorMap tk, tv;
   pa.box = std::gcd(p->page_size, 2 * kDecBlock);
   if (!encode_pools(&tk, &tv, p, a.hkv, D, pa.box, D / 64) ||
       !allow_smem(di->paged_attr[(kHeads == 8 ? 4 : 0) + (kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel,
-                  C::smem_bytes(C::kMaxStages)))
+                  C::kSmemBytes))
     return CPATTN_ERR_CUDA;
   cudaError_t e =
-      launch_runs(kernel, ctas, kPagedThreads, a.nsplit, C::smem_bytes(pa.stages), kOwn, st, tk, tv, pa);
+      launch_runs(kernel, ctas, kPagedThreads, a.nsplit, C::kSmemBytes, kOwn, st, tk, tv, pa);
   const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
   if (e == cudaSuccess && kOwn) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
   if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
@@ -263,7 +271,7 @@ extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, in
   if (device_info(&di)) return 0;
   const int G = hq / hkv;
   const int64_t units = int64_t(b) * hkv * ((G + unit_heads(G) - 1) / unit_heads(G));
-  return workspace_for(b, hq, d, choose_split(di->num_sms, units, max_keys(cap, window, sinks)));
+  return workspace_for(b, hq, d, paged_split(di->num_sms, d, units, max_keys(cap, window, sinks)));
 }
 
 extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse,
@@ -280,7 +288,7 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   DecodeArgs& a = pa.d;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
-  a.nsplit = choose_split(di->num_sms, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
+  a.nsplit = paged_split(di->num_sms, d, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
   const size_t need = workspace_for(b, hq, d, a.nsplit);
   if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
   if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -316,7 +324,7 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   PagedArgs pa;
   fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
   DecodeArgs& a = pa.d;
-  a.nsplit = own_split(di->num_sms, int64_t(b) * hkv * a.row_groups, a.cap);
+  a.nsplit = own_split(di->num_sms, d, int64_t(b) * hkv * a.row_groups, a.cap);
   uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
   const auto take = [&ws](size_t bytes) {
     uint8_t* at = ws;

@@ -36,7 +36,6 @@ struct PagedArgs {
   SharedPlan sh;  // kOwn
   float* own_o;   // kOwn: [b, hq, D] normalised
   float* own_lse; // [b, hq], base 2
-  int stages;
   int box;  // tokens of a copy: gcd(page_size, 32)
 };
 
@@ -46,14 +45,15 @@ template <int D>
 struct PagedCfg {
   static constexpr int kTileBytes = kPagedRound * D * 2;  // keys or values of a round
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // Two CTAs fit an SM with kStages, one has it to itself with kMaxStages. Where
-  // there is no more than one CTA per SM, the deeper ring keeps twice as much on
-  // its way.
-  static constexpr int kStages = D == 128 ? 3 : 6, kMaxStages = 2 * kStages;
+  static constexpr int kStages = 3;
+  // CTAs that fit an SM with 8 heads to a unit. (d = 64 with six stages and two of
+  // them: 37 sequences of up to 2928 keys, 2 KV heads, 12.4 us instead of 10.7; 64 of
+  // 8192, 8 KV heads, 135 instead of 120.)
+  static constexpr int kPerSm = D == 128 ? 2 : 4;
   // barriers (full and empty per stage) and the flag come first, the ring (1024-byte aligned) behind them
-  static constexpr int kOffFlag = 2 * kMaxStages * 8;
+  static constexpr int kOffFlag = 2 * kStages * 8;
   static constexpr int kOffRing = 1024;
-  static constexpr int smem_bytes(int stages) { return kOffRing + stages * kStageBytes + 1024; }  // + alignment slack
+  static constexpr int kSmemBytes = kOffRing + kStages * kStageBytes + 1024;  // + alignment slack
   // the join of the warps reuses the ring, kJoinBytes for each: O and pairs, as in DecodeCfg, and the CTA's result
   static constexpr int kResult = 16 * D * 4 + 16 * 8;
   static constexpr int kJoinBytes = kStages * kStageBytes / kDecWarps;
@@ -176,7 +176,7 @@ struct DecodeCols {
 
 // kHeads: query heads of a unit, 8 (DecodeCols) or 16 (DecodeRows).
 template <int D, bool kOwn, int kHeads>
-__global__ void __launch_bounds__(kPagedThreads)
+__global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPerSm : 2)
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
   const DecodeArgs& a = pa.d;
@@ -185,13 +185,12 @@ __global__ void __launch_bounds__(kPagedThreads)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = pa.stages;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + stages;
+  uint64_t* empty = full + C::kStages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffFlag);
   if (threadIdx.x == 0) *abort_flag = 0;
-  if (threadIdx.x < 2 * stages) {
-    mbar_init(&full[threadIdx.x], threadIdx.x < stages ? 1 : kDecWarps);
+  if (threadIdx.x < 2 * C::kStages) {
+    mbar_init(&full[threadIdx.x], threadIdx.x < C::kStages ? 1 : kDecWarps);
     fence_mbar_init();
   }
   __syncthreads();
@@ -268,15 +267,15 @@ __global__ void __launch_bounds__(kPagedThreads)
       on = next_on;
       slot = next_slot;
       page = next_page;
-      if (++stage == stages) {
+      if (++stage == C::kStages) {
         stage = 0;
         ++turn;
       }
     }
     if (!ok) {  // gave up: what was asked for arrives before the shared memory is used otherwise
       if (lane == 0) atomicOr(a.status, kStatusCopies);
-      for (int u = t > stages ? t - stages : 0; u < t; ++u)
-        mbar_wait_drain_warp(&full[u % stages], (u / stages) & 1, kWaitLimitNs);
+      for (int u = t > C::kStages ? t - C::kStages : 0; u < t; ++u)
+        mbar_wait_drain_warp(&full[u % C::kStages], (u / C::kStages) & 1, kWaitLimitNs);
     }
   } else {
     // ------------------------------------------------------------ products
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(kPagedThreads)
         __syncwarp();  // all lanes have read the stage
       }
       if (lane == 0) mbar_arrive(&empty[stage]);
-      if (++stage == stages) {
+      if (++stage == C::kStages) {
         stage = 0;
         ++turn;
       }
