@@ -25,7 +25,7 @@ struct DeviceInfo {
   std::atomic<bool> win_fwd_attr[4] = {};  // window form: [d == 128][tile pairs]
   std::atomic<bool> win_bwd_attr[2] = {};  // window form: [d == 128]
   std::atomic<bool> decode_attr[2] = {};   // [d == 128]
-  std::atomic<bool> paged_attr[8] = {};    // [units of 8 heads][own keys of a group's member][d == 128]
+  std::atomic<bool> paged_attr[12] = {};   // [PagedKind][units of 16 rows][d == 128]
   std::atomic<bool> prefix_attr[2] = {};   // [d == 128]
   std::atomic<bool> qk_bwd_attr[4] = {};   // [d == 128][interleaved]
 };

@@ -32,9 +32,9 @@ __device__ __forceinline__ bool page_ok(int page, const PagedPlace& pg, unsigned
 // Sequences offsets[g] .. offsets[g + 1] - 1 are group g, which has its first
 // shared[g] tokens in common. A member that holds fewer tokens, or comes after
 // max_group others, shares nothing. The rows of a group for one KV head are
-// its members' query heads, G of each; kSharedRows of them are a unit, whose
-// common keys are cut into runs of whole tiles, one CTA each.
-constexpr int kSharedRows = 256;
+// its members' query heads, G of each; unit_rows of them are a unit, whose
+// common keys are cut into runs, one CTA each.
+constexpr int kSharedRows = 256;  // the prefix kernel's units
 
 // Of a group: the first of its runs' CTAs, and the runs of each of its units.
 struct GroupRuns {
@@ -49,7 +49,11 @@ struct SharedPlan {
   int b, hkv, G, cap;
   float token_bytes;  // of a token's key and value in one KV head
   int ctas;       // runs at most
-  int part_rows;  // rows kept of each CTA
+  int unit_rows;
+  int part_rows;  // rows kept of each CTA, min(unit_rows, a group's)
+  // Without the prefix kernel (fixed_runs > 0) every unit has so many runs and
+  // every group the units of the largest one; with it both follow the counts.
+  int fixed_runs, fixed_units;
   GroupRuns* runs;
   float* part_o;    // [ctas][part_rows][D], normalised
   float* part_lse;  // [ctas][part_rows], base 2
@@ -74,7 +78,7 @@ __device__ __forceinline__ int shared_count(const SharedPlan& s, int g) {
   return c < 0 ? 0 : (c < s.cap ? c : s.cap);
 }
 __device__ __forceinline__ int shared_units(const SharedPlan& s, int size) {
-  return (size * s.G + kSharedRows - 1) / kSharedRows;
+  return (size * s.G + s.unit_rows - 1) / s.unit_rows;
 }
 
 // A sequence's place in its group, and the keys that it leaves to the group (0: none).
@@ -96,14 +100,15 @@ __device__ __forceinline__ SharedSeq shared_seq(const SharedPlan& s, int bi, int
   int first, size;
   shared_group(s, r.group, first, size);
   r.member = bi - first;
-  r.units = shared_units(s, size);
+  r.units = s.fixed_runs > 0 ? s.fixed_units : shared_units(s, size);
   const int c = shared_count(s, r.group);
   r.keys = r.member >= 0 && r.member < size && n >= c ? c : 0;
-  r.at = {0, 0};
+  r.at = {r.group * s.hkv * s.fixed_units * s.fixed_runs, s.fixed_runs};
   return r;
 }
 // (after the prefix kernel)
 __device__ __forceinline__ void shared_runs(const SharedPlan& s, SharedSeq& r) {
+  if (s.fixed_runs > 0) return;
   const int2 v = __ldcg(reinterpret_cast<const int2*>(s.runs + r.group));
   r.at = {v.x, v.y};
 }
@@ -112,8 +117,8 @@ __device__ __forceinline__ void shared_runs(const SharedPlan& s, SharedSeq& r) {
 // apart). `head`: query head within the KV head's.
 __device__ __forceinline__ int64_t shared_at(const SharedPlan& s, const SharedSeq& r, int kvh, int head) {
   const int row = r.member * s.G + head;
-  const int64_t cta = r.at.first + int64_t(kvh * r.units + row / kSharedRows) * r.at.runs;
-  return cta * s.part_rows + row % kSharedRows;
+  const int64_t cta = r.at.first + int64_t(kvh * r.units + row / s.unit_rows) * r.at.runs;
+  return cta * s.part_rows + row % s.unit_rows;
 }
 
 }  // namespace cpattn

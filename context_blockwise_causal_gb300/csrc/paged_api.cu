@@ -71,8 +71,8 @@ int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int windo
   return p ? check_pages(p, hkv, d) : CPATTN_OK;
 }
 
-// Query heads of a unit: 8 where they suffice (half of the work), or 16.
-int unit_heads(int G) { return G <= 8 ? 8 : 16; }
+// Rows of a unit: 8 where they suffice (half of the work), or 16.
+int unit_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
 // Runs over pages: the same rule, with twice the places at d = 64, and 16 runs
 // rather than a cluster's 8 from 8192 keys on, where the second kernel that
@@ -98,7 +98,7 @@ void fill_decode(PagedArgs* pa, const void* q, const cpattn_pages* p, const int*
   a->hkv = hkv;
   a->G = hq / hkv;
   a->cap = int(capacity(p));
-  a->row_groups = (a->G + unit_heads(a->G) - 1) / unit_heads(a->G);
+  a->row_groups = (a->G + unit_rows(a->G) - 1) / unit_rows(a->G);
   a->scale_log2 = float(1.4426950408889634 * (scale == 0.f ? default_scale(d) : double(scale)));
   a->status = di->status;
   pa->pg = place_of(p);
@@ -113,43 +113,59 @@ int check_pointers(const void* q, const int* lengths, const void* o, const float
   return CPATTN_OK;
 }
 
-// Runs of the common keys and where their results go.
+// Common keys by the prefix kernel, whose matrix tiles have 128 rows, or, for
+// groups of few rows, by the kernel that reads the own keys.
+constexpr int kFewRows = 32;
+
+// Runs of the common and of the own keys and where their results go.
 struct SharedShape {
-  int64_t ctas;
-  int part_rows;
+  bool few;
+  int unit_rows, part_rows, fixed_runs, fixed_units, own_rows, own_runs;
+  int64_t ctas;  // of the common keys
   size_t runs_bytes, lse_bytes, o_bytes, own_lse_bytes, own_o_bytes;
   // (results are stored in whole sectors, so the parts begin at the first multiple of 256)
   size_t bytes() const { return 256 + runs_bytes + lse_bytes + o_bytes + own_lse_bytes + own_o_bytes; }
 };
 
-// One run per SM, or as many as it takes for the units to be at most half of
-// them (so that runs of about the same length exist, whatever the groups'
-// lengths turn out to be).
 bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
-  const int64_t rows = int64_t(max_group) * (hq / hkv);
+  const int64_t G = hq / hkv, rows = int64_t(max_group) * G;
   if (rows >= int64_t(1) << 30) return false;
-  const int64_t units = (rows + kSharedRows - 1) / kSharedRows * hkv * groups;
-  s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
-  if (units >= int64_t(1) << 30 || s->ctas >= int64_t(1) << 31) return false;
-  s->part_rows = rows < kSharedRows ? int((rows + 15) / 16 * 16) : kSharedRows;
-  const size_t parts = size_t(s->ctas) * s->part_rows;
+  s->few = rows <= kFewRows;
+  s->own_rows = unit_rows(s->few ? rows : G);
+  const int64_t own_units = int64_t(b) * hkv * ((G + s->own_rows - 1) / s->own_rows);
+  // Own keys are mostly few, and how many is not known here: runs only where sequences are few.
+  s->own_runs = 1;
+  while (s->own_runs < kDecMaxCluster && 2 * s->own_runs * own_units <= 64) s->own_runs *= 2;
+  s->unit_rows = s->few ? s->own_rows : kSharedRows;
+  const int64_t row_units = (rows + s->unit_rows - 1) / s->unit_rows, units = row_units * hkv * groups;
+  if (units >= int64_t(1) << 30) return false;
+  s->fixed_units = int(row_units);
+  s->fixed_runs = 0;
+  if (s->few) {
+    // as many runs as fill the places that the own keys' CTAs leave
+    const int64_t places = int64_t(s->own_rows == 8 && d == 64 ? 4 : 2) * num_sms, own = own_units * s->own_runs;
+    const int64_t runs = (places - std::min(own, places / 2)) / units;
+    s->fixed_runs = int(runs < 1 ? 1 : runs > kDecMaxSplit ? kDecMaxSplit : runs);
+    s->ctas = units * s->fixed_runs;
+  } else {
+    // One run per SM, or as many as it takes for the units to be at most half of
+    // them (so that runs of about the same length exist, whatever the groups'
+    // lengths turn out to be).
+    s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
+  }
+  if (s->ctas + own_units * s->own_runs >= int64_t(1) << 31) return false;
+  s->part_rows = int(std::min<int64_t>(s->unit_rows, (rows + 15) / 16 * 16));
+  const size_t parts = size_t(s->ctas) * s->part_rows, own_parts = size_t(b) * hq * s->own_runs;
   s->runs_bytes = align256(size_t(groups) * sizeof(GroupRuns));
   s->lse_bytes = align256(parts * 4);
   s->o_bytes = align256(parts * d * 4);
-  s->own_lse_bytes = align256(size_t(b) * hq * 4);
-  s->own_o_bytes = align256(size_t(b) * hq * d * 4);
+  s->own_lse_bytes = align256(own_parts * 4);
+  s->own_o_bytes = align256(own_parts * d * 4);
   return true;
 }
 
 int check_groups(int b, int groups, int max_group) {
   return groups < 1 || groups > b || max_group < 1 || max_group > b ? CPATTN_ERR_INVALID_ARG : CPATTN_OK;
-}
-
-// CTAs per unit of a member's own keys: as for any decode of up to cap keys,
-// within a cluster, whose join also takes in the group's results.
-int own_split(int num_sms, int d, int64_t units, int64_t cap) {
-  const int s = paged_split(num_sms, d, units, cap);
-  return s < kDecMaxCluster ? s : kDecMaxCluster;
 }
 
 // Descriptors of the pools for copies of `box` tokens and 64 `cols` features.
@@ -158,41 +174,42 @@ bool encode_pools(CUtensorMap* tk, CUtensorMap* tv, const cpattn_pages* p, int h
          encode_bf16_pages(tv, p->v, p->pages, p->page_size, hkv, d, p->v_page, p->v_token, p->v_head, box, cols);
 }
 
-template <int D, bool kOwn, int kHeads>
+template <int D, PagedKind kKind, int kT>
 int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
   using C = PagedCfg<D>;
+  constexpr bool kParts = kKind != PagedKind::kWhole;
   const DecodeArgs& a = pa.d;
-  const int64_t ctas = int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
-  const auto kernel = cpattn_decode_paged_kernel<D, kOwn, kHeads>;
+  const int64_t ctas = pa.common_ctas + int64_t(a.b) * a.hkv * a.row_groups * a.nsplit;
+  const auto kernel = cpattn_decode_paged_kernel<D, kKind, kT>;
   CUtensorMap tk, tv;
   pa.box = std::gcd(p->page_size, 2 * kDecBlock);
   if (!encode_pools(&tk, &tv, p, a.hkv, D, pa.box, D / 64) ||
-      !allow_smem(di->paged_attr[(kHeads == 8 ? 4 : 0) + (kOwn ? 2 : 0) + (D == 128 ? 1 : 0)], kernel,
-                  C::kSmemBytes))
+      !allow_smem(di->paged_attr[int(kKind) * 4 + (kT - 1) * 2 + (D == 128 ? 1 : 0)], kernel, C::kSmemBytes))
     return CPATTN_ERR_CUDA;
-  cudaError_t e =
-      launch_runs(kernel, ctas, kPagedThreads, a.nsplit, C::kSmemBytes, kOwn, st, tk, tv, pa);
+  cudaError_t e = launch_runs(kernel, ctas, kPagedThreads, kParts ? 1 : a.nsplit, C::kSmemBytes,
+                              kKind == PagedKind::kOwn, st, tk, tv, pa);
   const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
-  if (e == cudaSuccess && kOwn) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
-  if (e == cudaSuccess && !kOwn && a.nsplit > kDecMaxCluster)
+  if (e == cudaSuccess && kParts) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
+  if (e == cudaSuccess && !kParts && a.nsplit > kDecMaxCluster)
     e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
   return launched(e);
 }
-
-template <int D, bool kOwn>
-int launch_paged(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
-  return unit_heads(pa.d.G) == 8 ? launch_paged_as<D, kOwn, 8>(pa, p, di, st) : launch_paged_as<D, kOwn, 16>(pa, p, di, st);
+template <int D, PagedKind kKind>
+int launch_paged(int rows, PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+  return rows == 8 ? launch_paged_as<D, kKind, 1>(pa, p, di, st) : launch_paged_as<D, kKind, 2>(pa, p, di, st);
 }
 
 template <int D>
-int launch_shared(PagedArgs& pa, const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di, cudaStream_t st) {
+int launch_shared(bool few, int own_rows, PagedArgs& pa, const PrefixArgs& a, const cpattn_pages* p, DeviceInfo* di,
+                  cudaStream_t st) {
+  if (few) return launch_paged<D, PagedKind::kBoth>(own_rows, pa, p, di, st);
   CUtensorMap tk, tv;
   if (!encode_pools(&tk, &tv, p, a.sh.hkv, D, a.box, a.box == kTile ? D / 64 : 1) ||
       !allow_smem(di->prefix_attr[D == 128 ? 1 : 0], cpattn_prefix_kernel<D>, PrefixCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
   cpattn_prefix_kernel<D><<<unsigned(a.sh.ctas), kFwdThreads, PrefixCfg<D>::kSmemBytes, st>>>(tk, tv, a);
   const int rc = launched(cudaGetLastError());
-  return rc ? rc : launch_paged<D, true>(pa, p, di, st);
+  return rc ? rc : launch_paged<D, PagedKind::kOwn>(own_rows, pa, p, di, st);
 }
 
 template <int D, bool kInter>
@@ -270,7 +287,7 @@ extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, in
   DeviceInfo* di = nullptr;
   if (device_info(&di)) return 0;
   const int G = hq / hkv;
-  const int64_t units = int64_t(b) * hkv * ((G + unit_heads(G) - 1) / unit_heads(G));
+  const int64_t units = int64_t(b) * hkv * ((G + unit_rows(G) - 1) / unit_rows(G));
   return workspace_for(b, hq, d, paged_split(di->num_sms, d, units, max_keys(cap, window, sinks)));
 }
 
@@ -295,7 +312,9 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged<128, false>(pa, pages, di, st) : launch_paged<64, false>(pa, pages, di, st);
+  const int rows = unit_rows(a.G);
+  return d == 128 ? launch_paged<128, PagedKind::kWhole>(rows, pa, pages, di, st)
+                  : launch_paged<64, PagedKind::kWhole>(rows, pa, pages, di, st);
 }
 
 extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group) {
@@ -324,7 +343,9 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   PagedArgs pa;
   fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
   DecodeArgs& a = pa.d;
-  a.nsplit = own_split(di->num_sms, d, int64_t(b) * hkv * a.row_groups, a.cap);
+  a.nsplit = shape.own_runs;
+  a.row_groups = (a.G + shape.own_rows - 1) / shape.own_rows;
+  pa.common_ctas = shape.few ? int(shape.ctas) : 0;
   uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
   const auto take = [&ws](size_t bytes) {
     uint8_t* at = ws;
@@ -343,12 +364,15 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   sh.cap = a.cap;
   sh.token_bytes = float(4 * d);
   sh.ctas = int(shape.ctas);
+  sh.unit_rows = shape.unit_rows;
+  sh.fixed_runs = shape.fixed_runs;
+  sh.fixed_units = shape.fixed_units;
   sh.part_rows = shape.part_rows;
   sh.runs = reinterpret_cast<GroupRuns*>(take(shape.runs_bytes));
   sh.part_lse = reinterpret_cast<float*>(take(shape.lse_bytes));
   sh.part_o = reinterpret_cast<float*>(take(shape.o_bytes));
-  pa.own_lse = reinterpret_cast<float*>(take(shape.own_lse_bytes));
-  pa.own_o = reinterpret_cast<float*>(take(shape.own_o_bytes));
+  a.part_lse = reinterpret_cast<float*>(take(shape.own_lse_bytes));
+  a.part_o = reinterpret_cast<float*>(take(shape.own_o_bytes));
   PrefixArgs p;
   p.sh = sh;
   p.pg = pa.pg;
@@ -360,5 +384,6 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   p.scale_log2 = a.scale_log2;
   p.status = di->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_shared<128>(pa, p, pages, di, st) : launch_shared<64>(pa, p, pages, di, st);
+  return d == 128 ? launch_shared<128>(shape.few, shape.own_rows, pa, p, pages, di, st)
+                  : launch_shared<64>(shape.few, shape.own_rows, pa, p, pages, di, st);
 }

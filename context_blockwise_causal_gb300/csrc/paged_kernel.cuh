@@ -19,7 +19,6 @@
 #include <cuda_bf16.h>
 
 #include <cstdint>
-#include <type_traits>
 
 #include "decode_kernel.cuh"
 #include "paged.cuh"
@@ -33,10 +32,9 @@ constexpr int kPagedThreads = (kDecWarps + 1) * 32;
 struct PagedArgs {
   DecodeArgs d;  // k and v are not used (the copies' descriptors name the pools)
   PagedPlace pg;
-  SharedPlan sh;  // kOwn
-  float* own_o;   // kOwn: [b, hq, D] normalised
-  float* own_lse; // [b, hq], base 2
-  int box;  // tokens of a copy: gcd(page_size, 32)
+  SharedPlan sh;    // kOwn, kBoth
+  int common_ctas;  // kBoth
+  int box;          // tokens of a copy: gcd(page_size, 32)
 };
 
 constexpr int kPagedRound = kDecWarps * kDecBlock;  // keys of a round
@@ -67,78 +65,99 @@ __device__ __forceinline__ uint32_t turn_8x8(uint32_t x) {
   return r;
 }
 
-// A warp's part of a unit of up to 8 query heads. Where decode_kernel.cuh has
-// the heads as the rows of the matrix tiles, which come in sixteens, here they
-// are the columns, which come in eights: S^T = K Q^T and O^T = V^T P^T, half of
-// the products, exponentials and registers. Lane: heads 2 c4 and 2 c4 + 1; of S^T
-// keys g4 and g4 + 8, of O^T features g4 and g4 + 8 of each 16.
-template <int D>
+// A warp's part of a unit of up to 8 kT rows (query heads of one KV head).
+// decode_kernel.cuh has them as the rows of the matrix tiles, which come in
+// sixteens; here they are the columns, which come in eights: S^T = K Q^T and
+// O^T = V^T P^T, so that 8 heads or fewer take half of the products,
+// exponentials and registers. Lane, for each tile of 8: rows 2 c4 and 2 c4 + 1;
+// of S^T keys g4 and g4 + 8, of O^T features g4 and g4 + 8 of each 16.
+template <int D, int kT>
 struct DecodeCols {
-  static constexpr int kHeads = 8, kSteps = D / 16;
-  uint32_t qf[kSteps][2];
-  float acc[kSteps][4];
-  float m[2], l[2];  // l: this lane's keys
+  static constexpr int kSteps = D / 16;
+  uint32_t qf[kT][kSteps][2];
+  float acc[kT][kSteps][4];
+  float m[kT][2], l[kT][2];  // l: this lane's keys
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* qp, int rows) {
+  // row(r): the queries of row r, or nullptr past the unit's rows
+  template <class R>
+  __device__ __forceinline__ void load(R row) {
     const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int t = 0; t < kT; ++t) {
+      const __nv_bfloat16* q = row(8 * t + g4);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        qf[s][e] = g4 < rows ? *reinterpret_cast<const uint32_t*>(qp + int64_t(g4) * D + s * 16 + e * 8 + 2 * c4) : 0u;
-      acc[s][0] = acc[s][1] = acc[s][2] = acc[s][3] = 0.f;
+      for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qf[t][s][e] = q ? *reinterpret_cast<const uint32_t*>(q + s * 16 + e * 8 + 2 * c4) : 0u;
+        acc[t][s][0] = acc[t][s][1] = acc[t][s][2] = acc[t][s][3] = 0.f;
+      }
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
     }
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
   }
 
-  // As DecodeRows::block.
+  // One block of 16 keys, those in [from, to) of it visible. kat(r, p), vat(r, p):
+  // shared-memory address of 16-byte piece p of key r.
   template <class K, class V>
   __device__ __forceinline__ void block(K kat, V vat, int from, int to, float scale_log2) {
     const int lane = threadIdx.x & 31, g4 = lane >> 2;
-    // two chains of products, which are added: half as long
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    // two chains of products for each tile, which are added: half as long
+    float sa[kT][4], sb[kT][4];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sa[t][e] = sb[t][e] = 0.f;
     {
       const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         uint32_t kb[4];
         ldmatrix4(kat(r, 2 * s + (lane >> 4)), kb);
-        mma_16x8x16(s & 1 ? s1 : s0, kb, qf[s][0], qf[s][1]);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) mma_16x8x16(s & 1 ? sb[t] : sa[t], kb, qf[t][s][0], qf[t][s][1]);
       }
     }
-    float x[4];  // [key g4, g4 + 8][head]
+    float alpha[kT][2];
+    uint32_t p0[kT], p1[kT];
+    bool moved = false;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int key = g4 + (e >> 1) * 8;
-      x[e] = key >= from && key < to ? (s0[e] + s1[e]) * scale_log2 : -INFINITY;
-    }
-    float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])}, alpha[2];
+    for (int t = 0; t < kT; ++t) {
+      float x[4];  // [key g4, g4 + 8][row]
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-      mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-    }
-    const bool moved = mx[0] > m[0] || mx[1] > m[1];
+      for (int e = 0; e < 4; ++e) {
+        const int key = g4 + (e >> 1) * 8;
+        x[e] = key >= from && key < to ? (sa[t][e] + sb[t][e]) * scale_log2 : -INFINITY;
+      }
+      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float mn = fmaxf(m[h], mx[h]);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      alpha[h] = ex2_approx(m[h] - base);
-      m[h] = mn;
-      x[h] = ex2_approx(x[h] - base);
-      x[2 + h] = ex2_approx(x[2 + h] - base);
-      l[h] = l[h] * alpha[h] + (x[h] + x[2 + h]);
+      for (int o = 4; o < 32; o <<= 1) {
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+      }
+      moved |= mx[0] > m[t][0] || mx[1] > m[t][1];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float mn = fmaxf(m[t][h], mx[h]);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        alpha[t][h] = ex2_approx(m[t][h] - base);
+        m[t][h] = mn;
+        x[h] = ex2_approx(x[h] - base);
+        x[2 + h] = ex2_approx(x[2 + h] - base);
+        l[t][h] = l[t][h] * alpha[t][h] + (x[h] + x[2 + h]);
+      }
+      p0[t] = turn_8x8(pack_bf16x2(x[0], x[1]));
+      p1[t] = turn_8x8(pack_bf16x2(x[2], x[3]));
     }
-    const uint32_t p0 = turn_8x8(pack_bf16x2(x[0], x[1])), p1 = turn_8x8(pack_bf16x2(x[2], x[3]));
     if (__any_sync(0xffffffffu, moved)) {  // seldom, after a few blocks
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        acc[s][0] *= alpha[0];
-        acc[s][1] *= alpha[1];
-        acc[s][2] *= alpha[0];
-        acc[s][3] *= alpha[1];
-      }
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          acc[t][s][0] *= alpha[t][0];
+          acc[t][s][1] *= alpha[t][1];
+          acc[t][s][2] *= alpha[t][0];
+          acc[t][s][3] *= alpha[t][1];
+        }
     }
     {
       const int r = (lane & 7) + (lane >> 4) * 8;
@@ -146,41 +165,51 @@ struct DecodeCols {
       for (int s = 0; s < kSteps; ++s) {
         uint32_t vb[4];
         ldmatrix4_trans(vat(r, 2 * s + ((lane >> 3) & 1)), vb);
-        mma_16x8x16(acc[s], vb, p0, p1);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) mma_16x8x16(acc[t][s], vb, p0[t], p1[t]);
       }
     }
   }
 
-  // As DecodeRows::store (8 rows of the 16).
+  // For the join of the CTA's warps: O [16][D], then m[16] and l[16], at jo.
   __device__ __forceinline__ void store(float* jo) {
     const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
-      l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
-    }
+    for (int t = 0; t < kT; ++t) {
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+      for (int o = 4; o < 32; o <<= 1) {
+        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], o);
+        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], o);
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) jo[(2 * c4 + (e & 1)) * D + s * 16 + g4 + (e >> 1) * 8] = acc[s][e];
-    if (g4 == 0) {
-      float* jm = jo + 16 * D;
+      for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        jm[2 * c4 + h] = m[h];
-        jm[16 + 2 * c4 + h] = l[h];
+        for (int e = 0; e < 4; ++e) jo[(8 * t + 2 * c4 + (e & 1)) * D + s * 16 + g4 + (e >> 1) * 8] = acc[t][s][e];
+      if (g4 == 0) {
+        float* jm = jo + 16 * D;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          jm[8 * t + 2 * c4 + h] = m[t][h];
+          jm[16 + 8 * t + 2 * c4 + h] = l[t][h];
+        }
       }
     }
   }
 };
 
-// kHeads: query heads of a unit, 8 (DecodeCols) or 16 (DecodeRows).
-template <int D, bool kOwn, int kHeads>
-__global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPerSm : 2)
+// What a launch computes: whole sequences; the own keys of sequences whose
+// common ones the prefix kernel takes; or both, common keys in its first CTAs.
+enum class PagedKind { kWhole, kOwn, kBoth };
+
+// kT: rows of a unit in eights.
+template <int D, PagedKind kKind, int kT>
+__global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm : 2)
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
+  constexpr bool kParts = kKind != PagedKind::kWhole;  // results go to the join kernel
+  constexpr int kRows = 8 * kT;
   const DecodeArgs& a = pa.d;
-  if (kOwn || a.nsplit > kDecMaxCluster) chain_next();
+  if (kParts || a.nsplit > kDecMaxCluster) chain_next();
   using C = PagedCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -195,27 +224,46 @@ __global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPer
   }
   __syncthreads();
   smem += C::kOffRing;
-  // unit: (batch, KV head, group of kHeads query heads), then the run of keys
-  int x = blockIdx.x;
-  const int split = x % a.nsplit;
-  x /= a.nsplit;
-  const int rg = x % a.row_groups;
-  x /= a.row_groups;
+  // unit: (sequence or group, KV head, kRows of its rows), then the run of keys
+  const bool common = kKind == PagedKind::kBoth && int(blockIdx.x) < pa.common_ctas;
+  const int nsplit = common ? pa.sh.fixed_runs : a.nsplit, row_groups = common ? pa.sh.fixed_units : a.row_groups;
+  int x = blockIdx.x - (kKind == PagedKind::kBoth && !common ? pa.common_ctas : 0);
+  const int split = x % nsplit;
+  x /= nsplit;
+  const int unit = x;
+  const int row0 = x % row_groups * kRows;  // first row of the unit
+  x /= row_groups;
   const int kvh = x % a.hkv;
-  const int bi = x / a.hkv;
-  const int rows = a.G - rg * kHeads < kHeads ? a.G - rg * kHeads : kHeads;  // query heads of this CTA
-  const int h0 = kvh * a.G + rg * kHeads;
-
-  int n = a.lengths[bi];
-  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
-  int lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
-  if constexpr (kOwn) lo = shared_seq(pa.sh, bi, n).keys;    // those before it are the prefix kernel's
-  const int ns = kOwn ? 0 : (a.sinks < lo ? a.sinks : lo);
+  const int bi = x / a.hkv;  // (of common keys: the group)
+  int rows, n, lo = 0, ns = 0;
+  int first = bi;  // sequence of row 0
+  int named = bi;  // sequence whose table names the pages
+  if (common) {
+    int size;
+    shared_group(pa.sh, bi, first, size);
+    n = shared_count(pa.sh, bi);
+    rows = size * a.G - row0;
+    // the first member that holds all of the common tokens (no more than 32 rows, so members)
+    const unsigned full_members = __ballot_sync(0xffffffffu, lane < size && a.lengths[first + lane] >= n);
+    if (!full_members || rows <= 0) rows = n = 0;
+    named = first + (full_members ? __ffs(full_members) - 1 : 0);
+  } else {
+    rows = a.G - row0;
+    n = a.lengths[bi];
+    n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+    if constexpr (kParts) {
+      lo = shared_seq(pa.sh, bi, n).keys;  // those before it are the group's
+    } else {
+      lo = a.window > 0 && n > a.window ? n - a.window : 0;  // first key of the window
+      ns = a.sinks < lo ? a.sinks : lo;
+    }
+  }
+  rows = rows < kRows ? rows : kRows;
   // rounds that hold visible keys: the first tokens', then the window's
   const int sink_rounds = (ns + kPagedRound - 1) / kPagedRound, lo_round = lo / kPagedRound;
   const int all = sink_rounds + (n > lo ? (n + kPagedRound - 1) / kPagedRound - lo_round : 0);
   // this CTA's run
-  const int per = (all + a.nsplit - 1) / a.nsplit;
+  const int per = (all + nsplit - 1) / nsplit;
   const int64_t begin64 = int64_t(split) * per;
   const int begin = begin64 < all ? int(begin64) : all;
   const int rounds = all - begin < per ? all - begin : per;
@@ -228,14 +276,14 @@ __global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPer
     to = (early ? ns : n) - key0;
     return key0;
   };
-  std::conditional_t<kHeads == 8, DecodeCols<D>, DecodeRows<D>> part;
+  DecodeCols<D, kT> part;
   if (warp == kDecWarps) {
     // ------------------------------------------------------------ copies
     // lane: its box of the keys or of the values
     const int boxes = kPagedRound / pa.box, box = lane % boxes;
     const bool mine = lane < 2 * boxes, values = lane >= boxes;
     const int box_bytes = pa.box * (D * 2);
-    const int* table = pa.pg.tables + int64_t(bi) * pa.pg.tables_row;
+    const int* table = pa.pg.tables + int64_t(named) * pa.pg.tables_row;
     const CUtensorMap* map = values ? &tmv : &tmk;
     uint8_t* dst = smem + (values ? C::kTileBytes : 0) + box * box_bytes;
     // whether this lane's box of a round holds visible keys, its slot in its page, and the page
@@ -279,7 +327,16 @@ __global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPer
     }
   } else {
     // ------------------------------------------------------------ products
-    part.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
+    part.load([&](int r) -> const __nv_bfloat16* {
+      if (r >= rows) return nullptr;
+      int seq = first, head = row0 + r;
+      if (common) {
+        seq += head / a.G;
+        head %= a.G;
+      }
+      bounds_ok(seq < a.b && kvh * a.G + head < a.hq, a.status);
+      return a.q + int64_t(seq) * a.q_batch + int64_t(kvh * a.G + head) * D;
+    });
     // this warp's 16 keys of a round: in a box, whose features come 64 at a time
     const int half_bytes = pa.box * 128;
     const int mine = (warp * kDecBlock / pa.box) * pa.box * (D * 2) + (warp * kDecBlock % pa.box) * 128;
@@ -325,44 +382,85 @@ __global__ void __launch_bounds__(kPagedThreads, kHeads == 8 ? PagedCfg<D>::kPer
   __syncthreads();  // the ring is idle: the join reuses it
   if (warp < kDecWarps) part.store(reinterpret_cast<float*>(smem + warp * C::kJoinBytes));
   __syncthreads();
-  const auto put = [&](int64_t row, int c, const DecodeResult& r) {
-    if constexpr (kOwn) {
-      *reinterpret_cast<float2*>(pa.own_o + row * D + c) = make_float2(r.o0, r.o1);
-      if (c == 0) pa.own_lse[row] = r.l2;
-    } else {
-      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(r.o0, r.o1);
-      if (c == 0) a.lse[row] = r.l2 * kLn2;
-    }
+  const int64_t out0 = int64_t(bi) * a.hq + kvh * a.G + row0;  // (not of common keys)
+  const auto put = [&](int r, int c, const DecodeResult& v) {
+    *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * D + c) = pack_bf16x2(v.o0, v.o1);
+    if (c == 0) a.lse[out0 + r] = v.l2 * kLn2;
   };
   for (int i = threadIdx.x; i < rows * (D / 2); i += kPagedThreads) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
     const DecodeResult v = decode_join_warps<D>(smem, C::kJoinBytes, r, c);
-    const int64_t row = int64_t(bi) * a.hq + h0 + r;
-    if (!bounds_ok(bi < a.b && h0 + r < a.hq, a.status)) continue;
-    if (a.nsplit == 1) {
-      put(row, c, v);
-    } else if (a.nsplit <= kDecMaxCluster) {
+    if (common) {
+      const int64_t at = (int64_t(unit) * nsplit + split) * pa.sh.part_rows + r;
+      if (!bounds_ok(r < pa.sh.part_rows && unit * nsplit + split < pa.common_ctas, a.status)) continue;
+      *reinterpret_cast<float2*>(pa.sh.part_o + at * D + c) = make_float2(v.o0, v.o1);
+      if (c == 0) pa.sh.part_lse[at] = v.l2;
+      continue;
+    }
+    if (!bounds_ok(bi < a.b && row0 + r < a.G, a.status)) continue;
+    if (!kParts && a.nsplit == 1) {
+      put(r, c, v);
+    } else if (!kParts && a.nsplit <= kDecMaxCluster) {
       float* res = reinterpret_cast<float*>(smem + C::kResult);
       *reinterpret_cast<float2*>(res + r * D + c) = make_float2(v.o0, v.o1);
       if (c == 0) res[16 * D + r] = v.l2;
     } else {
-      const int64_t pr = row * a.nsplit + split;
+      const int64_t pr = (out0 + r) * a.nsplit + split;
       *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(v.o0, v.o1);
       if (c == 0) a.part_lse[pr] = v.l2;
     }
   }
-  if (a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
+  if (!kParts && a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
     // the cluster's CTAs are the runs of one unit: each joins its share of the features
     cluster_sync();
     for (int i = split * kPagedThreads + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kPagedThreads) {
       const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-      put(int64_t(bi) * a.hq + h0 + r, c, decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c));
+      put(r, c, decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c));
     }
     cluster_sync();  // no CTA leaves while another still reads its results
   }
   // This kernel is over only when the prefix kernel is, beside which it may run: the join waits for this one.
-  if (kOwn && blockIdx.x == gridDim.x - 1) chain_wait();
+  if (kKind == PagedKind::kOwn && blockIdx.x == gridDim.x - 1) chain_wait();
 }
+
+// The running sum of partial results of one row, a warp's: features kPer lane ...
+template <int kPer>
+struct RowJoin {
+  float m = -INFINITY, l = 0.f, o[kPer] = {};
+  // Adds `runs` results: their l2 at pl, features at po (this lane's), `step` rows of `pitch` floats apart.
+  __device__ __forceinline__ void add(const float* pl, const float* po, int runs, int64_t step, int pitch) {
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < runs; s0 += 32) {
+      const float mine = s0 + lane < runs ? __ldcg(pl + (s0 + lane) * step) : -INFINITY;
+      float mm = fmaxf(m, mine);
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+      const float base = mm == -INFINITY ? 0.f : mm;
+      const float old = ex2_approx(m - base), weight = ex2_approx(mine - base);
+      m = mm;
+      l *= old;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) o[i] *= old;
+      const int count = runs - s0 < 32 ? runs - s0 : 32;
+#pragma unroll 8
+      for (int s = 0; s < count; ++s) {
+        const float w = __shfl_sync(0xffffffffu, weight, s);
+        const float* p = po + (s0 + s) * step * pitch;
+        float v[kPer];
+        if constexpr (kPer == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
+          v[0] = f.x, v[1] = f.y;
+        }
+        l += w;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) o[i] = fmaf(w, v[i], o[i]);
+      }
+    }
+  }
+};
 
 // Joins a row's own keys and its group's: one warp per (sequence, query head).
 template <int D>
@@ -378,52 +476,19 @@ __global__ void __launch_bounds__(128) cpattn_shared_join_kernel(const __grid_co
   n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
   SharedSeq mate = shared_seq(pa.sh, bi, n);
   chain_wait();
-  const float own = __ldcg(pa.own_lse + row);
-  float o[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] = __ldcg(pa.own_o + row * D + lane * kPer + i);
-  int64_t at = 0;
+  RowJoin<kPer> sum;
+  sum.add(a.part_lse + row * a.nsplit, a.part_o + row * a.nsplit * D + lane * kPer, a.nsplit, 1, D);
   if (mate.keys > 0) {
     shared_runs(pa.sh, mate);
-    at = shared_at(pa.sh, mate, kvh, h - kvh * a.G);
-    if (!bounds_ok(at + int64_t(mate.at.runs - 1) * pa.sh.part_rows < int64_t(pa.sh.ctas) * pa.sh.part_rows, a.status)) return;
+    const int64_t at = shared_at(pa.sh, mate, kvh, h - kvh * a.G);
+    if (bounds_ok(at + int64_t(mate.at.runs - 1) * pa.sh.part_rows < int64_t(pa.sh.ctas) * pa.sh.part_rows, a.status))
+      sum.add(pa.sh.part_lse + at, pa.sh.part_o + at * D + lane * kPer, mate.at.runs, pa.sh.part_rows, D);
   }
-  const float* pl = pa.sh.part_lse + at;
-  const float* po = pa.sh.part_o + at * D + lane * kPer;
-  const int64_t step = pa.sh.part_rows;
-  float mm = own;
-  for (int s = lane; s < mate.at.runs; s += 32) mm = fmaxf(mm, __ldcg(pl + s * step));
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = ex2_approx(own - base);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] *= ll;
-  for (int s0 = 0; s0 < mate.at.runs; s0 += 32) {
-    const float mine = s0 + lane < mate.at.runs ? ex2_approx(__ldcg(pl + (s0 + lane) * step) - base) : 0.f;
-    const int count = mate.at.runs - s0 < 32 ? mate.at.runs - s0 : 32;
-#pragma unroll 8
-    for (int s = 0; s < count; ++s) {
-      const float w = __shfl_sync(0xffffffffu, mine, s);
-      const float* p = po + (s0 + s) * step * D;
-      float v[kPer];
-      if constexpr (kPer == 4) {
-        const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-      } else {
-        const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
-        v[0] = f.x, v[1] = f.y;
-      }
-      ll += w;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] = fmaf(w, v[i], o[i]);
-    }
-  }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
-  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(sum.o[i] * inv, sum.o[i + 1] * inv);
+  if (lane == 0) a.lse[row] = sum.l == 0.f ? -INFINITY : (sum.m + log2f(sum.l)) * kLn2;
 }
 
 }  // namespace cpattn

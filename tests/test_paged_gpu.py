@@ -342,6 +342,16 @@ SHARED = [
     ([9, 30, 1, 2], [2049, 130, 1, 4000], [i % 40 for i in range(42)], 64, 16, 2, 128, None, False),
     ([2] * 40, [(i * 37) % 300 for i in range(40)], [i % 3 for i in range(80)], 16, 4, 4, 64, None, False),  # more groups than a warp has lanes
     ([2], [30000], [10, 3], 512, 4, 1, 128, None, False),                    # one unit over the whole chip
+    # the same edges with more than 32 rows to a group
+    ([9], [1], [0, 1, 15, 16, 17, 2, 3, 4, 5], 16, 8, 1, 64, None, False),
+    ([9], [127], [0, 1, 15, 16, 17, 2, 3, 4, 5], 32, 16, 2, 128, None, True),
+    ([9], [128], [0, 1, 15, 16, 17, 2, 3, 4, 5], 64, 16, 2, 64, None, False),
+    ([9], [129], [0, 1, 15, 16, 17, 2, 3, 4, 5], 48, 12, 2, 128, 0.2, False),
+    ([9], [257], [0, 1, 15, 16, 17, 2, 3, 4, 5], 144, 8, 1, 128, None, False),  # three tiles, pages of 144
+    ([20, 1, 0, 12], [400, 0, 50, 77], [i % 33 for i in range(33)], 32, 6, 2, 64, None, False),  # an empty group
+    ([2], [30000], [10, 3], 512, 17, 1, 64, None, False),
+    ([9] * 33, [(i * 37) % 300 for i in range(33)], [i % 3 for i in range(297)], 16, 4, 1, 64, None, False),
+    ([8], [2000], [i * 90 for i in range(8)], 128, 4, 1, 128, None, False),      # exactly 32 rows
 ]
 
 
@@ -369,10 +379,11 @@ def test_shared_all_elements_and_what_is_not_seen(groups, prefix, own, size, hq,
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
-def test_shared_members_that_do_not_share():
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (20, 2)])
+def test_shared_members_that_do_not_share(hq, hkv):
     """Finished sequences (length 0, a cleared table), sequences with fewer tokens
     than the group, behind max_group others, outside of every group."""
-    groups, prefix, size, hq, hkv, d = [4, 5], [300, 200], 32, 4, 2, 128
+    groups, prefix, size, d = [4, 5], [300, 200], 32, 128
     k, v, tables, lengths, _ = _group_state(groups + [2], prefix + [40], [20, 5, 0, 60, 1, 2, 3, 4, 5, 7, 9], size, hq, hkv, d, False, 71)
     lengths[0], lengths[1], lengths[6] = 0, 100, 199
     tables[0] = -1  # the first member's table is gone
@@ -397,11 +408,12 @@ def test_shared_members_that_do_not_share():
     assert o.isfinite().all()
 
 
-def test_shared_bad_pages_count_as_zeros():
-    k, v, tables, lengths, _ = _group_state([3], [200], [5, 6, 7], 32, 4, 2, 64, False, 81)
+@pytest.mark.parametrize("hq", [4, 24])
+def test_shared_bad_pages_count_as_zeros(hq):
+    k, v, tables, lengths, _ = _group_state([3], [200], [5, 6, 7], 32, hq, 2, 64, False, 81)
     tables[:, 2] = 1 << 30
     tables[:, 4] = -2
-    q = _randn(3, 4, 64, seed=84)
+    q = _randn(3, hq, 64, seed=84)
     assert _status() == 0
     o, lse = cpattn_decode_shared(q.cuda(), k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda(), _i32([200]).cuda())
     torch.cuda.synchronize()
@@ -488,9 +500,10 @@ def test_a_server_appends_and_decodes():
         _rotated(oracle.held_tokens(kh, tables[i], n), ref, src[:, hq:hq + hkv], d, "half", 1.0)
 
 
-def test_given_streams_and_calls_at_once():
-    k, v, tables, lengths, off = _group_state([3, 4], [900, 1300], [5, 50, 500, 1, 2, 3, 4], 32, 8, 2, 64, False, 111)
-    q, kd, vd, td, ln = _randn(7, 8, 64, seed=114).cuda(), k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda()
+@pytest.mark.parametrize("hq", [8, 24])
+def test_given_streams_and_calls_at_once(hq):
+    k, v, tables, lengths, off = _group_state([3, 4], [900, 1300], [5, 50, 500, 1, 2, 3, 4], 32, hq, 2, 64, False, 111)
+    q, kd, vd, td, ln = _randn(7, hq, 64, seed=114).cuda(), k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda()
     kw = {"group_offsets": off.cuda(), "max_group": 4}
     counts = [_i32([900, 1300]).cuda(), _i32([33, 1024]).cuda()]
     want = [cpattn_decode_shared(q, kd, vd, td, ln, c, **kw) for c in counts]
@@ -505,14 +518,15 @@ def test_given_streams_and_calls_at_once():
             assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
-def test_shared_calls_one_after_another_on_one_workspace():
-    """Each call's second kernel is placed while its first one runs; each call
+@pytest.mark.parametrize("b", [7, 40])
+def test_shared_calls_one_after_another_on_one_workspace(b):
+    """Each call's later kernels are placed while its first one runs; each call
     takes the one before's output as its queries."""
-    k, v, tables, lengths, _ = _group_state([40], [3000], [i * 5 for i in range(40)], 64, 8, 2, 128, False, 121)
+    k, v, tables, lengths, _ = _group_state([b], [3000], [i * 5 for i in range(b)], 64, 8, 2, 128, False, 121)
     kd, vd, td, ln = k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda()
     sh = _i32([3000]).cuda()
-    q = _randn(40, 8, 128, seed=124).cuda()
-    ws = torch.empty(pkg.cpattn_decode_shared_workspace_bytes(40, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    q = _randn(b, 8, 128, seed=124).cuda()
+    ws = torch.empty(pkg.cpattn_decode_shared_workspace_bytes(b, 8, 2, 128), dtype=torch.uint8, device="cuda")
 
     def chain(sync):
         x, out = q, []
@@ -559,7 +573,9 @@ def test_pool_offsets_beyond_32_bits():
         _check(q1, pk, pv, flat, n, 0, 0, None, o, lse)
 
 
-def test_checked_build_is_silent_and_identical():
+@pytest.mark.parametrize("hq", [2, 6])
+def test_checked_build_is_silent_and_identical(hq):
+    """hq 2: groups of few rows; hq 6: up to 60."""
     lib = pkg.checked_library()
 
     def status():
@@ -570,7 +586,7 @@ def test_checked_build_is_silent_and_identical():
     from test_paged_abi import Pages
     from test_operators_abi import Rotary, Rows
 
-    groups, hq, hkv, d, size = [3, 20, 2], 6, 2, 128, 48
+    groups, hkv, d, size = [3, 20, 2], 2, 128, 48
     k, v, tables, lengths, off = _group_state(groups, [333, 1000, 5], [i % 9 for i in range(25)], size, hq, hkv, d, False, 141)
     b = 25
     q, kd, vd, td, ln = _randn(b, hq, d, seed=144).cuda(), k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda()
