@@ -120,7 +120,7 @@ constexpr int kFewRows = 32;
 // Runs of the common and of the own keys and where their results go.
 struct SharedShape {
   bool few;
-  int unit_rows, part_rows, fixed_runs, fixed_units, own_rows, own_runs;
+  int unit_rows, part_rows, fixed_runs, fixed_units, own_rows, own_runs, join_warps;
   int64_t ctas;  // of the common keys
   size_t runs_bytes, lse_bytes, o_bytes, own_lse_bytes, own_o_bytes;
   // (results are stored in whole sectors, so the parts begin at the first multiple of 256)
@@ -147,11 +147,13 @@ bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, in
     const int64_t runs = (places - std::min(own, places / 2)) / units;
     s->fixed_runs = int(runs < 1 ? 1 : runs > kDecMaxSplit ? kDecMaxSplit : runs);
     s->ctas = units * s->fixed_runs;
+    s->join_warps = s->fixed_runs + s->own_runs > kJoinBatch ? 4 : 1;
   } else {
     // One run per SM, or as many as it takes for the units to be at most half of
     // them (so that runs of about the same length exist, whatever the groups'
     // lengths turn out to be).
     s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
+    s->join_warps = s->ctas / units + s->own_runs > kJoinBatch ? 4 : 1;
   }
   if (s->ctas + own_units * s->own_runs >= int64_t(1) << 31) return false;
   s->part_rows = int(std::min<int64_t>(s->unit_rows, (rows + 15) / 16 * 16));
@@ -188,8 +190,10 @@ int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaSt
     return CPATTN_ERR_CUDA;
   cudaError_t e = launch_runs(kernel, ctas, kPagedThreads, kParts ? 1 : a.nsplit, C::kSmemBytes,
                               kKind == PagedKind::kOwn, st, tk, tv, pa);
-  const int64_t join_ctas = (int64_t(a.b) * a.hq + 3) / 4;
-  if (e == cudaSuccess && kParts) e = launch_chained(cpattn_shared_join_kernel<D>, join_ctas, 128, st, pa);
+  const int64_t out_rows = int64_t(a.b) * a.hq, join_ctas = (out_rows + 3) / 4;
+  if (e == cudaSuccess && kParts)
+    e = pa.join_warps == 1 ? launch_chained(cpattn_shared_join_kernel<D, 1>, join_ctas, 128, st, pa)
+                           : launch_chained(cpattn_shared_join_kernel<D, 4>, out_rows, 128, st, pa);
   if (e == cudaSuccess && !kParts && a.nsplit > kDecMaxCluster)
     e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
   return launched(e);
@@ -345,6 +349,7 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   DecodeArgs& a = pa.d;
   a.nsplit = shape.own_runs;
   a.row_groups = (a.G + shape.own_rows - 1) / shape.own_rows;
+  pa.join_warps = shape.join_warps;
   pa.common_ctas = shape.few ? int(shape.ctas) : 0;
   uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
   const auto take = [&ws](size_t bytes) {

@@ -34,6 +34,7 @@ struct PagedArgs {
   PagedPlace pg;
   SharedPlan sh;    // kOwn, kBoth
   int common_ctas;  // kBoth
+  int join_warps;   // kOwn, kBoth
   int box;          // tokens of a copy: gcd(page_size, 32)
 };
 
@@ -382,32 +383,54 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
   __syncthreads();  // the ring is idle: the join reuses it
   if (warp < kDecWarps) part.store(reinterpret_cast<float*>(smem + warp * C::kJoinBytes));
   __syncthreads();
-  const int64_t out0 = int64_t(bi) * a.hq + kvh * a.G + row0;  // (not of common keys)
-  const auto put = [&](int r, int c, const DecodeResult& v) {
-    *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * D + c) = pack_bf16x2(v.o0, v.o1);
-    if (c == 0) a.lse[out0 + r] = v.l2 * kLn2;
-  };
-  for (int i = threadIdx.x; i < rows * (D / 2); i += kPagedThreads) {
-    const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    const DecodeResult v = decode_join_warps<D>(smem, C::kJoinBytes, r, c);
-    if (common) {
-      const int64_t at = (int64_t(unit) * nsplit + split) * pa.sh.part_rows + r;
-      if (!bounds_ok(r < pa.sh.part_rows && unit * nsplit + split < pa.common_ctas, a.status)) continue;
-      *reinterpret_cast<float2*>(pa.sh.part_o + at * D + c) = make_float2(v.o0, v.o1);
-      if (c == 0) pa.sh.part_lse[at] = v.l2;
-      continue;
+  // The warps' results are joined by weights, formed once for each row.
+  const auto of = [&](int w) { return reinterpret_cast<float*>(smem + w * C::kJoinBytes); };
+  if (threadIdx.x < rows) {
+    const int r = threadIdx.x;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, of(w)[16 * D + r]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float f[kDecWarps], ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      f[w] = ex2_approx(of(w)[16 * D + r] - base);
+      ll = fmaf(f[w], of(w)[16 * D + 16 + r], ll);
     }
-    if (!bounds_ok(bi < a.b && row0 + r < a.G, a.status)) continue;
-    if (!kParts && a.nsplit == 1) {
-      put(r, c, v);
-    } else if (!kParts && a.nsplit <= kDecMaxCluster) {
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) of(w)[16 * D + r] = f[w] * inv;
+    of(0)[16 * D + 16 + r] = ll == 0.f ? -INFINITY : mm + log2f(ll);
+  }
+  __syncthreads();
+  const int64_t out0 = int64_t(bi) * a.hq + kvh * a.G + row0;  // (not of common keys)
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kPagedThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float f = of(w)[16 * D + r];
+      const float4 y = *reinterpret_cast<const float4*>(of(w) + r * D + c);
+      v.x = fmaf(f, y.x, v.x);
+      v.y = fmaf(f, y.y, v.y);
+      v.z = fmaf(f, y.z, v.z);
+      v.w = fmaf(f, y.w, v.w);
+    }
+    const float l2 = of(0)[16 * D + 16 + r];
+    if (!bounds_ok(common ? r < pa.sh.part_rows && unit * nsplit + split < pa.common_ctas : bi < a.b && row0 + r < a.G,
+                   a.status))
+      continue;
+    if (kParts || a.nsplit > kDecMaxCluster) {  // to the join kernel
+      const int64_t at = common ? (int64_t(unit) * nsplit + split) * pa.sh.part_rows + r : (out0 + r) * a.nsplit + split;
+      *reinterpret_cast<float4*>((common ? pa.sh.part_o : a.part_o) + at * D + c) = v;
+      if (c == 0) (common ? pa.sh.part_lse : a.part_lse)[at] = l2;
+    } else if (a.nsplit > 1) {  // to the cluster
       float* res = reinterpret_cast<float*>(smem + C::kResult);
-      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(v.o0, v.o1);
-      if (c == 0) res[16 * D + r] = v.l2;
+      *reinterpret_cast<float4*>(res + r * D + c) = v;
+      if (c == 0) res[16 * D + r] = l2;
     } else {
-      const int64_t pr = (out0 + r) * a.nsplit + split;
-      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(v.o0, v.o1);
-      if (c == 0) a.part_lse[pr] = v.l2;
+      *reinterpret_cast<uint2*>(a.o + (out0 + r) * D + c) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      if (c == 0) a.lse[out0 + r] = l2 * kLn2;
     }
   }
   if (!kParts && a.nsplit > 1 && a.nsplit <= kDecMaxCluster) {
@@ -415,7 +438,9 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
     cluster_sync();
     for (int i = split * kPagedThreads + threadIdx.x; i < rows * (D / 2); i += a.nsplit * kPagedThreads) {
       const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-      put(r, c, decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c));
+      const DecodeResult v = decode_join_cluster<D>(smem_u32(smem) + C::kResult, a.nsplit, r, c);
+      *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * D + c) = pack_bf16x2(v.o0, v.o1);
+      if (c == 0) a.lse[out0 + r] = v.l2 * kLn2;
     }
     cluster_sync();  // no CTA leaves while another still reads its results
   }
@@ -423,72 +448,106 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
   if (kKind == PagedKind::kOwn && blockIdx.x == gridDim.x - 1) chain_wait();
 }
 
-// The running sum of partial results of one row, a warp's: features kPer lane ...
-template <int kPer>
-struct RowJoin {
-  float m = -INFINITY, l = 0.f, o[kPer] = {};
-  // Adds `runs` results: their l2 at pl, features at po (this lane's), `step` rows of `pitch` floats apart.
-  __device__ __forceinline__ void add(const float* pl, const float* po, int runs, int64_t step, int pitch) {
-    const int lane = threadIdx.x & 31;
-    for (int s0 = 0; s0 < runs; s0 += 32) {
-      const float mine = s0 + lane < runs ? __ldcg(pl + (s0 + lane) * step) : -INFINITY;
-      float mm = fmaxf(m, mine);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-      const float base = mm == -INFINITY ? 0.f : mm;
-      const float old = ex2_approx(m - base), weight = ex2_approx(mine - base);
-      m = mm;
-      l *= old;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[i] *= old;
-      const int count = runs - s0 < 32 ? runs - s0 : 32;
-#pragma unroll 8
-      for (int s = 0; s < count; ++s) {
-        const float w = __shfl_sync(0xffffffffu, weight, s);
-        const float* p = po + (s0 + s) * step * pitch;
-        float v[kPer];
-        if constexpr (kPer == 4) {
-          const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
-          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else {
-          const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
-          v[0] = f.x, v[1] = f.y;
-        }
-        l += w;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) o[i] = fmaf(w, v[i], o[i]);
-      }
-    }
-  }
-};
-
-// Joins a row's own keys and its group's: one warp per (sequence, query head).
-template <int D>
+// Joins the results of a row's own keys and of its group's, kWarps warps to a row
+// (sequence, query head). Results are numbered, own ones first; warp w takes w, w + kWarps
+// and so on, a batch at a time, whose values are on their way before their
+// weights are formed. With up to 8 results a warp does by itself; more of them
+// for four warps (30 results of 128 rows: 6 us by one warp, whose loads wait for
+// one another, 2.5 by four).
+constexpr int kJoinBatch = 8;
+template <int D, int kWarps>
 __global__ void __launch_bounds__(128) cpattn_shared_join_kernel(const __grid_constant__ PagedArgs pa) {
   const DecodeArgs& a = pa.d;
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= int64_t(a.b) * a.hq) return;
-  const int bi = int(row / a.hq), h = int(row - int64_t(bi) * a.hq);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = int64_t(blockIdx.x) * (4 / kWarps) + warp / kWarps;
+  const bool live = row < int64_t(a.b) * a.hq;
+  if (kWarps == 1 && !live) return;
+  const int bi = live ? int(row / a.hq) : 0, h = live ? int(row - int64_t(bi) * a.hq) : 0;
   const int kvh = h / a.G;
   int n = a.lengths[bi];
   n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
   SharedSeq mate = shared_seq(pa.sh, bi, n);
   chain_wait();
-  RowJoin<kPer> sum;
-  sum.add(a.part_lse + row * a.nsplit, a.part_o + row * a.nsplit * D + lane * kPer, a.nsplit, 1, D);
+  int64_t at = 0;
   if (mate.keys > 0) {
     shared_runs(pa.sh, mate);
-    const int64_t at = shared_at(pa.sh, mate, kvh, h - kvh * a.G);
-    if (bounds_ok(at + int64_t(mate.at.runs - 1) * pa.sh.part_rows < int64_t(pa.sh.ctas) * pa.sh.part_rows, a.status))
-      sum.add(pa.sh.part_lse + at, pa.sh.part_o + at * D + lane * kPer, mate.at.runs, pa.sh.part_rows, D);
+    at = shared_at(pa.sh, mate, kvh, h - kvh * a.G);
+    if (!bounds_ok(at + int64_t(mate.at.runs - 1) * pa.sh.part_rows < int64_t(pa.sh.ctas) * pa.sh.part_rows, a.status))
+      mate.keys = 0;
   }
-  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+  const int count = a.nsplit + (mate.keys > 0 ? mate.at.runs : 0);
+  const auto place = [&](int i, const float*& l2) {  // of result i: its values (this lane's)
+    const bool own = i < a.nsplit;
+    const int64_t x = own ? row * a.nsplit + i : at + int64_t(i - a.nsplit) * pa.sh.part_rows;
+    l2 = (own ? a.part_lse : pa.sh.part_lse) + x;
+    return (own ? a.part_o : pa.sh.part_o) + x * D + lane * kPer;
+  };
+  float m = -INFINITY, l = 0.f, o[kPer] = {};
+  for (int i0 = warp % kWarps; i0 < count; i0 += kWarps * kJoinBatch) {
+    float v[kJoinBatch][kPer], l2[kJoinBatch];
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const int i = i0 + k * kWarps;
+      l2[k] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[k][e] = 0.f;
+      if (i < count) {
+        const float* pl;
+        const float* p = place(i, pl);
+        l2[k] = __ldcg(pl);
+        if constexpr (kPer == 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+          v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
+          v[k][0] = f.x, v[k][1] = f.y;
+        }
+      }
+    }
+    float mm = m;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) mm = fmaxf(mm, l2[k]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    const float old = ex2_approx(m - base);
+    m = mm;
+    l *= old;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) o[e] *= old;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const float w = ex2_approx(l2[k] - base);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = fmaf(w, v[k][e], o[e]);
+    }
+  }
+  if constexpr (kWarps > 1) {
+    __shared__ float sm[kWarps], sl[kWarps];
+    __shared__ float so[kWarps][32][kPer];
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) so[warp][lane][e] = o[e];
+    __syncthreads();
+    if (warp > 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      const float mm = fmaxf(m, sm[w]), base = mm == -INFINITY ? 0.f : mm;
+      const float f0 = ex2_approx(m - base), f1 = ex2_approx(sm[w] - base);
+      m = mm;
+      l = l * f0 + sl[w] * f1;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = o[e] * f0 + so[w][lane][e] * f1;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(sum.o[i] * inv, sum.o[i + 1] * inv);
-  if (lane == 0) a.lse[row] = sum.l == 0.f ? -INFINITY : (sum.m + log2f(sum.l)) * kLn2;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+  if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace cpattn

@@ -104,7 +104,7 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     if (g < s.groups) {
       shared_group(s, g, x.first, x.size);
       x.keys = shared_count(s, g);
-      x.units = shared_units(s, x.size) * s.hkv;
+      x.units = (x.size * s.G + kSharedRows - 1) / kSharedRows * s.hkv;
       x.tiles = x.units > 0 ? (x.keys + kTile - 1) / kTile : 0;
     }
     return x;
@@ -172,7 +172,7 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
       const auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, l); };
       const int first = get(x.first), size = get(x.size), tiles = get(x.tiles), gruns = get(runs);
       const int local = cta - get(from);
-      const int unit = local / gruns, run = local % gruns, row_units = shared_units(s, size);
+      const int unit = local / gruns, run = local % gruns, row_units = (size * s.G + kSharedRows - 1) / kSharedRows;
       r.first = first;
       r.keys = get(x.keys);
       r.kvh = unit / row_units;
