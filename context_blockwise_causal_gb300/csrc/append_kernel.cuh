@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) cpattn_append_kernel(const __gr
   const int64_t units = int64_t(a.qk.b) * a.qk.n * a.qk.split;
   const int64_t step = int64_t(gridDim.x) * (kQkThreads / 32);
   int64_t idx = int64_t(blockIdx.x) * (kQkThreads / 32) + (threadIdx.x >> 5);
+  chain_wait();  // up to here beside what runs before this call
   if (idx >= units) return;
   AppendUnit<D> U;
   U.set(a, idx);

@@ -188,8 +188,7 @@ int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaSt
   if (!encode_pools(&tk, &tv, p, a.hkv, D, pa.box, D / 64) ||
       !allow_smem(di->paged_attr[int(kKind) * 4 + (kT - 1) * 2 + (D == 128 ? 1 : 0)], kernel, C::kSmemBytes))
     return CPATTN_ERR_CUDA;
-  cudaError_t e = launch_runs(kernel, ctas, kPagedThreads, kParts ? 1 : a.nsplit, C::kSmemBytes,
-                              kKind == PagedKind::kOwn, st, tk, tv, pa);
+  cudaError_t e = launch_runs(kernel, ctas, kPagedThreads, kParts ? 1 : a.nsplit, C::kSmemBytes, true, st, tk, tv, pa);
   const int64_t out_rows = int64_t(a.b) * a.hq, join_ctas = (out_rows + 3) / 4;
   if (e == cudaSuccess && kParts)
     e = pa.join_warps == 1 ? launch_chained(cpattn_shared_join_kernel<D, 1>, join_ctas, 128, st, pa)
@@ -211,8 +210,8 @@ int launch_shared(bool few, int own_rows, PagedArgs& pa, const PrefixArgs& a, co
   if (!encode_pools(&tk, &tv, p, a.sh.hkv, D, a.box, a.box == kTile ? D / 64 : 1) ||
       !allow_smem(di->prefix_attr[D == 128 ? 1 : 0], cpattn_prefix_kernel<D>, PrefixCfg<D>::kSmemBytes))
     return CPATTN_ERR_CUDA;
-  cpattn_prefix_kernel<D><<<unsigned(a.sh.ctas), kFwdThreads, PrefixCfg<D>::kSmemBytes, st>>>(tk, tv, a);
-  const int rc = launched(cudaGetLastError());
+  const int rc = launched(
+      launch_runs(cpattn_prefix_kernel<D>, a.sh.ctas, kFwdThreads, 1, PrefixCfg<D>::kSmemBytes, true, st, tk, tv, a));
   return rc ? rc : launch_paged<D, PagedKind::kOwn>(own_rows, pa, p, di, st);
 }
 
@@ -229,8 +228,7 @@ int launch_append(AppendArgs& a, DeviceInfo* di, cudaStream_t st) {
   a.qk.heads_per = int((groups + split - 1) / split * kRows);
   a.qk.split = int((heads + a.qk.heads_per - 1) / a.qk.heads_per);
   const int64_t ctas = (tokens * a.qk.split + kWarps - 1) / kWarps, most = int64_t(di->num_sms) * 2;  // resident at once
-  cpattn_append_kernel<D, kInter><<<int(ctas < most ? ctas : most), kQkThreads, 0, st>>>(a);
-  return launched(cudaGetLastError());
+  return launched(launch_chained(cpattn_append_kernel<D, kInter>, ctas < most ? ctas : most, kQkThreads, st, a));
 }
 
 }  // namespace

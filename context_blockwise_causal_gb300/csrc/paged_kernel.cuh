@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
   constexpr bool kParts = kKind != PagedKind::kWhole;  // results go to the join kernel
   constexpr int kRows = 8 * kT;
   const DecodeArgs& a = pa.d;
-  if (kParts || a.nsplit > kDecMaxCluster) chain_next();
   using C = PagedCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -225,6 +224,10 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
   }
   __syncthreads();
   smem += C::kOffRing;
+  // Up to here beside what runs before this call; a kernel behind this one finds
+  // that finished. (The own keys' kernel is behind the prefix kernel, which has waited.)
+  if constexpr (kKind != PagedKind::kOwn) chain_wait();
+  if (kParts || a.nsplit > kDecMaxCluster) chain_next();
   // unit: (sequence or group, KV head, kRows of its rows), then the run of keys
   const bool common = kKind == PagedKind::kBoth && int(blockIdx.x) < pa.common_ctas;
   const int nsplit = common ? pa.sh.fixed_runs : a.nsplit, row_groups = common ? pa.sh.fixed_units : a.row_groups;

@@ -201,7 +201,6 @@ template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     cpattn_prefix_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                          const __grid_constant__ PrefixArgs a) {
-  chain_next();
   using C = PrefixCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -221,6 +220,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // Up to here, and the barriers, beside what runs before this call; the own
+  // keys' kernel finds that finished.
+  chain_wait();
+  chain_next();
   if (warp == 0) {
     const PrefixRun r = prefix_plan(a.sh, blockIdx.x, a.sms, kRowTileNs<D>);
     if (lane == 0) *run = r;
@@ -242,10 +249,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(&kv_empty[i], 1);
     }
     fence_mbar_init();
-  }
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
