@@ -114,8 +114,12 @@ int check_pointers(const void* q, const int* lengths, const void* o, const float
 }
 
 // Common keys by the prefix kernel, whose matrix tiles have 128 rows, or, for
-// groups of few rows, by the kernel that reads the own keys.
-constexpr int kFewRows = 32;
+// groups of few rows, by the kernel that reads the own keys, a unit of its
+// rows at a time: 16 rows behind 8192 keys of 8 heads (d 128, up to 256 own keys
+// each) take 15.8 us there and 19.1 by the prefix kernel, 8 groups of 16 behind 2048
+// 23.2 and 26.8. With 32 rows, two units that read the same keys, one group gains
+// (17.5 and 20.0 behind 8192 keys) and four lose (35 and 29 behind 4096).
+bool few_rows(int64_t rows, int groups) { return rows <= (groups == 1 ? 32 : 16); }
 
 // Runs of the common and of the own keys and where their results go.
 struct SharedShape {
@@ -130,7 +134,7 @@ struct SharedShape {
 bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
   const int64_t G = hq / hkv, rows = int64_t(max_group) * G;
   if (rows >= int64_t(1) << 30) return false;
-  s->few = rows <= kFewRows;
+  s->few = few_rows(rows, groups);
   s->own_rows = unit_rows(s->few ? rows : G);
   const int64_t own_units = int64_t(b) * hkv * ((G + s->own_rows - 1) / s->own_rows);
   // Own keys are mostly few, and how many is not known here: runs only where sequences are few.

@@ -80,11 +80,12 @@ struct PrefixRun {
 // by the other SMs (paged_kernel.cuh runs beside this kernel), so each of the
 // two gets the SMs that let both end together: with tp and to the times that
 // they would take by themselves on all SMs, and kOwnShare the part of the SMs
-// that reads at the chip's full bandwidth, tp / x = to kOwnShare / (1 - x).
-template <int D>
-constexpr float kRowTileNs = D == 128 ? 875.f : 600.f;  // of an SM for 128 rows and a key tile, as measured
-constexpr float kOwnBytesPerNs = 6700.f;                // measured copy bandwidth
-constexpr float kOwnShare = 0.5f;
+// that reads at the chip's full bandwidth, tp / x = to kOwnShare / (1 - x). (64
+// sequences behind 32768 tokens with up to 1024 of their own, h32/8 d128: 66 us
+// for 0.35 to 0.5, 71 for 0.1 and 0.9; the whole chip first, then the own keys, 72.)
+constexpr float kRowTileNs = 875.f;       // of an SM for 128 rows and a key tile, d 64 and 128, as measured
+constexpr float kOwnBytesPerNs = 6700.f;  // measured copy bandwidth
+constexpr float kOwnShare = 0.4f;
 __device__ __forceinline__ float prefix_share(float tile_ns, float own_bytes, int sms) {
   const float tp = tile_ns / sms, to = own_bytes / kOwnBytesPerNs;
   return tp / (tp + to * kOwnShare);
@@ -109,34 +110,35 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     }
     return x;
   };
-  const auto sum = [](float v) {
+  // (lengths first: their loads are on their way while the groups' are waited for)
+  float held[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = lane; i < s.b; i += 128)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-  };
+    for (int k = 0; k < 4; ++k)
+      if (i + 32 * k < s.b) held[k] += float(s.lengths[i + 32 * k]);
   const Group mine = of(lane);
-  // work of all groups, in tiles and in time; bytes of the own keys (as if every member shared)
-  float held = 0.f;
-  for (int i = lane; i < s.b; i += 32) held += float(s.lengths[i] < s.cap ? s.lengths[i] : s.cap);
-  float total = 0.f, rows = 0.f, common = 0.f;
+  // work of all groups, in tiles and in row tiles; own keys (as if every member shared)
+  float total = 0.f, rows = 0.f, own = (held[0] + held[1]) + (held[2] + held[3]);
+  unsigned units = 0;
   for (int g0 = 0; g0 < s.groups; g0 += 32) {
     const Group x = g0 == 0 ? mine : of(g0 + lane);
-    total += float(x.tiles) * float(x.units);
-    rows += float(x.tiles) * float((x.size * s.G + kTile - 1) / kTile) * float(s.hkv);
-    common += float(x.keys) * float(x.size);
+    const float tiles = float(x.tiles) * float(s.hkv);
+    total += tiles * float((x.size * s.G + kSharedRows - 1) / kSharedRows);
+    rows += tiles * float((x.size * s.G + kTile - 1) / kTile);
+    own -= float(x.keys) * float(x.size);
+    units += __reduce_add_sync(0xffffffffu, x.tiles > 0 ? unsigned(x.units) : 0u);
   }
-  total = sum(total);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    own += __shfl_xor_sync(0xffffffffu, own, o);
+  }
   int ctas = s.ctas;
   if (ctas == sms) {  // (units take at most half of them)
-    rows = sum(rows);
-    const float own = fmaxf(sum(held - common), 0.f) * float(s.hkv) * s.token_bytes;
-    int units = 0;
-    for (int g0 = 0; g0 < s.groups; g0 += 32) {
-      const Group x = g0 == 0 ? mine : of(g0 + lane);
-      units += int(__reduce_add_sync(0xffffffffu, unsigned(x.tiles > 0 ? x.units : 0)));
-    }
-    ctas = int(prefix_share(rows * row_tile_ns, own, sms) * float(sms));
-    ctas = ctas < units ? units : ctas;
+    const float own_bytes = fmaxf(own, 0.f) * float(s.hkv) * s.token_bytes;
+    ctas = int(prefix_share(rows * row_tile_ns, own_bytes, sms) * float(sms));
+    ctas = ctas < int(units) ? int(units) : ctas;
     ctas = ctas < s.ctas ? ctas : s.ctas;
   }
   int len = int(total / float(ctas));
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   chain_wait();
   chain_next();
   if (warp == 0) {
-    const PrefixRun r = prefix_plan(a.sh, blockIdx.x, a.sms, kRowTileNs<D>);
+    const PrefixRun r = prefix_plan(a.sh, blockIdx.x, a.sms, kRowTileNs);
     if (lane == 0) *run = r;
   }
   if (warp == 8 && lane == 0) {
