@@ -619,10 +619,13 @@ int cpattn_zigzag_index(int s, int cp, int64_t* global_of_local);
  * (0 = no kernel gave up waiting) and clears it. Synchronises `stream`.
  * Returns CPATTN_ERR_TIMEOUT when the word was non-zero, else 0 or a CUDA
  * error code. Bits: forward producer / MMA / softmax role gave up (0, 1, 2);
- * forward copies or MMAs still in flight at the end after the time limit (3);
- * the same for the backward kernels (8, 9, 10; 12); a backward kernel's
- * shared memory base not 1024-byte aligned (11); the timeout self-test (16);
- * a page table named a page outside of the pools (17); a bounds test of a checked build failed (20).
+ * forward copies or MMAs still in flight at the end after the time limit (3;
+ * these four also for the common keys of cpattn_decode_shared); copies of
+ * single-token attention over pages did not arrive (4); the roles of the
+ * backward kernels, and what they had in flight (8, 9, 10; 12); a backward
+ * kernel's shared memory base not 1024-byte aligned (11); the timeout self-test
+ * (16); a page table named a page outside of the pools (17); a bounds test of a
+ * checked build failed (20).
  * A role that gives up makes the others leave too, but every role first waits
  * for the copies and MMAs it already issued, so no kernel frees memory that
  * asynchronous work still writes.

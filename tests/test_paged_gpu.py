@@ -352,6 +352,8 @@ SHARED = [
     ([2], [30000], [10, 3], 512, 17, 1, 64, None, False),
     ([9] * 33, [(i * 37) % 300 for i in range(33)], [i % 3 for i in range(297)], 16, 4, 1, 64, None, False),
     ([8], [2000], [i * 90 for i in range(8)], 128, 4, 1, 128, None, False),      # exactly 32 rows
+    ([9] * 20, [(i * 97) % 500 for i in range(20)], [i % 5 for i in range(180)], 32, 16, 4, 64, None, False),  # more units than half of the SMs
+    ([120], [600], [i % 70 for i in range(120)], 64, 16, 2, 128, None, False),   # 960 rows: three units and three quarters
 ]
 
 
