@@ -15,6 +15,16 @@
 // The first and last keys of what is visible are masked inside their blocks:
 // scores by the mask, and values, whose product with a weight of zero would
 // still be NaN if they are not finite, by zeros written over them.
+//
+// P is rounded to bf16 for its product, as everywhere in the package (2.0e-3 to
+// 2.3e-3 relative L2 of O with its own rounding, which alone is 1.7e-3); sums,
+// maxima and joins are fp32.
+//
+// HBM-bound where there are sequences enough: 16 of 32K to 64K keys, h64/8 d128,
+// 456 us (reads at 1.06 of the measured copy bandwidth, which counts writes
+// too), 64 with a window of 4096, h32/8, pages of 16, 157 us (1.03). A few short ones are bound by
+// what waits for one another: length, table, first copy, some rounds of 0.5 us, the join (one sequence of 8192
+// keys 11 us, 37 of up to 2928, 2 KV heads of 64, 11.8).
 #pragma once
 #include <cuda_bf16.h>
 

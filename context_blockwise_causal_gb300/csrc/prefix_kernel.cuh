@@ -28,6 +28,13 @@
 // every CTA adds up the tiles of all groups and takes the shortest length for
 // which all runs fit into the CTAs that were launched, so groups of different
 // lengths fill the chip evenly. CTA 0 leaves each group's place for the join.
+//
+// Measured, d128: 1.75 us for two row tiles and a key tile in the steady state
+// (1460 TFLOP/s over the chip, as the forward), 3 us to the plan, 3 to 6 more to
+// the first scores (queries and first keys of all CTAs come at once), 2 us to
+// store. 64 sequences behind 32768 tokens with up to 1024 of their own, h32/8: 66
+// us with the own keys and the join (45 us of bytes); 256 behind 16384 with up to
+// 2048, h64/8: 252 us (212).
 #pragma once
 #include <cuda_bf16.h>
 
