@@ -117,13 +117,18 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     }
     return x;
   };
-  // (lengths first: their loads are on their way while the groups' are waited for)
-  float held[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = lane; i < s.b; i += 128)
+  // (the first lengths are on their way while the groups' loads are waited for)
+  int head[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) head[k] = lane + 32 * k < s.b ? s.lengths[lane + 32 * k] : 0;
+  const Group mine = of(lane);
+  float held[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) held[k] = float(head[k]);
+  for (int i = lane + 128; i < s.b; i += 128)
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (i + 32 * k < s.b) held[k] += float(s.lengths[i + 32 * k]);
-  const Group mine = of(lane);
   // work of all groups, in tiles and in row tiles; own keys (as if every member shared)
   float total = 0.f, rows = 0.f, own = (held[0] + held[1]) + (held[2] + held[3]);
   unsigned units = 0;
@@ -149,6 +154,10 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     ctas = ctas < s.ctas ? ctas : s.ctas;
   }
   int len = int(total / float(ctas));
+  if (s.groups == 1 && units > 0) {  // the shortest that fits
+    const unsigned runs = unsigned(ctas) / units, tiles = unsigned(__shfl_sync(0xffffffffu, mine.tiles, 0));
+    len = int((tiles + runs - 1) / runs);
+  }
   if (len < kPrefixMinTiles) len = kPrefixMinTiles;
   // there are as many CTAs as units, so this ends: at the latest when no unit is cut
   while (true) {
