@@ -74,13 +74,15 @@ int check_decode(const cpattn_pages* p, int b, int hq, int hkv, int d, int windo
 // Rows of a unit: 8 where they suffice (half of the work), or 16.
 int unit_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-// Runs over pages: the same rule, with twice the places at d = 64, and 16 runs
-// rather than a cluster's 8 from 8192 keys on, where the second kernel that
-// joins them costs less than it saves (one sequence of 8192 keys, 2 KV heads, d
-// 64: 11.4 us in 8 runs, 9.3 in 16; 8 KV heads of 128: 14.4 and 13.9; at 4096 keys 10.5 and 10.7).
+// Runs over pages: the same rule, with twice the places at d = 64, and more runs
+// than a cluster's 8 already from 2048 keys on, of 256 keys or 16 of them: the
+// kernel that joins them has four warps to a row and costs less than it saves.
+// One sequence, d 128, us in 8 / 16 / 32 / 64 runs: 4096 keys, 8 KV heads 9.5 / 8.1 / 8.5
+// / 12.1; 8192 keys 13.7 / 11.2 / 11.4 / 16.1, 1 KV head 11.9 / 8.2 / 6.6 / 6.8; 32768
+// keys 36.6 / 26.1 / 25.6 / 29.7, 1 KV head 34.4 / 20.5 / 13.3 / 10.7.
 int paged_split(int num_sms, int d, int64_t units, int64_t keys) {
   const int64_t places = int64_t(d == 128 ? PagedCfg<128>::kPerSm : PagedCfg<64>::kPerSm) * num_sms;
-  return choose_split(places, units, keys, keys < 8192 ? 0 : std::max<int64_t>(16, keys / 2048));
+  return choose_split(places, units, keys, keys < 2048 ? 0 : std::max<int64_t>(16, keys / 256));
 }
 
 // What the calls' arguments have in common; o and lse as cpattn_decode.
@@ -195,12 +197,10 @@ int launch_paged_as(PagedArgs& pa, const cpattn_pages* p, DeviceInfo* di, cudaSt
       !allow_smem(di->paged_attr[int(kKind) * 4 + (kT - 1) * 2 + (D == 128 ? 1 : 0)], kernel, C::kSmemBytes))
     return CPATTN_ERR_CUDA;
   cudaError_t e = launch_runs(kernel, ctas, kPagedThreads, kParts ? 1 : a.nsplit, C::kSmemBytes, true, st, tk, tv, pa);
-  const int64_t out_rows = int64_t(a.b) * a.hq, join_ctas = (out_rows + 3) / 4;
-  if (e == cudaSuccess && kParts)
-    e = pa.join_warps == 1 ? launch_chained(cpattn_shared_join_kernel<D, 1>, join_ctas, 128, st, pa)
+  const int64_t out_rows = int64_t(a.b) * a.hq;
+  if (e == cudaSuccess && (kParts || a.nsplit > kDecMaxCluster))
+    e = pa.join_warps == 1 ? launch_chained(cpattn_shared_join_kernel<D, 1>, (out_rows + 3) / 4, 128, st, pa)
                            : launch_chained(cpattn_shared_join_kernel<D, 4>, out_rows, 128, st, pa);
-  if (e == cudaSuccess && !kParts && a.nsplit > kDecMaxCluster)
-    e = launch_chained(cpattn_decode_join_kernel<D>, join_ctas, 128, st, a);
   return launched(e);
 }
 template <int D, PagedKind kKind>
@@ -314,6 +314,7 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
   a.nsplit = paged_split(di->num_sms, d, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
+  pa.join_warps = 4;
   const size_t need = workspace_for(b, hq, d, a.nsplit);
   if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
   if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
   if (kKind == PagedKind::kOwn && blockIdx.x == gridDim.x - 1) chain_wait();
 }
 
-// Joins the results of a row's own keys and of its group's, kWarps warps to a row
+// Joins the results of a row's own keys (or of all its keys) and of its group's, kWarps warps to a row
 // (sequence, query head). Results are numbered, own ones first; warp w takes w, w + kWarps
 // and so on, a batch at a time, whose values are on their way before their
 // weights are formed. With up to 8 results a warp does by itself; more of them
@@ -478,9 +478,12 @@ __global__ void __launch_bounds__(128) cpattn_shared_join_kernel(const __grid_co
   if (kWarps == 1 && !live) return;
   const int bi = live ? int(row / a.hq) : 0, h = live ? int(row - int64_t(bi) * a.hq) : 0;
   const int kvh = h / a.G;
-  int n = a.lengths[bi];
-  n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
-  SharedSeq mate = shared_seq(pa.sh, bi, n);
+  SharedSeq mate = {};
+  if (pa.sh.groups > 0) {  // (0: whole sequences)
+    int n = a.lengths[bi];
+    n = n < 0 ? 0 : (n > a.cap ? a.cap : n);
+    mate = shared_seq(pa.sh, bi, n);
+  }
   chain_wait();
   int64_t at = 0;
   if (mate.keys > 0) {
