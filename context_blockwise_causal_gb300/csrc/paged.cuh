@@ -35,6 +35,7 @@ __device__ __forceinline__ bool page_ok(int page, const PagedPlace& pg, unsigned
 // its members' query heads, G of each; unit_rows of them are a unit, whose
 // common keys are cut into runs, one CTA each.
 constexpr int kSharedRows = 256;  // the prefix kernel's units
+constexpr int kSharedMaxCtas = 1 << 26;
 
 // Of a group: the first of its runs' CTAs, and the runs of each of its units.
 struct GroupRuns {

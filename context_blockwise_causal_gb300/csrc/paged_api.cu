@@ -80,8 +80,8 @@ int unit_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 // One sequence, d 128, us in 8 / 16 / 32 / 64 runs: 4096 keys, 8 KV heads 9.5 / 8.1 / 8.5
 // / 12.1; 8192 keys 13.7 / 11.2 / 11.4 / 16.1, 1 KV head 11.9 / 8.2 / 6.6 / 6.8; 32768
 // keys 36.6 / 26.1 / 25.6 / 29.7, 1 KV head 34.4 / 20.5 / 13.3 / 10.7.
-int paged_split(int num_sms, int d, int64_t units, int64_t keys) {
-  const int64_t places = int64_t(d == 128 ? PagedCfg<128>::kPerSm : PagedCfg<64>::kPerSm) * num_sms;
+int paged_split(int num_sms, int d, int G, int64_t units, int64_t keys) {
+  const int64_t places = int64_t(d == 128 ? 2 : unit_rows(G) == 8 ? 4 : 3) * num_sms;
   return choose_split(places, units, keys, keys < 2048 ? 0 : std::max<int64_t>(16, keys / 256));
 }
 
@@ -163,7 +163,7 @@ bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, in
     s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
     s->join_warps = s->ctas / units + s->own_runs > kJoinBatch ? 4 : 1;
   }
-  if (s->ctas + own_units * s->own_runs >= int64_t(1) << 31) return false;
+  if (s->ctas >= kSharedMaxCtas || s->ctas + own_units * s->own_runs >= int64_t(1) << 31) return false;
   s->part_rows = int(std::min<int64_t>(s->unit_rows, (rows + 15) / 16 * 16));
   const size_t parts = size_t(s->ctas) * s->part_rows, own_parts = size_t(b) * hq * s->own_runs;
   s->runs_bytes = align256(size_t(groups) * sizeof(GroupRuns));
@@ -296,7 +296,7 @@ extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, in
   if (device_info(&di)) return 0;
   const int G = hq / hkv;
   const int64_t units = int64_t(b) * hkv * ((G + unit_rows(G) - 1) / unit_rows(G));
-  return workspace_for(b, hq, d, paged_split(di->num_sms, d, units, max_keys(cap, window, sinks)));
+  return workspace_for(b, hq, d, paged_split(di->num_sms, d, G, units, max_keys(cap, window, sinks)));
 }
 
 extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse,
@@ -313,7 +313,7 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
   DecodeArgs& a = pa.d;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
-  a.nsplit = paged_split(di->num_sms, d, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
+  a.nsplit = paged_split(di->num_sms, d, a.G, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
   pa.join_warps = 4;
   const size_t need = workspace_for(b, hq, d, a.nsplit);
   if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;

@@ -22,9 +22,10 @@
 //
 // HBM-bound where there are sequences enough: 16 of 32K to 64K keys, h64/8 d128,
 // 456 us (reads at 1.06 of the measured copy bandwidth, which counts writes
-// too), 64 with a window of 4096, h32/8, pages of 16, 157 us (1.03). A few short ones are bound by
-// what waits for one another: length, table, first copy, some rounds of 0.5 us, the join (one sequence of 8192
-// keys 11 us, 37 of up to 2928, 2 KV heads of 64, 11.8).
+// too), 64 with a window of 4096, h32/8, pages of 16, 157 us (1.03). A few short
+// ones are bound by what waits for one another: length, table, first copy, some
+// rounds of 0.5 us, the joins (one sequence of 8192 keys 9 us, 37 of up to 2928, 2
+// KV heads of 64, 11.9).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -44,7 +45,7 @@ struct PagedArgs {
   PagedPlace pg;
   SharedPlan sh;    // kOwn, kBoth
   int common_ctas;  // kBoth
-  int join_warps;   // kOwn, kBoth
+  int join_warps;   // of the join kernel, to a row
   int box;          // tokens of a copy: gcd(page_size, 32)
 };
 
@@ -55,7 +56,7 @@ struct PagedCfg {
   static constexpr int kTileBytes = kPagedRound * D * 2;  // keys or values of a round
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = 3;
-  // CTAs that fit an SM with 8 heads to a unit. (d = 64 with six stages and two of
+  // CTAs that fit an SM with 8 heads to a unit (16 heads of 64: three). (d = 64 with six stages and two of
   // them: 37 sequences of up to 2928 keys, 2 KV heads, 12.4 us instead of 10.7; 64 of
   // 8192, 8 KV heads, 135 instead of 120.)
   static constexpr int kPerSm = D == 128 ? 2 : 4;
@@ -334,11 +335,10 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
         ++turn;
       }
     }
-    if (!ok) {  // gave up: what was asked for arrives before the shared memory is used otherwise
-      if (lane == 0) atomicOr(a.status, kStatusCopies);
-      for (int u = t > C::kStages ? t - C::kStages : 0; u < t; ++u)
-        mbar_wait_drain_warp(&full[u % C::kStages], (u / C::kStages) & 1, kWaitLimitNs);
-    }
+    // what was asked for arrives before the shared memory is used otherwise, whoever gave up
+    for (int u = t > C::kStages ? t - C::kStages : 0; u < t; ++u)
+      ok &= mbar_wait_drain_warp(&full[u % C::kStages], (u / C::kStages) & 1, kWaitLimitNs);
+    if (!ok && lane == 0) atomicOr(a.status, kStatusCopies);
   } else {
     // ------------------------------------------------------------ products
     part.load([&](int r) -> const __nv_bfloat16* {

@@ -34,7 +34,7 @@
 // the first scores (queries and first keys of all CTAs come at once), 2 us to
 // store. 64 sequences behind 32768 tokens with up to 1024 of their own, h32/8: 66
 // us with the own keys and the join (45 us of bytes); 256 behind 16384 with up to
-// 2048, h64/8: 252 us (212).
+// 2048, h64/8: 250 us (212).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -165,7 +165,7 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     for (int g0 = 0; g0 < s.groups; g0 += 32) {
       const Group x = g0 == 0 ? mine : of(g0 + lane);
       const unsigned long long v = (unsigned long long)(unsigned(x.tiles + len - 1) / unsigned(len)) * unsigned(x.units);
-      const unsigned most = 1u << 26;  // over any number of CTAs that the host admits; 32 of them fit a word
+      const unsigned most = kSharedMaxCtas;  // more than there are CTAs; 32 of them fit a word
       const unsigned add = __reduce_add_sync(0xffffffffu, v < most ? unsigned(v) : most);
       runs = runs + add < (1u << 31) ? runs + add : (1u << 31);
     }

@@ -115,6 +115,11 @@ def test_decode_shared_arguments(lib):  # noqa: F811
     for bad in ({"b": 0}, {"hq": 3}, {"d": 80}, {"groups": 0}, {"groups": 4}, {"most": 0}, {"most": 4}, {"off": None},
                 {"scale": -2.0}, {"q_batch": 4}):
         assert f(**bad) == ARG, bad
+    # more units than results are numbered for: every sequence a group of all of them
+    many = 1 << 15
+    if torch.cuda.is_available():
+        assert f(b=many, hq=64, hkv=64, groups=many, most=many, pg=pages(hkv=64), q_batch=4096) == ARG
+    assert lib.cpattn_decode_shared_workspace_bytes(many, 64, 64, 64, many, many) == 0
     for bad in ((3, 4, 2, 64, 0, 2), (3, 4, 2, 64, 4, 2), (3, 4, 2, 64, 2, 0), (3, 4, 2, 64, 2, 4), (3, 4, 3, 64, 2, 2),
                 (0, 4, 2, 64, 1, 1), (3, 4, 2, 96, 2, 2)):
         assert lib.cpattn_decode_shared_workspace_bytes(*bad) == 0
