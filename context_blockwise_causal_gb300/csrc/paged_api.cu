@@ -118,14 +118,20 @@ int check_pointers(const void* q, const int* lengths, const void* o, const float
 // Common keys by the prefix kernel, whose matrix tiles have 128 rows, or, for
 // groups of few rows, by the kernel that reads the own keys, a unit of its
 // rows at a time: 16 rows behind 8192 keys of 8 heads (d 128, up to 256 own keys
-// each) take 15.8 us there and 19.1 by the prefix kernel, 8 groups of 16 behind 2048
-// 23.2 and 26.8. With 32 rows, two units that read the same keys, one group gains
-// (17.5 and 20.0 behind 8192 keys) and four lose (35 and 29 behind 4096).
-bool few_rows(int64_t rows, int groups) { return rows <= (groups == 1 ? 32 : 16); }
+// each) take 13.2 us there and 19.1 by the prefix kernel, 8 groups of 16 behind
+// 2048 23.2 and 26.8. More rows are more units that read the same keys, which pays
+// where there are few of those: 32 rows behind 8192 keys 17.3 and 19.4, behind 32768
+// 45 and 36; 64 rows behind 1024 keys 9.8 and 13.3, behind 20000 of one head 12.8
+// and 15.0, behind 8192 of 8 heads 36 and 20. How many keys there are is
+// known here only as the tables' room for them.
+constexpr int kFewRows = 64, kFewMembers = 32;
+bool may_be_few(int64_t rows, int max_group) { return rows <= kFewRows && max_group <= kFewMembers; }
+bool is_few(int64_t rows, int hkv, int groups, int max_group, int64_t cap) {
+  return may_be_few(rows, max_group) && (rows <= 16 || (rows + 7) / 8 * hkv * groups * cap <= 300000);
+}
 
 // Runs of the common and of the own keys and where their results go.
 struct SharedShape {
-  bool few;
   int unit_rows, part_rows, fixed_runs, fixed_units, own_rows, own_runs, join_warps;
   int64_t ctas;  // of the common keys
   size_t runs_bytes, lse_bytes, o_bytes, own_lse_bytes, own_o_bytes;
@@ -133,23 +139,26 @@ struct SharedShape {
   size_t bytes() const { return 256 + runs_bytes + lse_bytes + o_bytes + own_lse_bytes + own_o_bytes; }
 };
 
-bool shared_shape(SharedShape* s, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
+bool shared_shape(SharedShape* s, bool few, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
   const int64_t G = hq / hkv, rows = int64_t(max_group) * G;
   if (rows >= int64_t(1) << 30) return false;
-  s->few = few_rows(rows, groups);
-  s->own_rows = unit_rows(s->few ? rows : G);
+  // Few rows of one group: units of 8 though they read the common keys twice, since
+  // theirs are the shorter rounds and the own keys need no more (16 rows behind 8192
+  // keys: 13.2 us, in one unit 16.0). Of several groups: units of 16, which leave more runs to each
+  // (8 groups of 16 rows behind 2048 keys: 23.2 us, with 8 rows 25.3).
+  s->own_rows = unit_rows(few && groups > 1 ? rows : G);
   const int64_t own_units = int64_t(b) * hkv * ((G + s->own_rows - 1) / s->own_rows);
   // Own keys are mostly few, and how many is not known here: runs only where
   // sequences are few (64 sequences behind 32768 tokens, up to 1024 of their own: 66
   // us in one run each, 71 in two; 256 behind 16384, up to 2048: 241 and 254).
   s->own_runs = 1;
   while (s->own_runs < kDecMaxCluster && 2 * s->own_runs * own_units <= 64) s->own_runs *= 2;
-  s->unit_rows = s->few ? s->own_rows : kSharedRows;
+  s->unit_rows = few ? s->own_rows : kSharedRows;
   const int64_t row_units = (rows + s->unit_rows - 1) / s->unit_rows, units = row_units * hkv * groups;
   if (units >= int64_t(1) << 30) return false;
   s->fixed_units = int(row_units);
   s->fixed_runs = 0;
-  if (s->few) {
+  if (few) {
     // as many runs as fill the places that the own keys' CTAs leave
     const int64_t places = int64_t(s->own_rows == 8 && d == 64 ? 4 : 2) * num_sms, own = own_units * s->own_runs;
     const int64_t runs = (places - std::min(own, places / 2)) / units;
@@ -330,8 +339,12 @@ extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, i
   if (check_decode(nullptr, b, hq, hkv, d, 0, 0) || check_groups(b, groups, max_group)) return 0;
   DeviceInfo* di = nullptr;
   SharedShape s;
-  if (device_info(&di) || !shared_shape(&s, di->num_sms, b, hq, hkv, d, groups, max_group)) return 0;
-  return s.bytes();
+  if (device_info(&di) || !shared_shape(&s, false, di->num_sms, b, hq, hkv, d, groups, max_group)) return 0;
+  size_t bytes = s.bytes();  // whichever kernel the call takes
+  if (may_be_few(int64_t(max_group) * (hq / hkv), max_group) &&
+      shared_shape(&s, true, di->num_sms, b, hq, hkv, d, groups, max_group))
+    bytes = std::max(bytes, s.bytes());
+  return bytes;
 }
 
 extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
@@ -347,15 +360,17 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
   SharedShape shape;
-  if (!shared_shape(&shape, di->num_sms, b, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < shape.bytes()) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  const bool few = is_few(int64_t(max_group) * (hq / hkv), hkv, groups, max_group, capacity(pages));
+  if (!shared_shape(&shape, few, di->num_sms, b, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < cpattn_decode_shared_workspace_bytes(b, hq, hkv, d, groups, max_group))
+    return CPATTN_ERR_WORKSPACE_TOO_SMALL;
   PagedArgs pa;
   fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
   DecodeArgs& a = pa.d;
   a.nsplit = shape.own_runs;
   a.row_groups = (a.G + shape.own_rows - 1) / shape.own_rows;
   pa.join_warps = shape.join_warps;
-  pa.common_ctas = shape.few ? int(shape.ctas) : 0;
+  pa.common_ctas = few ? int(shape.ctas) : 0;
   uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
   const auto take = [&ws](size_t bytes) {
     uint8_t* at = ws;
@@ -394,6 +409,6 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   p.scale_log2 = a.scale_log2;
   p.status = di->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_shared<128>(shape.few, shape.own_rows, pa, p, pages, di, st)
-                  : launch_shared<64>(shape.few, shape.own_rows, pa, p, pages, di, st);
+  return d == 128 ? launch_shared<128>(few, shape.own_rows, pa, p, pages, di, st)
+                  : launch_shared<64>(few, shape.own_rows, pa, p, pages, di, st);
 }

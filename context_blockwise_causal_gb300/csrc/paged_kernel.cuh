@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
     shared_group(pa.sh, bi, first, size);
     n = shared_count(pa.sh, bi);
     rows = size * a.G - row0;
-    // the first member that holds all of the common tokens (no more than 32 rows, so members)
+    // the first member that holds all of the common tokens (there are no more than 32)
     const unsigned full_members = __ballot_sync(0xffffffffu, lane < size && a.lengths[first + lane] >= n);
     if (!full_members || rows <= 0) rows = n = 0;
     named = first + (full_members ? __ffs(full_members) - 1 : 0);

@@ -354,6 +354,14 @@ SHARED = [
     ([8], [2000], [i * 90 for i in range(8)], 128, 4, 1, 128, None, False),      # exactly 32 rows
     ([9] * 20, [(i * 97) % 500 for i in range(20)], [i % 5 for i in range(180)], 32, 16, 4, 64, None, False),  # more units than half of the SMs
     ([120], [600], [i % 70 for i in range(120)], 64, 16, 2, 128, None, False),   # 960 rows: three units and three quarters
+    # and with more than 64
+    ([9], [129], [0, 1, 15, 16, 17, 2, 3, 4, 5], 48, 32, 2, 128, 0.2, False),
+    ([40, 1, 0, 33], [400, 0, 50, 77], [i % 33 for i in range(74)], 32, 6, 2, 64, None, False),
+    ([2], [30000], [10, 3], 512, 33, 1, 64, None, False),
+    ([9] * 33, [(i * 37) % 300 for i in range(33)], [i % 3 for i in range(297)], 16, 8, 1, 64, None, False),
+    ([9] * 20, [(i * 97) % 500 for i in range(20)], [i % 5 for i in range(180)], 32, 32, 4, 64, None, False),
+    ([13], [9000], [i * 7 for i in range(13)], 64, 40, 8, 128, None, False),     # 65 rows
+    ([16], [9000], [i * 7 for i in range(16)], 64, 32, 8, 128, None, True),      # 64 rows, many keys
 ]
 
 
@@ -381,7 +389,7 @@ def test_shared_all_elements_and_what_is_not_seen(groups, prefix, own, size, hq,
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
-@pytest.mark.parametrize("hq,hkv", [(4, 2), (20, 2)])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (20, 2), (40, 2)])
 def test_shared_members_that_do_not_share(hq, hkv):
     """Finished sequences (length 0, a cleared table), sequences with fewer tokens
     than the group, behind max_group others, outside of every group."""
@@ -410,7 +418,7 @@ def test_shared_members_that_do_not_share(hq, hkv):
     assert o.isfinite().all()
 
 
-@pytest.mark.parametrize("hq", [4, 24])
+@pytest.mark.parametrize("hq", [4, 24, 60])
 def test_shared_bad_pages_count_as_zeros(hq):
     k, v, tables, lengths, _ = _group_state([3], [200], [5, 6, 7], 32, hq, 2, 64, False, 81)
     tables[:, 2] = 1 << 30
@@ -502,7 +510,7 @@ def test_a_server_appends_and_decodes():
         _rotated(oracle.held_tokens(kh, tables[i], n), ref, src[:, hq:hq + hkv], d, "half", 1.0)
 
 
-@pytest.mark.parametrize("hq", [8, 24])
+@pytest.mark.parametrize("hq", [8, 24, 48])
 def test_given_streams_and_calls_at_once(hq):
     k, v, tables, lengths, off = _group_state([3, 4], [900, 1300], [5, 50, 500, 1, 2, 3, 4], 32, hq, 2, 64, False, 111)
     q, kd, vd, td, ln = _randn(7, hq, 64, seed=114).cuda(), k.cuda(), v.cuda(), tables.cuda(), _i32(lengths).cuda()
@@ -575,9 +583,9 @@ def test_pool_offsets_beyond_32_bits():
         _check(q1, pk, pv, flat, n, 0, 0, None, o, lse)
 
 
-@pytest.mark.parametrize("hq", [2, 6])
+@pytest.mark.parametrize("hq", [2, 6, 8])
 def test_checked_build_is_silent_and_identical(hq):
-    """hq 2: groups of few rows; hq 6: up to 60."""
+    """Groups of up to 20, 60 and 80 rows."""
     lib = pkg.checked_library()
 
     def status():
