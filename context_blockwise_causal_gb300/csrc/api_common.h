@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "../../include/cpattn.h"
+#include "align.h"
 
 namespace cpattn {
 
@@ -67,6 +68,5 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool valid_scale(float scale) { return scale > 0.f && scale <= 3.0e38f; }
 inline double default_scale(int d) { return 1.0 / std::sqrt(double(d)); }
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace cpattn

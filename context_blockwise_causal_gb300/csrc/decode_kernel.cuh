@@ -35,6 +35,7 @@
 
 #include <cstdint>
 
+#include "decode_split.h"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -42,8 +43,6 @@ namespace cpattn {
 constexpr int kDecWarps = 4;
 constexpr int kDecStages = 3;
 constexpr int kDecBlock = 16;  // keys per block
-constexpr int kDecMaxCluster = 8;  // the portable cluster size
-constexpr int kDecMaxSplit = 64;
 
 struct DecodeArgs {
   const __nv_bfloat16* q;  // [b, hq, D], batch stride q_batch

@@ -9,6 +9,7 @@
 #pragma once
 #include <cstdint>
 
+#include "paged_shape.h"
 #include "ptx.cuh"
 
 namespace cpattn {
@@ -34,14 +35,6 @@ __device__ __forceinline__ bool page_ok(int page, const PagedPlace& pg, unsigned
 // max_group others, shares nothing. The rows of a group for one KV head are
 // its members' query heads, G of each; unit_rows of them are a unit, whose
 // common keys are cut into runs, one CTA each.
-constexpr int kSharedRows = 256;  // the prefix kernel's units
-constexpr int kSharedMaxCtas = 1 << 26;
-
-// Of a group: the first of its runs' CTAs, and the runs of each of its units.
-struct GroupRuns {
-  int first, runs;
-};
-
 struct SharedPlan {
   const int* lengths;
   const int* shared;

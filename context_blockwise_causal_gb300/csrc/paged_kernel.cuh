@@ -467,7 +467,6 @@ __global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm :
 // weights are formed. With up to 8 results a warp does by itself; more of them
 // for four warps (30 results of 128 rows: 6 us by one warp, whose loads wait for
 // one another, 2.5 by four).
-constexpr int kJoinBatch = 8;
 template <int D, int kWarps>
 __global__ void __launch_bounds__(128) cpattn_shared_join_kernel(const __grid_constant__ PagedArgs pa) {
   const DecodeArgs& a = pa.d;

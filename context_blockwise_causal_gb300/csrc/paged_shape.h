@@ -1,0 +1,103 @@
+// Into how many runs the calls over a cache in pages cut their keys, which
+// kernel takes the common ones of groups, and the workspace that this takes. No
+// CUDA: host tests compile it by itself.
+#pragma once
+#include <algorithm>
+#include <cstdint>
+
+#include "decode_split.h"
+
+namespace cpattn {
+
+constexpr int kSharedRows = 256;  // the prefix kernel's units
+constexpr int kSharedMaxCtas = 1 << 26;
+constexpr int kJoinBatch = 8;  // results that a warp of the join kernel has on their way at once
+
+// Of a group: the first of its runs' CTAs, and the runs of each of its units.
+struct GroupRuns {
+  int first, runs;
+};
+
+// Rows of a unit: 8 where they suffice (half of the work), or 16.
+inline int unit_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+// Runs over pages: the same rule, with twice the places at d = 64, and more runs
+// than a cluster's 8 already from 2048 keys on, of 256 keys or 16 of them: the
+// kernel that joins them has four warps to a row and costs less than it saves.
+// One sequence, d 128, us in 8 / 16 / 32 / 64 runs: 4096 keys, 8 KV heads 9.5 / 8.1 / 8.5
+// / 12.1; 8192 keys 13.7 / 11.2 / 11.4 / 16.1, 1 KV head 11.9 / 8.2 / 6.6 / 6.8; 32768
+// keys 36.6 / 26.1 / 25.6 / 29.7, 1 KV head 34.4 / 20.5 / 13.3 / 10.7.
+inline int paged_split(int num_sms, int d, int G, int64_t units, int64_t keys) {
+  const int64_t places = int64_t(d == 128 ? 2 : unit_rows(G) == 8 ? 4 : 3) * num_sms;
+  return choose_split(places, units, keys, keys < 2048 ? 0 : std::max<int64_t>(16, keys / 256));
+}
+
+// Common keys by the prefix kernel, whose matrix tiles have 128 rows, or, for
+// groups of few rows, by the kernel that reads the own keys, a unit of its
+// rows at a time: 16 rows behind 8192 keys of 8 heads (d 128, up to 256 own keys
+// each) take 13.2 us there and 19.1 by the prefix kernel, 8 groups of 16 behind
+// 2048 23.2 and 26.8. More rows are more units that read the same keys, which pays
+// where there are few of those: 32 rows behind 8192 keys 17.3 and 19.4, behind 32768
+// 45 and 36; 64 rows behind 1024 keys 9.8 and 13.3, behind 20000 of one head 12.8
+// and 15.0, behind 8192 of 8 heads 36 and 20. How many keys there are is
+// known here only as the tables' room for them.
+constexpr int kFewRows = 64, kFewMembers = 32;
+inline bool may_be_few(int64_t rows, int max_group) { return rows <= kFewRows && max_group <= kFewMembers; }
+inline bool is_few(int64_t rows, int hkv, int groups, int max_group, int64_t cap) {
+  return may_be_few(rows, max_group) && (rows <= 16 || (rows + 7) / 8 * hkv * groups * cap <= 300000);
+}
+
+// Runs of the common and of the own keys and where their results go.
+struct SharedShape {
+  int unit_rows, part_rows, fixed_runs, fixed_units, own_rows, own_runs, join_warps;
+  int64_t ctas;  // of the common keys
+  size_t runs_bytes, lse_bytes, o_bytes, own_lse_bytes, own_o_bytes;
+  // (results are stored in whole sectors, so the parts begin at the first multiple of 256)
+  size_t bytes() const { return 256 + runs_bytes + lse_bytes + o_bytes + own_lse_bytes + own_o_bytes; }
+};
+
+inline bool shared_shape(SharedShape* s, bool few, int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
+  const int64_t G = hq / hkv, rows = int64_t(max_group) * G;
+  if (rows >= int64_t(1) << 30) return false;
+  // Few rows of one group: units of 8 though they read the common keys twice, since
+  // theirs are the shorter rounds and the own keys need no more (16 rows behind 8192
+  // keys: 13.2 us, in one unit 16.0). Of several groups: units of 16, which leave more runs to each
+  // (8 groups of 16 rows behind 2048 keys: 23.2 us, with 8 rows 25.3).
+  s->own_rows = unit_rows(few && groups > 1 ? rows : G);
+  const int64_t own_units = int64_t(b) * hkv * ((G + s->own_rows - 1) / s->own_rows);
+  // Own keys are mostly few, and how many is not known here: runs only where
+  // sequences are few (64 sequences behind 32768 tokens, up to 1024 of their own: 66
+  // us in one run each, 71 in two; 256 behind 16384, up to 2048: 241 and 254).
+  s->own_runs = 1;
+  while (s->own_runs < kDecMaxCluster && 2 * s->own_runs * own_units <= 64) s->own_runs *= 2;
+  s->unit_rows = few ? s->own_rows : kSharedRows;
+  const int64_t row_units = (rows + s->unit_rows - 1) / s->unit_rows, units = row_units * hkv * groups;
+  if (units >= int64_t(1) << 30) return false;
+  s->fixed_units = int(row_units);
+  s->fixed_runs = 0;
+  if (few) {
+    // as many runs as fill the places that the own keys' CTAs leave
+    const int64_t places = int64_t(s->own_rows == 8 && d == 64 ? 4 : 2) * num_sms, own = own_units * s->own_runs;
+    const int64_t runs = (places - std::min(own, places / 2)) / units;
+    s->fixed_runs = int(runs < 1 ? 1 : runs > kDecMaxSplit ? kDecMaxSplit : runs);
+    s->ctas = units * s->fixed_runs;
+    s->join_warps = s->fixed_runs + s->own_runs > kJoinBatch ? 4 : 1;
+  } else {
+    // One run per SM, or as many as it takes for the units to be at most half of
+    // them (so that runs of about the same length exist, whatever the groups'
+    // lengths turn out to be).
+    s->ctas = num_sms * ((2 * units + num_sms - 1) / num_sms);
+    s->join_warps = s->ctas / units + s->own_runs > kJoinBatch ? 4 : 1;
+  }
+  if (s->ctas >= kSharedMaxCtas || s->ctas + own_units * s->own_runs >= int64_t(1) << 31) return false;
+  s->part_rows = int(std::min<int64_t>(s->unit_rows, (rows + 15) / 16 * 16));
+  const size_t parts = size_t(s->ctas) * s->part_rows, own_parts = size_t(b) * hq * s->own_runs;
+  s->runs_bytes = align256(size_t(groups) * sizeof(GroupRuns));
+  s->lse_bytes = align256(parts * 4);
+  s->o_bytes = align256(parts * d * 4);
+  s->own_lse_bytes = align256(own_parts * 4);
+  s->own_o_bytes = align256(own_parts * d * 4);
+  return true;
+}
+
+}  // namespace cpattn
