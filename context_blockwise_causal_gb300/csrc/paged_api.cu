@@ -256,13 +256,8 @@ extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, con
 extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group) {
   if (check_decode(nullptr, b, hq, hkv, d, 0, 0) || check_groups(b, groups, max_group)) return 0;
   DeviceInfo* di = nullptr;
-  SharedShape s;
-  if (device_info(&di) || !shared_shape(&s, false, di->num_sms, b, hq, hkv, d, groups, max_group)) return 0;
-  size_t bytes = s.bytes();  // whichever kernel the call takes
-  if (may_be_few(int64_t(max_group) * (hq / hkv), max_group) &&
-      shared_shape(&s, true, di->num_sms, b, hq, hkv, d, groups, max_group))
-    bytes = std::max(bytes, s.bytes());
-  return bytes;
+  if (device_info(&di)) return 0;
+  return shared_forms(di->num_sms, b, hq, hkv, d, groups, max_group).bytes;  // whichever form the call takes
 }
 
 extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
@@ -277,11 +272,11 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
   if (!aligned4(shared) || !aligned4(group_offsets)) return CPATTN_ERR_MISALIGNED;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di))) return rc;
-  SharedShape shape;
-  const bool few = is_few(int64_t(max_group) * (hq / hkv), hkv, groups, max_group, capacity(pages));
-  if (!shared_shape(&shape, few, di->num_sms, b, hq, hkv, d, groups, max_group)) return CPATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < cpattn_decode_shared_workspace_bytes(b, hq, hkv, d, groups, max_group))
-    return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  const SharedForms forms = shared_forms(di->num_sms, b, hq, hkv, d, groups, max_group);
+  if (forms.bytes == 0) return CPATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < forms.bytes) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  const bool few = takes_few(forms, hq, hkv, groups, max_group, capacity(pages));
+  const SharedShape& shape = few ? forms.few : forms.prefix;
   PagedArgs pa;
   fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
   DecodeArgs& a = pa.d;

@@ -100,4 +100,27 @@ inline bool shared_shape(SharedShape* s, bool few, int num_sms, int b, int hq, i
   return true;
 }
 
+// The forms that a call may take, those whose results can be numbered, and the
+// workspace that holds either (0: the call is refused). One form may be there
+// without the other: 2^26 bounds the common keys' CTAs, which the prefix kernel
+// rounds up to whole SMs.
+struct SharedForms {
+  bool prefix_ok, few_ok;
+  SharedShape prefix, few;
+  size_t bytes;
+};
+inline SharedForms shared_forms(int num_sms, int b, int hq, int hkv, int d, int groups, int max_group) {
+  SharedForms f{};
+  f.prefix_ok = shared_shape(&f.prefix, false, num_sms, b, hq, hkv, d, groups, max_group);
+  f.few_ok = may_be_few(int64_t(max_group) * (hq / hkv), max_group) &&
+             shared_shape(&f.few, true, num_sms, b, hq, hkv, d, groups, max_group);
+  if (f.prefix_ok) f.bytes = f.prefix.bytes();
+  if (f.few_ok) f.bytes = std::max(f.bytes, f.few.bytes());
+  return f;
+}
+// Whether a call takes the form for few rows: by the rule where both are there.
+inline bool takes_few(const SharedForms& f, int hq, int hkv, int groups, int max_group, int64_t cap) {
+  return f.few_ok && (!f.prefix_ok || is_few(int64_t(max_group) * (hq / hkv), hkv, groups, max_group, cap));
+}
+
 }  // namespace cpattn
