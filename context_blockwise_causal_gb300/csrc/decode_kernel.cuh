@@ -26,10 +26,10 @@
 // shared memory: one launch and no workspace. More runs (a few very long
 // sequences) go through device memory and a second kernel.
 //
-// Measured, d128: 64 sequences of up to 16384 tokens, h32/8, window 4096: 154
-// us; 16 of up to 65537, h64/8, whole: 447 to 488 us (both at the measured copy
-// bandwidth and a few percent above it, as reads alone may be); one sequence,
-// h32/8, window 1024: 6.9 us, a launch and three rounds of loads.
+// Measured in captured graphs, caches cold, d128: 64 sequences of 8192 to 16384
+// tokens, h32/8, window 4096: 152 us; 16 of 32769 to 65537, h64/8, whole: 442 to
+// 447 (both above the measured copy bandwidth, as reads alone may be); one
+// sequence, h32/8, window 1024: 6.5 us, a launch and three rounds of loads.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -72,6 +72,11 @@ struct DecodeCfg {
   // warp; in warp 0's, behind it, the CTA's result for the cluster's join
   static constexpr int kResult = 16 * D * 4 + 16 * 8;
   static_assert(kResult + 16 * D * 4 + 16 * 4 <= kWarpBytes, "join buffers");
+  // CTAs that fit an SM by their shared memory. The compiler is told, so that it keeps registers for so many
+  // (194 and 122 a thread) instead of saving some for more: one sequence of 8192 keys, h32/8 d128, 16.5 -> 13.3
+  // us; 64 of 4096 to 8192, d64, 120.8 -> 118.2.
+  static constexpr int kPerSm = D == 64 ? 4 : 2;
+  static_assert(kPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
@@ -116,146 +121,10 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// A warp's part of a unit: up to 16 query heads as the rows of matrix tiles,
-// their running maximum and sum (rows g4 and g4 + 8 of the lane, the sum of its
-// own columns), and O.
-template <int D>
-struct DecodeRows {
-  static constexpr int kSteps = D / 16;  // 16-feature steps
-  uint32_t qf[kSteps][4];
-  float acc[D / 8][4];
-  float m[2], l[2];
-
-  // Q fragments (A operand) of `rows` heads from `qp`; the rows past them are zero.
-  __device__ __forceinline__ void load(const __nv_bfloat16* qp, int rows) {
-    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = g4 + (e & 1) * 8, c = s * 16 + (e >> 1) * 8 + 2 * c4;
-        qf[s][e] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + int64_t(r) * D + c) : 0u;
-      }
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
-  }
-
-  // One block of 16 keys, those in [from, to) of it visible. kat(r, p), vat(r, p):
-  // shared-memory address of 16-byte piece p of key r.
-  template <class K, class V>
-  __device__ __forceinline__ void block(K kat, V vat, int from, int to, float scale_log2) {
-    const int lane = threadIdx.x & 31, c4 = lane & 3;
-    // S = Q K^T: two 8-key column tiles. ldmatrix: lanes 0-7 and 8-15 address
-    // keys 0-7 at features +0 and +8, lanes 16-31 keys 8-15.
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      const int r = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint32_t kb[4];
-        ldmatrix4(kat(r, 2 * s + ((lane >> 3) & 1)), kb);
-        mma_16x8x16(s0, qf[s], kb[0], kb[1]);
-        mma_16x8x16(s1, qf[s], kb[2], kb[3]);
-      }
-    }
-    // columns 2*c4, +1 (s0: keys 0-7, s1: keys 8-15); [0], [1]: row g4, [2], [3]: row g4 + 8
-    float sc[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int col = 2 * c4 + (e & 1) + ((e >> 1) & 1) * 8;
-      sc[e] = col >= from && col < to ? sc[e] * scale_log2 : -INFINITY;
-    }
-    float alpha[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float mx = fmaxf(fmaxf(sc[4 * r], sc[4 * r + 1]), fmaxf(sc[4 * r + 2], sc[4 * r + 3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[r], mx);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      alpha[r] = ex2_approx(m[r] - base);
-      m[r] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sc[4 * r + e] = ex2_approx(sc[4 * r + e] - base);
-        sum += sc[4 * r + e];
-      }
-      l[r] = l[r] * alpha[r] + sum;
-    }
-    const uint32_t pf[4] = {pack_bf16x2(sc[0], sc[1]), pack_bf16x2(sc[4], sc[5]), pack_bf16x2(sc[2], sc[3]),
-                            pack_bf16x2(sc[6], sc[7])};
-    // O = alpha O + P V: V rows (keys) through transposing loads; lanes 0-15
-    // address the 16 keys at features +0, lanes 16-31 at +8
-    {
-      const int r = lane & 15;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        uint32_t vb[4];
-        ldmatrix4_trans(vat(r, 2 * s + (lane >> 4)), vb);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float(&c)[4] = acc[2 * s + t];
-          c[0] *= alpha[0];
-          c[1] *= alpha[0];
-          c[2] *= alpha[1];
-          c[3] *= alpha[1];
-          mma_16x8x16(c, pf, vb[2 * t], vb[2 * t + 1]);
-        }
-      }
-    }
-  }
-
-  // For the join of the CTA's warps: O [16][D], then m[16] and l[16], at jo.
-  __device__ __forceinline__ void store(float* jo) {
-    const int lane = threadIdx.x & 31, g4 = lane >> 2, c4 = lane & 3;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    float* jm = jo + 16 * D;
-#pragma unroll
-    for (int t = 0; t < D / 8; ++t) {
-      *reinterpret_cast<float2*>(jo + g4 * D + t * 8 + 2 * c4) = make_float2(acc[t][0], acc[t][1]);
-      *reinterpret_cast<float2*>(jo + (g4 + 8) * D + t * 8 + 2 * c4) = make_float2(acc[t][2], acc[t][3]);
-    }
-    if (c4 == 0) {
-      jm[g4] = m[0];
-      jm[g4 + 8] = m[1];
-      jm[16 + g4] = l[0];
-      jm[16 + g4 + 8] = l[1];
-    }
-  }
-};
-
 // A row's result in two features: values, and their log-sum-exp in base 2.
 struct DecodeResult {
   float o0, o1, l2;
 };
-// Joins the warps' parts of row r at features c, c + 1; those of warp w lie at
-// smem + w * warp_bytes.
-template <int D>
-__device__ __forceinline__ DecodeResult decode_join_warps(const uint8_t* smem, int warp_bytes, int r, int c) {
-  float mm = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w)
-    mm = fmaxf(mm, reinterpret_cast<const float*>(smem + w * warp_bytes)[16 * D + r]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    const float* p = reinterpret_cast<const float*>(smem + w * warp_bytes);
-    const float f = ex2_approx(p[16 * D + r] - base);
-    ll = fmaf(f, p[16 * D + 16 + r], ll);
-    o0 = fmaf(f, p[r * D + c], o0);
-    o1 = fmaf(f, p[r * D + c + 1], o1);
-  }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  return {o0 * inv, o1 * inv, ll == 0.f ? -INFINITY : mm + log2f(ll)};
-}
 // Joins the results of a cluster's n CTAs, each at shared-memory address res: O [16][D], then the 16 l2.
 template <int D>
 __device__ __forceinline__ DecodeResult decode_join_cluster(uint32_t res, int n, int r, int c) {
@@ -279,12 +148,14 @@ __device__ __forceinline__ DecodeResult decode_join_cluster(uint32_t res, int n,
 constexpr float kLn2 = 0.69314718055994530942f;
 
 template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kDecWarps * 32, DecodeCfg<D>::kPerSm) cpattn_decode_kernel(const DecodeArgs a) {
   if (a.nsplit > kDecMaxCluster) chain_next();
   using C = DecodeCfg<D>;
   constexpr int kPieces = D / 8;          // 16-byte pieces of a row
+  constexpr int kSteps = D / 16;          // 16-feature steps
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g4 = lane >> 2, c4 = lane & 3;
   // unit: (batch, KV head, group of 16 query rows), then the run of keys
   int x = blockIdx.x;
   const int split = x % a.nsplit;
@@ -343,8 +214,22 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
     cp_async_commit();
   }
 
-  DecodeRows<D> rows_of;
-  rows_of.load(a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D, rows);
+  // Q fragments (A operand): rows g4 and g4 + 8; rows past the group's heads are zero
+  uint32_t qf[kSteps][4];
+  {
+    const __nv_bfloat16* qp = a.q + int64_t(bi) * a.q_batch + int64_t(h0) * D;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = g4 + (e & 1) * 8, c = s * 16 + (e >> 1) * 8 + 2 * c4;
+        qf[s][e] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + int64_t(r) * D + c) : 0u;
+      }
+  }
+  float acc[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // rows g4, g4 + 8 (l: this thread's columns)
 
   for (int i = 0; i < mine; ++i) {
     cp_async_wait<kDecStages - 2>();
@@ -352,33 +237,124 @@ __global__ void __launch_bounds__(kDecWarps * 32) cpattn_decode_kernel(const Dec
     if (i + kDecStages - 1 < mine) load(i + kDecStages - 1);
     cp_async_commit();
     const uint32_t sk = ring + (i % kDecStages) * C::kStageBytes, sv = sk + C::kTileBytes;
+    // S = Q K^T: two 8-key column tiles. ldmatrix: lanes 0-7 and 8-15 address
+    // keys 0-7 at features +0 and +8, lanes 16-31 keys 8-15.
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int r = (lane & 7) + ((lane >> 4) << 3);
+      const uint32_t row = sk + r * D * 2;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int p = 2 * s + ((lane >> 3) & 1);
+        uint32_t kb[4];
+        ldmatrix4(row + ((p ^ (r & 7)) * 16), kb);
+        mma_16x8x16(s0, qf[s], kb[0], kb[1]);
+        mma_16x8x16(s1, qf[s], kb[2], kb[3]);
+      }
+    }
+    // columns 2*c4, +1 (s0: keys 0-7, s1: keys 8-15); [0], [1]: row g4, [2], [3]: row g4 + 8
     const int left = end - (begin + (warp + i * kDecWarps) * kDecBlock);
-    const auto at = [](uint32_t tile) {
-      return [tile](int r, int p) { return tile + r * D * 2 + ((p ^ (r & 7)) * 16); };
-    };
-    rows_of.block(at(sk), at(sv), 0, left, a.scale_log2);
+    float sc[8] = {s0[0], s0[1], s1[0], s1[1], s0[2], s0[3], s1[2], s1[3]};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = 2 * c4 + (e & 1) + ((e >> 1) & 1) * 8;
+      sc[e] = col < left ? sc[e] * a.scale_log2 : -INFINITY;
+    }
+    float alpha[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float mx = fmaxf(fmaxf(sc[4 * r], sc[4 * r + 1]), fmaxf(sc[4 * r + 2], sc[4 * r + 3]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[r], mx);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      alpha[r] = ex2_approx(m[r] - base);
+      m[r] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[4 * r + e] = ex2_approx(sc[4 * r + e] - base);
+        sum += sc[4 * r + e];
+      }
+      l[r] = l[r] * alpha[r] + sum;
+    }
+    const uint32_t pf[4] = {pack_bf16x2(sc[0], sc[1]), pack_bf16x2(sc[4], sc[5]), pack_bf16x2(sc[2], sc[3]),
+                            pack_bf16x2(sc[6], sc[7])};
+    // O = alpha O + P V: V rows (keys) through transposing loads; lanes 0-15
+    // address the 16 keys at features +0, lanes 16-31 at +8
+    {
+      const int r = lane & 15;
+      const uint32_t row = sv + r * D * 2;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int p = 2 * s + (lane >> 4);
+        uint32_t vb[4];
+        ldmatrix4_trans(row + ((p ^ (r & 7)) * 16), vb);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float(&c)[4] = acc[2 * s + t];
+          c[0] *= alpha[0];
+          c[1] *= alpha[0];
+          c[2] *= alpha[1];
+          c[3] *= alpha[1];
+          mma_16x8x16(c, pf, vb[2 * t], vb[2 * t + 1]);
+        }
+      }
+    }
     __syncwarp();  // all lanes have read the stage before the next turn refills it
   }
   cp_async_wait<0>();
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+  }
   __syncthreads();  // the rings are idle: reuse them for the join
-  rows_of.store(reinterpret_cast<float*>(smem + warp * C::kWarpBytes));
+  float* jo = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);  // [16][D], then m[16], l[16]
+  float* jm = jo + 16 * D;
+#pragma unroll
+  for (int t = 0; t < D / 8; ++t) {
+    *reinterpret_cast<float2*>(jo + g4 * D + t * 8 + 2 * c4) = make_float2(acc[t][0], acc[t][1]);
+    *reinterpret_cast<float2*>(jo + (g4 + 8) * D + t * 8 + 2 * c4) = make_float2(acc[t][2], acc[t][3]);
+  }
+  if (c4 == 0) {
+    jm[g4] = m[0];
+    jm[g4 + 8] = m[1];
+    jm[16 + g4] = l[0];
+    jm[16 + g4 + 8] = l[1];
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (D / 2); i += kDecWarps * 32) {
     const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-    const DecodeResult x = decode_join_warps<D>(smem, C::kWarpBytes, r, c);
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w)
+      mm = fmaxf(mm, reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[16 * D + r]);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float* p = reinterpret_cast<const float*>(smem + w * C::kWarpBytes);
+      const float f = ex2_approx(p[16 * D + r] - base);
+      ll = fmaf(f, p[16 * D + 16 + r], ll);
+      o0 = fmaf(f, p[r * D + c], o0);
+      o1 = fmaf(f, p[r * D + c + 1], o1);
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
     const int64_t row = int64_t(bi) * a.hq + h0 + r;
+    const float l2 = ll == 0.f ? -INFINITY : mm + log2f(ll);
     if (!bounds_ok(bi < a.b && h0 + r < a.hq, a.status)) continue;
     if (a.nsplit == 1) {
-      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(x.o0, x.o1);
-      if (c == 0) a.lse[row] = x.l2 * kLn2;
+      *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o0 * inv, o1 * inv);
+      if (c == 0) a.lse[row] = l2 * 0.69314718055994530942f;
     } else if (a.nsplit <= kDecMaxCluster) {
       float* res = reinterpret_cast<float*>(smem + C::kResult);
-      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(x.o0, x.o1);
-      if (c == 0) res[16 * D + r] = x.l2;
+      *reinterpret_cast<float2*>(res + r * D + c) = make_float2(o0 * inv, o1 * inv);
+      if (c == 0) res[16 * D + r] = l2;
     } else {
       const int64_t pr = row * a.nsplit + split;
-      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(x.o0, x.o1);
-      if (c == 0) a.part_lse[pr] = x.l2;
+      *reinterpret_cast<float2*>(a.part_o + pr * D + c) = make_float2(o0 * inv, o1 * inv);
+      if (c == 0) a.part_lse[pr] = l2;
     }
   }
   if (a.nsplit == 1 || a.nsplit > kDecMaxCluster) return;
@@ -428,7 +404,7 @@ __global__ void __launch_bounds__(128) cpattn_decode_join_kernel(const DecodeArg
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
     *reinterpret_cast<uint32_t*>(a.o + row * D + lane * kPer + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  if (lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994530942f;
 }
 
 }  // namespace cpattn
