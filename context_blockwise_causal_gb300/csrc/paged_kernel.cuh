@@ -56,10 +56,8 @@ struct PagedCfg {
   static constexpr int kTileBytes = kPagedRound * D * 2;  // keys or values of a round
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kStages = 3;
-  // CTAs that fit an SM with 8 heads to a unit (16 heads of 64: three). (d = 64 with six stages and two of
-  // them: 37 sequences of up to 2928 keys, 2 KV heads, 12.4 us instead of 10.7; 64 of
-  // 8192, 8 KV heads, 135 instead of 120.)
-  static constexpr int kPerSm = D == 128 ? 2 : 4;
+  // (d = 64 with six stages and two CTAs an SM: 64 sequences of 4096 to 8192 keys, 8 KV heads, 132 us instead of
+  // 125; 37 of 1464 to 2928, 2 KV heads, 12.5 either way.)
   // barriers (full and empty per stage) and the flag come first, the ring (1024-byte aligned) behind them
   static constexpr int kOffFlag = 2 * kStages * 8;
   static constexpr int kOffRing = 1024;
@@ -68,6 +66,7 @@ struct PagedCfg {
   static constexpr int kResult = 16 * D * 4 + 16 * 8;
   static constexpr int kJoinBytes = kStages * kStageBytes / kDecWarps;
   static_assert(kResult + 16 * D * 4 + 16 * 4 <= kJoinBytes, "join buffers");
+  static_assert(paged_per_sm(D, 8) * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // An 8x8 matrix of 16-bit elements, turned over (as ldmatrix lays them out).
@@ -215,7 +214,7 @@ enum class PagedKind { kWhole, kOwn, kBoth };
 
 // kT: rows of a unit in eights.
 template <int D, PagedKind kKind, int kT>
-__global__ void __launch_bounds__(kPagedThreads, kT == 1 ? PagedCfg<D>::kPerSm : 2)
+__global__ void __launch_bounds__(kPagedThreads, paged_per_sm(D, 8 * kT))
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
   constexpr bool kParts = kKind != PagedKind::kWhole;  // results go to the join kernel

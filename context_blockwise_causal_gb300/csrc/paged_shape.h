@@ -21,14 +21,20 @@ struct GroupRuns {
 // Rows of a unit: 8 where they suffice (half of the work), or 16.
 inline int unit_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
-// Runs over pages: the same rule, with twice the places at d = 64, and more runs
+// CTAs of the paged kernel that an SM holds: its launch bounds ask the compiler for registers for so many, and
+// no more fit (units of 16 heads of 64: five warps of 136 registers, of which three fit each quarter of an SM.
+// Counted as three CTAs an SM, 24 sequences of 1000 to 2000 keys, 2 KV heads, were cut into runs that took
+// two turns, 16.2 us; in one turn 10.5).
+constexpr int paged_per_sm(int d, int unit_rows) { return d == 64 && unit_rows == 8 ? 4 : 2; }
+
+// Runs over pages: the same rule, with the places of paged_per_sm, and more runs
 // than a cluster's 8 already from 2048 keys on, of 256 keys or 16 of them: the
 // kernel that joins them has four warps to a row and costs less than it saves.
 // One sequence, d 128, us in 8 / 16 / 32 / 64 runs: 4096 keys, 8 KV heads 9.5 / 8.1 / 8.5
 // / 12.1; 8192 keys 13.7 / 11.2 / 11.4 / 16.1, 1 KV head 11.9 / 8.2 / 6.6 / 6.8; 32768
 // keys 36.6 / 26.1 / 25.6 / 29.7, 1 KV head 34.4 / 20.5 / 13.3 / 10.7.
 inline int paged_split(int num_sms, int d, int G, int64_t units, int64_t keys) {
-  const int64_t places = int64_t(d == 128 ? 2 : unit_rows(G) == 8 ? 4 : 3) * num_sms;
+  const int64_t places = int64_t(paged_per_sm(d, unit_rows(G))) * num_sms;
   return choose_split(places, units, keys, keys < 2048 ? 0 : std::max<int64_t>(16, keys / 256));
 }
 
@@ -77,7 +83,7 @@ inline bool shared_shape(SharedShape* s, bool few, int num_sms, int b, int hq, i
   s->fixed_runs = 0;
   if (few) {
     // as many runs as fill the places that the own keys' CTAs leave
-    const int64_t places = int64_t(s->own_rows == 8 && d == 64 ? 4 : 2) * num_sms, own = own_units * s->own_runs;
+    const int64_t places = int64_t(paged_per_sm(d, s->own_rows)) * num_sms, own = own_units * s->own_runs;
     const int64_t runs = (places - std::min(own, places / 2)) / units;
     s->fixed_runs = int(runs < 1 ? 1 : runs > kDecMaxSplit ? kDecMaxSplit : runs);
     s->ctas = units * s->fixed_runs;

@@ -1,13 +1,21 @@
 // The shapes of calls over a cache in pages (csrc/paged_shape.h). Prints, for
 // each line "sms b hq hkv d groups max_group cap" of the input,
 //   <workspace asked for> <form: 0 prefix, 1 few, -1 refused> <CTAs> <rows kept of each> <runs of own keys>
+// and, with any argument, for each line "sms d G units keys" the runs of a call over whole sequences
 #include <cstdio>
 
 #include "../context_blockwise_causal_gb300/csrc/paged_shape.h"
 
 using namespace cpattn;
 
-int main() {
+int main(int argc, char**) {
+  if (argc > 1) {
+    int sms, d, G;
+    long long units, keys;
+    while (std::scanf("%d %d %d %lld %lld", &sms, &d, &G, &units, &keys) == 5)
+      std::printf("%d\n", paged_split(sms, d, G, units, keys));
+    return 0;
+  }
   int sms, b, hq, hkv, d, groups, most;
   long long cap;
   while (std::scanf("%d %d %d %d %d %d %d %lld", &sms, &b, &hq, &hkv, &d, &groups, &most, &cap) == 8) {

@@ -13,10 +13,14 @@ Shape = namedtuple("Shape", "bytes form ctas part_rows own_runs")
 
 
 @pytest.fixture(scope="module")
-def shapes(tmp_path_factory):
+def exe(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("shapes") / "paged_shape_check")
     subprocess.run(["g++", "-std=c++17", "-O2", os.path.join(HERE, "paged_shape_check.cpp"), "-o", exe], check=True)
+    return exe
 
+
+@pytest.fixture(scope="module")
+def shapes(exe):
     def run(cases):
         text = "\n".join(" ".join(map(str, c)) for c in cases)
         r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=300, check=True)
@@ -72,3 +76,17 @@ def test_the_tables_room_does_not_change_the_workspace(shapes):
     for b, hq, hkv, groups, most in ((4, 32, 8, 1, 4), (46, 24, 8, 5, 20), (16, 32, 8, 1, 16), (64, 32, 8, 1, 64)):
         got = shapes([(152, b, hq, hkv, 128, groups, most, cap) for cap in (16, 1024, 1 << 20, 1 << 30)])
         assert len({s.bytes for s in got}) == 1
+
+
+def test_runs_fill_the_places_that_there_are(exe):
+    """A quarter of an SM's registers holds 16384 / 32 threads' worth: units of 16
+    heads take 129 registers or more, so three of a CTA's five warps fit it
+    and two CTAs an SM; units of 8 heads of 64 stay within 102, four CTAs. Runs below
+    2048 keys never take a second turn for the sake of their number."""
+    cases = [(152, d, G, units, keys) for d in (64, 128) for G in (1, 8, 9, 16, 40) for units in (1, 2, 7, 19, 24, 40, 57, 100, 152, 300)
+             for keys in (100, 1000, 1500, 4000, 8000)]
+    r = subprocess.run([exe, "runs"], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True,
+                       timeout=60, check=True)
+    for (sms, d, G, units, keys), runs in zip(cases, map(int, r.stdout.split())):
+        places = sms * (4 if d == 64 and G <= 8 else 2)
+        assert runs == 1 or keys / runs >= 2048 or units * runs <= places, (d, G, units, keys, runs)
