@@ -714,7 +714,9 @@ def cpattn_decode_shared(q, k_pages, v_pages, tables, lengths, shared, group_off
     batch); ``max_group`` (default b): members of the largest group, which
     bounds the workspace. A sequence outside of every group, behind max_group
     others or with fewer tokens than its group shares is computed by itself.
-    Returns (o [b, hq, d], lse [b, hq])."""
+    For common parts that outweigh the sequences' own, and up to some dozens of
+    groups; otherwise cpattn_decode_paged is faster. Returns (o [b, hq, d],
+    lse [b, hq])."""
     return _done("cpattn_decode_shared", _native().decode_shared(
         library().calls, q, k_pages, v_pages, tables, lengths, shared, group_offsets, max_group, scale, o, lse, workspace,
         stream))

@@ -596,9 +596,20 @@ int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* len
  *             current device; 0 for a shape or device that is refused), 16-byte
  *             aligned, contents irrelevant. Calls that may overlap need one each.
  * shared and group_offsets are read on the device, so a captured call follows
- * them. Deterministic; bits depend on how the group's keys are cut into runs,
- * which follows from the counts and the number of SMs. Errors as cpattn_decode,
- * CUDA where the pools cannot be described to the copy engine.
+ * them. Deterministic; a row's bits depend on which kernel takes the common keys
+ * and on how keys are cut into runs, and so on every argument: the shapes,
+ * groups and max_group, the tables' room (table_cols * page_size), all lengths,
+ * counts and offsets, not only its own sequence's, and the number of SMs.
+ * Runs are made for common keys. A member's own keys take one run per KV head, or
+ * a few where b * hkv is below 32, so a call whose sequences hold far more keys
+ * of their own than their groups have in common belongs to cpattn_decode_paged
+ * (5 sequences, h32/8 d128, with 8192 to 32768 keys of their own behind 64 common
+ * ones: 262 us here, 67 there). With groups of more than 16 query rows to a KV
+ * head the kernel looks through all groups in every CTA: 100 groups are 10 us
+ * of that, 1000 are half a millisecond.
+ * Errors as cpattn_decode, CUDA where the pools cannot be described to the copy
+ * engine; INVALID_ARG also for more results than can be numbered (about 2^25
+ * units of 256 rows, of a group and KV head).
  */
 size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group);
 int cpattn_decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
