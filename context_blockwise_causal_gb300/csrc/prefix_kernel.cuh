@@ -484,12 +484,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t tS = tbase + lane_off + sub * kTile;
     const uint32_t tO = tbase + lane_off + C::kColO + sub * D;
     const float sl2 = a.scale_log2;
-    bool ok = true;
+    bool ok = true;  // (waits are the whole warp's: TMEM is read and written by all lanes or none)
     float m_used = -INFINITY, l = 0.f;
     const int mine = pair ? n : (n - sub + 1) / 2;  // tiles of this sub-tile
     for (int j = 0; j < mine; ++j) {
       const int t = pair ? j : 2 * j + sub;
-      if (!(ok = mbar_wait_bounded(&s_full[sub], j & 1, abort_flag, kWaitLimitNs))) break;
+      if (!(ok = mbar_wait_warp(&s_full[sub], j & 1, abort_flag, kWaitLimitNs))) break;
       tc_fence_after();
       float s[kTile];
       float m_raw;
@@ -566,9 +566,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       return reinterpret_cast<float4*>(sKV) + row * kChunks + (c ^ (row & (kChunks - 1)));
     };
     float2* sML = reinterpret_cast<float2*>(smem);
-    if (ok && mine > 0) ok = mbar_wait_bounded(&o_full[sub], 0, abort_flag, kWaitLimitNs);
+    if (ok && mine > 0) ok = mbar_wait_warp(&o_full[sub], 0, abort_flag, kWaitLimitNs);
     if (!pair) {
-      if (ok && n > 1) ok = mbar_wait_bounded(&o_full[1 - sub], 0, abort_flag, kWaitLimitNs);
+      if (ok && n > 1) ok = mbar_wait_warp(&o_full[1 - sub], 0, abort_flag, kWaitLimitNs);
       tc_fence_after();
       if (sub == 1 && ok && mine > 0) {  // (with one tile the queries may still be read)
 #pragma unroll
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
     tc_fence_after();
-    if (ok && !*abort_flag && (pair || sub == 0)) {
+    if (__all_sync(0xffffffffu, ok && !*abort_flag) && (pair || sub == 0)) {
       float w0 = 1.f, w1 = 0.f;
       const bool other = !pair && n > 1;
       if (other) {
