@@ -217,6 +217,8 @@ def _declare(lib):
     lib.cpattn_device_status.restype = _i
     lib.cpattn_selftest_abort.argtypes = [_p] * 10 + [_sz] + [_i] * 6 + [ctypes.c_ulonglong, _p]
     lib.cpattn_selftest_abort.restype = _i
+    lib.cpattn_selftest_abort_paged.argtypes = [_p] * 7 + [_sz] + [_i] * 4 + [_i64, ctypes.c_uint, _p]
+    lib.cpattn_selftest_abort_paged.restype = _i
     lib.cpattn_selftest_wait_timeout.argtypes = [ctypes.c_ulonglong, _p]
     lib.cpattn_selftest_wait_timeout.restype = _i
     lib.cpattn_strerror.argtypes = [_i]

@@ -15,6 +15,7 @@
 namespace cpattn {
 
 constexpr unsigned int kStatusPage = 1u << 17;
+constexpr uint32_t kAllWaits = 0xffffffffu;  // none of a copying warp's waits is made to run out (abort self-test)
 
 struct PagedPlace {
   const int* tables;  // [b][cols], rows tables_row apart

@@ -164,6 +164,102 @@ int launch_append(AppendArgs& a, DeviceInfo* di, cudaStream_t st) {
   return launched(launch_chained(cpattn_append_kernel<D, kInter>, ctas < most ? ctas : most, kQkThreads, st, a));
 }
 
+int decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse, void* workspace,
+                 size_t workspace_bytes, int b, int hq, int hkv, int d, int64_t q_batch, int window, int sinks,
+                 float scale, void* stream, uint32_t waits) {
+  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
+  if (rc) return rc;
+  if (!pages) return CPATTN_ERR_NULL_PTR;
+  if ((rc = check_decode(pages, b, hq, hkv, d, window, sinks))) return rc;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  PagedArgs pa;
+  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  DecodeArgs& a = pa.d;
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.nsplit = paged_split(di->num_sms, d, a.G, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
+  pa.join_warps = 4;
+  pa.copy_waits = waits;
+  const size_t need = workspace_for(b, hq, d, a.nsplit);
+  if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
+  if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int rows = unit_rows(a.G);
+  return d == 128 ? launch_paged<128, PagedKind::kWhole>(rows, pa, pages, di, st)
+                  : launch_paged<64, PagedKind::kWhole>(rows, pa, pages, di, st);
+}
+
+int decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
+                  const int* group_offsets, int groups, int max_group, void* o, float* lse, void* workspace,
+                  size_t workspace_bytes, int b, int hq, int hkv, int d, int64_t q_batch, float scale, void* stream,
+                  uint32_t waits) {
+  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
+  if (rc) return rc;
+  if (!pages || !shared || !workspace) return CPATTN_ERR_NULL_PTR;
+  if ((rc = check_decode(pages, b, hq, hkv, d, 0, 0)) || (rc = check_groups(b, groups, max_group))) return rc;
+  if (!group_offsets && groups != 1) return CPATTN_ERR_INVALID_ARG;
+  if (!aligned4(shared) || !aligned4(group_offsets)) return CPATTN_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di))) return rc;
+  const SharedForms forms = shared_forms(di->num_sms, b, hq, hkv, d, groups, max_group);
+  if (forms.bytes == 0) return CPATTN_ERR_INVALID_ARG;
+  if (workspace_bytes < forms.bytes) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
+  const bool few = takes_few(forms, hq, hkv, groups, max_group, capacity(pages));
+  const SharedShape& shape = few ? forms.few : forms.prefix;
+  PagedArgs pa;
+  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
+  DecodeArgs& a = pa.d;
+  a.nsplit = shape.own_runs;
+  a.row_groups = (a.G + shape.own_rows - 1) / shape.own_rows;
+  pa.join_warps = shape.join_warps;
+  pa.copy_waits = waits;
+  pa.common_ctas = few ? int(shape.ctas) : 0;
+  uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
+  const auto take = [&ws](size_t bytes) {
+    uint8_t* at = ws;
+    ws += bytes;
+    return at;
+  };
+  SharedPlan& sh = pa.sh;
+  sh.lengths = lengths;
+  sh.shared = shared;
+  sh.offsets = group_offsets;
+  sh.groups = groups;
+  sh.max_group = max_group;
+  sh.b = b;
+  sh.hkv = hkv;
+  sh.G = a.G;
+  sh.cap = a.cap;
+  sh.token_bytes = float(4 * d);
+  sh.ctas = int(shape.ctas);
+  sh.unit_rows = shape.unit_rows;
+  sh.fixed_runs = shape.fixed_runs;
+  sh.fixed_units = shape.fixed_units;
+  sh.part_rows = shape.part_rows;
+  sh.runs = reinterpret_cast<GroupRuns*>(take(shape.runs_bytes));
+  sh.part_lse = reinterpret_cast<float*>(take(shape.lse_bytes));
+  sh.part_o = reinterpret_cast<float*>(take(shape.o_bytes));
+  a.part_lse = reinterpret_cast<float*>(take(shape.own_lse_bytes));
+  a.part_o = reinterpret_cast<float*>(take(shape.own_o_bytes));
+  PrefixArgs p;
+  p.sh = sh;
+  p.pg = pa.pg;
+  p.q = a.q;
+  p.q_batch = q_batch;
+  p.hq = hq;
+  p.sms = di->num_sms;
+  p.box = std::gcd(pages->page_size, kTile);
+  p.scale_log2 = a.scale_log2;
+  p.status = di->status;
+  p.producer_waits = waits;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_shared<128>(few, shape.own_rows, pa, p, pages, di, st)
+                  : launch_shared<64>(few, shape.own_rows, pa, p, pages, di, st);
+}
+
 }  // namespace
 
 extern "C" int cpattn_append_paged(const cpattn_rows* k, const cpattn_rows* v, const cpattn_pages* pages,
@@ -229,28 +325,8 @@ extern "C" size_t cpattn_decode_paged_workspace_bytes(int b, int hq, int hkv, in
 extern "C" int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* lengths, void* o, float* lse,
                                    void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d,
                                    int64_t q_batch, int window, int sinks, float scale, void* stream) {
-  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
-  if (rc) return rc;
-  if (!pages) return CPATTN_ERR_NULL_PTR;
-  if ((rc = check_decode(pages, b, hq, hkv, d, window, sinks))) return rc;
-  DeviceInfo* di = nullptr;
-  if ((rc = device_info(&di))) return rc;
-  PagedArgs pa;
-  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
-  DecodeArgs& a = pa.d;
-  a.window = window;
-  a.sinks = window > 0 ? sinks : 0;
-  a.nsplit = paged_split(di->num_sms, d, a.G, int64_t(b) * hkv * a.row_groups, max_keys(a.cap, window, sinks));
-  pa.join_warps = 4;
-  const size_t need = workspace_for(b, hq, d, a.nsplit);
-  if (need > 0 && !workspace) return CPATTN_ERR_NULL_PTR;
-  if (workspace_bytes < need) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256(size_t(b) * hq * a.nsplit * d * 4));
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int rows = unit_rows(a.G);
-  return d == 128 ? launch_paged<128, PagedKind::kWhole>(rows, pa, pages, di, st)
-                  : launch_paged<64, PagedKind::kWhole>(rows, pa, pages, di, st);
+  return decode_paged(q, pages, lengths, o, lse, workspace, workspace_bytes, b, hq, hkv, d, q_batch, window, sinks, scale,
+                      stream, kAllWaits);
 }
 
 extern "C" size_t cpattn_decode_shared_workspace_bytes(int b, int hq, int hkv, int d, int groups, int max_group) {
@@ -264,64 +340,19 @@ extern "C" int cpattn_decode_shared(const void* q, const cpattn_pages* pages, co
                                     const int* group_offsets, int groups, int max_group, void* o, float* lse,
                                     void* workspace, size_t workspace_bytes, int b, int hq, int hkv, int d,
                                     int64_t q_batch, float scale, void* stream) {
-  int rc = check_pointers(q, lengths, o, lse, workspace, q_batch, scale);
-  if (rc) return rc;
-  if (!pages || !shared || !workspace) return CPATTN_ERR_NULL_PTR;
-  if ((rc = check_decode(pages, b, hq, hkv, d, 0, 0)) || (rc = check_groups(b, groups, max_group))) return rc;
-  if (!group_offsets && groups != 1) return CPATTN_ERR_INVALID_ARG;
-  if (!aligned4(shared) || !aligned4(group_offsets)) return CPATTN_ERR_MISALIGNED;
-  DeviceInfo* di = nullptr;
-  if ((rc = device_info(&di))) return rc;
-  const SharedForms forms = shared_forms(di->num_sms, b, hq, hkv, d, groups, max_group);
-  if (forms.bytes == 0) return CPATTN_ERR_INVALID_ARG;
-  if (workspace_bytes < forms.bytes) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
-  const bool few = takes_few(forms, hq, hkv, groups, max_group, capacity(pages));
-  const SharedShape& shape = few ? forms.few : forms.prefix;
-  PagedArgs pa;
-  fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);
-  DecodeArgs& a = pa.d;
-  a.nsplit = shape.own_runs;
-  a.row_groups = (a.G + shape.own_rows - 1) / shape.own_rows;
-  pa.join_warps = shape.join_warps;
-  pa.common_ctas = few ? int(shape.ctas) : 0;
-  uint8_t* ws = reinterpret_cast<uint8_t*>(align256(reinterpret_cast<uintptr_t>(workspace)));
-  const auto take = [&ws](size_t bytes) {
-    uint8_t* at = ws;
-    ws += bytes;
-    return at;
-  };
-  SharedPlan& sh = pa.sh;
-  sh.lengths = lengths;
-  sh.shared = shared;
-  sh.offsets = group_offsets;
-  sh.groups = groups;
-  sh.max_group = max_group;
-  sh.b = b;
-  sh.hkv = hkv;
-  sh.G = a.G;
-  sh.cap = a.cap;
-  sh.token_bytes = float(4 * d);
-  sh.ctas = int(shape.ctas);
-  sh.unit_rows = shape.unit_rows;
-  sh.fixed_runs = shape.fixed_runs;
-  sh.fixed_units = shape.fixed_units;
-  sh.part_rows = shape.part_rows;
-  sh.runs = reinterpret_cast<GroupRuns*>(take(shape.runs_bytes));
-  sh.part_lse = reinterpret_cast<float*>(take(shape.lse_bytes));
-  sh.part_o = reinterpret_cast<float*>(take(shape.o_bytes));
-  a.part_lse = reinterpret_cast<float*>(take(shape.own_lse_bytes));
-  a.part_o = reinterpret_cast<float*>(take(shape.own_o_bytes));
-  PrefixArgs p;
-  p.sh = sh;
-  p.pg = pa.pg;
-  p.q = a.q;
-  p.q_batch = q_batch;
-  p.hq = hq;
-  p.sms = di->num_sms;
-  p.box = std::gcd(pages->page_size, kTile);
-  p.scale_log2 = a.scale_log2;
-  p.status = di->status;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_shared<128>(few, shape.own_rows, pa, p, pages, di, st)
-                  : launch_shared<64>(few, shape.own_rows, pa, p, pages, di, st);
+  return decode_shared(q, pages, lengths, shared, group_offsets, groups, max_group, o, lse, workspace, workspace_bytes, b, hq,
+                       hkv, d, q_batch, scale, stream, kAllWaits);
+}
+
+// Self-test of the abort path: as the two calls, but the copying warps give up
+// at their next wait for free room after so many.
+extern "C" int cpattn_selftest_abort_paged(const void* q, const cpattn_pages* pages, const int* lengths,
+                                           const int* shared, void* o, float* lse, void* workspace,
+                                           size_t workspace_bytes, int b, int hq, int hkv, int d, int64_t q_batch,
+                                           unsigned int waits, void* stream) {
+  if (!shared)
+    return decode_paged(q, pages, lengths, o, lse, workspace, workspace_bytes, b, hq, hkv, d, q_batch, 0, 0, 0.f, stream,
+                        waits);
+  return decode_shared(q, pages, lengths, shared, nullptr, 1, b, o, lse, workspace, workspace_bytes, b, hq, hkv, d, q_batch,
+                       0.f, stream, waits);
 }

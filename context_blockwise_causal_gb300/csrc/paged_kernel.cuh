@@ -47,6 +47,7 @@ struct PagedArgs {
   int common_ctas;  // kBoth
   int join_warps;   // of the join kernel, to a row
   int box;          // tokens of a copy: gcd(page_size, 32)
+  uint32_t copy_waits;  // the copying warp gives up at the wait for a free stage after so many (kAllWaits: never)
 };
 
 constexpr int kPagedRound = kDecWarps * kDecBlock;  // keys of a round
@@ -317,10 +318,17 @@ __global__ void __launch_bounds__(kPagedThreads, paged_per_sm(D, 8 * kT))
     bool ok = true;
     int t = 0, stage = 0;
     uint32_t turn = 0;  // of the ring
+    uint32_t waits = pa.copy_waits;
     for (; t < rounds; ++t) {
       int next_slot = 0, next_page = 0;
       const bool next_on = look(t + 1, next_slot, next_page);
-      if (turn > 0 && !(ok = mbar_wait_warp_lean(&empty[stage], (turn - 1) & 1, abort_flag, kWaitLimitNs))) break;
+      if (turn > 0) {
+        ok = waits-- > 0 && mbar_wait_warp_lean(&empty[stage], (turn - 1) & 1, abort_flag, kWaitLimitNs);
+        if (!ok) {
+          *abort_flag = 1;
+          break;
+        }
+      }
       if (on) page_ok(page, pa.pg, a.status);  // (a copy from outside of the pool brings zeros)
       const int count = __popc(__ballot_sync(0xffffffffu, on));
       if (lane == 0) mbar_arrive_expect_tx(&full[stage], uint32_t(count * box_bytes));

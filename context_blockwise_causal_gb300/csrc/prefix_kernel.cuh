@@ -54,6 +54,7 @@ struct PrefixArgs {
   int sms;
   float scale_log2;
   unsigned int* status;
+  uint32_t producer_waits;  // as PagedArgs::copy_waits, of the producer's for free slots
 };
 
 template <int D>
@@ -298,11 +299,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         return t < n && lane < boxes && key < run->keys ? table[unsigned(key) / unsigned(a.pg.page_size)] : 0;
       };
       bool ok = true;
-      uint32_t nload = 0;
+      uint32_t nload = 0, waits = a.producer_waits;
       // Tile t's keys or values into the next slot of the ring, from this lane's page.
       const auto load = [&](const CUtensorMap* map, int t, int page) {
         const uint32_t slot = nload % slots, turn = nload / slots;
-        if (turn > 0 && !mbar_wait_warp(&kv_empty[slot], (turn - 1) & 1, abort_flag, kWaitLimitNs)) return false;
+        if (turn > 0 && !(waits-- > 0 && mbar_wait_warp(&kv_empty[slot], (turn - 1) & 1, abort_flag, kWaitLimitNs))) {
+          *abort_flag = 1;
+          return false;
+        }
         const int key = key0 + t * kTile;
         const int live = t < n - 1 ? boxes : (tail + a.box - 1) / a.box;  // boxes that hold common keys
         if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], uint32_t(live) * a.box * (D * 2));

@@ -693,6 +693,19 @@ int cpattn_selftest_abort(const void* q, const void* k, const void* v, void* o, 
                           int hq, int hkv, int d, int cp, unsigned long long limit_ns, void* stream);
 
 /*
+ * The same for single-token attention over pages: cpattn_decode_paged over
+ * every key (shared NULL), or cpattn_decode_shared with the batch as one group,
+ * whose copying warps act as if the wait for free room that follows their first
+ * `waits` had run out. Status bits as for the calls: 4, or 0 to 2 where the
+ * common keys have a kernel of their own; bit 3 would say that a wait for what
+ * had been asked for ran out. The outputs are left incomplete. Arguments
+ * otherwise as those calls, with the default scale.
+ */
+int cpattn_selftest_abort_paged(const void* q, const cpattn_pages* pages, const int* lengths, const int* shared,
+                                void* o, float* lse, void* workspace, size_t workspace_bytes, int b, int hq, int hkv,
+                                int d, int64_t q_batch, unsigned int waits, void* stream);
+
+/*
  * Checked builds (libcpattn_checked.so, compiled with -DCPATTN_CHECKS; the
  * library's debug form in place of a memory checker): every kernel tests the
  * rows, heads and vector positions of its global accesses against the
