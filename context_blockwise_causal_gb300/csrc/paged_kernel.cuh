@@ -16,9 +16,15 @@
 // scores by the mask, and values, whose product with a weight of zero would
 // still be NaN if they are not finite, by zeros written over them.
 //
-// P is rounded to bf16 for its product, as everywhere in the package (2.0e-3 to
-// 2.3e-3 relative L2 of O with its own rounding, which alone is 1.7e-3); sums,
-// maxima and joins are fp32.
+// P enters its product in two bf16 pieces, the rounded value and what the rounding
+// left, for whole sequences: their products have time to spare. Relative L2
+// of O 1.66e-3 to 1.68e-3, its own rounding and no more, with one piece
+// 2.0e-3 to 2.2e-3; it costs 0.2 to 1.5 % with 8 heads or fewer to a KV head (one
+// sequence of 8192 keys 11.3 -> 11.45 us, 16 of 32K to 64K keys 469 -> 471), 2 to 4 %
+// with 16 (120 of 1000 to 2000 keys, d 64, 15.8 -> 16.45). Where common keys are
+// computed, here and in prefix_kernel.cuh, P is rounded to one piece, as by the other
+// attention kernels (2.1e-3 to 2.3e-3): units of many rows have no such time
+// (32 rows behind 8192 keys 17.5 -> 18.6 us). Sums, maxima and joins are fp32.
 //
 // HBM-bound where there are sequences enough: 16 of 32K to 64K keys, h64/8 d128,
 // 456 us (reads at 1.06 of the measured copy bandwidth, which counts writes
@@ -109,8 +115,9 @@ struct DecodeCols {
   }
 
   // One block of 16 keys, those in [from, to) of it visible. kat(r, p), vat(r, p):
-  // shared-memory address of 16-byte piece p of key r.
-  template <class K, class V>
+  // shared-memory address of 16-byte piece p of key r. kPieces: bf16 pieces that P has
+  // in its product.
+  template <int kPieces, class K, class V>
   __device__ __forceinline__ void block(K kat, V vat, int from, int to, float scale_log2) {
     const int lane = threadIdx.x & 31, g4 = lane >> 2;
     // two chains of products for each tile, which are added: half as long
@@ -130,7 +137,7 @@ struct DecodeCols {
       }
     }
     float alpha[kT][2];
-    uint32_t p0[kT], p1[kT];
+    uint32_t p0[kPieces][kT], p1[kPieces][kT];
     bool moved = false;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
@@ -157,8 +164,16 @@ struct DecodeCols {
         x[2 + h] = ex2_approx(x[2 + h] - base);
         l[t][h] = l[t][h] * alpha[t][h] + (x[h] + x[2 + h]);
       }
-      p0[t] = turn_8x8(pack_bf16x2(x[0], x[1]));
-      p1[t] = turn_8x8(pack_bf16x2(x[2], x[3]));
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const uint32_t lo = pack_bf16x2(x[0], x[1]), hi = pack_bf16x2(x[2], x[3]);
+        p0[c][t] = turn_8x8(lo);
+        p1[c][t] = turn_8x8(hi);
+        x[0] -= __uint_as_float(lo << 16);  // exact
+        x[1] -= __uint_as_float(lo & 0xffff0000u);
+        x[2] -= __uint_as_float(hi << 16);
+        x[3] -= __uint_as_float(hi & 0xffff0000u);
+      }
     }
     if (__any_sync(0xffffffffu, moved)) {  // seldom, after a few blocks
 #pragma unroll
@@ -178,7 +193,9 @@ struct DecodeCols {
         uint32_t vb[4];
         ldmatrix4_trans(vat(r, 2 * s + ((lane >> 3) & 1)), vb);
 #pragma unroll
-        for (int t = 0; t < kT; ++t) mma_16x8x16(acc[t][s], vb, p0[t], p1[t]);
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) mma_16x8x16(acc[t][s], vb, p0[c][t], p1[c][t]);
       }
     }
   }
@@ -219,7 +236,7 @@ __global__ void __launch_bounds__(kPagedThreads, paged_per_sm(D, 8 * kT))
     cpattn_decode_paged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                const __grid_constant__ PagedArgs pa) {
   constexpr bool kParts = kKind != PagedKind::kWhole;  // results go to the join kernel
-  constexpr int kRows = 8 * kT;
+  constexpr int kRows = 8 * kT, kPieces = kParts ? 1 : 2;
   const DecodeArgs& a = pa.d;
   using C = PagedCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -390,7 +407,7 @@ __global__ void __launch_bounds__(kPagedThreads, paged_per_sm(D, 8 * kT))
           };
         };
         const uint32_t tile = smem_u32(sk);
-        part.block(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
+        part.template block<kPieces>(at(tile), at(tile + C::kTileBytes), from, to, a.scale_log2);
         __syncwarp();  // all lanes have read the stage
       }
       if (lane == 0) mbar_arrive(&empty[stage]);
