@@ -207,7 +207,11 @@ int decode_shared(const void* q, const cpattn_pages* pages, const int* lengths, 
   const SharedForms forms = shared_forms(di->num_sms, b, hq, hkv, d, groups, max_group);
   if (forms.bytes == 0) return CPATTN_ERR_INVALID_ARG;
   if (workspace_bytes < forms.bytes) return CPATTN_ERR_WORKSPACE_TOO_SMALL;
-  const bool few = takes_few(forms, hq, hkv, groups, max_group, capacity(pages));
+  const SharedForm form = shared_form(forms, hq, hkv, groups, max_group, capacity(pages));
+  if (form == SharedForm::kAlone)  // (so many sequences need no workspace)
+    return decode_paged(q, pages, lengths, o, lse, workspace, workspace_bytes, b, hq, hkv, d, q_batch, 0, 0, scale, stream,
+                        waits);
+  const bool few = form == SharedForm::kFew;
   const SharedShape& shape = few ? forms.few : forms.prefix;
   PagedArgs pa;
   fill_decode(&pa, q, pages, lengths, o, lse, b, hq, hkv, d, q_batch, scale, di);

@@ -124,9 +124,20 @@ inline SharedForms shared_forms(int num_sms, int b, int hq, int hkv, int d, int 
   if (f.few_ok) f.bytes = std::max(f.bytes, f.few.bytes());
   return f;
 }
-// Whether a call takes the form for few rows: by the rule where both are there.
-inline bool takes_few(const SharedForms& f, int hq, int hkv, int groups, int max_group, int64_t cap) {
-  return f.few_ok && (!f.prefix_ok || is_few(int64_t(max_group) * (hq / hkv), hkv, groups, max_group, cap));
+
+// The form that a call takes. Every CTA of the prefix kernel looks through all
+// groups (prefix_plan), some 36 us of them for 1000, and there are as many CTAs as
+// groups: so groups of few rows take the other form from 129 on (5 sequences of
+// 4 heads behind 256 keys, d 64, us by the prefix kernel and the other one: 64 groups
+// 14.6 and 12.5, 256 61 and 33, 1000 488 and 125, 4000 7600 and 515; 16 of them behind 2048,
+// 8 KV heads, d 128: 128 groups 619 and 691, 256 1465 and 1382, 1000 11100 and 5470), and
+// sequences of more than 1024 larger groups are computed by themselves.
+constexpr int kManyGroups = 128, kPlanGroups = 1024;
+enum class SharedForm { kPrefix, kFew, kAlone };
+inline SharedForm shared_form(const SharedForms& f, int hq, int hkv, int groups, int max_group, int64_t cap) {
+  if (f.few_ok && (!f.prefix_ok || groups > kManyGroups || is_few(int64_t(max_group) * (hq / hkv), hkv, groups, max_group, cap)))
+    return SharedForm::kFew;
+  return groups > kPlanGroups ? SharedForm::kAlone : SharedForm::kPrefix;
 }
 
 }  // namespace cpattn

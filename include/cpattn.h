@@ -604,9 +604,9 @@ int cpattn_decode_paged(const void* q, const cpattn_pages* pages, const int* len
  * a few where b * hkv is below 32, so a call whose sequences hold far more keys
  * of their own than their groups have in common belongs to cpattn_decode_paged
  * (5 sequences, h32/8 d128, with 8192 to 32768 keys of their own behind 64 common
- * ones: 262 us here, 67 there). With groups of more than 16 query rows to a KV
- * head the kernel looks through all groups in every CTA: 100 groups are 10 us
- * of that, 1000 are half a millisecond.
+ * ones: 262 us here, 67 there), and so does one of hundreds of groups with short
+ * common parts. Members of more than 1024 groups of more than 64 query rows to
+ * a KV head (or more than 32 members) are all computed by themselves.
  * Errors as cpattn_decode, CUDA where the pools cannot be described to the copy
  * engine; INVALID_ARG also for more results than can be numbered (about 2^25
  * units of 256 rows, of a group and KV head).

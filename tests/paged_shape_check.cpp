@@ -1,6 +1,6 @@
 // The shapes of calls over a cache in pages (csrc/paged_shape.h). Prints, for
 // each line "sms b hq hkv d groups max_group cap" of the input,
-//   <workspace asked for> <form: 0 prefix, 1 few, -1 refused> <CTAs> <rows kept of each> <runs of own keys>
+//   <workspace asked for> <form: 0 prefix, 1 few, 2 sequences by themselves, -1 refused> <CTAs> <rows kept of each> <runs of own keys>
 // and, with any argument, for each line "sms d G units keys" the runs of a call over whole sequences
 #include <cstdio>
 
@@ -24,8 +24,15 @@ int main(int argc, char**) {
       std::printf("0 -1 0 0 0\n");
       continue;
     }
-    const bool few = takes_few(f, hq, hkv, groups, most, cap);
-    const SharedShape& s = few ? f.few : f.prefix;
-    std::printf("%zu %d %lld %d %d\n", f.bytes, few ? 1 : 0, static_cast<long long>(s.ctas), s.part_rows, s.own_runs);
+    const SharedForm form = shared_form(f, hq, hkv, groups, most, cap);
+    const SharedShape& s = form == SharedForm::kFew ? f.few : f.prefix;
+    if (form == SharedForm::kAlone) {
+      const int G = hq / hkv;
+      const int runs = paged_split(sms, d, G, int64_t(b) * hkv * ((G + unit_rows(G) - 1) / unit_rows(G)), cap);
+      std::printf("%zu 2 0 0 %d\n", f.bytes, runs > kDecMaxCluster ? runs : 0);  // (runs whose results need a workspace)
+      continue;
+    }
+    std::printf("%zu %d %lld %d %d\n", f.bytes, form == SharedForm::kFew ? 1 : 0, static_cast<long long>(s.ctas), s.part_rows,
+                s.own_runs);
   }
 }

@@ -37,6 +37,9 @@ def _agrees(case, s):
     if s.form < 0:
         assert s.bytes == 0
         return
+    if s.form == 2:  # as cpattn_decode_paged, in so few runs that they need none
+        assert s.own_runs == 0 and groups > 1024
+        return
     rows = s.ctas * s.part_rows + b * hq * s.own_runs
     assert s.bytes >= groups * 8 + rows * (d + 1) * 4, case
     assert 0 < s.ctas < 1 << 26 and s.ctas + b * hq * s.own_runs < 1 << 31
@@ -69,7 +72,18 @@ def test_workspace_of_all_sorts_of_shapes(shapes):
     got = shapes(cases)
     for c, s in zip(cases, got):
         _agrees(c, s)
-    assert {s.form for s in got} == {-1, 0, 1}
+    assert {s.form for s in got} == {-1, 0, 1, 2}
+
+
+def test_no_kernel_looks_through_more_groups_than_pays(shapes):
+    """Every CTA of the prefix kernel looks through all groups, of which there
+    may be as many as CTAs: 128 of few rows, 1024 of others at most."""
+    cases = [(152, g * most, 4 * hkv, hkv, d, g, most, cap) for g in (1, 100, 128, 129, 1000, 1024, 1025, 5000, 60000) for hkv in (1, 8)
+             for d in (64, 128) for most in (5, 16, 17, 40) for cap in (256, 131072) if g * most * 4 * hkv < 1 << 24]
+    for c, s in zip(cases, shapes(cases)):
+        _agrees(c, s)
+        groups, most = c[5], c[6]
+        assert s.form in ((1,) if most <= 16 and groups > 128 else (0, 1) if groups <= 1024 else (2,)), (c, s)
 
 
 def test_the_tables_room_does_not_change_the_workspace(shapes):

@@ -70,19 +70,22 @@ def test_group_offsets_outside_of_the_batch(offsets, hq):
         _check(q, k, v, tables, lengths, 0, 0, None, **out)
 
 
-def test_hundreds_of_groups():
-    """More groups than a warp has lanes many times over, of 20 rows each."""
-    groups, size, hq, hkv, d = [5] * 230, 16, 4, 1, 64
-    prefix = [(i * 29) % 70 for i in range(230)]
-    k, v, tables, lengths, offsets = _group_state(groups, prefix, [i % 4 for i in range(1150)], size, hq, hkv, d, False, 221)
-    q = _randn(1150, hq, d, seed=224)
+@pytest.mark.parametrize("count,members,hq", [(110, 5, 4), (230, 5, 4), (230, 2, 40), (1030, 2, 34)])
+def test_hundreds_of_groups(count, members, hq):
+    """More groups than a warp has lanes many times over: of 20 rows, in either
+    kernel, and of 80, and so many that their sequences share nothing."""
+    groups, size, hkv, d = [members] * count, 16, 1, 64
+    b, prefix = count * members, [(i * 29) % 70 for i in range(count)]
+    k, v, tables, lengths, offsets = _group_state(groups, prefix, [i % 4 for i in range(b)], size, hq, hkv, d, False, 221)
+    q = _randn(b, hq, d, seed=224)
     kd, vd = _hide(k.cuda(), v.cuda(), tables, lengths, 0, 0)
-    out = _outputs(1150, hq, d)
-    cpattn_decode_shared(q.cuda(), kd, vd, tables.cuda(), _i32(lengths).cuda(), _i32(prefix).cuda(),
-                         group_offsets=offsets.cuda(), max_group=5, **out)
-    torch.cuda.synchronize()
-    assert _status() == 0
-    _check(q, k, v, tables, lengths, 0, 0, None, **out)
+    for t in (tables, _wide(tables, 131072, size)):
+        out = _outputs(b, hq, d)
+        cpattn_decode_shared(q.cuda(), kd, vd, t.cuda(), _i32(lengths).cuda(), _i32(prefix).cuda(),
+                             group_offsets=offsets.cuda(), max_group=members, **out)
+        torch.cuda.synchronize()
+        assert _status() == 0
+        _check(q, k, v, tables, lengths, 0, 0, None, **out)
 
 
 @pytest.mark.parametrize("hq,hkv", [(16, 8), (36, 2)])
