@@ -200,10 +200,13 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
       const int per = (tiles + gruns - 1) / gruns;  // no run is empty: per <= len
       r.tile0 = run * per;
       r.tiles = tiles - r.tile0 < per ? tiles - r.tile0 : per;
-      // the first member that holds all of the common tokens names their pages
-      for (int m0 = 0; m0 < size; m0 += 32) {
+      // The first of the unit's members that holds all of the common tokens names
+      // their pages; without one, nobody reads the unit's results. (The whole
+      // group's members may be many, and each CTA would look through them.)
+      const int end = (r.row0 + r.rows - 1) / s.G + 1;
+      for (int m0 = r.row0 / s.G; m0 < end; m0 += 32) {
         const int m = m0 + lane;
-        const unsigned full = __ballot_sync(0xffffffffu, m < size && s.lengths[first + m] >= r.keys);
+        const unsigned full = __ballot_sync(0xffffffffu, m < end && s.lengths[first + m] >= r.keys);
         if (full) {
           r.table = first + m0 + __ffs(full) - 1;
           r.go = 1;

@@ -99,3 +99,22 @@ def test_long_own_parts_behind_a_short_common_one(hq, hkv):
     torch.cuda.synchronize()
     assert _status() == 0
     _check(q, k, v, tables, lengths, 0, 0, None, **out)
+
+
+@pytest.mark.parametrize("hq,d", [(2, 64), (3, 128), (300, 64)])
+def test_units_whose_members_have_finished(hq, d):
+    """The first members of a large group have finished, and all of those of a
+    later unit of 256 rows; a unit's pages are named by one of its own."""
+    b, p, size = (400 if hq < 100 else 6), 200, 32
+    k, v, tables, lengths, _ = _group_state([b], [p], [i % 5 for i in range(b)], size, hq, 1, d, False, 241)
+    gone = list(range(0, b // 3)) + list(range(b // 2, b - 1))
+    for i in gone:
+        lengths[i] = (0, p - 1, 7)[i % 3]
+        tables[i, -(-lengths[i] // size):] = -1
+    q = _randn(b, hq, d, seed=244)
+    kd, vd = _hide(k.cuda(), v.cuda(), tables, lengths, 0, 0)
+    out = _outputs(b, hq, d)
+    cpattn_decode_shared(q.cuda(), kd, vd, tables.cuda(), _i32(lengths).cuda(), _i32([p]).cuda(), **out)
+    torch.cuda.synchronize()
+    assert _status() == 0
+    _check(q, k, v, tables, lengths, 0, 0, None, **out)
