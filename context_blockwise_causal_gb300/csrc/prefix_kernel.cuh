@@ -118,18 +118,22 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     }
     return x;
   };
+  // Whether the SMs are shared with the own keys' kernel (units take at most half
+  // of them); with more units nobody asks how long the sequences are.
+  const bool shares = s.ctas == sms;
   // (the first lengths are on their way while the groups' loads are waited for)
   int head[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) head[k] = lane + 32 * k < s.b ? s.lengths[lane + 32 * k] : 0;
+  for (int k = 0; k < 4; ++k) head[k] = shares && lane + 32 * k < s.b ? s.lengths[lane + 32 * k] : 0;
   const Group mine = of(lane);
   float held[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) held[k] = float(head[k]);
-  for (int i = lane + 128; i < s.b; i += 128)
+  if (shares)
+    for (int i = lane + 128; i < s.b; i += 128)
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + 32 * k < s.b) held[k] += float(s.lengths[i + 32 * k]);
+      for (int k = 0; k < 4; ++k)
+        if (i + 32 * k < s.b) held[k] += float(s.lengths[i + 32 * k]);
   // work of all groups, in tiles and in row tiles; own keys (as if every member shared)
   float total = 0.f, rows = 0.f, own = (held[0] + held[1]) + (held[2] + held[3]);
   unsigned units = 0;
@@ -148,7 +152,7 @@ __device__ __forceinline__ PrefixRun prefix_plan(const SharedPlan& s, int cta, i
     own += __shfl_xor_sync(0xffffffffu, own, o);
   }
   int ctas = s.ctas;
-  if (ctas == sms) {  // (units take at most half of them)
+  if (shares) {
     const float own_bytes = fmaxf(own, 0.f) * float(s.hkv) * s.token_bytes;
     ctas = int(prefix_share(rows * row_tile_ns, own_bytes, sms) * float(sms));
     ctas = ctas < int(units) ? int(units) : ctas;
