@@ -10,10 +10,11 @@
 // launch. A token's heads, queries, keys and values in one run, stay with one
 // warp, or spread over several when tokens are few; the warp looks up where its
 // token goes once and loads its next rows, of its next token too, while it
-// works on these. Measured: one token of 32 + 8 + 8 heads of 128 takes 2.5 us, 128
-// sequences' tokens 2.9, 5331 tokens of 6 + 2 + 2 heads of 64 in seven chunks 6.6 (2
-// us of copying; the rest is the launch and loads that wait for one another:
-// offsets, length, page), 32768 tokens 125 us, 0.96 of the measured copy bandwidth.
+// works on these. Measured in captured graphs, caches cold: one token of 32 + 8 + 8
+// heads of 128 takes 2.7 us, 128 sequences' tokens 4.1 (2.9 where they lie in L2), 5331
+// tokens of 6 + 2 + 2 heads of 64 in seven chunks 8.0 (6.7; 2 us of copying; the rest
+// is the launch and loads that wait for one another: offsets, length, page), 32768
+// tokens 125.5 us, 0.96 of the measured copy bandwidth.
 // Looking up several tokens at once, a lane each, is no faster (6.9 and 128 us: a
 // warp's tokens then have to follow one another).
 #pragma once

@@ -20,15 +20,15 @@ inline int64_t max_keys(int cap, int window, int sinks) {
 // Runs per (sequence, KV head group), for places CTAs at once: two fit an SM.
 //  * As many as fill the places without a second wave, of 64 keys or more (one
 //    round of a CTA's warps), up to a cluster: 8 of one 1028-key sequence with
-//    8 KV heads take 6.7 us, 4 take 7.7; with 8 such sequences 4 take 9.6 us
-//    and 8, a second wave, 15.5.
+//    8 KV heads take 6.5 us, 4 take 7.1; with 8 such sequences 4 take 10.7 us
+//    and 8, a second wave, 16.9.
 //  * Runs of 2048 keys or more may fill the places twice, which levels out
-//    different lengths: 16 sequences of 32K to 64K keys take 447 us in 4 runs,
-//    507 in 2 and 465 in 8.
+//    different lengths: 16 sequences of 32K to 64K keys take 442 us in 4 runs,
+//    478 in 2 and 453 in 8.
 //  * Where a cluster's 8 leave half of the places empty, such long runs go up
 //    to all places through device memory (one 131K-key sequence, 8 KV heads:
-//    92 us in 38 runs with their join, 188 in 8). Clusters of 16 find too few
-//    places together (122 us there).
+//    91 us in 38 runs with their join, 132 in 8). Clusters of 16 find too few
+//    places together.
 inline int choose_split(int64_t places, int64_t units, int64_t keys, int64_t long_runs) {
   int64_t s = 1;
   while (2 * s <= kDecMaxCluster) {

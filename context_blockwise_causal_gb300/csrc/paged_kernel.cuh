@@ -27,11 +27,11 @@
 // (32 rows behind 8192 keys 17.5 -> 18.6 us). Sums, maxima and joins are fp32.
 //
 // HBM-bound where there are sequences enough: 16 of 32K to 64K keys, h64/8 d128,
-// 456 us (reads at 1.06 of the measured copy bandwidth, which counts writes
+// 471 us (reads at 1.02 of the measured copy bandwidth, which counts writes
 // too), 64 with a window of 4096, h32/8, pages of 16, 157 us (1.03). A few short
 // ones are bound by what waits for one another: length, table, first copy, some
-// rounds of 0.5 us, the joins (one sequence of 8192 keys 9 us, 37 of up to 2928, 2
-// KV heads of 64, 11.9).
+// rounds of 0.5 us, the joins (one sequence of 8192 keys, h32/8, 11.5 us, 9.0 where the
+// keys lie in L2; 37 of 1464 to 2928, 2 KV heads of 64, 12.6).
 #pragma once
 #include <cuda_bf16.h>
 

@@ -30,9 +30,14 @@ constexpr int paged_per_sm(int d, int unit_rows) { return d == 64 && unit_rows =
 // Runs over pages: the same rule, with the places of paged_per_sm, and more runs
 // than a cluster's 8 already from 2048 keys on, of 256 keys or 16 of them: the
 // kernel that joins them has four warps to a row and costs less than it saves.
-// One sequence, d 128, us in 8 / 16 / 32 / 64 runs: 4096 keys, 8 KV heads 9.5 / 8.1 / 8.5
-// / 12.1; 8192 keys 13.7 / 11.2 / 11.4 / 16.1, 1 KV head 11.9 / 8.2 / 6.6 / 6.8; 32768
-// keys 36.6 / 26.1 / 25.6 / 29.7, 1 KV head 34.4 / 20.5 / 13.3 / 10.7.
+// One sequence, d 128, us in 8 / 16 / 32 / 64 runs (captured graphs, caches cold): 4096
+// keys, 8 KV heads 9.6 / 8.65 / 9.15 / 13.2, 1 KV head 9.4 / 7.4 / 6.8 / 7.3; 8192 keys
+// 13.7 / 11.1 / 11.3 / 15.8 and 13.2 / 9.3 / 7.8 / 7.95; 32768 keys 36.3 / 25.9 / 25.4 /
+// 29.4 (in the 38 that the rule takes 26.5) and 35.7 / 20.5 / 13.4 / 11.0.
+// `keys` is what the tables have room for, since the lengths are on the device:
+// wide tables are cut as if they were full. 16 sequences of 500 to 1000 keys, 64/8 heads,
+// take 14.65 us in two runs each with tables for 1000, 19.4 in four, which take two turns,
+// with tables for 131072; one of 1000 keys, 32/8 heads, 7.2 and 7.8.
 inline int paged_split(int num_sms, int d, int G, int64_t units, int64_t keys) {
   const int64_t places = int64_t(paged_per_sm(d, unit_rows(G))) * num_sms;
   return choose_split(places, units, keys, keys < 2048 ? 0 : std::max<int64_t>(16, keys / 256));
@@ -41,12 +46,15 @@ inline int paged_split(int num_sms, int d, int G, int64_t units, int64_t keys) {
 // Common keys by the prefix kernel, whose matrix tiles have 128 rows, or, for
 // groups of few rows, by the kernel that reads the own keys, a unit of its
 // rows at a time: 16 rows behind 8192 keys of 8 heads (d 128, up to 256 own keys
-// each) take 13.2 us there and 19.1 by the prefix kernel, 8 groups of 16 behind
-// 2048 23.2 and 26.8. More rows are more units that read the same keys, which pays
-// where there are few of those: 32 rows behind 8192 keys 17.3 and 19.4, behind 32768
-// 45 and 36; 64 rows behind 1024 keys 9.8 and 13.3, behind 20000 of one head 12.8
-// and 15.0, behind 8192 of 8 heads 36 and 20. How many keys there are is
-// known here only as the tables' room for them.
+// each) take 12.8 us there and 18.3 by the prefix kernel, 8 groups of 16 behind
+// 2048 24.0 and 35.0. More rows are more units that read the same keys, which pays
+// where there are few of those: 32 rows behind 1024 keys 8.7 and 12.8, behind 8192 17.4
+// and 19.0, behind 32768 45.5 and 34.7; 64 rows behind 1024 keys 10.1 and 14.0, behind
+// 20000 of one head 13.2 and 15.5, behind 8192 of 8 heads 35.6 and 20.2. The border is
+// where the rounds take longer than the prefix kernel's plan, 128-row tiles and
+// stores: 64 keys of a unit are 0.5 us of one of 304 places, 300000 keys of all units 7.7
+// us of the call. How many keys there are is known here only as the tables' room for
+// them: behind wide tables 32 rows take the prefix kernel whatever they share.
 constexpr int kFewRows = 64, kFewMembers = 32;
 inline bool may_be_few(int64_t rows, int max_group) { return rows <= kFewRows && max_group <= kFewMembers; }
 inline bool is_few(int64_t rows, int hkv, int groups, int max_group, int64_t cap) {
@@ -67,13 +75,15 @@ inline bool shared_shape(SharedShape* s, bool few, int num_sms, int b, int hq, i
   if (rows >= int64_t(1) << 30) return false;
   // Few rows of one group: units of 8 though they read the common keys twice, since
   // theirs are the shorter rounds and the own keys need no more (16 rows behind 8192
-  // keys: 13.2 us, in one unit 16.0). Of several groups: units of 16, which leave more runs to each
-  // (8 groups of 16 rows behind 2048 keys: 23.2 us, with 8 rows 25.3).
+  // keys: 12.8 us, in one unit 15.8). Of several groups: units of 16, which leave more runs to each
+  // (8 groups of 16 rows behind 2048 keys: 23.9 us, with 8 rows 25.9).
   s->own_rows = unit_rows(few && groups > 1 ? rows : G);
   const int64_t own_units = int64_t(b) * hkv * ((G + s->own_rows - 1) / s->own_rows);
   // Own keys are mostly few, and how many is not known here: runs only where
   // sequences are few (64 sequences behind 32768 tokens, up to 1024 of their own: 66
-  // us in one run each, 71 in two; 256 behind 16384, up to 2048: 241 and 254).
+  // us in one run each, 71 in two; 256 behind 16384, up to 2048: 243 and 254). Where
+  // they are many this is slow: 5 sequences, 8 KV heads, of 2048 own keys at most 21 us, of
+  // 32768 265; over whole sequences 11 and 67.
   s->own_runs = 1;
   while (s->own_runs < kDecMaxCluster && 2 * s->own_runs * own_units <= 64) s->own_runs *= 2;
   s->unit_rows = few ? s->own_rows : kSharedRows;

@@ -5,8 +5,8 @@
 // rows of one matrix product: |group| G of them against the group's common
 // keys, 4 d flops a row and key for 4 d bytes a key. So few rows are HBM-bound,
 // and from about 290 on (measured peaks) the tensor cores are the limit; single
-// rows' matrix tiles, as in decode_kernel.cuh, would read the keys again for
-// each member. The members' own keys and the join are that kernel's.
+// rows' matrix tiles, as in paged_kernel.cuh, would read the keys again for
+// each member. The members' own keys and the join are that file's kernels'.
 //
 // One CTA per run (see SharedPlan): a unit of up to 256 rows and some of its
 // key tiles of 128. The warps' roles, TMEM and the online softmax are the
@@ -34,7 +34,7 @@
 // the first scores (queries and first keys of all CTAs come at once), 2 us to
 // store. 64 sequences behind 32768 tokens with up to 1024 of their own, h32/8: 66
 // us with the own keys and the join (45 us of bytes); 256 behind 16384 with up to
-// 2048, h64/8: 250 us (212).
+// 2048, h64/8: 242 to 250 us (212).
 #pragma once
 #include <cuda_bf16.h>
 
